@@ -96,7 +96,11 @@ typedef enum {
 typedef enum { TQ_FMT_B3 = 0, TQ_FMT_2B = 1, TQ_FMT_BP = 2, TQ_FMT_B3R = 3 } tq_format;
 typedef enum { TQ_F16 = 0, TQ_F32 = 1 } tq_dtype;
 
+/* How tq_kv_append pairs the rotated elements: element i with i + rot / 2, or 2i with 2i + 1. */
+typedef enum { TQ_ROPE_HALVES = 0, TQ_ROPE_PAIRS = 1 } tq_rope_mode;
+
 #define TQ_GROUP 128
+#define TQ_KV_PAGE 64 /* tokens of a cache page, which share a scale */
 #define TQ_BLOCK_ROWS 64
 #define TQ_GEMV_MAX_M 16
 #define TQ_STACK_MAX_ROWS 4 /* token rows of tq_decode_stack_batch */
@@ -392,7 +396,125 @@ size_t tq_gemm_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K);
 int tq_gemm(int fmt, int64_t M, int64_t N, int64_t K, const void *W, const int8_t *q,
             const float *a_scale, float *y, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- device: between the projections of a layer ------------------------
+ *
+ * A decoder layer's steps between its QKV and O projections and around its
+ * blocks: the quantised key/value cache and the attention over it (the pages
+ * run their model with FlashAttention over a quantised KV cache, "Ternary
+ * Bonsai 2 27B：8GB 显卡硬塞 27B 三元模型…"), and the residual norm.
+ *
+ * The paged 8-bit cache.  A page holds TQ_KV_PAGE consecutive tokens of one
+ * sequence for every KV head; page_table[seqs][max_pages] (int32) names the
+ * page of tokens 64 i .. 64 i + 63 of a sequence.
+ *   k_cache  uint8 [num_pages][kv_heads][64][head_dim]
+ *   v_cache  uint8 [num_pages][kv_heads][head_dim][64]   (token fastest)
+ *   k_scale, v_scale  fp32 [num_pages][kv_heads]
+ * A byte b stands for (b - 127.5) * scale: tq_kv_append's scales are powers
+ * of two (0 for a page of zeros only), and a value is within scale / 2 of
+ * what was appended.  The cache needs no initial contents.
+ *
+ * Rows.  cu_rows[seqs + 1] (int32, ascending from 0): sequence s has rows
+ * cu_rows[s] .. cu_rows[s+1] - 1 of the call, possibly none; rows behind
+ * cu_rows[seqs] are padding and are neither read nor written.  kv_len[seqs]
+ * (int32): tokens of the sequence including the call's rows, so its rows
+ * take the last positions, kv_len[s] - n .. kv_len[s] - 1.  These arrays are
+ * read on the device, so a graph that was captured once serves changing
+ * lengths.  A bad entry (a page outside 0..num_pages-1, a position below 0,
+ * behind the page table or behind the rope table, cu_rows out of order)
+ * leads to no access outside the arrays: such tokens are not stored and not
+ * seen, and a query row at such a position is written as zeros by
+ * tq_kv_append.
+ *
+ * Heads: head_dim 64 or 128 (else TQ_ERR_SHAPE), q_heads a multiple of
+ * kv_heads; query head h reads KV head h / (q_heads / kv_heads). */
+
+/* Host: table[positions][rot] of fp32, cos(p base^(-2i/rot)) for i < rot / 2,
+ * then the sines, from angles in double.  rot a multiple of 8, 8..128;
+ * base > 1 and finite (TQ_ERR_VALUE). */
+int tq_rope_table(int64_t positions, int64_t rot, double base, float *table);
+
+/* Append the keys and values of `rows` new rows to the cache, rotating
+ * queries and keys by their positions.  Row r of qkv (dtype TQ_F16 or
+ * TQ_F32, row_stride elements apart, a multiple of 8) holds q_heads query
+ * heads, kv_heads key heads and kv_heads value heads of head_dim elements, as
+ * the QKV projection writes them.  The first rot elements (a multiple of 8;
+ * 0: no rotation, rope may be NULL) of each query and key head are turned:
+ *   (a, b) -> (a c - b s, b c + a s),   c, s = rope[position][i], [rot/2 + i]
+ * with pairs as rope_mode says, each result rounded once to fp32.  Rotated
+ * queries go to q_out (rounded on to fp16, [rows][q_heads][head_dim]; NULL: none are made).
+ * A page's scale becomes the smallest power of two with max |x| < 128 scale
+ * over its tokens and codes are floor(x / scale) + 128; where a token needs
+ * a larger scale the page's earlier codes are shifted to it, so the cache
+ * holds the same bytes however its tokens were cut into calls.  Bytes of
+ * slots behind the sequence's last token keep what they held.
+ * Two sequences of a call must not append to the same page (its contents
+ * are then unspecified); full pages may be shared.  A token at a page's
+ * start begins the page anew: rewriting a sequence from such a position (or,
+ * with the page's scale kept at least as large, from any) is allowed.
+ * Non-finite keys or values leave that page and head unspecified.  qkv,
+ * rope, the caches and q_out 16-byte aligned. */
+int tq_kv_append(int dtype, int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                 int64_t head_dim, const void *qkv, int64_t row_stride, const float *rope,
+                 int64_t rope_rows, int64_t rot, int rope_mode, const int32_t *cu_rows,
+                 const int32_t *kv_len, const int32_t *page_table, int64_t max_pages,
+                 uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale,
+                 int64_t num_pages, void *q_out, void *stream);
+
+/* Workspace bytes of tq_kv_attn (0 when the keys are not split, or on a bad
+ * shape); same zero-fill rule as tq_gemv_workspace_bytes. */
+size_t tq_kv_attn_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                                  int64_t head_dim, int64_t max_kv_len);
+
+/* Attention of the rows over the cache, causal:
+ *   out[r][h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(softmax_scale q[r][h] . k_j)
+ * over the keys j <= position of r and, with window > 0, j > position -
+ * window or j < sinks (the first tokens, visible from everywhere).  A row
+ * that sees no key gives zeros.  q and out fp16, rows q_stride and
+ * out_stride elements apart (multiples of 8), 16-byte aligned; out may be
+ * q itself (same stride).  Scales of the cache may be any finite
+ * non-negative fp32.  Sums, maxima and outputs are held in fp32.
+ * max_kv_len: the largest kv_len of the call, which sets how the keys are
+ * split over workgroups (a larger kv_len gives the same results more
+ * slowly).  softmax_scale > 0 and finite, window and sinks >= 0
+ * (TQ_ERR_VALUE).  The result does not depend on the order in which
+ * workgroups finish.  One launch. */
+int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+               const void *q, int64_t q_stride, const int32_t *cu_rows, const int32_t *kv_len,
+               const int32_t *page_table, int64_t max_pages, const uint8_t *k_cache,
+               const uint8_t *v_cache, const float *k_scale, const float *v_scale,
+               int64_t num_pages, int64_t max_kv_len, float softmax_scale, int64_t window,
+               int64_t sinks, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
+               void *stream);
+
+/* The step from one block to the next, rms(v) = sqrt(mean v^2 + eps):
+ *   u  = y / rms(y) * post_w         (post_w NULL: u = y; y NULL: no block, r' = res)
+ *   r' = res + res_scale * gate * u  rounded to fp32, then to res_dtype, to res_out
+ *   x  = r' / rms(r') * pre_w        rounded to fp32 (pre_w NULL: ones)
+ * with every sum and product in double.  Outputs of x, either or both:
+ * x (x_dtype TQ_F16 or TQ_F32), and q, a_scale: fp32 x quantised per row by
+ * a = max |x| to a_scale = a / 127 and q = clamp(rint(x * (127 * (1 / a))),
+ * -127, 127), zeros for a = 0 (tq_quant_act but for the reciprocal: its code
+ * is the same or, for x at a rounding border, one step away).  gate (y_dtype; NULL: ones) has one row of H values
+ * for all rows (gate_stride 0) or rows gate_stride >= H elements apart (a
+ * multiple of 4 when H is).  y, res and outputs [M][H] contiguous, y and
+ * gate of y_dtype, res and res_out of res_dtype; post_w, pre_w fp32 [H].
+ * res_out may be res, and may be NULL when y is (else TQ_ERR_NULL, as is
+ * post_w or gate without y, or no output at all).  1 <= H <= 32768, any M.
+ * eps >= 0 (TQ_ERR_VALUE).  All arrays 16-byte aligned, a_scale 4-byte. */
+int tq_residual_norm(int y_dtype, int res_dtype, int x_dtype, int64_t M, int64_t H, const void *y,
+                     const float *post_w, const void *gate, int64_t gate_stride, double res_scale,
+                     const void *res, void *res_out, const float *pre_w, double eps, void *x,
+                     int8_t *q, float *a_scale, void *stream);
+
 /* ---- device: parity hooks (same decode / integer core as above) ------- */
+
+/* What `n` pages of the cache stand for: values[2][n][kv_heads][64][head_dim]
+ * (keys, then values; dtype TQ_F16, rounded, or TQ_F32, exact) of the pages
+ * named by pages[n] (device int32; zeros for one outside the cache). */
+int tq_debug_kv_read(int dtype, int64_t n, int64_t kv_heads, int64_t head_dim,
+                     const int32_t *pages, const uint8_t *k_cache, const uint8_t *v_cache,
+                     const float *k_scale, const float *v_scale, int64_t num_pages, void *values,
+                     void *stream);
 
 /* trits[N][K] (int8, device) decoded on the GPU with the decode kernels'
  * per-format decoder (B3 digit table, 2B code masks, BP plane masks). */

@@ -24,7 +24,10 @@ TQ_FMT_B3R = 3  # B3 bytes in row-major group order (the layout without the re-t
 TQ_F16 = 0
 TQ_F32 = 1
 TQ_STREAM_READ_WGS = 8192
+TQ_ROPE_HALVES = 0  # rotated pairs: element i with i + rot / 2
+TQ_ROPE_PAIRS = 1   # ... 2i with 2i + 1
 GROUP = 128
+KV_PAGE = 64
 GEMV_MAX_M = 16
 STACK_MAX_ROWS = 4
 
@@ -41,7 +44,9 @@ EXPORTS = ("tq_status_str", "tq_packed_bytes", "tq_pack", "tq_unpack", "tq_quant
            "tq_debug_gemv_quant_sums", "tq_decode_stack_persistent",
            "tq_gemv_noalloc", "tq_noalloc_scratch_bytes",
            "tq_decode_stack_batch_workspace_bytes", "tq_decode_stack_batch",
-           "tq_debug_gemv_quant_rows_sums", "tq_workspace_clear", "tq_workspace_check")
+           "tq_debug_gemv_quant_rows_sums", "tq_workspace_clear", "tq_workspace_check",
+           "tq_rope_table", "tq_kv_append", "tq_kv_attn_workspace_bytes", "tq_kv_attn",
+           "tq_residual_norm", "tq_debug_kv_read")
 
 
 class TqLayer(ctypes.Structure):
@@ -61,6 +66,7 @@ def _load():
         raise ImportError(f"libtq.so not built ({LIB_PATH}); run ternary_weight_base_amd/build.py")
     L = ctypes.CDLL(LIB_PATH)
     P, I64, SZ, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    F, F64 = ctypes.c_float, ctypes.c_double
     sig = {
         "tq_status_str": ([I], ctypes.c_char_p),
         "tq_packed_bytes": ([I, I64, I64], SZ),
@@ -91,6 +97,14 @@ def _load():
         "tq_debug_gemv_quant_sums": ([I, I64, I64, P, P, I, P, P, I64, P, P, P], I),
         "tq_workspace_clear": ([P, SZ, P], I),
         "tq_workspace_check": ([P, SZ, P, P], I),
+        "tq_rope_table": ([I64, I64, F64, P], I),
+        "tq_kv_append": ([I, I64, I64, I64, I64, I64, P, I64, P, I64, I64, I, P, P, P, I64, P, P, P, P, I64, P,
+                          P], I),
+        "tq_kv_attn_workspace_bytes": ([I64, I64, I64, I64, I64, I64], SZ),
+        "tq_kv_attn": ([I64, I64, I64, I64, I64, P, I64, P, P, P, I64, P, P, P, P, I64, I64, F, I64, I64, P, I64,
+                        P, SZ, P], I),
+        "tq_residual_norm": ([I, I, I, I64, I64, P, P, P, I64, F64, P, P, P, F64, P, P, P, P], I),
+        "tq_debug_kv_read": ([I, I64, I64, I64, P, P, P, P, P, I64, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -335,6 +349,172 @@ def tq_decode_stack_batch(fmt, rows, layers, hidden, inter, qkv_out, o_in, weigh
                                      ctypes.cast(arr, ctypes.c_void_p), _ptr(x_in), _ptr(a_in),
                                      _ptr(y_qkv), _ptr(y_o), _ptr(h), _ptr(y_out), _ptr(ffn_signs),
                                      wp, wb, _stream(stream)), "tq_decode_stack_batch")
+
+
+# ---- device: between the projections of a layer --------------------------
+
+def tq_rope_table(positions: int, rot: int, base: float) -> np.ndarray:
+    """fp32 [positions][2][rot/2] (host): cosines and sines of each position's angles."""
+    t = np.empty((max(positions, 1), 2, max(rot // 2, 1)), dtype=np.float32)
+    _check(lib.tq_rope_table(positions, rot, base, t.ctypes.data), "tq_rope_table")
+    return t
+
+
+def _act_dtypes():
+    import torch
+    return {torch.float16: TQ_F16, torch.float32: TQ_F32}
+
+
+def _args(what, *specs):
+    """Checks (name, tensor or None, dtype, shape) of a call's tensors: the
+    dtype, the shape (None: any length), contiguity, and that all are on the
+    current GPU, whose stream the call takes.  Raises ValueError."""
+    import torch
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for name, t, dtype, shape in specs:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise ValueError(f"{what}: {name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+        if t.get_device() != cur:
+            raise ValueError(f"{what}: {name} must be on the current GPU (cuda:{cur}), got {t.device}")
+        got = t.shape
+        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+            raise ValueError(f"{what}: {name} must have shape {list(shape)}, got {list(got)}")
+
+
+def _row_view(what, name, t):
+    """The distance of the rows of t [rows][...]: all but the first axis contiguous."""
+    want = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != want:
+            raise ValueError(f"{what}: {name} must be contiguous within a row")
+        want *= n
+    return t.stride(0) if t.shape[0] > 1 else want
+
+
+def _cache_args(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale):
+    import torch
+    if k_cache.dim() != 4:
+        raise ValueError(f"{what}: k_cache must have shape [pages][kv_heads][{KV_PAGE}][head_dim]")
+    pages, heads, _, dim = k_cache.shape
+    seqs = kv_len.numel()
+    i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+    _args(what, ("cu_rows", cu_rows, i32, (seqs + 1,)), ("kv_len", kv_len, i32, (seqs,)),
+          ("page_table", page_table, i32, (seqs, None)), ("k_cache", k_cache, u8, (pages, heads, KV_PAGE, dim)),
+          ("v_cache", v_cache, u8, (pages, heads, dim, KV_PAGE)), ("k_scale", k_scale, f32, (pages, heads)),
+          ("v_scale", v_scale, f32, (pages, heads)))
+    return pages, heads, dim, seqs
+
+
+def tq_kv_append(qkv, rope, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, q_out=None,
+                 rope_mode=TQ_ROPE_HALVES, q_heads=None, stream=None) -> None:
+    """Append the rows of qkv [rows][(q_heads + 2 kv_heads) head_dim] (fp16 or
+    fp32; rows may be strided) to the paged cache, rotating keys and queries
+    by rope [positions][2][rot/2] (fp32, as tq_rope_table; None: no rotation);
+    the rotated queries go to q_out fp16 [rows][q_heads][head_dim].  q_heads is
+    needed only without q_out and where qkv's rows are longer than the heads."""
+    import torch
+    what = "tq_kv_append"
+    pages, heads, dim, seqs = _cache_args(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
+    if qkv.dim() != 2:
+        raise ValueError(f"{what}: qkv must have two dimensions")
+    rows, width = qkv.shape
+    if q_heads is None:
+        q_heads = q_out.shape[1] if q_out is not None and q_out.dim() == 3 else width // dim - 2 * heads
+    if width != (q_heads + 2 * heads) * dim:
+        raise ValueError(f"{what}: qkv rows must hold {(q_heads + 2 * heads) * dim} values, got {width}")
+    stride = _row_view(what, "qkv", qkv)
+    _args(what, ("qkv", qkv[:1], qkv.dtype, (None, width)), ("q_out", q_out, torch.float16, (rows, q_heads, dim)),
+          ("rope", rope, torch.float32, (None, 2, None)))
+    rope_rows, rot = (0, 0) if rope is None else (rope.shape[0], 2 * rope.shape[2])
+    _check(lib.tq_kv_append(_act_dtypes().get(qkv.dtype, -1), rows, seqs, q_heads, heads, dim, qkv.data_ptr(), stride,
+                            _ptr(rope), rope_rows, rot, rope_mode, cu_rows.data_ptr(), kv_len.data_ptr(),
+                            page_table.data_ptr(), page_table.shape[1], k_cache.data_ptr(), v_cache.data_ptr(),
+                            k_scale.data_ptr(), v_scale.data_ptr(), pages, _ptr(q_out), _stream(stream)), what)
+
+
+def tq_kv_attn_workspace_bytes(rows, seqs, q_heads, kv_heads, head_dim, max_kv_len) -> int:
+    return int(lib.tq_kv_attn_workspace_bytes(rows, seqs, q_heads, kv_heads, head_dim, max_kv_len))
+
+
+def kv_attn_workspace(rows, seqs, q_heads, kv_heads, head_dim, max_kv_len, device="cuda"):
+    """A zero-filled workspace tensor for tq_kv_attn (None when it needs none)."""
+    import torch
+    nbytes = tq_kv_attn_workspace_bytes(rows, seqs, q_heads, kv_heads, head_dim, max_kv_len)
+    return torch.zeros((nbytes + 15) // 16 * 4, dtype=torch.int32, device=device) if nbytes else None
+
+
+def tq_kv_attn(q, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, out, max_kv_len,
+               softmax_scale=None, window=0, sinks=0, ws=None, stream=None) -> None:
+    """out = attention of q over the cache, both fp16 [rows][q_heads][head_dim]
+    (rows may be strided).  max_kv_len: the largest kv_len (a host number).
+    softmax_scale defaults to head_dim ** -0.5; window > 0 limits a row to its
+    last `window` keys and the first `sinks` ones."""
+    import torch
+    what = "tq_kv_attn"
+    pages, heads, dim, seqs = _cache_args(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 3 or q.shape != out.shape or q.shape[2] != dim:
+        raise ValueError(f"{what}: q and out must have shape [rows][q_heads][{dim}]")
+    rows, q_heads = q.shape[:2]
+    qs, os_ = _row_view(what, "q", q), _row_view(what, "out", out)
+    _args(what, ("q", q[:1], torch.float16, (None, q_heads, dim)), ("out", out[:1], torch.float16, (None, q_heads, dim)))
+    wp, wb = _ws(ws)
+    if ws is not None and ws.get_device() != q.get_device():
+        raise ValueError(f"{what}: ws must be on the current GPU")
+    _check(lib.tq_kv_attn(rows, seqs, q_heads, heads, dim, q.data_ptr(), qs, cu_rows.data_ptr(), kv_len.data_ptr(),
+                          page_table.data_ptr(), page_table.shape[1], k_cache.data_ptr(), v_cache.data_ptr(),
+                          k_scale.data_ptr(), v_scale.data_ptr(), pages, max_kv_len,
+                          dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, out.data_ptr(), os_,
+                          wp, wb, _stream(stream)), what)
+
+
+def tq_residual_norm(y, res, res_out, pre_w=None, x=None, q=None, a_scale=None, post_w=None, gate=None,
+                     res_scale=1.0, eps=1e-6, stream=None) -> None:
+    """res_out = res + res_scale * gate * norm(y; post_w); x (fp16 / fp32) and / or
+    q, a_scale (int8, fp32 [M]) = norm(res_out; pre_w).  All [M][H]; gate [H] or
+    [M][H] (rows may be strided); y None: norm(res) only."""
+    import torch
+    what = "tq_residual_norm"
+    if res.dim() != 2:
+        raise ValueError(f"{what}: res must have two dimensions")
+    M, H = res.shape
+    f32, acts = torch.float32, _act_dtypes()
+    yt = res.dtype if y is None else y.dtype
+    _args(what, ("res", res, res.dtype, (M, H)), ("y", y, yt, (M, H)), ("res_out", res_out, res.dtype, (M, H)),
+          ("x", x, f32 if x is None else x.dtype, (M, H)), ("q", q, torch.int8, (M, H)), ("a_scale", a_scale, f32, (M,)),
+          ("post_w", post_w, f32, (H,)), ("pre_w", pre_w, f32, (H,)))
+    gate_stride = 0
+    if gate is not None:
+        if gate.dim() == 2:
+            if gate.shape[0] != M:
+                raise ValueError(f"{what}: gate must have {M} rows, got {gate.shape[0]}")
+            gate_stride = _row_view(what, "gate", gate)
+            _args(what, ("gate", gate[:1], yt, (None, H)))
+        else:
+            _args(what, ("gate", gate, yt, (H,)))
+    _check(lib.tq_residual_norm(acts.get(yt, -1), acts.get(res.dtype, -1), TQ_F32 if x is None else acts.get(x.dtype, -1),
+                                M, H, _ptr(y), _ptr(post_w), None if gate is None else gate.data_ptr(), gate_stride,
+                                res_scale, res.data_ptr(), _ptr(res_out), _ptr(pre_w), eps, _ptr(x), _ptr(q),
+                                _ptr(a_scale), _stream(stream)), what)
+
+
+def tq_debug_kv_read(pages, k_cache, v_cache, k_scale, v_scale, values, stream=None) -> None:
+    """values (fp16 / fp32 [2][n][kv_heads][64][head_dim]) of the cache pages named by pages (int32 [n])."""
+    import torch
+    what = "tq_debug_kv_read"
+    if k_cache.dim() != 4 or pages.dim() != 1:
+        raise ValueError(f"{what}: k_cache must have four dimensions, pages one")
+    num, heads, _, dim = k_cache.shape
+    n, u8, f32 = pages.numel(), torch.uint8, torch.float32
+    _args(what, ("pages", pages, torch.int32, (n,)), ("k_cache", k_cache, u8, (num, heads, KV_PAGE, dim)),
+          ("v_cache", v_cache, u8, (num, heads, dim, KV_PAGE)), ("k_scale", k_scale, f32, (num, heads)),
+          ("v_scale", v_scale, f32, (num, heads)), ("values", values, values.dtype, (2, n, heads, KV_PAGE, dim)))
+    _check(lib.tq_debug_kv_read(_act_dtypes().get(values.dtype, -1), n, heads, dim, pages.data_ptr(), k_cache.data_ptr(),
+                                v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), num, values.data_ptr(),
+                                _stream(stream)), what)
 
 
 def stack_timeouts(ws) -> int:

@@ -54,7 +54,7 @@ def build() -> str:
     bdir = os.path.join(HERE, "_build")
     os.makedirs(bdir, exist_ok=True)
     host_objs = []
-    for src in ("tq_host.cpp", "tq_ternarize.cpp"):
+    for src in ("tq_host.cpp", "tq_ternarize.cpp", "tq_rope.cpp"):
         o = os.path.join(bdir, src.replace(".cpp", ".o"))
         _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fopenmp", "-Wall", "-Wextra", "-I", INC,
               "-c", os.path.join(CSRC, src), "-o", o])
@@ -67,7 +67,8 @@ def build() -> str:
     units = [(src, src.replace(".hip", ".o"), preload if src in ("tq_kernels.hip", "tq_gemv_mfma.hip",
                                                                    "tq_hadamard.hip") else [])
              for src in ("tq_kernels.hip", "tq_proj.hip", "tq_gemv_mfma.hip", "tq_hadamard.hip",
-                         "tq_gemm.hip", "tq_stream.hip", "tq_noalloc.hip", "tq_workspace.hip")]
+                         "tq_gemm.hip", "tq_stream.hip", "tq_noalloc.hip", "tq_workspace.hip",
+                         "tq_kv.hip", "tq_kv_attn.hip", "tq_norm.hip")]
     # the projection kernel: one object per (packed format, activation form, output kind)
     for fmt, fname in ((0, "b3"), (1, "2b"), (2, "bp"), (3, "b3r")):
         for lx in (1, 0):

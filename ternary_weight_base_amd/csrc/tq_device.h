@@ -68,6 +68,16 @@ __device__ __forceinline__ void half_sums(int v, int &lo, int &hi) {
   hi = __builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48);
 }
 
+// A double rounded to fp32, kept as such: where the result is rounded on to
+// fp16 the compiler would otherwise merge the two roundings into one from
+// the double, a long software conversion.  (The two together are off by at
+// most 2^-24 of the value more than half an fp16 step.)
+__device__ __forceinline__ float round_f32(double d) {
+  float f = (float)d;
+  asm("" : "+v"(f));
+  return f;
+}
+
 __device__ __forceinline__ float half_bits(uint32_t bits) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
 }
