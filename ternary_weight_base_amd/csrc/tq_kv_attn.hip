@@ -194,31 +194,103 @@ __device__ __forceinline__ void step(const AttnArgs &A, const Raw<D> &t, const h
   }
 }
 
-// Floats of one split's partial result: outputs, then (max, sum) per row.
-constexpr int partial_floats(int D) { return kRows * (D + 2); }
+// Floats of one split's partial result for R rows: outputs, then (max, sum)
+// of each row.
+constexpr int partial_floats(int R, int D) { return R * (D + 2); }
+
+// After a workgroup has stored its split's partial result (store_dev) at
+// `base` + c * partial_floats: whether it is the last of `splits`, in which
+// case it leaves the counter zero for the next call.
+__device__ __forceinline__ bool last_split(uint32_t *counter, int splits) {
+  __shared__ int last;
+  __builtin_amdgcn_s_waitcnt(0);  // this thread's words have reached device scope
+  __syncthreads();                // ... and so have every other thread's
+  if (threadIdx.x == 0) {
+    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(splits - 1);
+    if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return last;
+}
+
+// Joins the splits' partial results of one row's outputs d0 .. d0 + N - 1, in
+// order, and leaves the words it read zero (the row's maxima and sums are
+// cleared by the caller, after a barrier: other threads read them too).
+template <int R, int D, int N>
+__device__ __forceinline__ void join_row(float *base, int splits, int row, int d0, float &M, float &L, float (&o)[N]) {
+  M = kNone;
+  L = 0.0f;
+#pragma unroll
+  for (int j = 0; j < N; j++) o[j] = 0.0f;
+  for (int k = 0; k < splits; k++) {
+    float *p = base + (int64_t)k * partial_floats(R, D);
+    const float mk = load_dev(p + R * D + 2 * row), lk = load_dev(p + R * D + 2 * row + 1);
+    const float mn = fmaxf(M, mk), fa = __builtin_amdgcn_exp2f(M - mn), fb = __builtin_amdgcn_exp2f(mk - mn);
+    M = mn;
+    L = L * fa + lk * fb;
+#pragma unroll
+    for (int j = 0; j < N; j++) o[j] = o[j] * fa + load_dev(p + row * D + d0 + j) * fb;
+  }
+  for (int k = 0; k < splits; k++) {
+    float *p = base + (int64_t)k * partial_floats(R, D);
+#pragma unroll
+    for (int j = 0; j < N; j++) store_dev(p + row * D + d0 + j, 0.0f);
+  }
+}
+
+template <int R, int D>
+__device__ __forceinline__ void clear_row(float *base, int splits, int row) {
+  for (int k = 0; k < splits; k++) {
+    float *p = base + (int64_t)k * partial_floats(R, D) + R * D + 2 * row;
+    store_dev(p, 0.0f);
+    store_dev(p + 1, 0.0f);
+  }
+}
+
+// 1 / sum of weights; 0 for a row that saw no key.
+__device__ __forceinline__ float inverse(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
+
+// A workgroup's place: R consecutive (token, query head) rows of a sequence
+// and KV head, and its share of their pages.
+struct Place {
+  int h, s, begin, n, nrows, p0, pmin, pmax, lo, hi, splits, split;
+  int64_t f0, tile;
+  Tiles T;
+};
+
+template <int R>
+__device__ __forceinline__ bool find_place(const AttnArgs &A, Place &P) {
+  P.h = blockIdx.x % A.hkv;
+  P.split = blockIdx.x / A.hkv % A.nsplit;
+  const int slot = blockIdx.x / A.hkv / A.nsplit;
+  P.s = find_seq(A.cu, A.seqs, A.rows, slot, A.group, R, 1);
+  P.begin = cu_at(A.cu, P.s, A.rows);
+  P.n = max(cu_at(A.cu, P.s + 1, A.rows) - P.begin, 0);
+  P.f0 = (slot - slot_base(A.cu, P.s, A.rows, A.group, R, 1)) * R;
+  if (P.f0 < 0 || P.f0 >= (int64_t)P.n * A.group) return false;
+  P.nrows = (int)min((int64_t)R, (int64_t)P.n * A.group - P.f0);
+  P.p0 = max(A.kv_len[P.s], 0) - P.n;  // may be negative: such rows see nothing
+  P.pmin = P.p0 + (int)(P.f0 / A.group);
+  P.pmax = P.p0 + (int)((P.f0 + P.nrows - 1) / A.group);
+  P.T = visible_tiles(P.pmin, P.pmax, A.max_pages, A.window, A.sinks);
+  const int per = max(A.chunk, (P.T.count + A.nsplit - 1) / A.nsplit);
+  P.splits = max((P.T.count + per - 1) / per, 1);
+  P.lo = P.split * per;
+  P.hi = min(P.T.count, P.lo + per);
+  P.tile = (int64_t)slot * A.hkv + P.h;
+  return P.split < P.splits;
+}
 
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void decode_kernel(const AttnArgs A) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n16 = lane & 15, g = lane >> 4;
-  const int h = blockIdx.x % A.hkv, c = blockIdx.x / A.hkv % A.nsplit, slot = blockIdx.x / A.hkv / A.nsplit;
-  const int s = find_seq(A.cu, A.seqs, A.rows, slot, A.group, kRows, 1);
-  const int begin = cu_at(A.cu, s, A.rows), n = max(cu_at(A.cu, s + 1, A.rows) - begin, 0);
-  const int64_t f0 = (slot - slot_base(A.cu, s, A.rows, A.group, kRows, 1)) * kRows;
-  if (f0 < 0 || f0 >= (int64_t)n * A.group) return;
-  const int nrows = (int)min((int64_t)kRows, (int64_t)n * A.group - f0);
-  const int tok0 = (int)(f0 / A.group), tokl = (int)((f0 + nrows - 1) / A.group);
-  const int p0 = max(A.kv_len[s], 0) - n;  // may be negative: such rows see nothing
-  const int pmin = p0 + tok0, pmax = p0 + tokl;
-  const Tiles T = visible_tiles(pmin, pmax, A.max_pages, A.window, A.sinks);
-  const int per = max(A.chunk, (T.count + A.nsplit - 1) / A.nsplit);
-  const int splits = max((T.count + per - 1) / per, 1);
-  if (c >= splits) return;
-
-  const int64_t fl = f0 + n16;
-  const bool valid = n16 < nrows;
-  const int tok = (int)(fl / A.group), head = h * A.group + (int)(fl % A.group);
-  const int pos = valid ? p0 + tok : -1;
-  const _Float16 *qr = A.q + (int64_t)(begin + (valid ? tok : 0)) * A.q_stride + (valid ? head : 0) * D;
+  Place P;
+  if (!find_place<kRows>(A, P)) return;
+  const int64_t fl = P.f0 + n16;
+  const bool valid = n16 < P.nrows;
+  const int tok = (int)(fl / A.group), head = P.h * A.group + (int)(fl % A.group);
+  const int pos = valid ? P.p0 + tok : -1;
+  const _Float16 *qr = A.q + (int64_t)(P.begin + (valid ? tok : 0)) * A.q_stride + (valid ? head : 0) * D;
   h8 qf[D / 32];
   float qsum = 0.0f;
 #pragma unroll
@@ -243,21 +315,20 @@ __global__ __launch_bounds__(kThreads, 2) void decode_kernel(const AttnArgs A) {
   st.m = kNone;
   st.l = st.corr = 0.0f;
   st.unit = 1.0f;
-  const int end = min(T.count, (c + 1) * per);
   Raw<D> raw[2];
-  int i = c * per + wave;
+  int i = P.lo + wave;
   auto run = [&](const Raw<D> &t, int ti) {
-    const int pg = T.page(ti), j1 = pg * kPage + kPage - 1;
-    const bool all = j1 <= pmin && (A.window == 0 || pg * kPage > pmax - A.window || j1 < A.sinks);
+    const int pg = P.T.page(ti), j1 = pg * kPage + kPage - 1;
+    const bool all = j1 <= P.pmin && (A.window == 0 || pg * kPage > P.pmax - A.window || j1 < A.sinks);
     step<D>(A, t, qf, qsum, pg, pos, !all, st);
   };
-  if (i < end) load_tile<D>(A, s, h, T.page(i), raw[0]);
-  while (i < end) {
-    if (i + kWaves < end) load_tile<D>(A, s, h, T.page(i + kWaves), raw[1]);
+  if (i < P.hi) load_tile<D>(A, P.s, P.h, P.T.page(i), raw[0]);
+  while (i < P.hi) {
+    if (i + kWaves < P.hi) load_tile<D>(A, P.s, P.h, P.T.page(i + kWaves), raw[1]);
     run(raw[0], i);
     i += kWaves;
-    if (i >= end) break;
-    if (i + kWaves < end) load_tile<D>(A, s, h, T.page(i + kWaves), raw[0]);
+    if (i >= P.hi) break;
+    if (i + kWaves < P.hi) load_tile<D>(A, P.s, P.h, P.T.page(i + kWaves), raw[0]);
     run(raw[1], i);
     i += kWaves;
   }
@@ -297,12 +368,11 @@ __global__ __launch_bounds__(kThreads, 2) void decode_kernel(const AttnArgs A) {
     for (int j = 0; j < kPer; j++) o[j] += f * so[w][row][d0 + j];
   }
 
-  if (splits > 1) {
-    __shared__ int last;
-    const int64_t tile = (int64_t)slot * A.hkv + h;
-    float *base = A.partials + tile * A.nsplit * partial_floats(D);
-    float *mine = base + (int64_t)c * partial_floats(D);
-    if (row < nrows) {
+  const bool live = row < P.nrows;
+  if (P.splits > 1) {
+    float *base = A.partials + P.tile * A.nsplit * partial_floats(kRows, D);
+    float *mine = base + (int64_t)P.split * partial_floats(kRows, D);
+    if (live) {
 #pragma unroll
       for (int j = 0; j < kPer; j++) store_dev(mine + row * D + d0 + j, o[j]);
       if ((tid & 15) == 0) {
@@ -310,54 +380,281 @@ __global__ __launch_bounds__(kThreads, 2) void decode_kernel(const AttnArgs A) {
         store_dev(mine + kRows * D + 2 * row + 1, L);
       }
     }
-    __builtin_amdgcn_s_waitcnt(0);  // this thread's words have reached device scope
-    __syncthreads();                // ... and so have every other thread's
-    if (tid == 0)
-      last = __hip_atomic_fetch_add(&A.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-             (uint32_t)(splits - 1);
+    if (!last_split(A.counters + P.tile, P.splits)) return;  // another split finishes this tile
+    if (live) join_row<kRows, D, kPer>(base, P.splits, row, d0, M, L, o);
     __syncthreads();
-    if (!last) return;  // another split finishes this tile
-    M = kNone;
-    L = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kPer; j++) o[j] = 0.0f;
-    if (row < nrows) {
-      for (int k = 0; k < splits; k++) {
-        float *p = base + (int64_t)k * partial_floats(D);
-        const float mk = load_dev(p + kRows * D + 2 * row), lk = load_dev(p + kRows * D + 2 * row + 1);
-        const float mn = fmaxf(M, mk), fa = __builtin_amdgcn_exp2f(M - mn), fb = __builtin_amdgcn_exp2f(mk - mn);
-        M = mn;
-        L = L * fa + lk * fb;
-#pragma unroll
-        for (int j = 0; j < kPer; j++) o[j] = o[j] * fa + load_dev(p + row * D + d0 + j) * fb;
-      }
-      // consumed: leave the workspace zero for the next call, whatever its shape
-      for (int k = 0; k < splits; k++) {
-        float *p = base + (int64_t)k * partial_floats(D);
-#pragma unroll
-        for (int j = 0; j < kPer; j++) store_dev(p + row * D + d0 + j, 0.0f);
-      }
-    }
-    __syncthreads();  // every thread of the row has read its maximum and sum
-    if (row < nrows && (tid & 15) == 0)
-      for (int k = 0; k < splits; k++) {
-        float *p = base + (int64_t)k * partial_floats(D) + kRows * D + 2 * row;
-        store_dev(p, 0.0f);
-        store_dev(p + 1, 0.0f);
-      }
-    if (tid == 0) __hip_atomic_store(&A.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (live && (tid & 15) == 0) clear_row<kRows, D>(base, P.splits, row);
   }
-  if (row < nrows) {
-    const int64_t f = f0 + row;
-    _Float16 *dst = A.out + (int64_t)(begin + f / A.group) * A.out_stride + (h * A.group + f % A.group) * D + d0;
-    const float r = L > 0.0f || L != L ? 1.0f / L : 0.0f;  // no visible key: zeros
+  if (live) {
+    const int64_t f = P.f0 + row;
+    _Float16 *dst = A.out + (int64_t)(P.begin + f / A.group) * A.out_stride + (P.h * A.group + f % A.group) * D + d0;
+    const float r = inverse(L);
 #pragma unroll
     for (int j = 0; j < kPer; j++) dst[j] = (_Float16)(o[j] * r);
   }
 }
 
-// The launch of a call: how the keys are split, and the workspace it needs.
+// ---- many rows -----------------------------------------------------------
+//
+// A workgroup takes 128 (token, query head) rows, 32 a wave, over the same
+// pages.  Each page's codes are converted to fp16 once for all waves, on
+// their way into LDS (two buffers, the next page's bytes in registers
+// meanwhile, one barrier a page); K rows of D + 8 and V rows of 64 + 8 fp16
+// keep the 16-byte reads of both products free of bank conflicts.  Products
+// are v_mfma_f32_32x32x16_f16, scores transposed as in the decode kernel: with
+// key rows handed over in the order of row_token() a lane holds, for its query
+// row, 8 consecutive tokens per 16, half a wave each half: what the second
+// product's operand is.
+//
+// The running maximum is a reference, not the maximum: it moves only when a
+// score exceeds it by 2^8 in weight, so the output is hardly ever rescaled
+// (fp16 weights reach 2^8, times 2^4 for the page's value scale).
+constexpr int kTileRows = 128, kWaveRows = 32;
+typedef float f16x __attribute__((ext_vector_type(16)));
+
+// The token of a 32-token group that row r of the score product takes.
+__device__ __forceinline__ int row_token(int r) { return (r & 16) + ((r >> 2) & 1) * 8 + ((r >> 3) & 1) * 4 + (r & 3); }
+
+// The larger of a lane's value and its partner's in the other half of the wave.
+__device__ __forceinline__ float half_max(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+template <int D>
+struct Page {
+  uint4 k[D / 64], v[D / 64];
+  float ks, vs;  // ks < 0: no such page
+};
+
+template <int D>
+__device__ __forceinline__ void load_page(const AttnArgs &A, int s, int h, int pg, Page<D> &t) {
+  const int id = __builtin_amdgcn_readfirstlane(A.table[(int64_t)s * A.max_pages + pg]);
+  const bool ok = id >= 0 && id < A.num_pages;
+  const int64_t ph = (int64_t)(ok ? id : 0) * A.hkv + h;
+  t.ks = ok ? A.ks[ph] : -1.0f;
+  t.vs = A.vs[ph];
+  const uint4 *kp = reinterpret_cast<const uint4 *>(A.k + ph * (kPage * D));
+  const uint4 *vp = reinterpret_cast<const uint4 *>(A.v + ph * (kPage * D));
+#pragma unroll
+  for (int i = 0; i < D / 64; i++) {
+    t.k[i] = kp[i * kThreads + threadIdx.x];
+    t.v[i] = vp[i * kThreads + threadIdx.x];
+  }
+}
+
+template <int D>
+struct Lds {
+  _Float16 k[kPage][D + 8], v[D][kPage + 8];
+};
+
+template <int D>
+__device__ __forceinline__ void put_page(const Page<D> &t, Lds<D> &l) {
+#pragma unroll
+  for (int i = 0; i < D / 64; i++) {
+    const int idx = i * kThreads + threadIdx.x;
+    h8 *kd = reinterpret_cast<h8 *>(&l.k[idx / (D / 16)][idx % (D / 16) * 16]);
+    kd[0] = codes8(t.k[i].x, t.k[i].y);
+    kd[1] = codes8(t.k[i].z, t.k[i].w);
+    h8 *vd = reinterpret_cast<h8 *>(&l.v[idx / 4][idx % 4 * 16]);
+    vd[0] = codes8(t.v[i].x, t.v[i].y);
+    vd[1] = codes8(t.v[i].z, t.v[i].w);
+  }
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) {
+  __shared__ __attribute__((aligned(16))) Lds<D> lds[2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31, half = lane >> 5;
+  Place P;
+  if (!find_place<kTileRows>(A, P)) return;
+  const int row = wave * kWaveRows + n;
+  const bool valid = row < P.nrows;
+  const int64_t fl = P.f0 + row;
+  const int tok = valid ? (int)(fl / A.group) : 0, head = P.h * A.group + (valid ? (int)(fl % A.group) : 0);
+  const int pos = valid ? P.p0 + tok : -1;
+  const _Float16 *qr = A.q + (int64_t)(P.begin + tok) * A.q_stride + head * D;
+  h8 qf[D / 16];
+  float qsum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < D / 16; j++) {
+    h8 x = *reinterpret_cast<const h8 *>(qr + 16 * j + 8 * half);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      x[i] = valid ? x[i] : (_Float16)0.0f;
+      qsum += (float)x[i];
+    }
+    qf[j] = x;
+  }
+  qsum = 0.5f * half_sum(qsum);
+  // the wave's own rows: positions wmin .. wmax (none: wmax = -1)
+  const int r0 = wave * kWaveRows, r1 = min(r0 + kWaveRows, P.nrows) - 1;
+  const int wmin = P.p0 + (int)((P.f0 + r0) / A.group);
+  const int wmax = r1 < r0 ? -1 : P.p0 + (int)((P.f0 + r1) / A.group);
+
+  f16x o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; i++)
+#pragma unroll
+    for (int r = 0; r < 16; r++) o[i][r] = 0.0f;
+  float m = kNone, l = 0.0f, corr = 0.0f, unit = 1.0f;
+  Page<D> next;
+  float ks, vs;
+  if (P.lo < P.hi) {
+    load_page<D>(A, P.s, P.h, P.T.page(P.lo), next);
+    put_page<D>(next, lds[0]);
+  }
+  ks = next.ks;
+  vs = next.vs;
+  __syncthreads();
+  for (int i = P.lo; i < P.hi; i++) {
+    const Lds<D> &L = lds[(i - P.lo) & 1];
+    const bool more = i + 1 < P.hi;
+    if (more) load_page<D>(A, P.s, P.h, P.T.page(i + 1), next);
+    const int pg = P.T.page(i), j0 = pg * kPage, j1 = j0 + kPage - 1;
+    const bool none = ks < 0.0f || j0 > wmax || (A.window && j1 <= wmin - A.window && j0 >= A.sinks);
+    if (!none) {
+      f16x acc[2];
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+#pragma unroll
+        for (int r = 0; r < 16; r++) acc[t][r] = 0.0f;
+        const _Float16 *kr = &L.k[32 * t + row_token(n)][8 * half];
+#pragma unroll
+        for (int j = 0; j < D / 16; j++)
+          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8 *>(kr + 16 * j), qf[j], acc[t], 0, 0, 0);
+      }
+      const bool all = j1 <= wmin && (A.window == 0 || j0 > wmax - A.window || j1 < A.sinks);
+      if (!all) {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int r = 0; r < 16; r++) {
+            const int j = j0 + 32 * t + (r >> 3) * 16 + 8 * half + (r & 7);
+            const bool see = j <= pos && (A.window == 0 || j > pos - A.window || j < A.sinks);
+            acc[t][r] = see ? acc[t][r] : -__builtin_inff();
+          }
+      }
+      // a page of zeros has scale 0: its (zero) scores stay finite, masked ones -inf
+      const float sc = fmaxf(ks * A.scale_log2, 1e-37f);
+      float mx = acc[0][0];
+#pragma unroll
+      for (int r = 1; r < 16; r++) mx = fmaxf(mx, acc[0][r]);
+#pragma unroll
+      for (int r = 0; r < 16; r++) mx = fmaxf(mx, acc[1][r]);
+      mx = (half_max(mx) + qsum) * sc;
+      const bool has_v = vs > 0.0f;  // a page of zeros adds to the sum only
+      const float ratio = has_v ? vs / unit : 1.0f;
+      const bool far = !(ratio > 0.0625f && ratio < 16.0f);
+      const float shift = far ? 0.0f : __builtin_amdgcn_logf(ratio);
+      if (far || __any(mx > m + 8.0f)) {
+        const float mn = mx > m + 8.0f ? mx : m;
+        float alpha = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= alpha;
+        if (far) {
+          alpha *= fminf(unit / vs, 3.0e38f);
+          unit = vs;
+        }
+        corr *= alpha;
+#pragma unroll
+        for (int d = 0; d < D / 32; d++)
+#pragma unroll
+          for (int r = 0; r < 16; r++) o[d][r] *= alpha;
+      }
+      const float bias = qsum * sc + shift - m;
+      float sum = 0.0f;
+      h8 p[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) {
+          const float w = __builtin_amdgcn_exp2f(acc[t][r] * sc + bias);
+          sum += w;
+          p[t][r >> 3][r & 7] = (_Float16)w;
+        }
+      l += sum * __builtin_amdgcn_exp2f(-shift);
+      if (has_v) {
+        corr += sum;
+#pragma unroll
+        for (int d = 0; d < D / 32; d++)
+#pragma unroll
+          for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+              const h8 a = *reinterpret_cast<const h8 *>(&L.v[32 * d + n][32 * t + 16 * u + 8 * half]);
+              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, p[t][u], o[d], 0, 0, 0);
+            }
+      }
+    }
+    if (more) {
+      put_page<D>(next, lds[(i + 1 - P.lo) & 1]);
+      ks = next.ks;
+      vs = next.vs;
+    }
+    __syncthreads();
+  }
+  l = half_sum(l);
+  corr = 0.5f * half_sum(corr);
+#pragma unroll
+  for (int d = 0; d < D / 32; d++)
+#pragma unroll
+    for (int r = 0; r < 16; r++) o[d][r] = (o[d][r] + corr) * unit;
+
+  // element r of o[d] is output 32 d + 8 (r / 4) + 4 half + r % 4
+  if (P.splits > 1) {
+    float *base = A.partials + P.tile * A.nsplit * partial_floats(kTileRows, D);
+    float *mine = base + (int64_t)P.split * partial_floats(kTileRows, D);
+    if (valid) {
+#pragma unroll
+      for (int d = 0; d < D / 32; d++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) store_dev(mine + row * D + 32 * d + 8 * (r >> 2) + 4 * half + (r & 3), o[d][r]);
+      if (half == 0) {
+        store_dev(mine + kTileRows * D + 2 * row, m);
+        store_dev(mine + kTileRows * D + 2 * row + 1, l);
+      }
+    }
+    if (!last_split(A.counters + P.tile, P.splits)) return;  // another split finishes this tile
+    constexpr int kPer = 8;
+    for (int i = threadIdx.x; i < P.nrows * (D / kPer); i += kThreads) {
+      const int jr = i / (D / kPer), d0 = i % (D / kPer) * kPer;
+      float M, S, v[kPer];
+      join_row<kTileRows, D, kPer>(base, P.splits, jr, d0, M, S, v);
+      const int64_t f = P.f0 + jr;
+      const float inv = inverse(S);
+      h8 x;
+#pragma unroll
+      for (int j = 0; j < kPer; j++) x[j] = (_Float16)(v[j] * inv);
+      *reinterpret_cast<h8 *>(A.out + (int64_t)(P.begin + f / A.group) * A.out_stride + (P.h * A.group + f % A.group) * D + d0) = x;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < P.nrows; i += kThreads) clear_row<kTileRows, D>(base, P.splits, i);
+    return;
+  }
+  if (valid) {
+    const float inv = inverse(l);
+    _Float16 *dst = A.out + (int64_t)(P.begin + tok) * A.out_stride + head * D;
+#pragma unroll
+    for (int d = 0; d < D / 32; d++)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<h4 *>(dst + 32 * d + 2 * r + 4 * half) =
+            (h4){(_Float16)(o[d][r] * inv), (_Float16)(o[d][r + 1] * inv), (_Float16)(o[d][r + 2] * inv),
+                 (_Float16)(o[d][r + 3] * inv)};
+  }
+}
+
+// The launch of a call: which kernel, how the keys are split, and the
+// workspace that needs.
 struct Plan {
+  bool prefill;
   int64_t slots;
   int nsplit, chunk;
   size_t counter_bytes, bytes;
@@ -369,12 +666,14 @@ constexpr int kMinChunk = 4, kMaxChunk = 32;
 Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_kv) {
   Plan P;
   const int64_t group = q_heads / kv_heads;
-  P.slots = rows * group / kRows + seqs;
+  P.prefill = rows * group > 32 * seqs;
+  const int R = P.prefill ? kTileRows : kRows;
+  P.slots = rows * group / R + seqs;
   const int64_t tiles = (max_kv + kPage - 1) / kPage;
-  const int64_t full = (rows * group + kRows - 1) / kRows, units = (full > seqs ? full : seqs) * kv_heads;
+  const int64_t full = (rows * group + R - 1) / R, units = (full > seqs ? full : seqs) * kv_heads;
   int64_t chunk = (tiles * units + kTargetWgs - 1) / kTargetWgs;
   if (chunk < kMinChunk) chunk = kMinChunk;
-  if (full <= 4 * seqs && chunk > kMaxChunk) chunk = kMaxChunk;
+  if (!P.prefill && chunk > kMaxChunk) chunk = kMaxChunk;
   int64_t nsplit = (tiles + chunk - 1) / chunk;
   if (nsplit < 1) nsplit = 1;
   P.chunk = (int)(chunk < 0x7fffffff ? chunk : 0x7fffffff);
@@ -383,7 +682,7 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
   P.bytes = 0;
   if (nsplit > 1) {
     P.counter_bytes = ((size_t)P.slots * kv_heads * 4 + 15) / 16 * 16;
-    P.bytes = P.counter_bytes + (size_t)P.slots * kv_heads * nsplit * partial_floats((int)head_dim) * 4;
+    P.bytes = P.counter_bytes + (size_t)P.slots * kv_heads * nsplit * partial_floats(R, (int)head_dim) * 4;
   }
   return P;
 }
@@ -438,9 +737,13 @@ extern "C" int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t k
   A.window = (int)window; A.sinks = (int)sinks;
   A.nsplit = P.nsplit; A.chunk = P.chunk;
   const dim3 grid((unsigned)wgs), block(kThreads);
-  if (head_dim == 128)
-    hipLaunchKernelGGL(decode_kernel<128>, grid, block, 0, (hipStream_t)stream, A);
-  else
-    hipLaunchKernelGGL(decode_kernel<64>, grid, block, 0, (hipStream_t)stream, A);
+  hipStream_t st = (hipStream_t)stream;
+  if (P.prefill) {
+    if (head_dim == 128) hipLaunchKernelGGL(prefill_kernel<128>, grid, block, 0, st, A);
+    else hipLaunchKernelGGL(prefill_kernel<64>, grid, block, 0, st, A);
+  } else {
+    if (head_dim == 128) hipLaunchKernelGGL(decode_kernel<128>, grid, block, 0, st, A);
+    else hipLaunchKernelGGL(decode_kernel<64>, grid, block, 0, st, A);
+  }
   return hipGetLastError() == hipSuccess ? TQ_OK : TQ_ERR_HIP;
 }
