@@ -426,7 +426,7 @@ int tq_gemm(int fmt, int64_t M, int64_t N, int64_t K, const void *W, const int8_
  * tq_kv_append.
  *
  * Heads: head_dim 64 or 128 (else TQ_ERR_SHAPE), q_heads a multiple of
- * kv_heads; query head h reads KV head h / (q_heads / kv_heads). */
+ * kv_heads, rows * q_heads below 2^30; query head h reads KV head h / (q_heads / kv_heads). */
 
 /* Host: table[positions][rot] of fp32, cos(p base^(-2i/rot)) for i < rot / 2,
  * then the sines, from angles in double.  rot a multiple of 8, 8..128;

@@ -22,24 +22,27 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ int cu_at(const int *cu, int i, int rows) { return min(max(cu[i], 0), rows); }
 
 // Work is numbered without a scan over the sequences: sequence s owns the
-// slots from base(s) = floor(cu[s] * mul / div) + s * add up to base(s+1).
-// With div units of work a slot, floor(x) + 1 slots hold ceil(x) of them
+// slots from base(s) = floor(cu[s] * mul / DIV) + s * ADD up to base(s+1).
+// With DIV units of work a slot, floor(x) + 1 slots hold ceil(x) of them
 // wherever the sequence starts, so every sequence has slots enough and the
-// number of slots, floor(rows * mul / div) + seqs * add, is known on the
-// host; slots past a sequence's need are left at once.
-__device__ __forceinline__ int64_t slot_base(const int *cu, int i, int rows, int mul, int div, int add) {
-  return (int64_t)cu_at(cu, i, rows) * mul / div + (int64_t)i * add;
+// number of slots, floor(rows * mul / DIV) + seqs * ADD, is known on the
+// host; slots past a sequence's need are left at once.  (shape_check bounds
+// rows * q_heads below 2^31.)
+template <int DIV, int ADD>
+__device__ __forceinline__ int slot_base(int cu, int i, int mul) {
+  return (int)((uint32_t)(cu * mul) / (uint32_t)DIV) + i * ADD;
 }
 
 // The last sequence whose base is <= w, searched 64 ways at a time by the
 // lanes of a wave (every lane active; one round for up to 64 sequences).
-__device__ __forceinline__ int find_seq(const int *cu, int seqs, int rows, int64_t w, int mul, int div, int add) {
+template <int DIV, int ADD>
+__device__ __forceinline__ int find_seq(const int *cu, int seqs, int rows, int w, int mul) {
   int lo = 0, hi = seqs;
   const int lane = threadIdx.x & 63;
   while (hi - lo > 1) {
-    const int step = (hi - lo + 63) / 64;
+    const int step = (int)((uint32_t)(hi - lo + 63) / 64u);
     const int i = lo + lane * step;
-    const bool le = i < hi && slot_base(cu, i, rows, mul, div, add) <= w;
+    const bool le = i < hi && slot_base<DIV, ADD>(cu_at(cu, i, rows), i, mul) <= w;
     const int k = max((int)__popcll(__ballot(le)), 1);
     lo += (k - 1) * step;
     hi = min(hi, lo + step);
@@ -64,7 +67,7 @@ inline int shape_check(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_h
                        int64_t max_pages, int64_t num_pages) {
   if (rows < 1 || rows > ((int64_t)1 << 24) || seqs < 1 || seqs > ((int64_t)1 << 20) || kv_heads < 1 ||
       q_heads < kv_heads || q_heads > 4096 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) ||
-      max_pages < 1 || max_pages > ((int64_t)1 << 25) || num_pages < 1 || num_pages > 0x7fffffff)
+      rows * q_heads >= ((int64_t)1 << 30) || max_pages < 1 || max_pages > ((int64_t)1 << 25) || num_pages < 1 || num_pages > 0x7fffffff)
     return TQ_ERR_SHAPE;
   return TQ_OK;
 }

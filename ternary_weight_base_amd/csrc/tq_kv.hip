@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs A) {
     blk -= A.page_wgs;
     const int row = blk / A.q_chunks, chunk = blk % A.q_chunks;
     if (row >= cu_at(A.cu, A.seqs, A.rows)) return;
-    const int s = find_seq(A.cu, A.seqs, A.rows, row, 1, 1, 0);
+    const int s = find_seq<1, 0>(A.cu, A.seqs, A.rows, row, 1);
     const int64_t pos = (int64_t)A.kv_len[s] - (cu_at(A.cu, s + 1, A.rows) - row);
     const bool ok = pos >= 0 && (A.rot == 0 || pos < A.rope_rows);
     const float *t = A.rope + (ok ? pos : 0) * A.rot;
@@ -128,9 +128,9 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs A) {
   }
   const bool is_v = blk & 1;
   const int h = (blk >> 1) % A.hkv, slot = (blk >> 1) / A.hkv;
-  const int s = find_seq(A.cu, A.seqs, A.rows, slot, 1, kPage, 2);
+  const int s = find_seq<kPage, 2>(A.cu, A.seqs, A.rows, slot, 1);
   const int begin = cu_at(A.cu, s, A.rows), end = max(cu_at(A.cu, s + 1, A.rows), begin);
-  const int64_t local = slot - slot_base(A.cu, s, A.rows, 1, kPage, 2);
+  const int local = slot - slot_base<kPage, 2>(begin, s, 1);
   const int64_t kvl = A.kv_len[s], p0 = kvl - (end - begin), first = p0 > 0 ? p0 : 0;
   const int64_t pg = first / kPage + local;
   if (local < 0 || pg >= A.max_pages) return;

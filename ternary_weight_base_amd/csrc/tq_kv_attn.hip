@@ -38,8 +38,12 @@ namespace {
 
 using namespace tqkv;
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
 constexpr int kRows = 16;  // (token, query head) rows of a decode workgroup
+constexpr int kDecThreads = 512, kDecWaves = kDecThreads / 64;
+constexpr int kDecSplits = 128;  // splits of the keys at most, decode
 constexpr float kNone = -1e30f;  // running maximum before the first visible key
 
 struct AttnArgs {
@@ -76,11 +80,48 @@ __device__ __forceinline__ Tiles visible_tiles(int pmin, int pmax, int64_t max_p
   return t;
 }
 
-__device__ __forceinline__ void store_dev(float *p, float v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// 16-byte accesses at device scope (past the XCD's own cache, as other XCDs'
+// workgroups read and write these words).
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr int kDevScope = 16;  // the sc1 bit of the cache policy
+__device__ __forceinline__ Rsrc make_rsrc(void *p) { return __builtin_amdgcn_make_buffer_rsrc(p, 0, 0x7fffffff, 0x00027000); }
+__device__ __forceinline__ void store_dev(Rsrc r, int i, f4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), r, i * 4, 0, kDevScope);
 }
-__device__ __forceinline__ float load_dev(const float *p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ f4 load_dev(Rsrc r, int i) {
+  return __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, kDevScope));
+}
+__device__ __forceinline__ void store_dev2(Rsrc r, int i, float a, float b) {
+  __builtin_amdgcn_raw_buffer_store_b64((u2){__float_as_uint(a), __float_as_uint(b)}, r, i * 4, 0, kDevScope);
+}
+__device__ __forceinline__ void load_dev2(Rsrc r, int i, float &a, float &b) {
+  const u2 v = __builtin_amdgcn_raw_buffer_load_b64(r, i * 4, 0, kDevScope);
+  a = __uint_as_float(v[0]);
+  b = __uint_as_float(v[1]);
+}
+
+// The larger of a lane's value and its partner's in the other half of the wave.
+__device__ __forceinline__ float half_max(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Over the four lanes lane % 16 + 16 g.
+__device__ __forceinline__ float quarter_max(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float quarter_sum(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
 // The bytes of one page and KV head that a lane takes part in.
@@ -91,9 +132,8 @@ struct Raw {
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs &A, int s, int h, int pg, Raw<D> &t) {
+__device__ __forceinline__ void load_tile(const AttnArgs &A, int h, int id, Raw<D> &t) {
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
-  const int id = __builtin_amdgcn_readfirstlane(A.table[(int64_t)s * A.max_pages + pg]);
   const bool ok = id >= 0 && id < A.num_pages;
   const int64_t ph = (int64_t)(ok ? id : 0) * A.hkv + h;
   const uint8_t *kp = A.k + ph * (kPage * D), *vp = A.v + ph * (kPage * D);
@@ -149,8 +189,7 @@ __device__ __forceinline__ void step(const AttnArgs &A, const Raw<D> &t, const h
   float mx = x[0];
 #pragma unroll
   for (int i = 1; i < 16; i++) mx = fmaxf(mx, x[i]);
-  mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-  mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+  mx = quarter_max(mx);
   float shift = 0.0f;  // log2 of this page's value scale over the unit
   float alpha = 1.0f;
   const float m_new = fmaxf(st.m, mx);
@@ -213,185 +252,216 @@ __device__ __forceinline__ bool last_split(uint32_t *counter, int splits) {
   return last;
 }
 
-// Joins the splits' partial results of one row's outputs d0 .. d0 + N - 1, in
-// order, and leaves the words it read zero (the row's maxima and sums are
-// cleared by the caller, after a barrier: other threads read them too).
-template <int R, int D, int N>
-__device__ __forceinline__ void join_row(float *base, int splits, int row, int d0, float &M, float &L, float (&o)[N]) {
-  M = kNone;
-  L = 0.0f;
-#pragma unroll
-  for (int j = 0; j < N; j++) o[j] = 0.0f;
-  for (int k = 0; k < splits; k++) {
-    float *p = base + (int64_t)k * partial_floats(R, D);
-    const float mk = load_dev(p + R * D + 2 * row), lk = load_dev(p + R * D + 2 * row + 1);
-    const float mn = fmaxf(M, mk), fa = __builtin_amdgcn_exp2f(M - mn), fb = __builtin_amdgcn_exp2f(mk - mn);
-    M = mn;
-    L = L * fa + lk * fb;
-#pragma unroll
-    for (int j = 0; j < N; j++) o[j] = o[j] * fa + load_dev(p + row * D + d0 + j) * fb;
-  }
-  for (int k = 0; k < splits; k++) {
-    float *p = base + (int64_t)k * partial_floats(R, D);
-#pragma unroll
-    for (int j = 0; j < N; j++) store_dev(p + row * D + d0 + j, 0.0f);
-  }
-}
-
-template <int R, int D>
-__device__ __forceinline__ void clear_row(float *base, int splits, int row) {
-  for (int k = 0; k < splits; k++) {
-    float *p = base + (int64_t)k * partial_floats(R, D) + R * D + 2 * row;
-    store_dev(p, 0.0f);
-    store_dev(p + 1, 0.0f);
-  }
-}
-
 // 1 / sum of weights; 0 for a row that saw no key.
 __device__ __forceinline__ float inverse(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
+
+// The last split's join of a tile: the partial results at `part`, summed in
+// the order of the splits; `out(row, d, f4)` takes the outputs.  First every
+// split's weight per row, then the outputs, 16 bytes a thread, several
+// splits' loads in flight; where the rows are fewer than the threads, the
+// splits are dealt over `parts` groups of threads that meet in LDS.  The
+// words read are left zero for the next call, whatever its shape.
+template <int R, int D, int NT, int MAXS, typename Out>
+__device__ __forceinline__ void join(Rsrc part, int splits, int nrows, float *lds, const Out &out) {
+  constexpr int PF = partial_floats(R, D), kBatch = 8;
+  const int tid = threadIdx.x;
+  float *wm = lds, *wl = lds + R * MAXS;
+  for (int i = tid; i < splits * R; i += NT) {
+    const int k = i / R, r = i % R;
+    float m = kNone, l = 0.0f;
+    if (r < nrows) {
+      load_dev2(part, k * PF + R * D + 2 * r, m, l);
+      store_dev2(part, k * PF + R * D + 2 * r, 0.0f, 0.0f);
+    }
+    wm[i] = m;
+    wl[i] = l;
+  }
+  __syncthreads();
+  if (tid < R) {
+    float M = kNone, L = 0.0f;
+    for (int k = 0; k < splits; k++) M = fmaxf(M, wm[k * R + tid]);
+    for (int k = 0; k < splits; k++) L += wl[k * R + tid] * __builtin_amdgcn_exp2f(wm[k * R + tid] - M);
+    const float inv = inverse(L);
+    for (int k = 0; k < splits; k++) wm[k * R + tid] = inv * __builtin_amdgcn_exp2f(wm[k * R + tid] - M);
+  }
+  __syncthreads();
+  const int quads = nrows * (D / 4);
+  const int parts = quads * 4 <= NT ? 4 : quads * 2 <= NT ? 2 : 1;
+  const int per = NT / parts, p = tid / per;
+  f4 *red = reinterpret_cast<f4 *>(lds + 2 * R * MAXS);
+  for (int q = tid - p * per; q < quads; q += per) {  // one round where parts > 1
+    const int row = q / (D / 4), w = q * 4;
+    f4 o = {0, 0, 0, 0};
+    for (int k0 = p; k0 < splits; k0 += kBatch * parts) {
+      f4 v[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; b++) v[b] = load_dev(part, min(k0 + b * parts, splits - 1) * PF + w);
+#pragma unroll
+      for (int b = 0; b < kBatch; b++)
+        if (k0 + b * parts < splits) o += v[b] * wm[(k0 + b * parts) * R + row];
+    }
+    for (int k = p; k < splits; k += parts) store_dev(part, k * PF + w, (f4){0, 0, 0, 0});
+    if (parts == 1)
+      out(row, w - row * D, o);
+    else
+      red[tid] = o;
+  }
+  if (parts == 1) return;
+  __syncthreads();
+  if (tid < quads) {
+    f4 o = red[tid];
+    for (int k = 1; k < parts; k++) o += red[k * per + tid];
+    out(tid / (D / 4), tid * 4 % D, o);
+  }
+}
+template <int R, int MAXS, int NT>
+constexpr int kJoinFloats = 2 * R * MAXS + 4 * NT;
 
 // A workgroup's place: R consecutive (token, query head) rows of a sequence
 // and KV head, and its share of their pages.
 struct Place {
-  int h, s, begin, n, nrows, p0, pmin, pmax, lo, hi, splits, split;
-  int64_t f0, tile;
+  int h, s, begin, n, nrows, f0, p0, pmin, pmax, lo, hi, splits, split;
+  int64_t tile;
   Tiles T;
 };
 
 template <int R>
 __device__ __forceinline__ bool find_place(const AttnArgs &A, Place &P) {
-  P.h = blockIdx.x % A.hkv;
-  P.split = blockIdx.x / A.hkv % A.nsplit;
-  const int slot = blockIdx.x / A.hkv / A.nsplit;
-  P.s = find_seq(A.cu, A.seqs, A.rows, slot, A.group, R, 1);
+  P.h = blockIdx.x % (uint32_t)A.hkv;
+  const uint32_t b = blockIdx.x / (uint32_t)A.hkv;
+  P.split = b % (uint32_t)A.nsplit;
+  const int slot = b / (uint32_t)A.nsplit;
+  P.s = find_seq<R, 1>(A.cu, A.seqs, A.rows, slot, A.group);
   P.begin = cu_at(A.cu, P.s, A.rows);
   P.n = max(cu_at(A.cu, P.s + 1, A.rows) - P.begin, 0);
-  P.f0 = (slot - slot_base(A.cu, P.s, A.rows, A.group, R, 1)) * R;
-  if (P.f0 < 0 || P.f0 >= (int64_t)P.n * A.group) return false;
-  P.nrows = (int)min((int64_t)R, (int64_t)P.n * A.group - P.f0);
+  const int local = slot - slot_base<R, 1>(P.begin, P.s, A.group), all = P.n * A.group;
+  P.f0 = local * R;
+  if (local < 0 || P.f0 >= all) return false;
+  P.nrows = min(R, all - P.f0);
   P.p0 = max(A.kv_len[P.s], 0) - P.n;  // may be negative: such rows see nothing
-  P.pmin = P.p0 + (int)(P.f0 / A.group);
-  P.pmax = P.p0 + (int)((P.f0 + P.nrows - 1) / A.group);
+  P.pmin = P.p0 + (uint32_t)P.f0 / (uint32_t)A.group;
+  P.pmax = P.p0 + (uint32_t)(P.f0 + P.nrows - 1) / (uint32_t)A.group;
   P.T = visible_tiles(P.pmin, P.pmax, A.max_pages, A.window, A.sinks);
-  const int per = max(A.chunk, (P.T.count + A.nsplit - 1) / A.nsplit);
-  P.splits = max((P.T.count + per - 1) / per, 1);
+  const int per = max(A.chunk, (int)((uint32_t)(P.T.count + A.nsplit - 1) / (uint32_t)A.nsplit));
+  P.splits = max((int)((uint32_t)(P.T.count + per - 1) / (uint32_t)per), 1);
   P.lo = P.split * per;
   P.hi = min(P.T.count, P.lo + per);
   P.tile = (int64_t)slot * A.hkv + P.h;
   return P.split < P.splits;
 }
 
+__device__ __forceinline__ int page_id(const AttnArgs &A, int s, int pg) {
+  return __builtin_amdgcn_readfirstlane(A.table[(int64_t)s * A.max_pages + pg]);
+}
+
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void decode_kernel(const AttnArgs A) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n16 = lane & 15, g = lane >> 4;
+__global__ __launch_bounds__(kDecThreads, 2) void decode_kernel(const AttnArgs A) {
+  constexpr int kStride = D + 4;
+  union Shared {
+    struct {
+      float o[kDecWaves][kRows][kStride], m[kDecWaves][kRows], l[kDecWaves][kRows];
+    } w;
+    float join[kJoinFloats<kRows, kDecSplits, kDecThreads>];
+  };
+  __shared__ __attribute__((aligned(16))) Shared S;
+  const int tid = threadIdx.x, lane = tid & 63, n16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   Place P;
   if (!find_place<kRows>(A, P)) return;
-  const int64_t fl = P.f0 + n16;
+  int i = P.lo + wave, id = 0, id_next = 0;
+  if (i < P.hi) id = page_id(A, P.s, P.T.page(i));
+  if (i + kDecWaves < P.hi) id_next = page_id(A, P.s, P.T.page(i + kDecWaves));
   const bool valid = n16 < P.nrows;
-  const int tok = (int)(fl / A.group), head = P.h * A.group + (int)(fl % A.group);
+  const uint32_t fl = P.f0 + (valid ? n16 : 0);
+  const int tok = fl / (uint32_t)A.group, head = P.h * A.group + fl % (uint32_t)A.group;
   const int pos = valid ? P.p0 + tok : -1;
-  const _Float16 *qr = A.q + (int64_t)(P.begin + (valid ? tok : 0)) * A.q_stride + (valid ? head : 0) * D;
+  const _Float16 *qr = A.q + (int64_t)(P.begin + tok) * A.q_stride + head * D;
   h8 qf[D / 32];
-  float qsum = 0.0f;
 #pragma unroll
   for (int j = 0; j < D / 64; j++)
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-      h8 x = *reinterpret_cast<const h8 *>(qr + 64 * j + 16 * g + 8 * u);
+    for (int u = 0; u < 2; u++) qf[2 * j + u] = *reinterpret_cast<const h8 *>(qr + 64 * j + 16 * g + 8 * u);
+  Raw<D> raw[2];
+  if (i < P.hi) load_tile<D>(A, P.h, id, raw[0]);
+  float qsum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        x[i] = valid ? x[i] : (_Float16)0.0f;
-        qsum += (float)x[i];
-      }
-      qf[2 * j + u] = x;
+  for (int j = 0; j < D / 32; j++)
+#pragma unroll
+    for (int r = 0; r < 8; r++) {
+      qf[j][r] = valid ? qf[j][r] : (_Float16)0.0f;
+      qsum += (float)qf[j][r];
     }
-  qsum += __shfl_xor(qsum, 16, 64);
-  qsum += __shfl_xor(qsum, 32, 64);
-  qsum *= 0.5f;
+  qsum = 0.5f * quarter_sum(qsum);
 
   State<D> st;
 #pragma unroll
-  for (int i = 0; i < D / 16; i++) st.o[i] = (f4){0, 0, 0, 0};
+  for (int d = 0; d < D / 16; d++) st.o[d] = (f4){0, 0, 0, 0};
   st.m = kNone;
   st.l = st.corr = 0.0f;
   st.unit = 1.0f;
-  Raw<D> raw[2];
-  int i = P.lo + wave;
   auto run = [&](const Raw<D> &t, int ti) {
     const int pg = P.T.page(ti), j1 = pg * kPage + kPage - 1;
     const bool all = j1 <= P.pmin && (A.window == 0 || pg * kPage > P.pmax - A.window || j1 < A.sinks);
     step<D>(A, t, qf, qsum, pg, pos, !all, st);
   };
-  if (i < P.hi) load_tile<D>(A, P.s, P.h, P.T.page(i), raw[0]);
+  // the next page's bytes are on their way while a page is worked on, the id
+  // of the one after that too
+  auto ahead = [&](Raw<D> &t) {
+    if (i + kDecWaves < P.hi) load_tile<D>(A, P.h, id_next, t);
+    if (i + 2 * kDecWaves < P.hi) id_next = page_id(A, P.s, P.T.page(i + 2 * kDecWaves));
+  };
   while (i < P.hi) {
-    if (i + kWaves < P.hi) load_tile<D>(A, P.s, P.h, P.T.page(i + kWaves), raw[1]);
+    ahead(raw[1]);
     run(raw[0], i);
-    i += kWaves;
+    i += kDecWaves;
     if (i >= P.hi) break;
-    if (i + kWaves < P.hi) load_tile<D>(A, P.s, P.h, P.T.page(i + kWaves), raw[0]);
+    ahead(raw[0]);
     run(raw[1], i);
-    i += kWaves;
+    i += kDecWaves;
   }
 
   // the waves' results meet in LDS
-  constexpr int kStride = D + 4;
-  __shared__ float so[kWaves][kRows][kStride];
-  __shared__ float sm[kWaves][kRows], sl[kWaves][kRows];
-  st.l += __shfl_xor(st.l, 16, 64);
-  st.l += __shfl_xor(st.l, 32, 64);
-  st.corr += __shfl_xor(st.corr, 16, 64);
-  st.corr += __shfl_xor(st.corr, 32, 64);
+  st.l = quarter_sum(st.l);
+  st.corr = 0.5f * quarter_sum(st.corr);
 #pragma unroll
-  for (int d = 0; d < D / 16; d++) {
-    f4 o;
-#pragma unroll
-    for (int r = 0; r < 4; r++) o[r] = (st.o[d][r] + 0.5f * st.corr) * st.unit;
-    *reinterpret_cast<f4 *>(&so[wave][n16][16 * d + 4 * g]) = o;
-  }
+  for (int d = 0; d < D / 16; d++)
+    *reinterpret_cast<f4 *>(&S.w.o[wave][n16][16 * d + 4 * g]) = (st.o[d] + st.corr) * st.unit;
   if (g == 0) {
-    sm[wave][n16] = st.m;
-    sl[wave][n16] = st.l;
+    S.w.m[wave][n16] = st.m;
+    S.w.l[wave][n16] = st.l;
   }
   __syncthreads();
-  constexpr int kPer = D / 16;  // outputs of a thread: row tid / 16
-  const int row = tid >> 4, d0 = (tid & 15) * kPer;
-  float M = kNone, L = 0.0f, o[kPer];
+  // outputs 4 c .. 4 c + 3 of a row, for the rows that are there
+  constexpr int kQuads = D / 4, kRound = kDecThreads / kQuads;
+  auto write_out = [&](int row, int d, f4 o) {
+    const uint32_t f = P.f0 + row;
+    _Float16 *dst = A.out + (int64_t)(P.begin + f / (uint32_t)A.group) * A.out_stride +
+                    (P.h * A.group + f % (uint32_t)A.group) * D + d;
+    *reinterpret_cast<h4 *>(dst) = (h4){(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]};
+  };
+  Rsrc base = make_rsrc(A.partials + P.tile * A.nsplit * partial_floats(kRows, D));
+  for (int row = tid / kQuads; row < P.nrows; row += kRound) {
+    const int c = tid % kQuads;
+    float M = kNone, L = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWaves; w++) M = fmaxf(M, sm[w][row]);
+    for (int w = 0; w < kDecWaves; w++) M = fmaxf(M, S.w.m[w][row]);
+    f4 o = {0, 0, 0, 0};
 #pragma unroll
-  for (int j = 0; j < kPer; j++) o[j] = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kWaves; w++) {
-    const float f = __builtin_amdgcn_exp2f(sm[w][row] - M);
-    L += f * sl[w][row];
-#pragma unroll
-    for (int j = 0; j < kPer; j++) o[j] += f * so[w][row][d0 + j];
-  }
-
-  const bool live = row < P.nrows;
-  if (P.splits > 1) {
-    float *base = A.partials + P.tile * A.nsplit * partial_floats(kRows, D);
-    float *mine = base + (int64_t)P.split * partial_floats(kRows, D);
-    if (live) {
-#pragma unroll
-      for (int j = 0; j < kPer; j++) store_dev(mine + row * D + d0 + j, o[j]);
-      if ((tid & 15) == 0) {
-        store_dev(mine + kRows * D + 2 * row, M);
-        store_dev(mine + kRows * D + 2 * row + 1, L);
-      }
+    for (int w = 0; w < kDecWaves; w++) {
+      const float f = __builtin_amdgcn_exp2f(S.w.m[w][row] - M);
+      L += f * S.w.l[w][row];
+      o += f * *reinterpret_cast<const f4 *>(&S.w.o[w][row][4 * c]);
     }
-    if (!last_split(A.counters + P.tile, P.splits)) return;  // another split finishes this tile
-    if (live) join_row<kRows, D, kPer>(base, P.splits, row, d0, M, L, o);
-    __syncthreads();
-    if (live && (tid & 15) == 0) clear_row<kRows, D>(base, P.splits, row);
+    if (P.splits > 1) {
+      const int at = P.split * partial_floats(kRows, D);
+      store_dev(base, at + row * D + 4 * c, o);
+      if (c == 0) store_dev2(base, at + kRows * D + 2 * row, M, L);
+    } else {
+      write_out(row, 4 * c, o * inverse(L));
+    }
   }
-  if (live) {
-    const int64_t f = P.f0 + row;
-    _Float16 *dst = A.out + (int64_t)(P.begin + f / A.group) * A.out_stride + (P.h * A.group + f % A.group) * D + d0;
-    const float r = inverse(L);
-#pragma unroll
-    for (int j = 0; j < kPer; j++) dst[j] = (_Float16)(o[j] * r);
-  }
+  if (P.splits > 1 && last_split(A.counters + P.tile, P.splits))
+    join<kRows, D, kDecThreads, kDecSplits>(base, P.splits, P.nrows, S.join, write_out);
 }
 
 // ---- many rows -----------------------------------------------------------
@@ -410,22 +480,12 @@ __global__ __launch_bounds__(kThreads, 2) void decode_kernel(const AttnArgs A) {
 // score exceeds it by 2^8 in weight, so the output is hardly ever rescaled
 // (fp16 weights reach 2^8, times 2^4 for the page's value scale).
 constexpr int kTileRows = 128, kWaveRows = 32;
+constexpr int kThreads = 256;
+constexpr int kPreSplits = 16;
 typedef float f16x __attribute__((ext_vector_type(16)));
 
 // The token of a 32-token group that row r of the score product takes.
 __device__ __forceinline__ int row_token(int r) { return (r & 16) + ((r >> 2) & 1) * 8 + ((r >> 3) & 1) * 4 + (r & 3); }
-
-// The larger of a lane's value and its partner's in the other half of the wave.
-__device__ __forceinline__ float half_max(float v) {
-  const uint32_t b = __float_as_uint(v);
-  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float half_sum(float v) {
-  const uint32_t b = __float_as_uint(v);
-  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
 
 template <int D>
 struct Page {
@@ -434,8 +494,7 @@ struct Page {
 };
 
 template <int D>
-__device__ __forceinline__ void load_page(const AttnArgs &A, int s, int h, int pg, Page<D> &t) {
-  const int id = __builtin_amdgcn_readfirstlane(A.table[(int64_t)s * A.max_pages + pg]);
+__device__ __forceinline__ void load_page(const AttnArgs &A, int h, int id, Page<D> &t) {
   const bool ok = id >= 0 && id < A.num_pages;
   const int64_t ph = (int64_t)(ok ? id : 0) * A.hkv + h;
   t.ks = ok ? A.ks[ph] : -1.0f;
@@ -470,14 +529,18 @@ __device__ __forceinline__ void put_page(const Page<D> &t, Lds<D> &l) {
 
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) {
-  __shared__ __attribute__((aligned(16))) Lds<D> lds[2];
+  union Shared {
+    Lds<D> page[2];
+    float join[kJoinFloats<kTileRows, kPreSplits, kThreads>];
+  };
+  __shared__ __attribute__((aligned(16))) Shared S;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31, half = lane >> 5;
   Place P;
   if (!find_place<kTileRows>(A, P)) return;
   const int row = wave * kWaveRows + n;
   const bool valid = row < P.nrows;
-  const int64_t fl = P.f0 + row;
-  const int tok = valid ? (int)(fl / A.group) : 0, head = P.h * A.group + (valid ? (int)(fl % A.group) : 0);
+  const uint32_t fl = P.f0 + (valid ? row : 0);
+  const int tok = fl / (uint32_t)A.group, head = P.h * A.group + fl % (uint32_t)A.group;
   const int pos = valid ? P.p0 + tok : -1;
   const _Float16 *qr = A.q + (int64_t)(P.begin + tok) * A.q_stride + head * D;
   h8 qf[D / 16];
@@ -495,8 +558,8 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) 
   qsum = 0.5f * half_sum(qsum);
   // the wave's own rows: positions wmin .. wmax (none: wmax = -1)
   const int r0 = wave * kWaveRows, r1 = min(r0 + kWaveRows, P.nrows) - 1;
-  const int wmin = P.p0 + (int)((P.f0 + r0) / A.group);
-  const int wmax = r1 < r0 ? -1 : P.p0 + (int)((P.f0 + r1) / A.group);
+  const int wmin = P.p0 + (uint32_t)(P.f0 + r0) / (uint32_t)A.group;
+  const int wmax = r1 < r0 ? -1 : P.p0 + (int)((uint32_t)(P.f0 + r1) / (uint32_t)A.group);
 
   f16x o[D / 32];
 #pragma unroll
@@ -506,17 +569,20 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) 
   float m = kNone, l = 0.0f, corr = 0.0f, unit = 1.0f;
   Page<D> next;
   float ks, vs;
+  int id_next = 0;
   if (P.lo < P.hi) {
-    load_page<D>(A, P.s, P.h, P.T.page(P.lo), next);
-    put_page<D>(next, lds[0]);
+    load_page<D>(A, P.h, page_id(A, P.s, P.T.page(P.lo)), next);
+    if (P.lo + 1 < P.hi) id_next = page_id(A, P.s, P.T.page(P.lo + 1));
+    put_page<D>(next, S.page[0]);
   }
   ks = next.ks;
   vs = next.vs;
   __syncthreads();
   for (int i = P.lo; i < P.hi; i++) {
-    const Lds<D> &L = lds[(i - P.lo) & 1];
+    const Lds<D> &L = S.page[(i - P.lo) & 1];
     const bool more = i + 1 < P.hi;
-    if (more) load_page<D>(A, P.s, P.h, P.T.page(i + 1), next);
+    if (more) load_page<D>(A, P.h, id_next, next);
+    if (i + 2 < P.hi) id_next = page_id(A, P.s, P.T.page(i + 2));
     const int pg = P.T.page(i), j0 = pg * kPage, j1 = j0 + kPage - 1;
     const bool none = ks < 0.0f || j0 > wmax || (A.window && j1 <= wmin - A.window && j0 >= A.sinks);
     if (!none) {
@@ -594,7 +660,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) 
       }
     }
     if (more) {
-      put_page<D>(next, lds[(i + 1 - P.lo) & 1]);
+      put_page<D>(next, S.page[(i + 1 - P.lo) & 1]);
       ks = next.ks;
       vs = next.vs;
     }
@@ -609,33 +675,23 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) 
 
   // element r of o[d] is output 32 d + 8 (r / 4) + 4 half + r % 4
   if (P.splits > 1) {
-    float *base = A.partials + P.tile * A.nsplit * partial_floats(kTileRows, D);
-    float *mine = base + (int64_t)P.split * partial_floats(kTileRows, D);
+    Rsrc base = make_rsrc(A.partials + P.tile * A.nsplit * partial_floats(kTileRows, D));
+    const int at = P.split * partial_floats(kTileRows, D);
     if (valid) {
 #pragma unroll
       for (int d = 0; d < D / 32; d++)
 #pragma unroll
-        for (int r = 0; r < 16; r++) store_dev(mine + row * D + 32 * d + 8 * (r >> 2) + 4 * half + (r & 3), o[d][r]);
-      if (half == 0) {
-        store_dev(mine + kTileRows * D + 2 * row, m);
-        store_dev(mine + kTileRows * D + 2 * row + 1, l);
-      }
+        for (int r = 0; r < 16; r += 4)
+          store_dev(base, at + row * D + 32 * d + 2 * r + 4 * half, (f4){o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]});
+      if (half == 0) store_dev2(base, at + kTileRows * D + 2 * row, m, l);
     }
-    if (!last_split(A.counters + P.tile, P.splits)) return;  // another split finishes this tile
-    constexpr int kPer = 8;
-    for (int i = threadIdx.x; i < P.nrows * (D / kPer); i += kThreads) {
-      const int jr = i / (D / kPer), d0 = i % (D / kPer) * kPer;
-      float M, S, v[kPer];
-      join_row<kTileRows, D, kPer>(base, P.splits, jr, d0, M, S, v);
-      const int64_t f = P.f0 + jr;
-      const float inv = inverse(S);
-      h8 x;
-#pragma unroll
-      for (int j = 0; j < kPer; j++) x[j] = (_Float16)(v[j] * inv);
-      *reinterpret_cast<h8 *>(A.out + (int64_t)(P.begin + f / A.group) * A.out_stride + (P.h * A.group + f % A.group) * D + d0) = x;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < P.nrows; i += kThreads) clear_row<kTileRows, D>(base, P.splits, i);
+    if (last_split(A.counters + P.tile, P.splits))
+      join<kTileRows, D, kThreads, kPreSplits>(base, P.splits, P.nrows, S.join, [&](int jr, int d, f4 v) {
+        const uint32_t f = P.f0 + jr;
+        *reinterpret_cast<h4 *>(A.out + (int64_t)(P.begin + f / (uint32_t)A.group) * A.out_stride +
+                                (P.h * A.group + f % (uint32_t)A.group) * D + d) =
+            (h4){(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+      });
     return;
   }
   if (valid) {
@@ -660,8 +716,8 @@ struct Plan {
   size_t counter_bytes, bytes;
 };
 
-constexpr int kTargetWgs = 512;  // two workgroups a CU
-constexpr int kMinChunk = 4, kMaxChunk = 32;
+constexpr int kCus = 256;
+constexpr int kMaxChunk = 64;
 
 Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_kv) {
   Plan P;
@@ -671,10 +727,12 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
   P.slots = rows * group / R + seqs;
   const int64_t tiles = (max_kv + kPage - 1) / kPage;
   const int64_t full = (rows * group + R - 1) / R, units = (full > seqs ? full : seqs) * kv_heads;
-  int64_t chunk = (tiles * units + kTargetWgs - 1) / kTargetWgs;
-  if (chunk < kMinChunk) chunk = kMinChunk;
+  const int64_t target = P.prefill ? 2 * kCus : kCus, least = P.prefill ? 4 : kDecWaves, most = P.prefill ? kPreSplits : kDecSplits;
+  int64_t chunk = (tiles * units + target - 1) / target;
+  if (chunk < least) chunk = least;
   if (!P.prefill && chunk > kMaxChunk) chunk = kMaxChunk;
   int64_t nsplit = (tiles + chunk - 1) / chunk;
+  if (nsplit > most) nsplit = most;
   if (nsplit < 1) nsplit = 1;
   P.chunk = (int)(chunk < 0x7fffffff ? chunk : 0x7fffffff);
   P.nsplit = (int)nsplit;
@@ -736,7 +794,7 @@ extern "C" int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t k
   A.rows = (int)rows; A.seqs = (int)seqs; A.hkv = (int)kv_heads; A.group = (int)(q_heads / kv_heads);
   A.window = (int)window; A.sinks = (int)sinks;
   A.nsplit = P.nsplit; A.chunk = P.chunk;
-  const dim3 grid((unsigned)wgs), block(kThreads);
+  const dim3 grid((unsigned)wgs), block(P.prefill ? kThreads : kDecThreads);
   hipStream_t st = (hipStream_t)stream;
   if (P.prefill) {
     if (head_dim == 128) hipLaunchKernelGGL(prefill_kernel<128>, grid, block, 0, st, A);
