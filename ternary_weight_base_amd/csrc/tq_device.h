@@ -46,6 +46,14 @@ __device__ __forceinline__ float row16_max(float v) {
   return fmaxf(v, __int_as_float(dpp_move<kDppRor8>(__float_as_int(v))));
 }
 
+// In every lane: the sum over its row of 16 lanes, in a fixed order.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += __int_as_float(dpp_move<kDppSwap1>(__float_as_int(v)));
+  v += __int_as_float(dpp_move<kDppSwap2>(__float_as_int(v)));
+  v += __int_as_float(dpp_move<kDppRor4>(__float_as_int(v)));
+  return v + __int_as_float(dpp_move<kDppRor8>(__float_as_int(v)));
+}
+
 // The maximum over the 64 lanes, wave-uniform.  fmaxf is exact and
 // order-free, so this equals any other reduction order.
 __device__ __forceinline__ float wave_max64(float v) {

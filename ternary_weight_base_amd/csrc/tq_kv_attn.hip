@@ -20,9 +20,10 @@
 // next within a lane: no LDS, no lane exchange, and every softmax quantity is
 // lane-local but for two exchanges of the running maximum.
 //
-// The weights are rounded to fp16 for the second product.  The decode kernel
-// adds the rounding error back as a second fp16 term (its matrix units are
-// idle anyway), so there only the output's own rounding to fp16 is left.
+// The weights are rounded to fp16 for the second product.  The kernel for up
+// to 16 rows adds the rounding error back as a second fp16 term (its matrix
+// units are idle anyway), so there only the output's own rounding to fp16 is
+// left; with more rows the term would cost 10 % and more.
 //
 // Bound: few rows (decode) read 2 head_dim bytes a token and KV head and are
 // bound by HBM; the work along the keys is split over workgroups, whose
@@ -32,6 +33,7 @@
 #include <stdint.h>
 
 #include "tq.h"
+#include "tq_device.h"
 #include "tq_kv.h"
 
 namespace {
@@ -42,8 +44,9 @@ typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 16;  // (token, query head) rows of a decode workgroup
-constexpr int kDecThreads = 512, kDecWaves = kDecThreads / 64;
-constexpr int kDecSplits = 128;  // splits of the keys at most, decode
+constexpr int kWaves = 8;  // of a decode workgroup
+constexpr int kDecPieces = 128;  // pieces of a unit at most (and one or two more)
+constexpr int kSnap = 4, kLeast = 8, kWhole = 16;  // pages: see "few rows"
 constexpr float kNone = -1e30f;  // running maximum before the first visible key
 
 struct AttnArgs {
@@ -57,7 +60,8 @@ struct AttnArgs {
   float *partials;
   float scale_log2;
   int rows, seqs, hkv, group, window, sinks;
-  int nsplit, chunk;  // splits of the keys at most; pages of a split at least
+  int nsplit, chunk;  // prefill: splits of the keys at most; pages of a split at least
+  int whole;          // decode: units of up to so many pages stay whole
 };
 
 // The visible pages of a row tile whose positions are pmin .. pmax: pages
@@ -124,7 +128,9 @@ __device__ __forceinline__ float quarter_sum(float v) {
   return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// The bytes of one page and KV head that a lane takes part in.
+// The bytes of one page and KV head that a lane takes part in.  Keys and
+// values are fetched apart: the next page's keys as soon as this page's have
+// been used, its values after this page's.
 template <int D>
 struct Raw {
   uint4 k[4][D / 64], v[D / 16];
@@ -132,105 +138,99 @@ struct Raw {
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs &A, int h, int id, Raw<D> &t) {
+__device__ __forceinline__ void load_keys(const AttnArgs &A, int h, int id, Raw<D> &t) {
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
   const bool ok = id >= 0 && id < A.num_pages;
   const int64_t ph = (int64_t)(ok ? id : 0) * A.hkv + h;
-  const uint8_t *kp = A.k + ph * (kPage * D), *vp = A.v + ph * (kPage * D);
+  const uint8_t *kp = A.k + ph * (kPage * D) + (16 * (m >> 2) + (m & 3)) * D + 16 * g;
   t.ks = ok ? A.ks[ph] : -1.0f;
-  t.vs = A.vs[ph];
 #pragma unroll
   for (int i = 0; i < 4; i++)
 #pragma unroll
-    for (int j = 0; j < D / 64; j++)
-      t.k[i][j] = *reinterpret_cast<const uint4 *>(kp + (16 * (m >> 2) + 4 * i + (m & 3)) * D + 64 * j + 16 * g);
+    for (int j = 0; j < D / 64; j++) t.k[i][j] = *reinterpret_cast<const uint4 *>(kp + 4 * i * D + 64 * j);
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(const AttnArgs &A, int h, int id, Raw<D> &t) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+  const int64_t ph = (int64_t)(id >= 0 && id < A.num_pages ? id : 0) * A.hkv + h;
+  const uint8_t *vp = A.v + ph * (kPage * D) + m * kPage + 16 * g;
+  t.vs = A.vs[ph];
 #pragma unroll
-  for (int i = 0; i < D / 16; i++) t.v[i] = *reinterpret_cast<const uint4 *>(vp + (16 * i + m) * kPage + 16 * g);
+  for (int i = 0; i < D / 16; i++) t.v[i] = *reinterpret_cast<const uint4 *>(vp + 16 * i * kPage);
 }
 
 // Running state of a lane's query row.  The output is held as
 //   unit * (o + corr / 2), corr = sum of the weights that o's products took,
-// where `unit` is a value scale: pages whose scale is within 2^4 of it have
-// the ratio folded into their weights, others move the state to their own.
+// where `unit` (one for the wave) is a value scale: pages whose scale is
+// within 2^4 of it have the ratio folded into their weights, others move the
+// state to their own.  m is a reference for the weights' exponents: it moves
+// only when a score exceeds it by 8 (weights reach 2^8, times 2^4 for the
+// scale, in fp16), so the outputs are hardly ever rescaled.
 template <int D>
 struct State {
   f4 o[D / 16];
-  float m, l, corr, unit;
+  float m, l, corr;
 };
 
-template <int D>
-__device__ __forceinline__ void step(const AttnArgs &A, const Raw<D> &t, const h8 (&qf)[D / 32], float qsum, int pg,
-                                     int pos, bool masked, State<D> &st) {
-  const int g = (threadIdx.x & 63) >> 4;
-  if (t.ks < 0.0f) return;  // wave-uniform
-  float x[16];
-  const float sc = t.ks * A.scale_log2;
+// Scores of RT tiles of 16 rows against a page's keys, before any scale.
+template <int D, int RT>
+__device__ __forceinline__ void scores(const Raw<D> &t, const h8 (&qf)[RT][D / 32], f4 (&x)[RT][4]) {
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    f4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int a = 0; a < RT; a++) x[a][i] = (f4){0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < D / 64; j++) {
       const uint4 w = t.k[i][j];
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(w.x, w.y), qf[2 * j], acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(w.z, w.w), qf[2 * j + 1], acc, 0, 0, 0);
-    }
+      const h8 k0 = codes8(w.x, w.y), k1 = codes8(w.z, w.w);
 #pragma unroll
-    for (int r = 0; r < 4; r++) x[4 * i + r] = (acc[r] + qsum) * sc;
+      for (int a = 0; a < RT; a++) {
+        x[a][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[a][2 * j], x[a][i], 0, 0, 0);
+        x[a][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[a][2 * j + 1], x[a][i], 0, 0, 0);
+      }
+    }
   }
+}
+
+// The weights of one row tile: hi (+ lo, if LO) fp16 terms of w * 2^shift.
+template <int D, bool LO>
+__device__ __forceinline__ void weights(const AttnArgs &A, f4 (&x)[4], float qsum, float sc, float shift, float unit_moves,
+                                        bool masked, int j0, int pos, bool has_v, State<D> &st, h8 (&hi)[2], h8 (&lo)[2]) {
   if (masked) {
-    const int j0 = pg * kPage + 16 * g;
 #pragma unroll
     for (int i = 0; i < 16; i++) {
       const int j = j0 + i;
       const bool see = j <= pos && (A.window == 0 || j > pos - A.window || j < A.sinks);
-      x[i] = see ? x[i] : -__builtin_inff();
+      x[i >> 2][i & 3] = see ? x[i >> 2][i & 3] : -__builtin_inff();
     }
   }
-  float mx = x[0];
+  float mx = x[0][0];
 #pragma unroll
-  for (int i = 1; i < 16; i++) mx = fmaxf(mx, x[i]);
-  mx = quarter_max(mx);
-  float shift = 0.0f;  // log2 of this page's value scale over the unit
-  float alpha = 1.0f;
-  const float m_new = fmaxf(st.m, mx);
-  alpha = __builtin_amdgcn_exp2f(st.m - m_new);
-  st.m = m_new;
-  st.l *= alpha;
-  const bool has_v = t.vs > 0.0f;  // a page of zeros adds to the sum only
-  if (has_v) {
-    const float ratio = t.vs / st.unit;
-    if (!(ratio > 0.0625f && ratio < 16.0f)) {
-      alpha *= fminf(st.unit / t.vs, 3.0e38f);
-      st.unit = t.vs;
-    } else {
-      shift = __builtin_amdgcn_logf(ratio);
-    }
+  for (int i = 1; i < 16; i++) mx = fmaxf(mx, x[i >> 2][i & 3]);
+  mx = (quarter_max(mx) + qsum) * sc;
+  if (unit_moves != 1.0f || __any(mx > st.m + 8.0f)) {
+    const float mn = mx > st.m + 8.0f ? mx : st.m;
+    float alpha = __builtin_amdgcn_exp2f(st.m - mn);
+    st.m = mn;
+    st.l *= alpha;
+    alpha *= unit_moves;
+    st.corr *= alpha;
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) st.o[i] *= alpha;
   }
-  st.corr *= alpha;
-#pragma unroll
-  for (int i = 0; i < D / 16; i++) st.o[i] *= alpha;
+  const float bias = qsum * sc + shift - st.m;
   float sum = 0.0f;
-  h8 p[2], e[2];
 #pragma unroll
   for (int i = 0; i < 16; i++) {
-    const float w = __builtin_amdgcn_exp2f(x[i] - m_new + shift);
+    const float w = __builtin_amdgcn_exp2f(x[i >> 2][i & 3] * sc + bias);
     sum += w;
     const _Float16 r = (_Float16)w;
-    p[i >> 3][i & 7] = r;
-    e[i >> 3][i & 7] = (_Float16)(w - (float)r);
+    hi[i >> 3][i & 7] = r;
+    if (LO) lo[i >> 3][i & 7] = (_Float16)(w - (float)r);
   }
   st.l += sum * __builtin_amdgcn_exp2f(-shift);
-  if (!has_v) return;
-  st.corr += sum;
-#pragma unroll
-  for (int i = 0; i < D / 16; i++) {
-    const uint4 w = t.v[i];
-    const h8 a = codes8(w.x, w.y), b = codes8(w.z, w.w);
-    st.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, p[0], st.o[i], 0, 0, 0);
-    st.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, p[1], st.o[i], 0, 0, 0);
-    st.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, e[0], st.o[i], 0, 0, 0);
-    st.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, e[1], st.o[i], 0, 0, 0);
-  }
+  if (has_v) st.corr += sum;
 }
 
 // Floats of one split's partial result for R rows: outputs, then (max, sum)
@@ -255,54 +255,76 @@ __device__ __forceinline__ bool last_split(uint32_t *counter, int splits) {
 // 1 / sum of weights; 0 for a row that saw no key.
 __device__ __forceinline__ float inverse(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
 
-// The last split's join of a tile: the partial results at `part`, summed in
-// the order of the splits; `out(row, d, f4)` takes the outputs.  First every
-// split's weight per row, then the outputs, 16 bytes a thread, several
-// splits' loads in flight; where the rows are fewer than the threads, the
-// splits are dealt over `parts` groups of threads that meet in LDS.  The
-// words read are left zero for the next call, whatever its shape.
-template <int R, int D, int NT, int MAXS, typename Out>
-__device__ __forceinline__ void join(Rsrc part, int splits, int nrows, float *lds, const Out &out) {
-  constexpr int PF = partial_floats(R, D), kBatch = 8;
-  const int tid = threadIdx.x;
-  float *wm = lds, *wl = lds + R * MAXS;
-  for (int i = tid; i < splits * R; i += NT) {
-    const int k = i / R, r = i % R;
-    float m = kNone, l = 0.0f;
-    if (r < nrows) {
-      load_dev2(part, k * PF + R * D + 2 * r, m, l);
-      store_dev2(part, k * PF + R * D + 2 * r, 0.0f, 0.0f);
-    }
-    wm[i] = m;
-    wl[i] = l;
-  }
-  __syncthreads();
-  if (tid < R) {
-    float M = kNone, L = 0.0f;
-    for (int k = 0; k < splits; k++) M = fmaxf(M, wm[k * R + tid]);
-    for (int k = 0; k < splits; k++) L += wl[k * R + tid] * __builtin_amdgcn_exp2f(wm[k * R + tid] - M);
-    const float inv = inverse(L);
-    for (int k = 0; k < splits; k++) wm[k * R + tid] = inv * __builtin_amdgcn_exp2f(wm[k * R + tid] - M);
-  }
-  __syncthreads();
+// The last piece's join of a tile of R rows: the partial results, piece k's at
+// float `at(k)` of `part`, summed in the order of the pieces;
+// `out(row, d, f4)` takes the outputs.  Each row's maximum and sum over the
+// pieces come from 16 lanes; the outputs take 16 bytes a thread with kBatch
+// pieces' loads in flight (the first of them before the weights are known);
+// where the rows are fewer than the threads, the pieces are dealt over
+// `parts` groups of threads that meet in LDS.  The words read are left zero
+// for the next call, whatever its shape.
+template <int R, int D, int NT, int MAXP, typename At, typename Out>
+__device__ __forceinline__ void join(int tid, Rsrc part, int pieces, int nrows, float *lds, const At &at, const Out &out) {
+  constexpr int kBatch = 8, kPer16 = (MAXP + 15) / 16;
   const int quads = nrows * (D / 4);
   const int parts = quads * 4 <= NT ? 4 : quads * 2 <= NT ? 2 : 1;
-  const int per = NT / parts, p = tid / per;
-  f4 *red = reinterpret_cast<f4 *>(lds + 2 * R * MAXS);
-  for (int q = tid - p * per; q < quads; q += per) {  // one round where parts > 1
-    const int row = q / (D / 4), w = q * 4;
-    f4 o = {0, 0, 0, 0};
-    for (int k0 = p; k0 < splits; k0 += kBatch * parts) {
-      f4 v[kBatch];
+  const int per = NT / parts, p = tid / per, q0 = tid - p * per;
+  f4 v[kBatch];
+  auto fetch = [&](int k0, int q) {
 #pragma unroll
-      for (int b = 0; b < kBatch; b++) v[b] = load_dev(part, min(k0 + b * parts, splits - 1) * PF + w);
+    for (int b = 0; b < kBatch; b++) v[b] = load_dev(part, at(min(k0 + b * parts, pieces - 1)) + 4 * q);
+  };
+  if (q0 < quads) fetch(p, q0);
+  float *wt = lds;  // the pieces' weights, [MAXP][R]
+  const int j = tid & 15;
+#pragma unroll 1
+  for (int r0 = 0; r0 < nrows; r0 += NT / 16) {
+    const int r = r0 + tid / 16, rr = min(r, nrows - 1);
+    float m[kPer16], l[kPer16], M = kNone, L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer16; i++) {
+      m[i] = kNone;
+      l[i] = 0.0f;
+      if (16 * i < pieces) load_dev2(part, at(min(16 * i + j, pieces - 1)) + R * D + 2 * rr, m[i], l[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer16; i++) {
+      if (16 * i + j >= pieces) m[i] = kNone, l[i] = 0.0f;
+      M = fmaxf(M, m[i]);
+    }
+    M = tqdev::row16_max(M);
+#pragma unroll
+    for (int i = 0; i < kPer16; i++) {
+      m[i] = __builtin_amdgcn_exp2f(m[i] - M);
+      L += m[i] * l[i];
+    }
+    const float inv = inverse(tqdev::row16_sum(L));
+#pragma unroll
+    for (int i = 0; i < kPer16; i++) {
+      const int k = 16 * i + j;
+      if (k < pieces && r < nrows) {
+        wt[k * R + r] = m[i] * inv;
+        store_dev2(part, at(k) + R * D + 2 * r, 0.0f, 0.0f);
+      }
+    }
+  }
+  __syncthreads();
+  f4 *red = reinterpret_cast<f4 *>(lds + R * MAXP);
+#pragma unroll 1
+  for (int q = q0; q < quads; q += per) {  // one round where parts > 1
+    const int row = q / (D / 4);
+    f4 o = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int k0 = p; k0 < pieces; k0 += kBatch * parts) {
+      if (q != q0 || k0 != p) fetch(k0, q);
 #pragma unroll
       for (int b = 0; b < kBatch; b++)
-        if (k0 + b * parts < splits) o += v[b] * wm[(k0 + b * parts) * R + row];
+        if (k0 + b * parts < pieces) o += v[b] * wt[(k0 + b * parts) * R + row];
     }
-    for (int k = p; k < splits; k += parts) store_dev(part, k * PF + w, (f4){0, 0, 0, 0});
+#pragma unroll 1
+    for (int k = p; k < pieces; k += parts) store_dev(part, at(k) + 4 * q, (f4){0, 0, 0, 0});
     if (parts == 1)
-      out(row, w - row * D, o);
+      out(row, 4 * q - row * D, o);
     else
       red[tid] = o;
   }
@@ -315,7 +337,7 @@ __device__ __forceinline__ void join(Rsrc part, int splits, int nrows, float *ld
   }
 }
 template <int R, int MAXS, int NT>
-constexpr int kJoinFloats = 2 * R * MAXS + 4 * NT;
+constexpr int kJoinFloats = R * MAXS + 4 * NT;
 
 // A workgroup's place: R consecutive (token, query head) rows of a sequence
 // and KV head, and its share of their pages.
@@ -354,114 +376,403 @@ __device__ __forceinline__ int page_id(const AttnArgs &A, int s, int pg) {
   return __builtin_amdgcn_readfirstlane(A.table[(int64_t)s * A.max_pages + pg]);
 }
 
-template <int D>
-__global__ __launch_bounds__(kDecThreads, 2) void decode_kernel(const AttnArgs A) {
-  constexpr int kStride = D + 4;
+// ---- few rows ------------------------------------------------------------
+//
+// A unit of work is a tile of R rows of a sequence and one KV head, and has
+// `pages` pages (the most that a row tile of the sequence sees; what a tile does not
+// see is cut off later).  The workgroups share the units out by the lengths
+// that they read, whatever the host knows of them:
+//  - as many units as workgroups at most: each is cut into equal pieces of up
+//    to `per` pages, `per` the least for which the pieces are no more than the
+//    workgroups; a workgroup has one piece.  (Shares of the same length that
+//    run over unit borders are two units' work for most workgroups, with two
+//    starts and ends: 39 against 26 us for 8 sequences with 4 drafted rows.)
+//  - more: workgroup w takes pages w * per .. (w + 1) * per - 1 of the list of
+//    all units' pages.  A border that would cut off less than kSnap pages of a
+//    unit, or that falls into a unit of at most `whole` pages, moves to the
+//    unit's end or start.
+// A unit that is cut is joined by the last of its workgroups; only a
+// workgroup's first and last unit can be cut, so two partial results a
+// workgroup are all the workspace there is.
+struct Seq {
+  int begin, n, kv, units, pages;  // units: row tiles * KV heads
+};
+
+template <int R>
+__device__ __forceinline__ Seq seq_at(const AttnArgs &A, int begin, int end, int kv) {
+  Seq q;
+  q.begin = begin;
+  q.n = max(end - begin, 0);
+  q.kv = max(kv, 0);
+  int64_t pages = min((int64_t)((q.kv + (int64_t)kPage - 1) / kPage), A.max_pages);
+  if (A.window) {
+    const int64_t seen = ((int64_t)A.sinks + kPage - 1) / kPage + ((int64_t)A.window + R) / kPage + 2;
+    pages = min(pages, seen);
+  }
+  q.pages = (int)max(pages, (int64_t)1);  // a unit that sees nothing still has its zeros to write
+  q.units = (int)((uint32_t)(q.n * A.group + R - 1) / (uint32_t)R) * A.hkv;
+  return q;
+}
+
+template <int R>
+__device__ __forceinline__ Seq seq_load(const AttnArgs &A, int s) {
+  return seq_at<R>(A, cu_at(A.cu, s, A.rows), cu_at(A.cu, s + 1, A.rows), A.kv_len[s]);
+}
+
+// The list of the units' pages, or of their pieces of `per` pages (per > 0):
+// its length, and the sequence of a position in it (the last one that starts
+// at or before it and is not empty).  Lanes take a sequence each, 64 at a
+// time; with up to 64 sequences everything stays in registers.
+template <int R>
+struct List {
+  int total, units, longest, per;
+  int count, incl;  // this lane's sequence
+  Seq seq;
+
+  __device__ __forceinline__ static int scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 of rows 0, 2 to rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2, 3
+    return v;
+  }
+
+  __device__ __forceinline__ void tally() {
+    count = seq.units * (per ? (int)((uint32_t)(seq.pages + per - 1) / (uint32_t)per) : seq.pages);
+    incl = scan(count);
+  }
+  __device__ __forceinline__ void load(const AttnArgs &A, int s) {
+    seq.pages = seq.units = 0;
+    if (s < A.seqs) seq = seq_load<R>(A, s);
+    tally();
+  }
+
+  // all units' pages
+  __device__ __forceinline__ void init(const AttnArgs &A) {
+    const int lane = threadIdx.x & 63;
+    total = units = per = 0;
+    float most = 0.0f;  // exact up to 2^24 pages, more than enough for a bound
+    for (int s0 = 0; s0 < A.seqs; s0 += 64) {
+      load(A, s0 + lane);
+      total += __builtin_amdgcn_readlane(incl, 63);
+      units += __builtin_amdgcn_readlane(scan(seq.units), 63);
+      most = fmaxf(most, count ? (float)seq.pages : 0.0f);
+    }
+    longest = (int)tqdev::wave_max64(most);
+  }
+  // all units' pieces of `p` pages at most
+  __device__ __forceinline__ void cut(const AttnArgs &A, int p) {
+    per = p;
+    if (A.seqs <= 64) {
+      tally();
+      total = __builtin_amdgcn_readlane(incl, 63);
+      return;
+    }
+    total = 0;
+    for (int s0 = 0; s0 < A.seqs; s0 += 64) {
+      load(A, s0 + (threadIdx.x & 63));
+      total += __builtin_amdgcn_readlane(incl, 63);
+    }
+  }
+
+  // -> the sequence, its first position in `start`
+  __device__ __forceinline__ int find(const AttnArgs &A, int b, int &start, Seq &q) {
+    int s0 = 0, before = 0;
+    if (A.seqs > 64) {
+      for (;; s0 += 64) {
+        load(A, s0 + (threadIdx.x & 63));
+        const int sum = __builtin_amdgcn_readlane(incl, 63);
+        if (b < before + sum || s0 + 64 >= A.seqs) break;
+        before += sum;
+      }
+    }
+    const uint64_t behind = __ballot(incl > b - before);
+    const int l = behind ? __builtin_ctzll(behind) : 63;
+    start = before + __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(count, l);
+    q.begin = __builtin_amdgcn_readlane(seq.begin, l);
+    q.n = __builtin_amdgcn_readlane(seq.n, l);
+    q.kv = __builtin_amdgcn_readlane(seq.kv, l);
+    q.units = __builtin_amdgcn_readlane(seq.units, l);
+    q.pages = __builtin_amdgcn_readlane(seq.pages, l);
+    return s0 + l;
+  }
+
+  // A border of the workgroups' shares, moved as said above.
+  __device__ __forceinline__ int snap(const AttnArgs &A, int64_t b64) {
+    if (b64 >= total) return total;
+    const int b = (int)b64;
+    if (b <= 0) return 0;
+    int start;
+    Seq q;
+    find(A, b, start, q);
+    const int u0 = start + (uint32_t)(b - start) / (uint32_t)q.pages * q.pages;
+    if (b == u0) return b;
+    if (q.pages <= A.whole || u0 + q.pages - b < kSnap) return u0 + q.pages;
+    return b - u0 < kSnap ? u0 : b;
+  }
+};
+
+// WHOLE: no unit is cut; a workgroup per unit, found as the prefill kernel
+// finds its tile, without the list and the join (2 to 4 us less for short
+// contexts, where the call is latency).
+template <int D, int RT, bool WHOLE, int NW>
+__global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const AttnArgs A) {
+  constexpr int kDecWaves = NW, kDecThreads = NW * 64;
+  constexpr int kStride = D + 4, R = kRows * RT, PF = partial_floats(R, D);
   union Shared {
     struct {
-      float o[kDecWaves][kRows][kStride], m[kDecWaves][kRows], l[kDecWaves][kRows];
+      float o[kDecWaves][R][kStride], m[kDecWaves][R], l[kDecWaves][R];
     } w;
-    float join[kJoinFloats<kRows, kDecSplits, kDecThreads>];
+    float join[WHOLE ? 1 : kJoinFloats<R, kDecPieces + 2, kDecThreads>];
   };
   __shared__ __attribute__((aligned(16))) Shared S;
-  const int tid = threadIdx.x, lane = tid & 63, n16 = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  Place P;
-  if (!find_place<kRows>(A, P)) return;
-  int i = P.lo + wave, id = 0, id_next = 0;
-  if (i < P.hi) id = page_id(A, P.s, P.T.page(i));
-  if (i + kDecWaves < P.hi) id_next = page_id(A, P.s, P.T.page(i + kDecWaves));
-  const bool valid = n16 < P.nrows;
-  const uint32_t fl = P.f0 + (valid ? n16 : 0);
-  const int tok = fl / (uint32_t)A.group, head = P.h * A.group + fl % (uint32_t)A.group;
-  const int pos = valid ? P.p0 + tok : -1;
-  const _Float16 *qr = A.q + (int64_t)(P.begin + tok) * A.q_stride + head * D;
-  h8 qf[D / 32];
-#pragma unroll
-  for (int j = 0; j < D / 64; j++)
-#pragma unroll
-    for (int u = 0; u < 2; u++) qf[2 * j + u] = *reinterpret_cast<const h8 *>(qr + 64 * j + 16 * g + 8 * u);
-  Raw<D> raw[2];
-  if (i < P.hi) load_tile<D>(A, P.h, id, raw[0]);
-  float qsum = 0.0f;
-#pragma unroll
-  for (int j = 0; j < D / 32; j++)
-#pragma unroll
-    for (int r = 0; r < 8; r++) {
-      qf[j][r] = valid ? qf[j][r] : (_Float16)0.0f;
-      qsum += (float)qf[j][r];
-    }
-  qsum = 0.5f * quarter_sum(qsum);
-
-  State<D> st;
-#pragma unroll
-  for (int d = 0; d < D / 16; d++) st.o[d] = (f4){0, 0, 0, 0};
-  st.m = kNone;
-  st.l = st.corr = 0.0f;
-  st.unit = 1.0f;
-  auto run = [&](const Raw<D> &t, int ti) {
-    const int pg = P.T.page(ti), j1 = pg * kPage + kPage - 1;
-    const bool all = j1 <= P.pmin && (A.window == 0 || pg * kPage > P.pmax - A.window || j1 < A.sinks);
-    step<D>(A, t, qf, qsum, pg, pos, !all, st);
-  };
-  // the next page's bytes are on their way while a page is worked on, the id
-  // of the one after that too
-  auto ahead = [&](Raw<D> &t) {
-    if (i + kDecWaves < P.hi) load_tile<D>(A, P.h, id_next, t);
-    if (i + 2 * kDecWaves < P.hi) id_next = page_id(A, P.s, P.T.page(i + 2 * kDecWaves));
-  };
-  while (i < P.hi) {
-    ahead(raw[1]);
-    run(raw[0], i);
-    i += kDecWaves;
-    if (i >= P.hi) break;
-    ahead(raw[0]);
-    run(raw[1], i);
-    i += kDecWaves;
-  }
-
-  // the waves' results meet in LDS
-  st.l = quarter_sum(st.l);
-  st.corr = 0.5f * quarter_sum(st.corr);
-#pragma unroll
-  for (int d = 0; d < D / 16; d++)
-    *reinterpret_cast<f4 *>(&S.w.o[wave][n16][16 * d + 4 * g]) = (st.o[d] + st.corr) * st.unit;
-  if (g == 0) {
-    S.w.m[wave][n16] = st.m;
-    S.w.l[wave][n16] = st.l;
-  }
-  __syncthreads();
-  // outputs 4 c .. 4 c + 3 of a row, for the rows that are there
-  constexpr int kQuads = D / 4, kRound = kDecThreads / kQuads;
-  auto write_out = [&](int row, int d, f4 o) {
-    const uint32_t f = P.f0 + row;
-    _Float16 *dst = A.out + (int64_t)(P.begin + f / (uint32_t)A.group) * A.out_stride +
-                    (P.h * A.group + f % (uint32_t)A.group) * D + d;
-    *reinterpret_cast<h4 *>(dst) = (h4){(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]};
-  };
-  Rsrc base = make_rsrc(A.partials + P.tile * A.nsplit * partial_floats(kRows, D));
-  for (int row = tid / kQuads; row < P.nrows; row += kRound) {
-    const int c = tid % kQuads;
-    float M = kNone, L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kDecWaves; w++) M = fmaxf(M, S.w.m[w][row]);
-    f4 o = {0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < kDecWaves; w++) {
-      const float f = __builtin_amdgcn_exp2f(S.w.m[w][row] - M);
-      L += f * S.w.l[w][row];
-      o += f * *reinterpret_cast<const f4 *>(&S.w.o[w][row][4 * c]);
-    }
-    if (P.splits > 1) {
-      const int at = P.split * partial_floats(kRows, D);
-      store_dev(base, at + row * D + 4 * c, o);
-      if (c == 0) store_dev2(base, at + kRows * D + 2 * row, M, L);
+  const int wg = blockIdx.x;
+  List<R> list;
+  int at = 0, stop = 1, per = 1;
+  bool equal = false;  // one piece a workgroup
+  if constexpr (!WHOLE) {
+    list.init(A);
+    const int wgs = gridDim.x;
+    const int even = (int)((uint32_t)(list.total + wgs - 1) / (uint32_t)wgs);
+    per = max(max(even, kLeast), (list.longest + kDecPieces - 1) / kDecPieces);
+    equal = list.units <= wgs;
+    if (equal) {
+      for (list.cut(A, per); list.total > wgs; list.cut(A, per)) per += max(per / 8, 1);
+      at = wg;
+      stop = min(wg + 1, list.total);
     } else {
-      write_out(row, 4 * c, o * inverse(L));
+      at = list.snap(A, (int64_t)wg * per);
+      stop = list.snap(A, (int64_t)(wg + 1) * per);
     }
   }
-  if (P.splits > 1 && last_split(A.counters + P.tile, P.splits))
-    join<kRows, D, kDecThreads, kDecSplits>(base, P.splits, P.nrows, S.join, write_out);
+  const Rsrc parts = make_rsrc(A.partials);
+  const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // What a workgroup works on: rows f0 .. f0 + nrows - 1 of a sequence and KV
+  // head, pages i, i + kDecWaves, ... < hi of its list T (i: this wave's first).
+  struct Unit {
+    int s, h, begin, f0, nrows, p0, pmin, pmax, i, hi, pieces, first;
+    Tiles T;
+  };
+  // the unit at list position `at`, which moves behind it; false: none
+  auto next_unit = [&](Unit &u) -> bool {
+    Seq q;
+    int from = 0, upto = 0x7fffffff;
+    u.pieces = 1;
+    u.first = wg;
+    if constexpr (WHOLE) {
+      u.h = wg % (uint32_t)A.hkv;
+      const int slot = wg / (uint32_t)A.hkv;
+      u.s = find_seq<R, 1>(A.cu, A.seqs, A.rows, slot, A.group);
+      q = seq_load<R>(A, u.s);
+      u.f0 = (slot - slot_base<R, 1>(q.begin, u.s, A.group)) * R;
+      at = stop;
+      if (u.f0 < 0 || u.f0 >= q.n * A.group) return false;
+    } else {
+      if (at >= stop) return false;
+      int start;
+      u.s = list.find(A, at, start, q);
+      int unit;
+      if (equal) {
+        u.pieces = (uint32_t)(q.pages + per - 1) / (uint32_t)per;
+        unit = (uint32_t)(at - start) / (uint32_t)u.pieces;
+        const int k = at - start - unit * u.pieces, size = (uint32_t)(q.pages + u.pieces - 1) / (uint32_t)u.pieces;
+        u.first = wg - k;
+        from = k * size;
+        upto = min(from + size, q.pages);
+        at = stop;
+      } else {
+        unit = (uint32_t)(at - start) / (uint32_t)q.pages;
+        const int u0 = start + unit * q.pages, end = min(u0 + q.pages, stop);
+        // the pieces of a cut unit belong to workgroups first, first + 1, ...
+        if (at != u0 || end != u0 + q.pages) {
+          const int cut = (uint32_t)(u0 + kSnap + per - 1) / (uint32_t)per;
+          u.pieces = (int)((uint32_t)(u0 + q.pages - kSnap) / (uint32_t)per) - cut + 2;
+          u.first = cut - 1;
+        }
+        from = at - u0;
+        upto = end - u0;
+        at = end;
+      }
+      u.h = (uint32_t)unit % (uint32_t)A.hkv;
+      u.f0 = (int)((uint32_t)unit / (uint32_t)A.hkv) * R;
+    }
+    u.begin = q.begin;
+    u.nrows = min(R, q.n * A.group - u.f0);
+    u.p0 = q.kv - q.n;  // may be negative: such rows see nothing
+    u.pmin = u.p0 + (uint32_t)u.f0 / (uint32_t)A.group;
+    u.pmax = u.p0 + (uint32_t)(u.f0 + u.nrows - 1) / (uint32_t)A.group;
+    u.T = visible_tiles(u.pmin, u.pmax, A.max_pages, A.window, A.sinks);
+    u.i = from + wave;
+    u.hi = min(upto, u.T.count);
+    return true;
+  };
+  int id_next = 0, pos[RT];
+  h8 qf[RT][D / 32];
+  Raw<D> raw;
+  // sends for the first page's bytes and the queries
+  auto fetch = [&](const Unit &u) {
+    if (u.i < u.hi) {
+      const int id = page_id(A, u.s, u.T.page(u.i));
+      if (u.i + kDecWaves < u.hi) id_next = page_id(A, u.s, u.T.page(u.i + kDecWaves));
+      load_keys<D>(A, u.h, id, raw);
+      load_values<D>(A, u.h, id, raw);
+    }
+#pragma unroll
+    for (int a = 0; a < RT; a++) {
+      const int row = kRows * a + n16;
+      const bool valid = row < u.nrows;
+      const uint32_t fl = u.f0 + (valid ? row : 0);
+      const int tok = fl / (uint32_t)A.group, head = u.h * A.group + fl % (uint32_t)A.group;
+      pos[a] = valid ? u.p0 + tok : -1;
+      const _Float16 *qr = A.q + (int64_t)(u.begin + tok) * A.q_stride + head * D;
+#pragma unroll
+      for (int j = 0; j < D / 64; j++)
+#pragma unroll
+        for (int k = 0; k < 2; k++) qf[a][2 * j + k] = *reinterpret_cast<const h8 *>(qr + 64 * j + 16 * g + 8 * k);
+    }
+  };
+
+  Unit u;
+  if (!next_unit(u)) return;
+  fetch(u);
+  for (;;) {
+    const int s = u.s, h = u.h, pmin = u.pmin, pmax = u.pmax, hi = u.hi;
+    const Tiles T = u.T;
+    int i = u.i, id;
+    State<D> st[RT];
+    float qsum[RT], unit_scale = 1.0f;
+#pragma unroll
+    for (int a = 0; a < RT; a++) {
+      qsum[a] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 32; j++)
+#pragma unroll
+        for (int r = 0; r < 8; r++) {
+          qf[a][j][r] = pos[a] >= 0 ? qf[a][j][r] : (_Float16)0.0f;
+          qsum[a] += (float)qf[a][j][r];
+        }
+      qsum[a] = 0.5f * quarter_sum(qsum[a]);
+#pragma unroll
+      for (int d = 0; d < D / 16; d++) st[a].o[d] = (f4){0, 0, 0, 0};
+      st[a].m = kNone;
+      st[a].l = st[a].corr = 0.0f;
+    }
+    for (; i < hi; i += kDecWaves) {
+      const bool more = i + kDecWaves < hi;
+      const int pg = T.page(i), j0 = pg * kPage, j1 = j0 + kPage - 1;
+      const bool masked = !(j1 <= pmin && (A.window == 0 || j0 > pmax - A.window || j1 < A.sinks));
+      const float ks = raw.ks, vs = raw.vs;
+      f4 x[RT][4];
+      scores<D, RT>(raw, qf, x);
+      id = id_next;
+      if (more) load_keys<D>(A, h, id, raw);
+      if (i + 2 * kDecWaves < hi) id_next = page_id(A, s, T.page(i + 2 * kDecWaves));
+      if (ks >= 0.0f) {  // wave-uniform, as all of this page's scales
+        // a page of zeros has scale 0: its (zero) scores stay finite, masked ones -inf
+        const float sc = fmaxf(ks * A.scale_log2, 1e-37f);
+        const bool has_v = vs > 0.0f;  // a page of zeros adds to the sum only
+        const float ratio = has_v ? vs / unit_scale : 1.0f;
+        const bool far = !(ratio > 0.0625f && ratio < 16.0f);
+        const float shift = far ? 0.0f : __builtin_amdgcn_logf(ratio);
+        const float moves = far ? fminf(unit_scale / vs, 3.0e38f) : 1.0f;
+        if (far) unit_scale = vs;
+        h8 hi16[RT][2], lo16[RT][2];
+#pragma unroll
+        for (int a = 0; a < RT; a++)
+          weights<D, RT == 1>(A, x[a], qsum[a], sc, shift, moves, masked, j0 + 16 * g, pos[a], has_v, st[a], hi16[a], lo16[a]);
+        if (has_v) {
+#pragma unroll
+          for (int d = 0; d < D / 16; d++) {
+            const uint4 w = raw.v[d];
+            const h8 v0 = codes8(w.x, w.y), v1 = codes8(w.z, w.w);
+#pragma unroll
+            for (int a = 0; a < RT; a++) {
+              st[a].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, hi16[a][0], st[a].o[d], 0, 0, 0);
+              st[a].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, hi16[a][1], st[a].o[d], 0, 0, 0);
+              if (RT == 1) {
+                st[a].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, lo16[a][0], st[a].o[d], 0, 0, 0);
+                st[a].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, lo16[a][1], st[a].o[d], 0, 0, 0);
+              }
+            }
+          }
+        }
+      }
+      if (more) load_values<D>(A, h, id, raw);
+    }
+
+    // the next unit's first bytes are on their way through this one's end
+    Unit n;
+    bool go_on = false;
+    if constexpr (!WHOLE) {
+      if (at < stop) {
+        list.load(A, lane);  // (not kept in registers through the loop)
+        go_on = next_unit(n);
+        fetch(n);
+      }
+    }
+
+    // the waves' results meet in LDS (the thread number through an empty asm:
+    // what follows is not to be computed ahead of the loop and kept)
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+#pragma unroll
+    for (int a = 0; a < RT; a++) {
+      const int row = kRows * a + n16;
+      const float l = quarter_sum(st[a].l), corr = 0.5f * quarter_sum(st[a].corr);
+      if (row < u.nrows) {
+#pragma unroll
+        for (int d = 0; d < D / 16; d++)
+          *reinterpret_cast<f4 *>(&S.w.o[wave][row][16 * d + 4 * g]) = (st[a].o[d] + corr) * unit_scale;
+        if (g == 0) {
+          S.w.m[wave][row] = st[a].m;
+          S.w.l[wave][row] = l;
+        }
+      }
+    }
+    __syncthreads();
+    // outputs 4 c .. 4 c + 3 of a row, for the rows that are there
+    constexpr int kQuads = D / 4, kRound = kDecThreads / kQuads;
+    auto write_out = [&](int row, int d, f4 o) {
+      const uint32_t f = u.f0 + row;
+      _Float16 *dst = A.out + (int64_t)(u.begin + f / (uint32_t)A.group) * A.out_stride +
+                      (h * A.group + f % (uint32_t)A.group) * D + d;
+      *reinterpret_cast<h4 *>(dst) = (h4){(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]};
+    };
+    const int mine = (2 * wg + (u.first == wg)) * PF;
+    for (int row = tid / kQuads; row < u.nrows; row += kRound) {
+      const int c = tid % kQuads;
+      float M = kNone, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kDecWaves; w++) M = fmaxf(M, S.w.m[w][row]);
+      f4 o = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kDecWaves; w++) {
+        const float f = __builtin_amdgcn_exp2f(S.w.m[w][row] - M);
+        L += f * S.w.l[w][row];
+        o += f * *reinterpret_cast<const f4 *>(&S.w.o[w][row][4 * c]);
+      }
+      if (u.pieces > 1) {
+        store_dev(parts, mine + row * D + 4 * c, o);
+        if (c == 0) store_dev2(parts, mine + R * D + 2 * row, M, L);
+      } else {
+        write_out(row, 4 * c, o * inverse(L));
+      }
+    }
+    if constexpr (WHOLE) {
+      return;
+    } else {
+      if (u.pieces > 1 && last_split(A.counters + u.first, u.pieces))
+        join<R, D, kDecThreads, kDecPieces + 2>(tid, parts, u.pieces, u.nrows, S.join,
+                                                [&](int k) { return (2 * (u.first + k) + (k == 0)) * PF; }, write_out);
+      if (!go_on) return;
+      __syncthreads();  // LDS is used anew
+      u = n;
+    }
+  }
 }
 
 // ---- many rows -----------------------------------------------------------
@@ -686,7 +997,9 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) 
       if (half == 0) store_dev2(base, at + kTileRows * D + 2 * row, m, l);
     }
     if (last_split(A.counters + P.tile, P.splits))
-      join<kTileRows, D, kThreads, kPreSplits>(base, P.splits, P.nrows, S.join, [&](int jr, int d, f4 v) {
+      join<kTileRows, D, kThreads, kPreSplits>(threadIdx.x, base, P.splits, P.nrows, S.join,
+                                                [](int k) { return k * partial_floats(kTileRows, D); },
+                                                [&](int jr, int d, f4 v) {
         const uint32_t f = P.f0 + jr;
         *reinterpret_cast<h4 *>(A.out + (int64_t)(P.begin + f / (uint32_t)A.group) * A.out_stride +
                                 (P.h * A.group + f % (uint32_t)A.group) * D + d) =
@@ -707,41 +1020,62 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) 
   }
 }
 
-// The launch of a call: which kernel, how the keys are split, and the
-// workspace that needs.
+// The launch of a call: which kernel, its workgroups, how the keys are split,
+// and the workspace that needs.
 struct Plan {
-  bool prefill;
-  int64_t slots;
+  int tile_rows;  // 16, 32: decode; 128: prefill
+  int64_t wgs;
+  int waves;  // of a workgroup
   int nsplit, chunk;
+  int whole;  // decode: units of up to so many pages stay whole; 0: all do
   size_t counter_bytes, bytes;
 };
 
 constexpr int kCus = 256;
-constexpr int kMaxChunk = 64;
 
 Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_kv) {
   Plan P;
-  const int64_t group = q_heads / kv_heads;
-  P.prefill = rows * group > 32 * seqs;
-  const int R = P.prefill ? kTileRows : kRows;
-  P.slots = rows * group / R + seqs;
+  const int64_t group = q_heads / kv_heads, flat = rows * group;
+  const bool prefill = flat > 32 * seqs;
+  const int R = prefill ? kTileRows : flat > kRows * seqs ? 2 * kRows : kRows;
+  P.tile_rows = R;
   const int64_t tiles = (max_kv + kPage - 1) / kPage;
-  const int64_t full = (rows * group + R - 1) / R, units = (full > seqs ? full : seqs) * kv_heads;
-  const int64_t target = P.prefill ? 2 * kCus : kCus, least = P.prefill ? 4 : kDecWaves, most = P.prefill ? kPreSplits : kDecSplits;
-  int64_t chunk = (tiles * units + target - 1) / target;
-  if (chunk < least) chunk = least;
-  if (!P.prefill && chunk > kMaxChunk) chunk = kMaxChunk;
-  int64_t nsplit = (tiles + chunk - 1) / chunk;
-  if (nsplit > most) nsplit = most;
-  if (nsplit < 1) nsplit = 1;
-  P.chunk = (int)(chunk < 0x7fffffff ? chunk : 0x7fffffff);
-  P.nsplit = (int)nsplit;
-  P.counter_bytes = 0;
-  P.bytes = 0;
-  if (nsplit > 1) {
-    P.counter_bytes = ((size_t)P.slots * kv_heads * 4 + 15) / 16 * 16;
-    P.bytes = P.counter_bytes + (size_t)P.slots * kv_heads * nsplit * partial_floats(R, (int)head_dim) * 4;
+  const int64_t full = (flat + R - 1) / R, units = (full > seqs ? full : seqs) * kv_heads;
+  P.nsplit = 1;
+  P.chunk = 0x7fffffff;
+  P.whole = 0;
+  P.waves = prefill ? kThreads / 64 : kWaves;
+  P.counter_bytes = P.bytes = 0;
+  if (prefill) {
+    int64_t chunk = (tiles * units + 2 * kCus - 1) / (2 * kCus);
+    if (chunk < 4) chunk = 4;
+    int64_t nsplit = (tiles + chunk - 1) / chunk;
+    if (nsplit > kPreSplits) nsplit = kPreSplits;
+    const int64_t slots = flat / R + seqs;
+    P.wgs = slots * kv_heads * nsplit;
+    if (nsplit > 1) {
+      P.nsplit = (int)nsplit;
+      P.chunk = (int)(chunk < 0x7fffffff ? chunk : 0x7fffffff);
+      P.counter_bytes = ((size_t)slots * kv_heads * 4 + 15) / 16 * 16;
+      P.bytes = P.counter_bytes + (size_t)slots * kv_heads * nsplit * partial_floats(R, (int)head_dim) * 4;
+    }
+    return P;
   }
+  if (tiles <= kWhole) {
+    // eight waves where there is a CU for each unit (9 pages: 9.1 against 9.4
+    // us), else four and three workgroups a CU (512 units of up to 11 pages:
+    // 17.5 against 23.4 us)
+    P.wgs = (flat / R + seqs) * kv_heads;
+    if (units > kCus && R == kRows) P.waves = 4;
+    return P;
+  }
+  // one workgroup a CU: a second one's start and end cost more than its
+  // waves bring (131001 tokens: 58 against 82 us with two a CU)
+  P.whole = kWhole;
+  P.wgs = (units * tiles + kLeast - 1) / kLeast;
+  if (P.wgs > kCus) P.wgs = kCus;
+  P.counter_bytes = ((size_t)P.wgs * 4 + 15) / 16 * 16;
+  P.bytes = P.counter_bytes + (size_t)P.wgs * 2 * partial_floats(R, (int)head_dim) * 4;
   return P;
 }
 
@@ -781,8 +1115,9 @@ extern "C" int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t k
   const Plan P = make_plan(rows, seqs, q_heads, kv_heads, head_dim, max_kv_len);
   if (P.bytes && !ws) return TQ_ERR_NULL;
   if (ws_bytes < P.bytes) return TQ_ERR_SIZE;
-  const int64_t wgs = P.slots * kv_heads * P.nsplit;
-  if (wgs > 0x7fffffff) return TQ_ERR_SHAPE;
+  // the kernels count pages of all sequences and heads in 32 bits
+  const int64_t units = (rows * (q_heads / kv_heads) / P.tile_rows + seqs) * kv_heads;
+  if (P.wgs > 0x7fffffff || units > 0x7fffffff / max_pages) return TQ_ERR_SHAPE;
   AttnArgs A;
   A.q = (const _Float16 *)q; A.out = (_Float16 *)out;
   A.cu = cu_rows; A.kv_len = kv_len; A.table = page_table;
@@ -793,15 +1128,28 @@ extern "C" int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t k
   A.scale_log2 = softmax_scale * 1.4426950408889634f;
   A.rows = (int)rows; A.seqs = (int)seqs; A.hkv = (int)kv_heads; A.group = (int)(q_heads / kv_heads);
   A.window = (int)window; A.sinks = (int)sinks;
-  A.nsplit = P.nsplit; A.chunk = P.chunk;
-  const dim3 grid((unsigned)wgs), block(P.prefill ? kThreads : kDecThreads);
+  A.nsplit = P.nsplit; A.chunk = P.chunk; A.whole = P.whole;
+  const dim3 grid((unsigned)P.wgs), block(P.waves * 64);
   hipStream_t st = (hipStream_t)stream;
-  if (P.prefill) {
-    if (head_dim == 128) hipLaunchKernelGGL(prefill_kernel<128>, grid, block, 0, st, A);
-    else hipLaunchKernelGGL(prefill_kernel<64>, grid, block, 0, st, A);
-  } else {
-    if (head_dim == 128) hipLaunchKernelGGL(decode_kernel<128>, grid, block, 0, st, A);
-    else hipLaunchKernelGGL(decode_kernel<64>, grid, block, 0, st, A);
+#define TQ_ATTN(...) hipLaunchKernelGGL((__VA_ARGS__), grid, block, 0, st, A)
+#define TQ_DECODE(D)                                              \
+  if (P.tile_rows == kRows) {                                     \
+    if (P.whole) TQ_ATTN(decode_kernel<D, 1, false, kWaves>);     \
+    else if (P.waves == 4) TQ_ATTN(decode_kernel<D, 1, true, 4>); \
+    else TQ_ATTN(decode_kernel<D, 1, true, kWaves>);              \
+  } else {                                                        \
+    if (P.whole) TQ_ATTN(decode_kernel<D, 2, false, kWaves>);     \
+    else TQ_ATTN(decode_kernel<D, 2, true, kWaves>);              \
   }
+  if (P.tile_rows == kTileRows) {
+    if (head_dim == 128) TQ_ATTN(prefill_kernel<128>);
+    else TQ_ATTN(prefill_kernel<64>);
+  } else if (head_dim == 128) {
+    TQ_DECODE(128)
+  } else {
+    TQ_DECODE(64)
+  }
+#undef TQ_ATTN
+#undef TQ_DECODE
   return hipGetLastError() == hipSuccess ? TQ_OK : TQ_ERR_HIP;
 }
