@@ -360,53 +360,73 @@ def tq_rope_table(positions: int, rot: int, base: float) -> np.ndarray:
     return t
 
 
-def _act_dtypes():
+def _act_dtype(t) -> int:
+    """TQ_F16 / TQ_F32 of a tensor's type, -1 for another."""
     import torch
-    return {torch.float16: TQ_F16, torch.float32: TQ_F32}
+    return TQ_F32 if t.dtype is torch.float32 else TQ_F16 if t.dtype is torch.float16 else -1
 
 
-def _args(what, *specs):
-    """Checks (name, tensor or None, dtype, shape) of a call's tensors: the
-    dtype, the shape (None: any length), contiguity, and that all are on the
-    current GPU, whose stream the call takes.  Raises ValueError."""
+def _bad(what, name, t, dtype, shape, dev):
+    """The error that a tensor's check found (the checks themselves stand in
+    one line each below: a decode step makes these calls by the hundred)."""
+    if t.dtype is not dtype:
+        return ValueError(f"{what}: {name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        return ValueError(f"{what}: {name} must be on the current GPU (cuda:{dev}), got {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        return ValueError(f"{what}: {name} must have shape {list(shape)}, got {list(t.shape)}")
+    return ValueError(f"{what}: {name} must be contiguous")
+
+
+def _need(what, name, t, dtype, shape, dev):
+    """Checks that t is a contiguous tensor of that type and shape on GPU `dev`, the
+    current one, whose stream the call takes; -> its address."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise _bad(what, name, t, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _rows_need(what, name, t, dtype, shape, dev):
+    """The same for rows that may lie apart; -> (address, elements from row to row)."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise _bad(what, name, t, dtype, shape, dev)
+    if t.is_contiguous():
+        n = 1
+        for d in shape[1:]:
+            n *= d
+        return t.data_ptr(), n
+    if not t[0].is_contiguous():
+        raise ValueError(f"{what}: {name} must be contiguous within a row")
+    return t.data_ptr(), t.stride(0)
+
+
+def _cache_need(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev):
+    """Checks the cache's tensors; -> ((seqs, pages of the table's rows, pages, heads, dim), their addresses)."""
     import torch
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, t, dtype, shape in specs:
-        if t is None:
-            continue
-        if t.dtype is not dtype:
-            raise ValueError(f"{what}: {name} must be {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: {name} must be contiguous")
-        if t.get_device() != cur:
-            raise ValueError(f"{what}: {name} must be on the current GPU (cuda:{cur}), got {t.device}")
-        got = t.shape
-        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
-            raise ValueError(f"{what}: {name} must have shape {list(shape)}, got {list(got)}")
-
-
-def _row_view(what, name, t):
-    """The distance of the rows of t [rows][...]: all but the first axis contiguous."""
-    want = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and st != want:
-            raise ValueError(f"{what}: {name} must be contiguous within a row")
-        want *= n
-    return t.stride(0) if t.shape[0] > 1 else want
-
-
-def _cache_args(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale):
-    import torch
-    if k_cache.dim() != 4:
-        raise ValueError(f"{what}: k_cache must have shape [pages][kv_heads][{KV_PAGE}][head_dim]")
-    pages, heads, _, dim = k_cache.shape
-    seqs = kv_len.numel()
     i32, u8, f32 = torch.int32, torch.uint8, torch.float32
-    _args(what, ("cu_rows", cu_rows, i32, (seqs + 1,)), ("kv_len", kv_len, i32, (seqs,)),
-          ("page_table", page_table, i32, (seqs, None)), ("k_cache", k_cache, u8, (pages, heads, KV_PAGE, dim)),
-          ("v_cache", v_cache, u8, (pages, heads, dim, KV_PAGE)), ("k_scale", k_scale, f32, (pages, heads)),
-          ("v_scale", v_scale, f32, (pages, heads)))
-    return pages, heads, dim, seqs
+    if k_cache.dim() != 4 or page_table.dim() != 2:
+        raise ValueError(f"{what}: k_cache must have shape [pages][kv_heads][{KV_PAGE}][head_dim], page_table two dimensions")
+    pages, heads, _, dim = k_cache.shape
+    seqs, width = page_table.shape
+    return ((seqs, width, pages, heads, dim),
+            (_need(what, "cu_rows", cu_rows, i32, (seqs + 1,), dev), _need(what, "kv_len", kv_len, i32, (seqs,), dev),
+             _need(what, "page_table", page_table, i32, (seqs, width), dev), width,
+             _need(what, "k_cache", k_cache, u8, (pages, heads, KV_PAGE, dim), dev),
+             _need(what, "v_cache", v_cache, u8, (pages, heads, dim, KV_PAGE), dev),
+             _need(what, "k_scale", k_scale, f32, (pages, heads), dev), _need(what, "v_scale", v_scale, f32, (pages, heads), dev),
+             pages))
+
+
+def _current(stream, t):
+    """(index of the current GPU, the call's stream as an integer) for a call on t and others."""
+    if t.get_device() < 0:
+        return -1, 0  # the checks still run; the library reports that there is no GPU memory
+    import torch
+    dev = torch.cuda.current_device()
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without making a Stream object
+        return dev, raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
+    return dev, stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def tq_kv_append(qkv, rope, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, q_out=None,
@@ -414,26 +434,26 @@ def tq_kv_append(qkv, rope, cu_rows, kv_len, page_table, k_cache, v_cache, k_sca
     """Append the rows of qkv [rows][(q_heads + 2 kv_heads) head_dim] (fp16 or
     fp32; rows may be strided) to the paged cache, rotating keys and queries
     by rope [positions][2][rot/2] (fp32, as tq_rope_table; None: no rotation);
-    the rotated queries go to q_out fp16 [rows][q_heads][head_dim].  q_heads is
-    needed only without q_out and where qkv's rows are longer than the heads."""
+    the rotated queries go to q_out fp16 [rows][q_heads][head_dim]."""
     import torch
     what = "tq_kv_append"
-    pages, heads, dim, seqs = _cache_args(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
+    dev, st = _current(stream, k_cache)
+    (seqs, _, _, heads, dim), cache = _cache_need(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev)
     if qkv.dim() != 2:
         raise ValueError(f"{what}: qkv must have two dimensions")
     rows, width = qkv.shape
     if q_heads is None:
-        q_heads = q_out.shape[1] if q_out is not None and q_out.dim() == 3 else width // dim - 2 * heads
-    if width != (q_heads + 2 * heads) * dim:
-        raise ValueError(f"{what}: qkv rows must hold {(q_heads + 2 * heads) * dim} values, got {width}")
-    stride = _row_view(what, "qkv", qkv)
-    _args(what, ("qkv", qkv[:1], qkv.dtype, (None, width)), ("q_out", q_out, torch.float16, (rows, q_heads, dim)),
-          ("rope", rope, torch.float32, (None, 2, None)))
-    rope_rows, rot = (0, 0) if rope is None else (rope.shape[0], 2 * rope.shape[2])
-    _check(lib.tq_kv_append(_act_dtypes().get(qkv.dtype, -1), rows, seqs, q_heads, heads, dim, qkv.data_ptr(), stride,
-                            _ptr(rope), rope_rows, rot, rope_mode, cu_rows.data_ptr(), kv_len.data_ptr(),
-                            page_table.data_ptr(), page_table.shape[1], k_cache.data_ptr(), v_cache.data_ptr(),
-                            k_scale.data_ptr(), v_scale.data_ptr(), pages, _ptr(q_out), _stream(stream)), what)
+        q_heads = width // dim - 2 * heads
+    x, stride = _rows_need(what, "qkv", qkv, qkv.dtype, (rows, (q_heads + 2 * heads) * dim), dev)
+    q = None if q_out is None else _need(what, "q_out", q_out, torch.float16, (rows, q_heads, dim), dev)
+    r, rope_rows, rot = None, 0, 0
+    if rope is not None:
+        if rope.dim() != 3:
+            raise ValueError(f"{what}: rope must have shape [positions][2][rot/2]")
+        rope_rows, rot = rope.shape[0], 2 * rope.shape[2]
+        r = _need(what, "rope", rope, torch.float32, (rope_rows, 2, rot // 2), dev)
+    _check(lib.tq_kv_append(_act_dtype(qkv), rows, seqs, q_heads, heads, dim, x, stride, r, rope_rows, rot, rope_mode,
+                            *cache, q, st), what)
 
 
 def tq_kv_attn_workspace_bytes(rows, seqs, q_heads, kv_heads, head_dim, max_kv_len) -> int:
@@ -455,20 +475,20 @@ def tq_kv_attn(q, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scal
     last `window` keys and the first `sinks` ones."""
     import torch
     what = "tq_kv_attn"
-    pages, heads, dim, seqs = _cache_args(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3 or q.shape != out.shape or q.shape[2] != dim:
-        raise ValueError(f"{what}: q and out must have shape [rows][q_heads][{dim}]")
-    rows, q_heads = q.shape[:2]
-    qs, os_ = _row_view(what, "q", q), _row_view(what, "out", out)
-    _args(what, ("q", q[:1], torch.float16, (None, q_heads, dim)), ("out", out[:1], torch.float16, (None, q_heads, dim)))
-    wp, wb = _ws(ws)
-    if ws is not None and ws.get_device() != q.get_device():
-        raise ValueError(f"{what}: ws must be on the current GPU")
-    _check(lib.tq_kv_attn(rows, seqs, q_heads, heads, dim, q.data_ptr(), qs, cu_rows.data_ptr(), kv_len.data_ptr(),
-                          page_table.data_ptr(), page_table.shape[1], k_cache.data_ptr(), v_cache.data_ptr(),
-                          k_scale.data_ptr(), v_scale.data_ptr(), pages, max_kv_len,
-                          dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, out.data_ptr(), os_,
-                          wp, wb, _stream(stream)), what)
+    dev, st = _current(stream, k_cache)
+    (seqs, _, _, heads, dim), cache = _cache_need(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 3:
+        raise ValueError(f"{what}: q must have three dimensions")
+    rows, q_heads, _ = q.shape
+    qp, qs = _rows_need(what, "q", q, torch.float16, (rows, q_heads, dim), dev)
+    op, os_ = _rows_need(what, "out", out, torch.float16, (rows, q_heads, dim), dev)
+    wp, wb = None, 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"{what}: ws must be contiguous and on the current GPU")
+        wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
+    _check(lib.tq_kv_attn(rows, seqs, q_heads, heads, dim, qp, qs, *cache, max_kv_len,
+                          dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, op, os_, wp, wb, st), what)
 
 
 def tq_residual_norm(y, res, res_out, pre_w=None, x=None, q=None, a_scale=None, post_w=None, gate=None,
@@ -478,43 +498,45 @@ def tq_residual_norm(y, res, res_out, pre_w=None, x=None, q=None, a_scale=None, 
     [M][H] (rows may be strided); y None: norm(res) only."""
     import torch
     what = "tq_residual_norm"
+    dev, st = _current(stream, res)
     if res.dim() != 2:
         raise ValueError(f"{what}: res must have two dimensions")
-    M, H = res.shape
-    f32, acts = torch.float32, _act_dtypes()
+    shape = M, H = res.shape
+    f32 = torch.float32
     yt = res.dtype if y is None else y.dtype
-    _args(what, ("res", res, res.dtype, (M, H)), ("y", y, yt, (M, H)), ("res_out", res_out, res.dtype, (M, H)),
-          ("x", x, f32 if x is None else x.dtype, (M, H)), ("q", q, torch.int8, (M, H)), ("a_scale", a_scale, f32, (M,)),
-          ("post_w", post_w, f32, (H,)), ("pre_w", pre_w, f32, (H,)))
-    gate_stride = 0
+    gp, gs = None, 0
     if gate is not None:
         if gate.dim() == 2:
-            if gate.shape[0] != M:
-                raise ValueError(f"{what}: gate must have {M} rows, got {gate.shape[0]}")
-            gate_stride = _row_view(what, "gate", gate)
-            _args(what, ("gate", gate[:1], yt, (None, H)))
+            gp, gs = _rows_need(what, "gate", gate, yt, shape, dev)
         else:
-            _args(what, ("gate", gate, yt, (H,)))
-    _check(lib.tq_residual_norm(acts.get(yt, -1), acts.get(res.dtype, -1), TQ_F32 if x is None else acts.get(x.dtype, -1),
-                                M, H, _ptr(y), _ptr(post_w), None if gate is None else gate.data_ptr(), gate_stride,
-                                res_scale, res.data_ptr(), _ptr(res_out), _ptr(pre_w), eps, _ptr(x), _ptr(q),
-                                _ptr(a_scale), _stream(stream)), what)
+            gp = _need(what, "gate", gate, yt, (H,), dev)
+    _check(lib.tq_residual_norm(
+        TQ_F32 if y is None else _act_dtype(y), _act_dtype(res), TQ_F32 if x is None else _act_dtype(x), M, H,
+        None if y is None else _need(what, "y", y, yt, shape, dev),
+        None if post_w is None else _need(what, "post_w", post_w, f32, (H,), dev), gp, gs, res_scale,
+        _need(what, "res", res, res.dtype, shape, dev),
+        None if res_out is None else _need(what, "res_out", res_out, res.dtype, shape, dev),
+        None if pre_w is None else _need(what, "pre_w", pre_w, f32, (H,), dev), eps,
+        None if x is None else _need(what, "x", x, x.dtype, shape, dev),
+        None if q is None else _need(what, "q", q, torch.int8, shape, dev),
+        None if a_scale is None else _need(what, "a_scale", a_scale, f32, (M,), dev), st), what)
 
 
 def tq_debug_kv_read(pages, k_cache, v_cache, k_scale, v_scale, values, stream=None) -> None:
     """values (fp16 / fp32 [2][n][kv_heads][64][head_dim]) of the cache pages named by pages (int32 [n])."""
     import torch
     what = "tq_debug_kv_read"
+    dev, st = _current(stream, k_cache)
     if k_cache.dim() != 4 or pages.dim() != 1:
         raise ValueError(f"{what}: k_cache must have four dimensions, pages one")
     num, heads, _, dim = k_cache.shape
-    n, u8, f32 = pages.numel(), torch.uint8, torch.float32
-    _args(what, ("pages", pages, torch.int32, (n,)), ("k_cache", k_cache, u8, (num, heads, KV_PAGE, dim)),
-          ("v_cache", v_cache, u8, (num, heads, dim, KV_PAGE)), ("k_scale", k_scale, f32, (num, heads)),
-          ("v_scale", v_scale, f32, (num, heads)), ("values", values, values.dtype, (2, n, heads, KV_PAGE, dim)))
-    _check(lib.tq_debug_kv_read(_act_dtypes().get(values.dtype, -1), n, heads, dim, pages.data_ptr(), k_cache.data_ptr(),
-                                v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), num, values.data_ptr(),
-                                _stream(stream)), what)
+    n, u8, f32 = pages.shape[0], torch.uint8, torch.float32
+    _check(lib.tq_debug_kv_read(
+        _act_dtype(values), n, heads, dim, _need(what, "pages", pages, torch.int32, (n,), dev),
+        _need(what, "k_cache", k_cache, u8, (num, heads, KV_PAGE, dim), dev),
+        _need(what, "v_cache", v_cache, u8, (num, heads, dim, KV_PAGE), dev),
+        _need(what, "k_scale", k_scale, f32, (num, heads), dev), _need(what, "v_scale", v_scale, f32, (num, heads), dev), num,
+        _need(what, "values", values, values.dtype, (2, n, heads, KV_PAGE, dim), dev), st), what)
 
 
 def stack_timeouts(ws) -> int:
