@@ -32,6 +32,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "tq.h"
 #include "tq_device.h"
 #include "tq_kv.h"
@@ -60,6 +62,7 @@ struct AttnArgs {
   float *partials;
   float scale_log2;
   int rows, seqs, hkv, group, window, sinks;
+  int slots;          // prefill: row tiles
   int nsplit, chunk;  // prefill: splits of the keys at most; pages of a split at least
   int whole;          // decode: units of up to so many pages stay whole
 };
@@ -352,7 +355,9 @@ __device__ __forceinline__ bool find_place(const AttnArgs &A, Place &P) {
   P.h = blockIdx.x % (uint32_t)A.hkv;
   const uint32_t b = blockIdx.x / (uint32_t)A.hkv;
   P.split = b % (uint32_t)A.nsplit;
-  const int slot = b / (uint32_t)A.nsplit;
+  // from the last tile on: the later rows of a sequence see more keys, and the
+  // longest work should start first
+  const int slot = A.slots - 1 - b / (uint32_t)A.nsplit;
   P.s = find_seq<R, 1>(A.cu, A.seqs, A.rows, slot, A.group);
   P.begin = cu_at(A.cu, P.s, A.rows);
   P.n = max(cu_at(A.cu, P.s + 1, A.rows) - P.begin, 0);
@@ -644,7 +649,7 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
     const Tiles T = u.T;
     int i = u.i, id;
     State<D> st[RT];
-    float qsum[RT], unit_scale = 1.0f;
+    float qsum[RT], unit = 0.0f;  // log2 of the outputs' unit
 #pragma unroll
     for (int a = 0; a < RT; a++) {
       qsum[a] = 0.0f;
@@ -675,11 +680,11 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
         // a page of zeros has scale 0: its (zero) scores stay finite, masked ones -inf
         const float sc = fmaxf(ks * A.scale_log2, 1e-37f);
         const bool has_v = vs > 0.0f;  // a page of zeros adds to the sum only
-        const float ratio = has_v ? vs / unit_scale : 1.0f;
-        const bool far = !(ratio > 0.0625f && ratio < 16.0f);
-        const float shift = far ? 0.0f : __builtin_amdgcn_logf(ratio);
-        const float moves = far ? fminf(unit_scale / vs, 3.0e38f) : 1.0f;
-        if (far) unit_scale = vs;
+        const float over = has_v ? __builtin_amdgcn_logf(vs) - unit : 0.0f;
+        const bool far = !(fabsf(over) < 4.0f);
+        const float shift = far ? 0.0f : over;
+        const float moves = far ? fminf(__builtin_amdgcn_exp2f(-over), 3.0e38f) : 1.0f;
+        if (far) unit += over;
         h8 hi16[RT][2], lo16[RT][2];
 #pragma unroll
         for (int a = 0; a < RT; a++)
@@ -719,6 +724,7 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
     // what follows is not to be computed ahead of the loop and kept)
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
+    const float unit_scale = __builtin_amdgcn_exp2f(unit);
 #pragma unroll
     for (int a = 0; a < RT; a++) {
       const int row = kRows * a + n16;
@@ -790,62 +796,66 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
 // The running maximum is a reference, not the maximum: it moves only when a
 // score exceeds it by 2^8 in weight, so the output is hardly ever rescaled
 // (fp16 weights reach 2^8, times 2^4 for the page's value scale).
-constexpr int kTileRows = 128, kWaveRows = 32;
-constexpr int kThreads = 256;
+constexpr int kWaveRows = 32;
+constexpr int kPreWaves = 4, kTileRows = kPreWaves * kWaveRows;
 constexpr int kPreSplits = 16;
 typedef float f16x __attribute__((ext_vector_type(16)));
 
 // The token of a 32-token group that row r of the score product takes.
 __device__ __forceinline__ int row_token(int r) { return (r & 16) + ((r >> 2) & 1) * 8 + ((r >> 3) & 1) * 4 + (r & 3); }
 
-template <int D>
-struct Page {
-  uint4 k[D / 64], v[D / 64];
-  float ks, vs;  // ks < 0: no such page
-};
+// The 16-byte pieces of a page's keys (and of its values) that a thread of NT fetches.
+template <int D, int NT>
+constexpr int kPieces = kPage * D / 16 / NT;
 
-template <int D>
-__device__ __forceinline__ void load_page(const AttnArgs &A, int h, int id, Page<D> &t) {
-  const bool ok = id >= 0 && id < A.num_pages;
-  const int64_t ph = (int64_t)(ok ? id : 0) * A.hkv + h;
-  t.ks = ok ? A.ks[ph] : -1.0f;
-  t.vs = A.vs[ph];
-  const uint4 *kp = reinterpret_cast<const uint4 *>(A.k + ph * (kPage * D));
-  const uint4 *vp = reinterpret_cast<const uint4 *>(A.v + ph * (kPage * D));
+// The same bytes of a page, keys or values, on their way into LDS.
+template <int D, int NT>
+struct Half {
+  uint4 r[kPieces<D, NT>];
+  __device__ __forceinline__ void load(const uint8_t *p) {
 #pragma unroll
-  for (int i = 0; i < D / 64; i++) {
-    t.k[i] = kp[i * kThreads + threadIdx.x];
-    t.v[i] = vp[i * kThreads + threadIdx.x];
+    for (int i = 0; i < kPieces<D, NT>; i++) r[i] = reinterpret_cast<const uint4 *>(p)[i * NT + threadIdx.x];
   }
-}
+};
 
 template <int D>
 struct Lds {
   _Float16 k[kPage][D + 8], v[D][kPage + 8];
 };
 
-template <int D>
-__device__ __forceinline__ void put_page(const Page<D> &t, Lds<D> &l) {
+template <int D, int NT>
+__device__ __forceinline__ void put_keys(const Half<D, NT> &t, Lds<D> &l) {
 #pragma unroll
-  for (int i = 0; i < D / 64; i++) {
-    const int idx = i * kThreads + threadIdx.x;
-    h8 *kd = reinterpret_cast<h8 *>(&l.k[idx / (D / 16)][idx % (D / 16) * 16]);
-    kd[0] = codes8(t.k[i].x, t.k[i].y);
-    kd[1] = codes8(t.k[i].z, t.k[i].w);
-    h8 *vd = reinterpret_cast<h8 *>(&l.v[idx / 4][idx % 4 * 16]);
-    vd[0] = codes8(t.v[i].x, t.v[i].y);
-    vd[1] = codes8(t.v[i].z, t.v[i].w);
+  for (int i = 0; i < kPieces<D, NT>; i++) {
+    const int idx = i * NT + threadIdx.x;
+    h8 *d = reinterpret_cast<h8 *>(&l.k[idx / (D / 16)][idx % (D / 16) * 16]);
+    d[0] = codes8(t.r[i].x, t.r[i].y);
+    d[1] = codes8(t.r[i].z, t.r[i].w);
+  }
+}
+// (live: the page's scale is not 0; else its bytes, whatever they are, stand for zeros)
+template <int D, int NT>
+__device__ __forceinline__ void put_values(const Half<D, NT> &t, bool live, Lds<D> &l) {
+  const uint32_t zero = 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < kPieces<D, NT>; i++) {
+    const int idx = i * NT + threadIdx.x;
+    h8 *d = reinterpret_cast<h8 *>(&l.v[idx / 4][idx % 4 * 16]);
+    d[0] = codes8(live ? t.r[i].x : zero, live ? t.r[i].y : zero);
+    d[1] = codes8(live ? t.r[i].z : zero, live ? t.r[i].w : zero);
   }
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) {
+template <int D, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
+  constexpr int kThreads = NW * 64, kTileRows = NW * kWaveRows;
   union Shared {
     Lds<D> page[2];
     float join[kJoinFloats<kTileRows, kPreSplits, kThreads>];
   };
   __shared__ __attribute__((aligned(16))) Shared S;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31, half = lane >> 5;
+  const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place P;
   if (!find_place<kTileRows>(A, P)) return;
   const int row = wave * kWaveRows + n;
@@ -877,108 +887,254 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnArgs A) 
   for (int i = 0; i < D / 32; i++)
 #pragma unroll
     for (int r = 0; r < 16; r++) o[i][r] = 0.0f;
-  float m = kNone, l = 0.0f, corr = 0.0f, unit = 1.0f;
-  Page<D> next;
-  float ks, vs;
-  int id_next = 0;
-  if (P.lo < P.hi) {
-    load_page<D>(A, P.h, page_id(A, P.s, P.T.page(P.lo)), next);
-    if (P.lo + 1 < P.hi) id_next = page_id(A, P.s, P.T.page(P.lo + 1));
-    put_page<D>(next, S.page[0]);
-  }
-  ks = next.ks;
-  vs = next.vs;
-  __syncthreads();
-  for (int i = P.lo; i < P.hi; i++) {
-    const Lds<D> &L = S.page[(i - P.lo) & 1];
-    const bool more = i + 1 < P.hi;
-    if (more) load_page<D>(A, P.h, id_next, next);
-    if (i + 2 < P.hi) id_next = page_id(A, P.s, P.T.page(i + 2));
-    const int pg = P.T.page(i), j0 = pg * kPage, j1 = j0 + kPage - 1;
-    const bool none = ks < 0.0f || j0 > wmax || (A.window && j1 <= wmin - A.window && j0 >= A.sinks);
-    if (!none) {
-      f16x acc[2];
+  // keys up to `lowest` are outside the row's window (no window: none are)
+  const int lowest = A.window ? pos - A.window : -1;
+  float m = kNone, l = 0.0f, corr = 0.0f, unit = 0.0f;  // unit: its log2
+
+  // A page's scales: the score's factor (finite for a page of zeros, so that a
+  // masked score stays -inf), log2 of the value scale (a page of zeros adds to
+  // the sum only: its values are put into LDS as zeros).
+  struct Scales {
+    float sc, lv;
+    bool there, live;
+  };
+  auto scales = [&](int id) {
+    Scales t;
+    t.there = id >= 0 && id < A.num_pages;
+    const int64_t ph = (int64_t)(t.there ? id : 0) * A.hkv + P.h;
+    const float ks = A.ks[ph], vs = A.vs[ph];
+    t.there = t.there && ks >= 0.0f;
+    t.sc = fmaxf(ks * A.scale_log2, 1e-37f);
+    t.live = vs > 0.0f;
+    t.lv = __builtin_amdgcn_logf(vs);
+    return t;
+  };
+  auto key_bytes = [&](int id) { return A.k + ((int64_t)(id >= 0 && id < A.num_pages ? id : 0) * A.hkv + P.h) * (kPage * D); };
+  auto value_bytes = [&](int id) { return A.v + ((int64_t)(id >= 0 && id < A.num_pages ? id : 0) * A.hkv + P.h) * (kPage * D); };
+  auto id_at = [&](int i) { return page_id(A, P.s, P.T.page(i)); };
+
+  // S^T of a page's keys
+  auto dot = [&](const Lds<D> &L, f16x (&acc)[2]) {
 #pragma unroll
-      for (int t = 0; t < 2; t++) {
+    for (int t = 0; t < 2; t++) {
 #pragma unroll
-        for (int r = 0; r < 16; r++) acc[t][r] = 0.0f;
-        const _Float16 *kr = &L.k[32 * t + row_token(n)][8 * half];
+      for (int r = 0; r < 16; r++) acc[t][r] = 0.0f;
+      const _Float16 *kr = &L.k[32 * t + row_token(n)][8 * half];
 #pragma unroll
-        for (int j = 0; j < D / 16; j++)
-          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8 *>(kr + 16 * j), qf[j], acc[t], 0, 0, 0);
+      for (int j = 0; j < D / 16; j++)
+        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8 *>(kr + 16 * j), qf[j], acc[t], 0, 0, 0);
+    }
+  };
+  auto largest = [&](const f16x (&acc)[2]) {
+    float mx = acc[0][0];
+#pragma unroll
+    for (int r = 1; r < 16; r++) mx = fmaxf(mx, acc[0][r]);
+#pragma unroll
+    for (int r = 0; r < 16; r++) mx = fmaxf(mx, acc[1][r]);
+    return mx;
+  };
+  // moves the references to a page's scores and value scale; -> log2 of the factor its weights take
+  auto refer = [&](const Scales &t, float mx) {
+    mx = t.there ? (half_max(mx) + qsum) * t.sc : -__builtin_inff();
+    const float over = t.live ? t.lv - unit : 0.0f;
+    const bool far = !(fabsf(over) < 4.0f);
+    if (far || __any(mx > m + 8.0f)) {
+      const float mn = mx > m + 8.0f ? mx : m;
+      float alpha = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= alpha;
+      if (far) {
+        alpha *= fminf(__builtin_amdgcn_exp2f(-over), 3.0e38f);
+        unit += over;
       }
-      const bool all = j1 <= wmin && (A.window == 0 || j0 > wmax - A.window || j1 < A.sinks);
-      if (!all) {
+      corr *= alpha;
 #pragma unroll
-        for (int t = 0; t < 2; t++)
+      for (int d = 0; d < D / 32; d++)
 #pragma unroll
-          for (int r = 0; r < 16; r++) {
-            const int j = j0 + 32 * t + (r >> 3) * 16 + 8 * half + (r & 7);
-            const bool see = j <= pos && (A.window == 0 || j > pos - A.window || j < A.sinks);
-            acc[t][r] = see ? acc[t][r] : -__builtin_inff();
-          }
+        for (int r = 0; r < 16; r++) o[d][r] *= alpha;
+    }
+    return far ? 0.0f : over;
+  };
+  // the weights of a page's scores (in fp16), summed into l and corr
+  auto weigh = [&](const Scales &t, float shift, const f16x (&acc)[2], h8 (&p)[2][2]) {
+    const float bias = t.there ? qsum * t.sc + shift - m : -__builtin_inff();
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) {
+        const float w = __builtin_amdgcn_exp2f(acc[k][r] * t.sc + bias);
+        sum += w;
+        p[k][r >> 3][r & 7] = (_Float16)w;
       }
-      // a page of zeros has scale 0: its (zero) scores stay finite, masked ones -inf
-      const float sc = fmaxf(ks * A.scale_log2, 1e-37f);
-      float mx = acc[0][0];
+    l += sum * __builtin_amdgcn_exp2f(-shift);
+    corr += t.live ? sum : 0.0f;
+  };
+  auto add_values = [&](const Lds<D> &L, const h8 (&p)[2][2]) {
 #pragma unroll
-      for (int r = 1; r < 16; r++) mx = fmaxf(mx, acc[0][r]);
-#pragma unroll
-      for (int r = 0; r < 16; r++) mx = fmaxf(mx, acc[1][r]);
-      mx = (half_max(mx) + qsum) * sc;
-      const bool has_v = vs > 0.0f;  // a page of zeros adds to the sum only
-      const float ratio = has_v ? vs / unit : 1.0f;
-      const bool far = !(ratio > 0.0625f && ratio < 16.0f);
-      const float shift = far ? 0.0f : __builtin_amdgcn_logf(ratio);
-      if (far || __any(mx > m + 8.0f)) {
-        const float mn = mx > m + 8.0f ? mx : m;
-        float alpha = __builtin_amdgcn_exp2f(m - mn);
-        m = mn;
-        l *= alpha;
-        if (far) {
-          alpha *= fminf(unit / vs, 3.0e38f);
-          unit = vs;
-        }
-        corr *= alpha;
-#pragma unroll
-        for (int d = 0; d < D / 32; d++)
-#pragma unroll
-          for (int r = 0; r < 16; r++) o[d][r] *= alpha;
-      }
-      const float bias = qsum * sc + shift - m;
-      float sum = 0.0f;
-      h8 p[2][2];
+    for (int d = 0; d < D / 32; d++)
 #pragma unroll
       for (int t = 0; t < 2; t++)
 #pragma unroll
-        for (int r = 0; r < 16; r++) {
-          const float w = __builtin_amdgcn_exp2f(acc[t][r] * sc + bias);
-          sum += w;
-          p[t][r >> 3][r & 7] = (_Float16)w;
+        for (int u = 0; u < 2; u++) {
+          const h8 a = *reinterpret_cast<const h8 *>(&L.v[32 * d + n][32 * t + 16 * u + 8 * half]);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, p[t][u], o[d], 0, 0, 0);
         }
-      l += sum * __builtin_amdgcn_exp2f(-shift);
-      if (has_v) {
-        corr += sum;
+  };
+
+  // Pages [ca, cb) of the list are seen whole by every row; the few before
+  // (sinks, a window's first pages) and behind (the rows' own) go one by one, with masks.
+  int ca = P.T.sink, cb = P.pmin < 0 ? 0 : (P.pmin + 1) / kPage - P.T.first + P.T.sink;
+  if (A.window && P.pmax >= A.window) ca = max(ca, (P.pmax - A.window) / kPage + 1 - P.T.first + P.T.sink);
+  ca = max(ca, P.lo);
+  cb = min(cb, P.hi);
+  if (cb - ca < 2) ca = cb = P.hi;
+  Half<D, kThreads> rk, rv;
+#pragma unroll 1
+  for (int part = 0; part < 2; part++) {
+    const int lo = part ? cb : P.lo, hi = part ? P.hi : ca;
+    if (lo < hi) {
+      // one page after the other, the next one's bytes on their way
+      int id = id_at(lo), id1 = lo + 1 < hi ? id_at(lo + 1) : 0;
+      Scales t = scales(id);
+      rk.load(key_bytes(id));
+      rv.load(value_bytes(id));
+      put_keys<D, kThreads>(rk, S.page[0]);
+      put_values<D, kThreads>(rv, t.live, S.page[0]);
+      __syncthreads();
+#pragma unroll 1
+      for (int i = lo; i < hi; i++) {
+        const Lds<D> &L = S.page[(i - lo) & 1];
+        const bool more = i + 1 < hi;
+        if (more) {
+          rk.load(key_bytes(id1));
+          rv.load(value_bytes(id1));
+        }
+        const Scales next = scales(id1);
+        if (i + 2 < hi) id1 = id_at(i + 2);
+        const int j0 = P.T.page(i) * kPage, j1 = j0 + kPage - 1;
+        if (t.there && j0 <= wmax && !(A.window && j1 <= wmin - A.window && j0 >= A.sinks)) {
+          f16x acc[2];
+          h8 p[2][2];
+          dot(L, acc);
+          // (whole expressions, no short cuts: branches would cost more)
 #pragma unroll
-        for (int d = 0; d < D / 32; d++)
+          for (int k = 0; k < 2; k++)
 #pragma unroll
-          for (int t = 0; t < 2; t++)
-#pragma unroll
-            for (int u = 0; u < 2; u++) {
-              const h8 a = *reinterpret_cast<const h8 *>(&L.v[32 * d + n][32 * t + 16 * u + 8 * half]);
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, p[t][u], o[d], 0, 0, 0);
+            for (int r = 0; r < 16; r++) {
+              const int j = j0 + 32 * k + (r >> 3) * 16 + 8 * half + (r & 7);
+              const bool see = (j <= pos) & ((j > lowest) | (j < A.sinks));
+              acc[k][r] = see ? acc[k][r] : -__builtin_inff();
             }
+          const float shift = refer(t, largest(acc));
+          weigh(t, shift, acc, p);
+          add_values(L, p);
+        }
+        if (more) {
+          put_keys<D, kThreads>(rk, S.page[(i + 1 - lo) & 1]);
+          put_values<D, kThreads>(rv, next.live, S.page[(i + 1 - lo) & 1]);
+          t = next;
+        }
+        __syncthreads();
       }
     }
-    if (more) {
-      put_page<D>(next, S.page[(i + 1 - P.lo) & 1]);
-      ks = next.ks;
-      vs = next.vs;
-    }
+    if (part || ca >= cb) continue;
+    // The run of whole pages, two pages deep: while page i's weights are made
+    // (vector unit) the scores of page i + 1 are (matrix unit), while its values
+    // are added (matrix unit) the next pages' bytes are converted into LDS and
+    // page i + 1's maximum is taken.  The order is asked of the compiler by
+    // the sched_group_barriers: one product, then what the vector unit does
+    // beside it.
+    const int id0 = id_at(ca);
+    int id1 = id_at(ca + 1), id2 = id_at(min(ca + 2, cb - 1)), id3 = id_at(min(ca + 3, cb - 1));
+    Scales t = scales(id0), t1;
+    rk.load(key_bytes(id0));
+    rv.load(value_bytes(id0));
+    put_keys<D, kThreads>(rk, S.page[0]);
+    put_values<D, kThreads>(rv, t.live, S.page[0]);
+    rk.load(key_bytes(id1));
+    put_keys<D, kThreads>(rk, S.page[1]);
+    rk.load(key_bytes(id2));
+    rv.load(value_bytes(id1));
     __syncthreads();
+    f16x even[2], odd[2];
+    dot(S.page[0], even);
+    float shift = refer(t, largest(even));
+    __syncthreads();  // page[0]'s keys are read by all
+    // page i: `cur` its scores, `here` its values, `there` page i + 1's keys;
+    // on their way: the keys of page i + 2 and the values of page i + 1
+    auto step = [&](int i, f16x (&cur)[2], f16x (&nxt)[2], Lds<D> &here, Lds<D> &there) {
+      t1 = scales(id1);
+      // piece u of the 16-byte halves that this thread converts into LDS: keys, then values
+      auto put = [&](int u) {
+        constexpr int N = 2 * kPieces<D, kThreads>;
+        const uint32_t zero = 0x80808080u;
+        const int q = u % N / 2, idx = q * kThreads + threadIdx.x;
+        const uint4 w = u < N ? rk.r[q] : rv.r[q];
+        uint32_t a = u & 1 ? w.z : w.x, b = u & 1 ? w.w : w.y;
+        if (u >= N) a = t1.live ? a : zero, b = t1.live ? b : zero;
+        h8 *d = u < N ? reinterpret_cast<h8 *>(&here.k[idx / (D / 16)][idx % (D / 16) * 16])
+                      : reinterpret_cast<h8 *>(&there.v[idx / 4][idx % 4 * 16]);
+        d[u & 1] = codes8(a, b);
+      };
+      // products of page i + 1's keys and the weights of page i, side by side
+      constexpr int NQ = D / 8, E = 32 / NQ, AHEAD = 2;
+      const _Float16 *kr = &there.k[row_token(n)][8 * half], *vr = &here.v[n][8 * half];
+      // operand z of the score products (32 tokens, then the other 32) and of the value products
+      auto key = [&](int z) { return *reinterpret_cast<const h8 *>(kr + z / (D / 16) * 32 * (D + 8) + z % (D / 16) * 16); };
+      auto value = [&](int z) { return *reinterpret_cast<const h8 *>(vr + z / 4 * 32 * (kPage + 8) + z % 4 * 16); };
+      h8 ops[AHEAD + 1], p[2][2];
+      const float bias = t.there ? qsum * t.sc + shift - m : -__builtin_inff();
+      float sum = 0.0f;
+#pragma unroll
+      for (int z = 0; z < AHEAD; z++) ops[z] = key(z);
+#pragma unroll
+      for (int z = 0; z < NQ; z++) {
+        ops[(z + AHEAD) % (AHEAD + 1)] = z + AHEAD < NQ ? key(z + AHEAD) : value(z + AHEAD - NQ);
+        const int k = z / (D / 16), jj = z % (D / 16);
+        nxt[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ops[z % (AHEAD + 1)], qf[jj],
+                                                        jj == 0 ? (f16x)(0.0f) : nxt[k], 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+          const int x = z * E + e;
+          const float w = __builtin_amdgcn_exp2f(cur[x >> 4][x & 15] * t.sc + bias);
+          sum += w;
+          p[x >> 4][(x & 15) >> 3][x & 7] = (_Float16)w;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      l += sum * __builtin_amdgcn_exp2f(-shift);
+      corr += t.live ? sum : 0.0f;
+      // page i's values; beside them page i + 1's maximum and the bytes for LDS
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int z = 0; z < NQ; z++) {
+        if (z + AHEAD < NQ) ops[(NQ + z + AHEAD) % (AHEAD + 1)] = value(z + AHEAD);
+        o[z / 4] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ops[(NQ + z) % (AHEAD + 1)], p[(z >> 1) & 1][z & 1], o[z / 4], 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < E; e++) mx = fmaxf(mx, nxt[(z * E + e) >> 4][(z * E + e) & 15]);
+        if (z & 1) put(z >> 1);
+        // as soon as a half's registers are free its next bytes are sent for
+        if (z == NQ / 2) rk.load(key_bytes(id3));
+        if (z == NQ - 1) rv.load(value_bytes(id2));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      id1 = id2;
+      id2 = id3;
+      id3 = id_at(min(i + 4, cb - 1));
+      t = t1;
+      if (i + 1 < cb) shift = refer(t, mx);
+      __syncthreads();
+    };
+#pragma unroll 1
+    for (int i = ca; i < cb; i += 2) {
+      step(i, even, odd, S.page[0], S.page[1]);
+      if (i + 1 < cb) step(i + 1, odd, even, S.page[1], S.page[0]);
+    }
   }
   l = half_sum(l);
   corr = 0.5f * half_sum(corr);
+  unit = __builtin_amdgcn_exp2f(unit);
 #pragma unroll
   for (int d = 0; d < D / 32; d++)
 #pragma unroll
@@ -1044,13 +1200,22 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
   P.nsplit = 1;
   P.chunk = 0x7fffffff;
   P.whole = 0;
-  P.waves = prefill ? kThreads / 64 : kWaves;
+  P.waves = prefill ? kPreWaves : kWaves;
   P.counter_bytes = P.bytes = 0;
   if (prefill) {
-    int64_t chunk = (tiles * units + 2 * kCus - 1) / (2 * kCus);
-    if (chunk < 4) chunk = 4;
-    int64_t nsplit = (tiles + chunk - 1) / chunk;
-    if (nsplit > kPreSplits) nsplit = kPreSplits;
+    // Two workgroups a CU run together: the split that makes the fewest
+    // rounds times pages, with some 4 pages' time for a workgroup's start and
+    // end.  (With many rounds the longest-first order levels the load by itself.)
+    const int64_t slots2 = 2 * kCus;
+    int64_t nsplit = 1, chunk = tiles, best = INT64_MAX;
+    for (int64_t n = 1; n <= kPreSplits && units < 4 * slots2; n++) {
+      const int64_t c = (tiles + n - 1) / n, cost = (units * n + slots2 - 1) / slots2 * (c + 4);
+      if (cost < best && (n == 1 || c >= 4)) {
+        best = cost;
+        nsplit = n;
+        chunk = c;
+      }
+    }
     const int64_t slots = flat / R + seqs;
     P.wgs = slots * kv_heads * nsplit;
     if (nsplit > 1) {
@@ -1128,7 +1293,10 @@ extern "C" int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t k
   A.scale_log2 = softmax_scale * 1.4426950408889634f;
   A.rows = (int)rows; A.seqs = (int)seqs; A.hkv = (int)kv_heads; A.group = (int)(q_heads / kv_heads);
   A.window = (int)window; A.sinks = (int)sinks;
-  A.nsplit = P.nsplit; A.chunk = P.chunk; A.whole = P.whole;
+  A.slots = (int)(rows * (q_heads / kv_heads) / P.tile_rows + seqs);
+  A.nsplit = P.nsplit;
+  A.chunk = window && P.nsplit > 1 ? 4 : P.chunk;  // a window leaves fewer pages than max_kv_len says
+  A.whole = P.whole;
   const dim3 grid((unsigned)P.wgs), block(P.waves * 64);
   hipStream_t st = (hipStream_t)stream;
 #define TQ_ATTN(...) hipLaunchKernelGGL((__VA_ARGS__), grid, block, 0, st, A)
@@ -1142,8 +1310,8 @@ extern "C" int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t k
     else TQ_ATTN(decode_kernel<D, 2, true, kWaves>);              \
   }
   if (P.tile_rows == kTileRows) {
-    if (head_dim == 128) TQ_ATTN(prefill_kernel<128>);
-    else TQ_ATTN(prefill_kernel<64>);
+    if (head_dim == 128) TQ_ATTN(prefill_kernel<128, kPreWaves>);
+    else TQ_ATTN(prefill_kernel<64, kPreWaves>);
   } else if (head_dim == 128) {
     TQ_DECODE(128)
   } else {
