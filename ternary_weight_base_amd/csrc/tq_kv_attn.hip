@@ -62,8 +62,8 @@ struct AttnArgs {
   float *partials;
   float scale_log2;
   int rows, seqs, hkv, group, window, sinks;
-  int slots;          // prefill: row tiles
-  int nsplit, chunk;  // prefill: splits of the keys at most; pages of a split at least
+  int slots, solo;    // prefill: row tiles; units that stay whole
+  int nsplit, chunk;  // prefill: pieces of the others at most; pages of a piece at least
   int whole;          // decode: units of up to so many pages stay whole
 };
 
@@ -268,14 +268,19 @@ __device__ __forceinline__ float inverse(float l) { return l > 0.0f || l != l ? 
 // for the next call, whatever its shape.
 template <int R, int D, int NT, int MAXP, typename At, typename Out>
 __device__ __forceinline__ void join(int tid, Rsrc part, int pieces, int nrows, float *lds, const At &at, const Out &out) {
-  constexpr int kBatch = 8, kPer16 = (MAXP + 15) / 16;
+  // 8 loads of 16 bytes in flight a thread: of 8 pieces, or (many rows, few
+  // pieces) of 2 pieces for each of 4 outputs
+  constexpr int kPer16 = (MAXP + 15) / 16, kQ = R > 32 ? 4 : 1, kBatch = 8 / kQ;
   const int quads = nrows * (D / 4);
   const int parts = quads * 4 <= NT ? 4 : quads * 2 <= NT ? 2 : 1;
   const int per = NT / parts, p = tid / per, q0 = tid - p * per;
-  f4 v[kBatch];
+  f4 v[kQ][kBatch];
   auto fetch = [&](int k0, int q) {
 #pragma unroll
-    for (int b = 0; b < kBatch; b++) v[b] = load_dev(part, at(min(k0 + b * parts, pieces - 1)) + 4 * q);
+    for (int a = 0; a < kQ; a++)
+#pragma unroll
+      for (int b = 0; b < kBatch; b++)
+        v[a][b] = load_dev(part, at(min(k0 + b * parts, pieces - 1)) + 4 * min(q + a * per, quads - 1));
   };
   if (q0 < quads) fetch(p, q0);
   float *wt = lds;  // the pieces' weights, [MAXP][R]
@@ -314,22 +319,31 @@ __device__ __forceinline__ void join(int tid, Rsrc part, int pieces, int nrows, 
   __syncthreads();
   f4 *red = reinterpret_cast<f4 *>(lds + R * MAXP);
 #pragma unroll 1
-  for (int q = q0; q < quads; q += per) {  // one round where parts > 1
-    const int row = q / (D / 4);
-    f4 o = {0, 0, 0, 0};
+  for (int q = q0; q < quads; q += kQ * per) {  // one round where parts > 1
+    f4 o[kQ];
+#pragma unroll
+    for (int a = 0; a < kQ; a++) o[a] = (f4){0, 0, 0, 0};
 #pragma unroll 1
     for (int k0 = p; k0 < pieces; k0 += kBatch * parts) {
       if (q != q0 || k0 != p) fetch(k0, q);
 #pragma unroll
       for (int b = 0; b < kBatch; b++)
-        if (k0 + b * parts < pieces) o += v[b] * wt[(k0 + b * parts) * R + row];
+        if (k0 + b * parts < pieces)
+#pragma unroll
+          for (int a = 0; a < kQ; a++)
+            o[a] += v[a][b] * wt[(k0 + b * parts) * R + min(q + a * per, quads - 1) / (D / 4)];
     }
+#pragma unroll
+    for (int a = 0; a < kQ; a++) {
+      const int e = q + a * per;
+      if (e >= quads) break;
 #pragma unroll 1
-    for (int k = p; k < pieces; k += parts) store_dev(part, at(k) + 4 * q, (f4){0, 0, 0, 0});
-    if (parts == 1)
-      out(row, 4 * q - row * D, o);
-    else
-      red[tid] = o;
+      for (int k = p; k < pieces; k += parts) store_dev(part, at(k) + 4 * e, (f4){0, 0, 0, 0});
+      if (parts == 1)
+        out(e / (D / 4), 4 * e % D, o[a]);
+      else if (a == 0)
+        red[tid] = o[a];
+    }
   }
   if (parts == 1) return;
   __syncthreads();
@@ -345,19 +359,27 @@ constexpr int kJoinFloats = R * MAXS + 4 * NT;
 // A workgroup's place: R consecutive (token, query head) rows of a sequence
 // and KV head, and its share of their pages.
 struct Place {
-  int h, s, begin, n, nrows, f0, p0, pmin, pmax, lo, hi, splits, split;
-  int64_t tile;
+  int h, s, begin, n, nrows, f0, p0, pmin, pmax, lo, hi, splits, split, nsplit, tile;
   Tiles T;
 };
 
 template <int R>
 __device__ __forceinline__ bool find_place(const AttnArgs &A, Place &P) {
-  P.h = blockIdx.x % (uint32_t)A.hkv;
-  const uint32_t b = blockIdx.x / (uint32_t)A.hkv;
-  P.split = b % (uint32_t)A.nsplit;
-  // from the last tile on: the later rows of a sequence see more keys, and the
-  // longest work should start first
-  const int slot = A.slots - 1 - b / (uint32_t)A.nsplit;
+  // units are numbered from the last tile on: the later rows of a sequence
+  // see more keys, and the longest work should start first.  The first `solo`
+  // units are whole, the others in up to nsplit pieces.
+  int unit = blockIdx.x;
+  P.split = 0;
+  P.nsplit = 1;
+  if (unit >= A.solo) {
+    const uint32_t b = unit - A.solo;
+    unit = A.solo + b / (uint32_t)A.nsplit;
+    P.split = b % (uint32_t)A.nsplit;
+    P.nsplit = A.nsplit;
+  }
+  P.h = unit % (uint32_t)A.hkv;
+  const int slot = A.slots - 1 - (int)(unit / (uint32_t)A.hkv);
+  P.tile = unit - A.solo;
   P.s = find_seq<R, 1>(A.cu, A.seqs, A.rows, slot, A.group);
   P.begin = cu_at(A.cu, P.s, A.rows);
   P.n = max(cu_at(A.cu, P.s + 1, A.rows) - P.begin, 0);
@@ -369,11 +391,10 @@ __device__ __forceinline__ bool find_place(const AttnArgs &A, Place &P) {
   P.pmin = P.p0 + (uint32_t)P.f0 / (uint32_t)A.group;
   P.pmax = P.p0 + (uint32_t)(P.f0 + P.nrows - 1) / (uint32_t)A.group;
   P.T = visible_tiles(P.pmin, P.pmax, A.max_pages, A.window, A.sinks);
-  const int per = max(A.chunk, (int)((uint32_t)(P.T.count + A.nsplit - 1) / (uint32_t)A.nsplit));
+  const int per = max(A.chunk, (int)((uint32_t)(P.T.count + P.nsplit - 1) / (uint32_t)P.nsplit));
   P.splits = max((int)((uint32_t)(P.T.count + per - 1) / (uint32_t)per), 1);
   P.lo = P.split * per;
   P.hi = min(P.T.count, P.lo + per);
-  P.tile = (int64_t)slot * A.hkv + P.h;
   return P.split < P.splits;
 }
 
@@ -1142,7 +1163,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
 
   // element r of o[d] is output 32 d + 8 (r / 4) + 4 half + r % 4
   if (P.splits > 1) {
-    Rsrc base = make_rsrc(A.partials + P.tile * A.nsplit * partial_floats(kTileRows, D));
+    Rsrc base = make_rsrc(A.partials + (int64_t)P.tile * A.nsplit * partial_floats(kTileRows, D));
     const int at = P.split * partial_floats(kTileRows, D);
     if (valid) {
 #pragma unroll
@@ -1180,7 +1201,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
 // and the workspace that needs.
 struct Plan {
   int tile_rows;  // 16, 32: decode; 128: prefill
-  int64_t wgs;
+  int64_t wgs, solo;
   int waves;  // of a workgroup
   int nsplit, chunk;
   int whole;  // decode: units of up to so many pages stay whole; 0: all do
@@ -1198,31 +1219,32 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
   const int64_t tiles = (max_kv + kPage - 1) / kPage;
   const int64_t full = (flat + R - 1) / R, units = (full > seqs ? full : seqs) * kv_heads;
   P.nsplit = 1;
+  P.solo = 0;
   P.chunk = 0x7fffffff;
   P.whole = 0;
   P.waves = prefill ? kPreWaves : kWaves;
   P.counter_bytes = P.bytes = 0;
   if (prefill) {
-    // Two workgroups a CU run together: the split that makes the fewest
-    // rounds times pages, with some 4 pages' time for a workgroup's start and
-    // end.  (With many rounds the longest-first order levels the load by itself.)
-    const int64_t slots2 = 2 * kCus;
-    int64_t nsplit = 1, chunk = tiles, best = INT64_MAX;
-    for (int64_t n = 1; n <= kPreSplits && units < 4 * slots2; n++) {
-      const int64_t c = (tiles + n - 1) / n, cost = (units * n + slots2 - 1) / slots2 * (c + 4);
-      if (cost < best && (n == 1 || c >= 4)) {
-        best = cost;
-        nsplit = n;
-        chunk = c;
-      }
-    }
-    const int64_t slots = flat / R + seqs;
-    P.wgs = slots * kv_heads * nsplit;
+    // Two workgroups a CU run together.  Full rounds of them take whole units;
+    // the rest of a last round is cut into pieces for all CUs (a piece costs a
+    // tile's partial outputs written and read, 66 KB, so not more than the
+    // rest is cut).  With many rounds the longest-first order levels the load
+    // by itself.
+    const int64_t slots = flat / R + seqs, all = slots * kv_heads, round = 2 * kCus;
+    const int64_t rest = all < 4 * round ? all % round : 0;
+    const int64_t idle = all - units, real = rest > idle ? rest - idle : rest;  // some tiles may hold no row
+    int64_t nsplit = rest ? round / real : 1;
+    if (nsplit > kPreSplits) nsplit = kPreSplits;
+    if (nsplit > tiles / 4) nsplit = tiles / 4;
+    P.wgs = P.solo = all;
     if (nsplit > 1) {
       P.nsplit = (int)nsplit;
+      P.solo = all - rest;
+      P.wgs = P.solo + rest * nsplit;
+      const int64_t chunk = (tiles + nsplit - 1) / nsplit;
       P.chunk = (int)(chunk < 0x7fffffff ? chunk : 0x7fffffff);
-      P.counter_bytes = ((size_t)slots * kv_heads * 4 + 15) / 16 * 16;
-      P.bytes = P.counter_bytes + (size_t)slots * kv_heads * nsplit * partial_floats(R, (int)head_dim) * 4;
+      P.counter_bytes = ((size_t)rest * 4 + 15) / 16 * 16;
+      P.bytes = P.counter_bytes + (size_t)rest * nsplit * partial_floats(R, (int)head_dim) * 4;
     }
     return P;
   }
@@ -1295,6 +1317,7 @@ extern "C" int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t k
   A.window = (int)window; A.sinks = (int)sinks;
   A.slots = (int)(rows * (q_heads / kv_heads) / P.tile_rows + seqs);
   A.nsplit = P.nsplit;
+  A.solo = (int)P.solo;
   A.chunk = window && P.nsplit > 1 ? 4 : P.chunk;  // a window leaves fewer pages than max_kv_len says
   A.whole = P.whole;
   const dim3 grid((unsigned)P.wgs), block(P.waves * 64);
