@@ -415,7 +415,7 @@ int tq_gemm(int fmt, int64_t M, int64_t N, int64_t K, const void *W, const int8_
  *
  * Rows.  cu_rows[seqs + 1] (int32, ascending from 0): sequence s has rows
  * cu_rows[s] .. cu_rows[s+1] - 1 of the call, possibly none; rows behind
- * cu_rows[seqs] are padding and are neither read nor written.  kv_len[seqs]
+ * cu_rows[seqs] are padding: what belongs to them is left as it was.  kv_len[seqs]
  * (int32): tokens of the sequence including the call's rows, so its rows
  * take the last positions, kv_len[s] - n .. kv_len[s] - 1.  These arrays are
  * read on the device, so a graph that was captured once serves changing

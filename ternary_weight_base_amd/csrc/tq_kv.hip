@@ -18,10 +18,14 @@
 //
 // Bound: memory, or launch latency for a few rows.  A prompt reads
 // (q_heads + 2 kv_heads) head_dim values a row once and writes the rotated
-// queries (fp16) and a byte per key and value element.  Workgroups: one per
-// (page that receives rows, KV head, key or value), which holds the page's
-// new rows in registers between its maximum and its codes, and after those
-// the queries' workgroups of the same launch.
+// queries (fp16) and a byte per key and value element.  A thread's piece is 8
+// elements of a head that are rotated together: 4 and their 4 partners, or 8
+// side by side.  Workgroups: one per (page that receives rows, KV head, key
+// or value), and after those the queries' of the same launch.  For many rows
+// (256 threads) a page's new rows stay in registers between its maximum and
+// its codes, and the values turn through LDS; for a few rows a sequence (one
+// wave) every lane still has a piece of a row, and values are merged into
+// their words straight from the rows.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -34,7 +38,6 @@ namespace {
 using namespace tqkv;
 
 constexpr int kThreads = 256;
-constexpr int kQuadsPerWg = 512;  // 4-element pieces of one row that a query workgroup rotates
 
 struct AppendArgs {
   const void *qkv;
@@ -46,6 +49,7 @@ struct AppendArgs {
   int64_t row_stride, max_pages, num_pages, rope_rows;
   int rows, seqs, hq, hkv, rot, pairs;
   int page_wgs, q_chunks;  // workgroups of the page part; query workgroups of a row
+  int by_row;              // page workgroups are numbered by rows, not by slots (tq_kv.h)
 };
 
 __device__ __forceinline__ f4 load4(const float *p) { return *reinterpret_cast<const f4 *>(p); }
@@ -54,35 +58,58 @@ __device__ __forceinline__ f4 load4(const _Float16 *p) {
   return (f4){(float)a[0], (float)a[1], (float)a[2], (float)a[3]};
 }
 
+// Piece i (of D / 8) of a head: two groups of 4 elements, at lo and hi.
+// Rotated pairs i, i + rot / 2: 4 elements and their partners; else, and
+// behind the rotated elements, 8 side by side.
+struct Piece {
+  int lo, hi;
+  bool turned;
+};
+__device__ __forceinline__ Piece piece_at(int i, int rot, bool pairs) {
+  Piece p;
+  p.turned = 8 * i < rot;
+  p.lo = p.turned && !pairs ? 4 * i : 8 * i;
+  p.hi = p.turned && !pairs ? 4 * i + (rot >> 1) : 8 * i + 4;
+  return p;
+}
+
 __device__ __forceinline__ float turn(float x, float c, float y, float s, bool plus) {
   const double p = (double)x * (double)c, q = (double)y * (double)s;  // both exact
   return tqdev::round_f32(plus ? p + q : p - q);
 }
 
-// Elements d..d+3 of the head vector at `head`, rotated.  t: the position's
-// row of the table, rot / 2 cosines, then rot / 2 sines.
-template <typename T>
-__device__ __forceinline__ f4 load_rotated(const T *head, int d, const float *t, int rot, bool pairs) {
-  const f4 x = load4(head + d);
-  if (d >= rot) return x;
-  const int h = rot >> 1;
-  f4 r;
+// Rotates a piece's 8 elements in place by c, s, the cosines and sines of
+// its four pairs.
+__device__ __forceinline__ void rotate(f4 &a, f4 &b, f4 c, f4 s, bool pairs) {
   if (pairs) {
-    const float c0 = t[d >> 1], c1 = t[(d >> 1) + 1], s0 = t[h + (d >> 1)], s1 = t[h + (d >> 1) + 1];
-    r[0] = turn(x[0], c0, x[1], s0, false);
-    r[1] = turn(x[1], c0, x[0], s0, true);
-    r[2] = turn(x[2], c1, x[3], s1, false);
-    r[3] = turn(x[3], c1, x[2], s1, true);
-    return r;
-  }
-  const bool hi = d >= h;
-  const int a = hi ? d - h : d;
-  const f4 y = load4(head + (hi ? d - h : d + h)), c = load4(t + a), s = load4(t + h + a);
+    const f4 x = a, y = b;
 #pragma unroll
-  for (int i = 0; i < 4; i++) r[i] = turn(x[i], c[i], y[i], s[i], hi);
-  return r;
+    for (int i = 0; i < 2; i++) {
+      a[2 * i] = turn(x[2 * i], c[i], x[2 * i + 1], s[i], false);
+      a[2 * i + 1] = turn(x[2 * i + 1], c[i], x[2 * i], s[i], true);
+      b[2 * i] = turn(y[2 * i], c[2 + i], y[2 * i + 1], s[2 + i], false);
+      b[2 * i + 1] = turn(y[2 * i + 1], c[2 + i], y[2 * i], s[2 + i], true);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const float x = a[i], y = b[i];
+    a[i] = turn(x, c[i], y, s[i], false);
+    b[i] = turn(y, c[i], x, s[i], true);
+  }
 }
 
+// A byte's code and the shift of earlier ones.
+//
+// x / s must not be rounded before its floor is taken: in double.
+__device__ __forceinline__ uint32_t code(float x, double inv) {
+  const double c = fmin(fmax(floor((double)x * inv), -128.0), 127.0);
+  return (uint32_t)((int)c + 128);
+}
+__device__ __forceinline__ uint32_t codes4(f4 x, double inv) {
+  return code(x[0], inv) | code(x[1], inv) << 8 | code(x[2], inv) << 16 | code(x[3], inv) << 24;
+}
 // The four biased codes of w, shifted: c = b - 128, c >> k.
 __device__ __forceinline__ uint32_t shift_codes(uint32_t w, int k) {
   uint32_t r = 0;
@@ -101,69 +128,156 @@ __device__ __forceinline__ int need_field(float m) {
   return b == 0 ? 0 : min(max((int)(b >> 23) - 6, 1), 248);
 }
 
+// Word `wd` (4 tokens) of a value row: the new codes in w where slots
+// a .. a + m - 1 are, earlier tokens' from `old`, shifted, later bytes as they are.
+__device__ __forceinline__ uint32_t merge_word(uint32_t w, uint32_t old, int wd, int a, int m, int grow) {
+  const uint32_t moved = grow ? shift_codes(old, grow) : old;
+  uint32_t mask_new = 0, mask_old = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const int t = 4 * wd + j;
+    if (t >= a && t < a + m) mask_new |= 255u << (8 * j);
+    if (t < a) mask_old |= 255u << (8 * j);
+  }
+  return (w & mask_new) | (moved & mask_old) | (old & ~(mask_new | mask_old));
+}
+
+// The rotated queries of one row: pieces chunk * NT * IT ..., IT a thread,
+// whose loads are sent for before the row's position is known.
+template <int D, typename T, int NT, int IT>
+__device__ __forceinline__ void rotate_queries(const AppendArgs &A, int row, int chunk) {
+  constexpr int kPieces = D / 8;
+  const int total = A.hq * kPieces, i0 = chunk * (NT * IT) + threadIdx.x;
+  const Piece p = piece_at(i0 % kPieces, A.rot, A.pairs);  // the same for each of a thread's: NT % kPieces = 0
+  const T *x = (const T *)A.qkv + (int64_t)row * A.row_stride;
+  f4 a[IT], b[IT];
+#pragma unroll
+  for (int k = 0; k < IT; k++) {
+    const int head = min(i0 + k * NT, total - 1) / kPieces;
+    a[k] = load4(x + head * D + p.lo);
+    b[k] = load4(x + head * D + p.hi);
+  }
+  if (row >= cu_at(A.cu, A.seqs, A.rows)) return;
+  const int s = find_seq<1, 0>(A.cu, A.seqs, A.rows, row, 1);
+  const int64_t pos = (int64_t)A.kv_len[s] - (cu_at(A.cu, s + 1, A.rows) - row);
+  const bool ok = pos >= 0 && (A.rot == 0 || pos < A.rope_rows);
+  f4 c = {0, 0, 0, 0}, sn = c;
+  if (ok && p.turned) {
+    const float *t = A.rope + pos * A.rot + 4 * (i0 % kPieces);
+    c = load4(t);
+    sn = load4(t + (A.rot >> 1));
+  }
+  _Float16 *o = A.q_out + (int64_t)row * A.hq * D;
+#pragma unroll
+  for (int k = 0; k < IT; k++) {
+    const int i = i0 + k * NT;
+    if (i >= total) break;
+    if (!ok) a[k] = b[k] = (f4){0, 0, 0, 0};
+    else if (p.turned) rotate(a[k], b[k], c, sn, A.pairs);
+    _Float16 *d = o + i / kPieces * D;
+    *reinterpret_cast<h4 *>(d + p.lo) = (h4){(_Float16)a[k][0], (_Float16)a[k][1], (_Float16)a[k][2], (_Float16)a[k][3]};
+    *reinterpret_cast<h4 *>(d + p.hi) = (h4){(_Float16)b[k][0], (_Float16)b[k][1], (_Float16)b[k][2], (_Float16)b[k][3]};
+  }
+}
+
+// The rows that a page workgroup stores: row0 .. row0 + m - 1 at positions
+// pos .. into slots a .. of a page (and KV head) ph.
+struct Run {
+  int64_t row0, pos, ph;
+  int a, m;
+};
+
+__device__ __forceinline__ bool find_run(const AppendArgs &A, int unit, int h, Run &r) {
+  int s, begin, end;
+  int64_t kvl, p0, pg;
+  if (A.by_row) {
+    // the workgroup of a sequence's first row, or of the row at a page's start
+    if (unit >= cu_at(A.cu, A.seqs, A.rows)) return false;
+    s = find_seq<1, 0>(A.cu, A.seqs, A.rows, unit, 1);
+    begin = cu_at(A.cu, s, A.rows);
+    end = max(cu_at(A.cu, s + 1, A.rows), begin);
+    kvl = A.kv_len[s];
+    p0 = kvl - (end - begin);
+    const int64_t pos = p0 + (unit - begin);
+    if (unit < begin || unit >= end || pos < 0) return false;
+    if (unit != begin && pos != 0 && pos % kPage != 0) return false;
+    pg = pos / kPage;
+  } else {
+    s = find_seq<kPage, 2>(A.cu, A.seqs, A.rows, unit, 1);
+    begin = cu_at(A.cu, s, A.rows);
+    end = max(cu_at(A.cu, s + 1, A.rows), begin);
+    const int local = unit - slot_base<kPage, 2>(begin, s, 1);
+    kvl = A.kv_len[s];
+    p0 = kvl - (end - begin);
+    if (local < 0) return false;
+    pg = (p0 > 0 ? p0 : 0) / kPage + local;
+  }
+  if (pg >= A.max_pages) return false;
+  int64_t last = kvl;  // tokens at `last` and behind are not stored
+  if (A.rot && last > A.rope_rows) last = A.rope_rows;
+  const int64_t first = p0 > 0 ? p0 : 0;
+  const int64_t lo = first > pg * kPage ? first : pg * kPage;
+  const int64_t hi = last < (pg + 1) * kPage ? last : (pg + 1) * kPage;
+  if (lo >= hi) return false;
+  const int64_t id = A.table[(int64_t)s * A.max_pages + pg];
+  if (id < 0 || id >= A.num_pages) return false;
+  r.a = (int)(lo - pg * kPage);
+  r.m = (int)(hi - lo);
+  r.row0 = begin + (lo - p0);
+  r.pos = lo;
+  r.ph = id * A.hkv + h;
+  return true;
+}
+
+// The exponent field of a page's present scale: 0 if the page is new (or
+// holds no power of two).
+__device__ __forceinline__ int present_field(const float *scale, int a) {
+  const uint32_t b = a > 0 ? __float_as_uint(*scale) : 0u;
+  return (b & 0x807fffffu) == 0 && (b >> 23) <= 248 ? (int)(b >> 23) : 0;
+}
+// 1 / s as a double; a page of zeros has the codes of 0
+__device__ __forceinline__ double inverse_scale(int f) {
+  return f ? __longlong_as_double((long long)(1023 + 127 - f) << 52) : 0.0;
+}
+
 template <int D, typename T>
 __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs A) {
-  constexpr int kQuads = D / 4, kRowsStep = kThreads / kQuads, kSteps = kPage / kRowsStep;
-  const int tid = threadIdx.x;
-  const T *qkv = (const T *)A.qkv;
-  int blk = blockIdx.x;
-  if (blk >= A.page_wgs) {  // queries: one row, kQuadsPerWg quads
-    blk -= A.page_wgs;
-    const int row = blk / A.q_chunks, chunk = blk % A.q_chunks;
-    if (row >= cu_at(A.cu, A.seqs, A.rows)) return;
-    const int s = find_seq<1, 0>(A.cu, A.seqs, A.rows, row, 1);
-    const int64_t pos = (int64_t)A.kv_len[s] - (cu_at(A.cu, s + 1, A.rows) - row);
-    const bool ok = pos >= 0 && (A.rot == 0 || pos < A.rope_rows);
-    const float *t = A.rope + (ok ? pos : 0) * A.rot;
-    const T *x = qkv + (int64_t)row * A.row_stride;
-    _Float16 *o = A.q_out + (int64_t)row * A.hq * D;
-    const int end = min((chunk + 1) * kQuadsPerWg, A.hq * kQuads);
-    for (int i = chunk * kQuadsPerWg + tid; i < end; i += kThreads) {
-      const int head = i / kQuads, d = (i % kQuads) * 4;
-      f4 r = {0, 0, 0, 0};
-      if (ok) r = load_rotated(x + head * D, d, t, A.rot, A.pairs);
-      *reinterpret_cast<h4 *>(o + i * 4) = (h4){(_Float16)r[0], (_Float16)r[1], (_Float16)r[2], (_Float16)r[3]};
-    }
+  constexpr int kPieces = D / 8, kRowsStep = kThreads / kPieces, kSteps = kPage / kRowsStep, kIt = 4;
+  const int tid = threadIdx.x, blk = blockIdx.x;
+  if (blk >= A.page_wgs) {
+    rotate_queries<D, T, kThreads, kIt>(A, (blk - A.page_wgs) / A.q_chunks, (blk - A.page_wgs) % A.q_chunks);
     return;
   }
   const bool is_v = blk & 1;
-  const int h = (blk >> 1) % A.hkv, slot = (blk >> 1) / A.hkv;
-  const int s = find_seq<kPage, 2>(A.cu, A.seqs, A.rows, slot, 1);
-  const int begin = cu_at(A.cu, s, A.rows), end = max(cu_at(A.cu, s + 1, A.rows), begin);
-  const int local = slot - slot_base<kPage, 2>(begin, s, 1);
-  const int64_t kvl = A.kv_len[s], p0 = kvl - (end - begin), first = p0 > 0 ? p0 : 0;
-  const int64_t pg = first / kPage + local;
-  if (local < 0 || pg >= A.max_pages) return;
-  int64_t last = kvl;  // tokens at `last` and behind are not stored
-  if (A.rot && last > A.rope_rows) last = A.rope_rows;
-  const int64_t lo = first > pg * kPage ? first : pg * kPage;
-  const int64_t hi = last < (pg + 1) * kPage ? last : (pg + 1) * kPage;
-  if (lo >= hi) return;
-  const int64_t id = A.table[(int64_t)s * A.max_pages + pg];
-  if (id < 0 || id >= A.num_pages) return;
-  const int a = (int)(lo - pg * kPage), m = (int)(hi - lo);  // slots a .. a + m - 1 receive rows
-  const int64_t row0 = begin + (lo - p0), ph = id * A.hkv + h;
-  float *scale = (is_v ? A.vs : A.ks) + ph;
-
+  const int h = (blk >> 1) % A.hkv;
+  Run R;
+  if (!find_run(A, (blk >> 1) / A.hkv, h, R)) return;
+  float *scale = (is_v ? A.vs : A.ks) + R.ph;
   __shared__ float wmax[kThreads / 64];
   __shared__ uint32_t tile[D * (kPage / 4 + 1)];
-  // the page's present scale: none if the page is new (or holds no power of two)
-  const uint32_t ob = a > 0 ? __float_as_uint(*scale) : 0u;
-  const int old_f = (ob & 0x807fffffu) == 0 && (ob >> 23) <= 248 ? (int)(ob >> 23) : 0;
-  const int quad = tid % kQuads, r0 = tid / kQuads, d = quad * 4;
-  const T *src = qkv + row0 * A.row_stride + (int64_t)(A.hq + (is_v ? A.hkv : 0) + h) * D;
-  f4 x[kSteps];
+  const int old_f = present_field(scale, R.a), i = tid % kPieces, r0 = tid / kPieces;
+  const Piece p = piece_at(i, is_v ? 0 : A.rot, A.pairs);
+  const T *src = (const T *)A.qkv + R.row0 * A.row_stride + (int64_t)(A.hq + (is_v ? A.hkv : 0) + h) * D;
+  f4 x[kSteps][2];
   float mx = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kSteps; i++) {
-    const int r = i * kRowsStep + r0;
-    x[i] = (f4){0, 0, 0, 0};
-    if (r < m) {
-      const T *p = src + r * A.row_stride;
-      x[i] = is_v ? load4(p + d) : load_rotated(p, d, A.rope + (lo + r) * A.rot, A.rot, A.pairs);
+  for (int k = 0; k < kSteps; k++) {
+    const int r = k * kRowsStep + r0;
+    x[k][0] = x[k][1] = (f4){0, 0, 0, 0};
+    if (r < R.m) {
+      x[k][0] = load4(src + r * A.row_stride + p.lo);
+      x[k][1] = load4(src + r * A.row_stride + p.hi);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kSteps; k++) {
+    const int r = k * kRowsStep + r0;
+    if (r < R.m && p.turned) {
+      const float *t = A.rope + (R.pos + r) * A.rot + 4 * i;
+      rotate(x[k][0], x[k][1], load4(t), load4(t + (A.rot >> 1)), A.pairs);
     }
 #pragma unroll
-    for (int j = 0; j < 4; j++) mx = fmaxf(mx, fabsf(x[i][j]));
+    for (int j = 0; j < 8; j++) mx = fmaxf(mx, fabsf(x[k][j >> 2][j & 3]));
   }
   mx = tqdev::wave_max64(mx);
   if ((tid & 63) == 0) wmax[tid >> 6] = mx;
@@ -173,51 +287,111 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs A) {
   const int f = max(need_field(mx), old_f);
   const int grow = old_f ? min(f - old_f, 8) : 0;
   if (tid == 0) *scale = __uint_as_float((uint32_t)f << 23);
-  // 1 / s as a double; codes of a page of zeros are those of 0
-  const double inv = f ? __longlong_as_double((long long)(1023 + 127 - f) << 52) : 0.0;
+  const double inv = inverse_scale(f);
 
-  uint32_t *page = reinterpret_cast<uint32_t *>((is_v ? A.v : A.k) + ph * (kPage * D));
+  constexpr int kWords = D / 4;
+  uint32_t *page = reinterpret_cast<uint32_t *>((is_v ? A.v : A.k) + R.ph * (kPage * D));
   if (!is_v && grow)
-    for (int i = tid; i < a * kQuads; i += kThreads) page[i] = shift_codes(page[i], grow);
+    for (int k = tid; k < R.a * kWords; k += kThreads) page[k] = shift_codes(page[k], grow);
 #pragma unroll
-  for (int i = 0; i < kSteps; i++) {
-    const int r = i * kRowsStep + r0;
-    if (r < m) {
-      uint32_t w = 0;
+  for (int k = 0; k < kSteps; k++) {
+    const int r = k * kRowsStep + r0;
+    if (r < R.m) {
+      if (is_v) {
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        // in double: x / s must not be rounded before its floor is taken
-        const double c = fmin(fmax(floor((double)x[i][j] * inv), -128.0), 127.0);
-        const uint32_t b = (uint32_t)((int)c + 128);
-        if (is_v)
-          reinterpret_cast<uint8_t *>(tile)[(d + j) * (kPage + 4) + a + r] = (uint8_t)b;
-        else
-          w |= b << (8 * j);
+        for (int j = 0; j < 8; j++)
+          reinterpret_cast<uint8_t *>(tile)[(8 * i + j) * (kPage + 4) + R.a + r] = (uint8_t)code(x[k][j >> 2][j & 3], inv);
+      } else {
+        page[(R.a + r) * kWords + p.lo / 4] = codes4(x[k][0], inv);
+        page[(R.a + r) * kWords + p.hi / 4] = codes4(x[k][1], inv);
       }
-      if (!is_v) page[(a + r) * kQuads + quad] = w;
     }
   }
   if (!is_v) return;
   // values lie with their tokens side by side: whole words from the tile, words
   // that also hold other tokens merged with what is there
   __syncthreads();
-  const int w0 = grow ? 0 : a >> 2, nw = ((a + m - 1) >> 2) - w0 + 1;
-  for (int i = tid; i < D * nw; i += kThreads) {
-    const int dim = i / nw, wd = w0 + i % nw, t0 = wd * 4;
+  const int w0 = grow ? 0 : R.a >> 2, nw = ((R.a + R.m - 1) >> 2) - w0 + 1;
+  for (int k = tid; k < D * nw; k += kThreads) {
+    const int dim = k / nw, wd = w0 + k % nw, at = dim * (kPage / 4) + wd;
     uint32_t w = tile[dim * (kPage / 4 + 1) + wd];
-    if (t0 < a || t0 + 4 > a + m) {
-      const uint32_t old = page[dim * (kPage / 4) + wd];
-      const uint32_t moved = grow ? shift_codes(old, grow) : old;
-      uint32_t mask_new = 0, mask_old = 0;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int t = t0 + j;
-        if (t >= a && t < a + m) mask_new |= 255u << (8 * j);
-        if (t < a) mask_old |= 255u << (8 * j);
-      }
-      w = (w & mask_new) | (moved & mask_old) | (old & ~(mask_new | mask_old));
+    if (4 * wd < R.a || 4 * wd + 4 > R.a + R.m) w = merge_word(w, page[at], wd, R.a, R.m, grow);
+    page[at] = w;
+  }
+}
+
+// The same for a few rows a sequence, one wave a workgroup (right for any
+// number: rows beyond the first four of a page are read twice).
+template <int D, typename T>
+__global__ __launch_bounds__(64) void append_few_kernel(const AppendArgs A) {
+  constexpr int kPieces = D / 8, kRowsStep = 64 / kPieces;
+  const int lane = threadIdx.x, blk = blockIdx.x;
+  if (blk >= A.page_wgs) {
+    rotate_queries<D, T, 64, 1>(A, (blk - A.page_wgs) / A.q_chunks, (blk - A.page_wgs) % A.q_chunks);
+    return;
+  }
+  const bool is_v = blk & 1;
+  const int h = (blk >> 1) % A.hkv;
+  Run R;
+  if (!find_run(A, (blk >> 1) / A.hkv, h, R)) return;
+  float *scale = (is_v ? A.vs : A.ks) + R.ph;
+  const int old_f = present_field(scale, R.a), i = lane % kPieces, r0 = lane / kPieces;
+  const Piece p = piece_at(i, is_v ? 0 : A.rot, A.pairs);
+  const T *src = (const T *)A.qkv + R.row0 * A.row_stride + (int64_t)(A.hq + (is_v ? A.hkv : 0) + h) * D;
+  auto fetch = [&](int r, f4 &a, f4 &b) {
+    a = b = (f4){0, 0, 0, 0};
+    if (r >= R.m) return;
+    a = load4(src + r * A.row_stride + p.lo);
+    b = load4(src + r * A.row_stride + p.hi);
+    if (p.turned) {
+      const float *t = A.rope + (R.pos + r) * A.rot + 4 * i;
+      rotate(a, b, load4(t), load4(t + (A.rot >> 1)), A.pairs);
     }
-    page[dim * (kPage / 4) + wd] = w;
+  };
+  f4 a0, b0;
+  fetch(r0, a0, b0);
+  float mx = 0.0f;
+  auto widen = [&](f4 a, f4 b) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) mx = fmaxf(mx, fmaxf(fabsf(a[j]), fabsf(b[j])));
+  };
+  widen(a0, b0);
+  for (int r = kRowsStep; r < R.m; r += kRowsStep) {
+    f4 a, b;
+    fetch(r + r0, a, b);
+    widen(a, b);
+  }
+  mx = tqdev::wave_max64(mx);
+  const int f = max(need_field(mx), old_f);
+  const int grow = old_f ? min(f - old_f, 8) : 0;
+  if (lane == 0) *scale = __uint_as_float((uint32_t)f << 23);
+  const double inv = inverse_scale(f);
+  constexpr int kWords = D / 4;
+  uint32_t *page = reinterpret_cast<uint32_t *>((is_v ? A.v : A.k) + R.ph * (kPage * D));
+  if (is_v) {
+    const int w0 = grow ? 0 : R.a >> 2, w1 = (R.a + R.m - 1) >> 2;
+    for (int dim = lane; dim < D; dim += 64)
+      for (int wd = w0; wd <= w1; wd++) {
+        const uint32_t old = page[dim * (kPage / 4) + wd];
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const int r = 4 * wd + j - R.a;
+          if (r >= 0 && r < R.m) w |= code((float)src[r * A.row_stride + dim], inv) << (8 * j);
+        }
+        page[dim * (kPage / 4) + wd] = merge_word(w, old, wd, R.a, R.m, grow);
+      }
+    return;
+  }
+  if (grow)
+    for (int k = lane; k < R.a * kWords; k += 64) page[k] = shift_codes(page[k], grow);
+  for (int r = 0; r < R.m; r += kRowsStep) {
+    f4 a = a0, b = b0;
+    if (r) fetch(r + r0, a, b);
+    if (r + r0 < R.m) {
+      page[(R.a + r + r0) * kWords + p.lo / 4] = codes4(a, inv);
+      page[(R.a + r + r0) * kWords + p.hi / 4] = codes4(b, inv);
+    }
   }
 }
 
@@ -226,8 +400,6 @@ template <int D, typename T>
 __global__ __launch_bounds__(kThreads) void read_kernel(const int *ids, int n, int hkv, int64_t num_pages,
                                                         const uint8_t *k, const uint8_t *v, const float *ks,
                                                         const float *vs, T *out) {
-  constexpr int kWords = kPage * D / 4;
-  __shared__ uint32_t tile[D * (kPage / 4 + 1)];
   const int tid = threadIdx.x;
   const bool is_v = (int)blockIdx.x >= n * hkv;
   const int b = blockIdx.x - (is_v ? n * hkv : 0), h = b % hkv;
@@ -237,18 +409,28 @@ __global__ __launch_bounds__(kThreads) void read_kernel(const int *ids, int n, i
   const float s = ok ? (is_v ? vs : ks)[ph] : 0.0f;
   const uint32_t *page = reinterpret_cast<const uint32_t *>((is_v ? v : k) + ph * (kPage * D));
   T *o = out + (int64_t)blockIdx.x * (kPage * D);
-  if (is_v) {
-    for (int i = tid; i < kWords; i += kThreads)
-      tile[(i / (kPage / 4)) * (kPage / 4 + 1) + i % (kPage / 4)] = page[i];
-    __syncthreads();
-  }
-  for (int i = tid; i < kWords; i += kThreads) {
-    const int t = i / (D / 4), d = (i % (D / 4)) * 4;
-    const uint32_t w = is_v ? 0u : page[i];
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  auto put = [&](int token, int d, uint32_t w) {  // elements d .. d + 3 of a token
+    T4 x;
+#pragma unroll
+    for (int j = 0; j < 4; j++) x[j] = ok ? (T)(((float)((w >> (8 * j)) & 255u) - 127.5f) * s) : (T)0.0f;
+    *reinterpret_cast<T4 *>(o + token * D + d) = x;
+  };
+  // 4 tokens by 4 elements a thread and turn
+  for (int i = tid; i < kPage * D / 16; i += kThreads) {
+    const int d = i % (D / 4) * 4, t = i / (D / 4) * 4;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) w[j] = is_v ? page[(d + j) * (kPage / 4) + t / 4] : page[(t + j) * (D / 4) + d / 4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const uint32_t c = is_v ? reinterpret_cast<const uint8_t *>(tile)[(d + j) * (kPage + 4) + t] : (w >> (8 * j)) & 255u;
-      o[i * 4 + j] = ok ? (T)(((float)c - 127.5f) * s) : (T)0.0f;
+      uint32_t x = w[j];
+      if (is_v) {
+        x = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++) x |= ((w[e] >> (8 * j)) & 255u) << (8 * e);
+      }
+      put(t + j, d, x);
     }
   }
 }
@@ -283,18 +465,26 @@ extern "C" int tq_kv_append(int dtype, int64_t rows, int64_t seqs, int64_t q_hea
   A.row_stride = row_stride; A.max_pages = max_pages; A.num_pages = num_pages; A.rope_rows = rope_rows;
   A.rows = (int)rows; A.seqs = (int)seqs; A.hq = (int)q_heads; A.hkv = (int)kv_heads; A.rot = (int)rot;
   A.pairs = rope_mode == TQ_ROPE_PAIRS;
+  // up to four rows a sequence: a row's worth of lanes has work in a wave, not in 256 threads
+  const bool few = rows <= 4 * seqs;
   const int64_t slots = rows / kPage + 2 * seqs;
-  A.q_chunks = (int)((q_heads * head_dim / 4 + kQuadsPerWg - 1) / kQuadsPerWg);
-  const int64_t page_wgs = slots * kv_heads * 2, wgs = page_wgs + (q_out ? rows * A.q_chunks : 0);
+  A.by_row = rows < slots;
+  const int64_t per_wg = few ? 64 : 4 * kThreads;
+  A.q_chunks = (int)((q_heads * head_dim / 8 + per_wg - 1) / per_wg);
+  const int64_t page_wgs = (A.by_row ? rows : slots) * kv_heads * 2, wgs = page_wgs + (q_out ? rows * A.q_chunks : 0);
   if (wgs > 0x7fffffff) return TQ_ERR_SHAPE;
   A.page_wgs = (int)page_wgs;
-  const dim3 grid((unsigned)wgs), block(kThreads);
+  const dim3 grid((unsigned)wgs), block(few ? 64 : kThreads);
   hipStream_t st = (hipStream_t)stream;
-#define TQ_APPEND(D, T) hipLaunchKernelGGL((append_kernel<D, T>), grid, block, 0, st, A)
+#define TQ_APPEND(D, T)                                                     \
+  {                                                                         \
+    if (few) hipLaunchKernelGGL((append_few_kernel<D, T>), grid, block, 0, st, A); \
+    else hipLaunchKernelGGL((append_kernel<D, T>), grid, block, 0, st, A);  \
+  }
   if (head_dim == 128) {
-    if (dtype == TQ_F16) TQ_APPEND(128, _Float16); else TQ_APPEND(128, float);
+    if (dtype == TQ_F16) TQ_APPEND(128, _Float16) else TQ_APPEND(128, float)
   } else {
-    if (dtype == TQ_F16) TQ_APPEND(64, _Float16); else TQ_APPEND(64, float);
+    if (dtype == TQ_F16) TQ_APPEND(64, _Float16) else TQ_APPEND(64, float)
   }
 #undef TQ_APPEND
   return hipGetLastError() == hipSuccess ? TQ_OK : TQ_ERR_HIP;

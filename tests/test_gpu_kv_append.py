@@ -82,6 +82,7 @@ CASES = [
     (5, 1, 128, 0, False, np.float32, [(33, 33)], 0),
     (2, 2, 64, 8, True, np.float16, [(9, 4)], 1),     # more rows than tokens: the first rows have no position
     (2, 1, 128, 128, False, np.float32, [(3, 0), (4, 4)], 0),
+    (4, 2, 128, 64, True, np.float32, [(21, 70)] + [(0, 5)] * 7 + [(1, 65)], 0),   # few rows a sequence, but many in one
 ] + [(4, 2, 64, 64, False, np.float32, [(1 + i % 3, 1 + i % 3) for i in range(150)], 2)]
 
 
