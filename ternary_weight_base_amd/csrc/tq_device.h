@@ -66,6 +66,28 @@ __device__ __forceinline__ float wave_max64(float v) {
   return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
 }
 
+// The double sum over the 64 lanes, wave-uniform, in a fixed order.
+template <int CTRL>
+__device__ __forceinline__ double dpp_move(double v) {
+  const long long b = __double_as_longlong(v);
+  const int lo = dpp_move<CTRL>((int)b), hi = dpp_move<CTRL>((int)(b >> 32));
+  return __longlong_as_double(((long long)hi << 32) | (uint32_t)lo);
+}
+__device__ __forceinline__ double wave_sum64(double v) {
+  v += dpp_move<kDppSwap1>(v);
+  v += dpp_move<kDppSwap2>(v);
+  v += dpp_move<kDppRor4>(v);
+  v += dpp_move<kDppRor8>(v);
+  const long long b = __double_as_longlong(v);
+  double r[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int lo = __builtin_amdgcn_readlane((int)b, 16 * i), hi = __builtin_amdgcn_readlane((int)(b >> 32), 16 * i);
+    r[i] = __longlong_as_double(((long long)hi << 32) | (uint32_t)lo);
+  }
+  return (r[0] + r[1]) + (r[2] + r[3]);
+}
+
 // The integer sums over lanes 0..31 (lo) and 32..63 (hi), wave-uniform.
 __device__ __forceinline__ void half_sums(int v, int &lo, int &hi) {
   v += dpp_move<kDppSwap1>(v);

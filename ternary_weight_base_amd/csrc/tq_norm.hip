@@ -74,8 +74,7 @@ __device__ __forceinline__ void store(_Float16 *p, const float (&v)[V]) {
 
 template <int NT>
 __device__ __forceinline__ double block_sum(double v, double *part) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  v = tqdev::wave_sum64(v);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   double s = 0.0;
@@ -84,7 +83,10 @@ __device__ __forceinline__ double block_sum(double v, double *part) {
   return s;
 }
 
-template <typename TY, typename TR, int V, int NT, int ITEMS>
+// EARLY: the weights and the gate are sent for with the row (a few rows: the
+// call is latency); else where they are used, from the caches (many rows:
+// fewer registers).
+template <typename TY, typename TR, int V, int NT, int ITEMS, bool EARLY>
 __global__ __launch_bounds__(NT) void residual_norm_kernel(const NormArgs A) {
   __shared__ double part[2][NT / 64];
   __shared__ float wmax[NT / 64];
@@ -94,6 +96,14 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(const NormArgs A) {
   const TY *gate = A.gate ? (const TY *)A.gate + row * A.gate_stride : nullptr;
   const TR *res = (const TR *)A.res + row * H;
   float r[ITEMS][V], u[ITEMS][V];
+  constexpr int EI = EARLY ? ITEMS : 1;
+  float ew[EI][V], eg[EI][V], ep[EI][V];
+  // weight, gate and next weight of item i (ones where there are none)
+  auto get = [&](const auto *p, int e, float (&v)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; j++) v[j] = 1.0f;
+    if (p && e < H) load<V>(p + e, v);
+  };
 #pragma unroll
   for (int i = 0; i < ITEMS; i++) {
     const int e = (i * NT + tid) * V;
@@ -102,6 +112,11 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(const NormArgs A) {
     if (e < H) {
       load<V>(res + e, r[i]);
       if (y) load<V>(y + e, u[i]);
+    }
+    if constexpr (EARLY) {
+      get(A.post_w, e, ew[i]);
+      get(gate, e, eg[i]);
+      get(A.pre_w, e, ep[i]);
     }
   }
   if (y) {
@@ -118,11 +133,11 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(const NormArgs A) {
     for (int i = 0; i < ITEMS; i++) {
       const int e = (i * NT + tid) * V;
       if (e < H) {
-        float w[V], g[V];
-#pragma unroll
-        for (int j = 0; j < V; j++) w[j] = g[j] = 1.0f;
-        if (A.post_w) load<V>(A.post_w + e, w);
-        if (gate) load<V>(gate + e, g);
+        float(&w)[V] = ew[EARLY ? i : 0], (&g)[V] = eg[EARLY ? i : 0];
+        if constexpr (!EARLY) {
+          get(A.post_w, e, w);
+          get(gate, e, g);
+        }
 #pragma unroll
         for (int j = 0; j < V; j++)
           r[i][j] = (float)(TR)tqdev::round_f32(
@@ -150,10 +165,8 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(const NormArgs A) {
   for (int i = 0; i < ITEMS; i++) {
     const int e = (i * NT + tid) * V;
     if (e < H) {
-      float w[V];
-#pragma unroll
-      for (int j = 0; j < V; j++) w[j] = 1.0f;
-      if (A.pre_w) load<V>(A.pre_w + e, w);
+      float(&w)[V] = ep[EARLY ? i : 0];
+      if constexpr (!EARLY) get(A.pre_w, e, w);
 #pragma unroll
       for (int j = 0; j < V; j++) {
         r[i][j] = tqdev::round_f32((double)r[i][j] * inv * (double)w[j]);
@@ -201,18 +214,30 @@ template <typename TY, typename TR>
 void launch(const NormArgs &A, int64_t M, hipStream_t st) {
   const dim3 grid((unsigned)M);
   const int H = A.H;
-#define TQ_NORM(V, NT, ITEMS) \
-  hipLaunchKernelGGL((residual_norm_kernel<TY, TR, V, NT, ITEMS>), grid, dim3(NT), 0, st, A)
+#define TQ_NORM(V, NT, ITEMS, EARLY) \
+  hipLaunchKernelGGL((residual_norm_kernel<TY, TR, V, NT, ITEMS, EARLY>), grid, dim3(NT), 0, st, A)
   if (H % 4 == 0) {
-    if (H <= 1024) TQ_NORM(4, 256, 1);
-    else if (H <= 4096) TQ_NORM(4, 256, 4);
-    else if (H <= 8192) TQ_NORM(4, 512, 4);
-    else if (H <= 16384) TQ_NORM(4, 1024, 4);
-    else TQ_NORM(4, 1024, 8);
+    // up to a row for each CU: latency; see EARLY
+    const bool few = M <= 256;
+    if (H <= 1024) {
+      TQ_NORM(4, 256, 1, true);
+    } else if (H <= 4096) {
+      if (few) TQ_NORM(4, 512, 2, true);
+      else TQ_NORM(4, 256, 4, false);
+    } else if (H <= 6144) {
+      if (few) TQ_NORM(4, 512, 3, true);
+      else TQ_NORM(4, 512, 3, false);
+    } else if (H <= 8192) {
+      TQ_NORM(4, 512, 4, false);
+    } else if (H <= 16384) {
+      TQ_NORM(4, 1024, 4, false);
+    } else {
+      TQ_NORM(4, 1024, 8, false);
+    }
   } else {
-    if (H <= 1024) TQ_NORM(1, 256, 4);
-    else if (H <= 8192) TQ_NORM(1, 512, 16);
-    else TQ_NORM(1, 1024, 32);
+    if (H <= 1024) TQ_NORM(1, 256, 4, false);
+    else if (H <= 8192) TQ_NORM(1, 512, 16, false);
+    else TQ_NORM(1, 1024, 32, false);
   }
 #undef TQ_NORM
 }
