@@ -470,7 +470,7 @@ struct List {
     incl = scan(count);
   }
   __device__ __forceinline__ void load(const AttnArgs &A, int s) {
-    seq.pages = seq.units = 0;
+    seq.pages = seq.units = seq.n = 0;
     if (s < A.seqs) seq = seq_load<R>(A, s);
     tally();
   }
@@ -479,14 +479,19 @@ struct List {
   __device__ __forceinline__ void init(const AttnArgs &A) {
     const int lane = threadIdx.x & 63;
     total = units = per = 0;
+    int64_t rows = 0;
     float most = 0.0f;  // exact up to 2^24 pages, more than enough for a bound
     for (int s0 = 0; s0 < A.seqs; s0 += 64) {
       load(A, s0 + lane);
       total += __builtin_amdgcn_readlane(incl, 63);
       units += __builtin_amdgcn_readlane(scan(seq.units), 63);
+      rows += __builtin_amdgcn_readlane(scan(seq.n), 63);
       most = fmaxf(most, count ? (float)seq.pages : 0.0f);
     }
     longest = (int)tqdev::wave_max64(most);
+    // sequences that overlap (cu_rows out of order) could make the list longer
+    // than 32 bits count: nothing is done
+    if (rows > A.rows) total = units = 0;
   }
   // all units' pieces of `p` pages at most
   __device__ __forceinline__ void cut(const AttnArgs &A, int p) {
@@ -563,6 +568,7 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
     const int wgs = gridDim.x;
     const int even = (int)((uint32_t)(list.total + wgs - 1) / (uint32_t)wgs);
     per = max(max(even, kLeast), (list.longest + kDecPieces - 1) / kDecPieces);
+    if (list.total <= 0) return;
     equal = list.units <= wgs;
     if (equal) {
       for (list.cut(A, per); list.total > wgs; list.cut(A, per)) per += max(per / 8, 1);

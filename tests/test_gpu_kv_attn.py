@@ -170,6 +170,55 @@ def test_holes_and_lengths_beyond_the_table():
         _check(d, _run(d, 100, 3), 100, 3)
 
 
+def test_rows_out_of_order_touch_nothing_else():
+    """cu_rows that is not ascending, or points outside: whatever the rows get,
+    the workspace is left zero and a following call is right."""
+    import ternary_weight_base_amd as tq
+    say("attention with bad cu_rows")
+    rng = np.random.default_rng(75)
+    for lens in ([(1, 2000), (2, 300), (1, 64)], [(70, 400), (33, 290), (1, 1)], [(1, 90)] * 3):
+        d = _inputs(rng, 4, 2, 128, lens)
+        rows = d["q"].shape[0]
+        ws = torch.zeros(tq.tq_kv_attn_workspace_bytes(rows, 3, 4, 2, 128, int(d["kv"].max())) // 4 + 4, dtype=torch.int32, device="cuda")
+        good = _run(d, ws=ws)
+        for cu in ([0, rows, 0, rows], [5, -3, rows + 9, 1 << 30], [rows, 1, 1, 0], [-1 << 30, rows, rows, rows], [1, 1, 1, 1]):
+            _run({**d, "cu": np.array(cu, np.int32)}, ws=ws)
+        assert np.array_equal(_run(d, ws=ws).view(np.uint16), good.view(np.uint16))
+
+
+def test_cache_beyond_32_bits():
+    """Pages whose bytes lie past 4 GiB in each cache, appended to and read."""
+    import ternary_weight_base_amd as tq
+    say("cache of more than 4 GiB")
+    rng = np.random.default_rng(77)
+    pages, hkv, dim, hq = 66000, 8, 128, 8
+    k, v = (torch.empty((pages, hkv) + s, dtype=torch.uint8, device="cuda") for s in ((PAGE, dim), (dim, PAGE)))
+    assert k.numel() > 1 << 32
+    ks, vs = torch.empty((pages, hkv), device="cuda"), torch.empty((pages, hkv), device="cuda")
+    for n in (1, 150):
+        used = pages - 1 - rng.permutation(400)[:3]
+        lens = np.array([n], np.int32)
+        table = np.full((1, 3), -1, np.int32)
+        table[0, :-(-n // PAGE)] = used[:-(-n // PAGE)]
+        x = rng.standard_normal((n, (hq + 2 * hkv) * dim)).astype(np.float32)
+        q, out = (torch.empty((n, hq, dim), dtype=torch.float16, device="cuda") for _ in range(2))
+        cu = dev(np.array([0, n], np.int32))
+        tq.tq_kv_append(dev(x), None, cu, dev(lens), dev(table), k, v, ks, vs, q)
+        tq.tq_kv_attn(q, cu, dev(lens), dev(table), k, v, ks, vs, out, n, ws=tq.kv_attn_workspace(n, 1, hq, hkv, dim, n))
+        ids = torch.from_numpy(used.astype(np.int64)).cuda()
+        small = np.array([[0, 1, 2]], np.int32)
+        d = {"q": q.cpu().numpy(), "cu": np.array([0, n]), "kv": lens, "table": small, "k": k[ids].cpu().numpy(), "v": v[ids].cpu().numpy(),
+             "ks": ks[ids].cpu().numpy(), "vs": vs[ids].cpu().numpy()}
+        assert np.array_equal(d["q"], x[:, :hq * dim].reshape(n, hq, dim).astype(np.float16))
+        for name, xs, c, s in (("k", x[:, hq * dim:(hq + hkv) * dim], d["k"], d["ks"]), ("v", x[:, (hq + hkv) * dim:], d["v"].transpose(0, 1, 3, 2), d["vs"])):
+            got = ((c.astype(np.float64) - 127.5) * s[:, :, None, None]).transpose(0, 2, 1, 3).reshape(3 * PAGE, hkv, dim)[:n]
+            half = np.repeat(s, PAGE, 0)[:n, :, None] / 2
+            assert np.all(np.abs(got - xs.reshape(n, hkv, dim)) <= half), name
+        _check(d, out.cpu().numpy())
+    del k, v
+    torch.cuda.empty_cache()
+
+
 def test_sharp_scores_and_large_queries():
     """A softmax that picks one key, and scores that grow along the keys (the
     running maximum moves in every tile)."""
