@@ -360,15 +360,26 @@ def tq_rope_table(positions: int, rot: int, base: float) -> np.ndarray:
     return t
 
 
-def _act_dtype(t) -> int:
-    """TQ_F16 / TQ_F32 of a tensor's type, -1 for another."""
-    import torch
-    return TQ_F32 if t.dtype is torch.float32 else TQ_F16 if t.dtype is torch.float16 else -1
+class _Torch:
+    """What the calls below take from torch, looked up once: a decode step
+    makes these calls by the hundred, and the host's time is theirs."""
+    f16 = None
+
+    @classmethod
+    def get(cls):
+        if cls.f16 is None:
+            import torch
+            cls.f32, cls.i32, cls.u8, cls.i8 = torch.float32, torch.int32, torch.uint8, torch.int8
+            cls.acts = {torch.float16: TQ_F16, torch.float32: TQ_F32}
+            cls.device = torch.cuda.current_device
+            # the stream's handle without a Stream object, where torch has it
+            cls.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+            cls.f16 = torch.float16
+        return cls
 
 
 def _bad(what, name, t, dtype, shape, dev):
-    """The error that a tensor's check found (the checks themselves stand in
-    one line each below: a decode step makes these calls by the hundred)."""
+    """The error that a tensor's check found."""
     if t.dtype is not dtype:
         return ValueError(f"{what}: {name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
@@ -391,41 +402,36 @@ def _rows_need(what, name, t, dtype, shape, dev):
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
         raise _bad(what, name, t, dtype, shape, dev)
     if t.is_contiguous():
-        n = 1
-        for d in shape[1:]:
-            n *= d
-        return t.data_ptr(), n
+        n = shape[1]
+        return t.data_ptr(), n if len(shape) == 2 else n * shape[2]
     if not t[0].is_contiguous():
         raise ValueError(f"{what}: {name} must be contiguous within a row")
     return t.data_ptr(), t.stride(0)
 
 
-def _cache_need(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev):
-    """Checks the cache's tensors; -> ((seqs, pages of the table's rows, pages, heads, dim), their addresses)."""
-    import torch
-    i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+def _cache_need(what, T, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev):
+    """Checks the cache's tensors; -> (seqs, kv_heads, head_dim, their arguments in the library's order)."""
+    i32, f32 = T.i32, T.f32
     if k_cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError(f"{what}: k_cache must have shape [pages][kv_heads][{KV_PAGE}][head_dim], page_table two dimensions")
     pages, heads, _, dim = k_cache.shape
     seqs, width = page_table.shape
-    return ((seqs, width, pages, heads, dim),
-            (_need(what, "cu_rows", cu_rows, i32, (seqs + 1,), dev), _need(what, "kv_len", kv_len, i32, (seqs,), dev),
-             _need(what, "page_table", page_table, i32, (seqs, width), dev), width,
-             _need(what, "k_cache", k_cache, u8, (pages, heads, KV_PAGE, dim), dev),
-             _need(what, "v_cache", v_cache, u8, (pages, heads, dim, KV_PAGE), dev),
-             _need(what, "k_scale", k_scale, f32, (pages, heads), dev), _need(what, "v_scale", v_scale, f32, (pages, heads), dev),
-             pages))
+    per = (pages, heads)
+    return seqs, heads, dim, (
+        _need(what, "cu_rows", cu_rows, i32, (seqs + 1,), dev), _need(what, "kv_len", kv_len, i32, (seqs,), dev),
+        _need(what, "page_table", page_table, i32, (seqs, width), dev), width,
+        _need(what, "k_cache", k_cache, T.u8, (pages, heads, KV_PAGE, dim), dev),
+        _need(what, "v_cache", v_cache, T.u8, (pages, heads, dim, KV_PAGE), dev),
+        _need(what, "k_scale", k_scale, f32, per, dev), _need(what, "v_scale", v_scale, f32, per, dev), pages)
 
 
-def _current(stream, t):
+def _current(T, stream, t):
     """(index of the current GPU, the call's stream as an integer) for a call on t and others."""
     if t.get_device() < 0:
         return -1, 0  # the checks still run; the library reports that there is no GPU memory
-    import torch
-    dev = torch.cuda.current_device()
+    dev = T.device()
     if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without making a Stream object
-        return dev, raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
+        return dev, T.stream(dev)
     return dev, stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -435,25 +441,27 @@ def tq_kv_append(qkv, rope, cu_rows, kv_len, page_table, k_cache, v_cache, k_sca
     fp32; rows may be strided) to the paged cache, rotating keys and queries
     by rope [positions][2][rot/2] (fp32, as tq_rope_table; None: no rotation);
     the rotated queries go to q_out fp16 [rows][q_heads][head_dim]."""
-    import torch
-    what = "tq_kv_append"
-    dev, st = _current(stream, k_cache)
-    (seqs, _, _, heads, dim), cache = _cache_need(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev)
+    what, T = "tq_kv_append", _Torch.get()
+    dev, st = _current(T, stream, k_cache)
+    seqs, heads, dim, cache = _cache_need(what, T, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev)
     if qkv.dim() != 2:
         raise ValueError(f"{what}: qkv must have two dimensions")
     rows, width = qkv.shape
     if q_heads is None:
         q_heads = width // dim - 2 * heads
     x, stride = _rows_need(what, "qkv", qkv, qkv.dtype, (rows, (q_heads + 2 * heads) * dim), dev)
-    q = None if q_out is None else _need(what, "q_out", q_out, torch.float16, (rows, q_heads, dim), dev)
+    q = None if q_out is None else _need(what, "q_out", q_out, T.f16, (rows, q_heads, dim), dev)
     r, rope_rows, rot = None, 0, 0
     if rope is not None:
         if rope.dim() != 3:
             raise ValueError(f"{what}: rope must have shape [positions][2][rot/2]")
-        rope_rows, rot = rope.shape[0], 2 * rope.shape[2]
-        r = _need(what, "rope", rope, torch.float32, (rope_rows, 2, rot // 2), dev)
-    _check(lib.tq_kv_append(_act_dtype(qkv), rows, seqs, q_heads, heads, dim, x, stride, r, rope_rows, rot, rope_mode,
-                            *cache, q, st), what)
+        rope_rows, _, half = rope.shape
+        rot = 2 * half
+        r = _need(what, "rope", rope, T.f32, (rope_rows, 2, half), dev)
+    rc = lib.tq_kv_append(T.acts.get(qkv.dtype, -1), rows, seqs, q_heads, heads, dim, x, stride, r, rope_rows, rot, rope_mode,
+                          *cache, q, st)
+    if rc:
+        raise TQError(rc, what)
 
 
 def tq_kv_attn_workspace_bytes(rows, seqs, q_heads, kv_heads, head_dim, max_kv_len) -> int:
@@ -473,22 +481,24 @@ def tq_kv_attn(q, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scal
     (rows may be strided).  max_kv_len: the largest kv_len (a host number).
     softmax_scale defaults to head_dim ** -0.5; window > 0 limits a row to its
     last `window` keys and the first `sinks` ones."""
-    import torch
-    what = "tq_kv_attn"
-    dev, st = _current(stream, k_cache)
-    (seqs, _, _, heads, dim), cache = _cache_need(what, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev)
+    what, T = "tq_kv_attn", _Torch.get()
+    dev, st = _current(T, stream, k_cache)
+    seqs, heads, dim, cache = _cache_need(what, T, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev)
     if q.dim() != 3:
         raise ValueError(f"{what}: q must have three dimensions")
     rows, q_heads, _ = q.shape
-    qp, qs = _rows_need(what, "q", q, torch.float16, (rows, q_heads, dim), dev)
-    op, os_ = _rows_need(what, "out", out, torch.float16, (rows, q_heads, dim), dev)
+    shape = (rows, q_heads, dim)
+    qp, qs = _rows_need(what, "q", q, T.f16, shape, dev)
+    op, os_ = _rows_need(what, "out", out, T.f16, shape, dev)
     wp, wb = None, 0
     if ws is not None:
         if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError(f"{what}: ws must be contiguous and on the current GPU")
         wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
-    _check(lib.tq_kv_attn(rows, seqs, q_heads, heads, dim, qp, qs, *cache, max_kv_len,
-                          dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, op, os_, wp, wb, st), what)
+    rc = lib.tq_kv_attn(rows, seqs, q_heads, heads, dim, qp, qs, *cache, max_kv_len,
+                        dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, op, os_, wp, wb, st)
+    if rc:
+        raise TQError(rc, what)
 
 
 def tq_residual_norm(y, res, res_out, pre_w=None, x=None, q=None, a_scale=None, post_w=None, gate=None,
@@ -496,47 +506,49 @@ def tq_residual_norm(y, res, res_out, pre_w=None, x=None, q=None, a_scale=None, 
     """res_out = res + res_scale * gate * norm(y; post_w); x (fp16 / fp32) and / or
     q, a_scale (int8, fp32 [M]) = norm(res_out; pre_w).  All [M][H]; gate [H] or
     [M][H] (rows may be strided); y None: norm(res) only."""
-    import torch
-    what = "tq_residual_norm"
-    dev, st = _current(stream, res)
+    what, T = "tq_residual_norm", _Torch.get()
+    dev, st = _current(T, stream, res)
     if res.dim() != 2:
         raise ValueError(f"{what}: res must have two dimensions")
-    shape = M, H = res.shape
-    f32 = torch.float32
-    yt = res.dtype if y is None else y.dtype
+    M, H = shape = res.shape
+    f32, row, rt = T.f32, (H,), res.dtype
+    yt = rt if y is None else y.dtype
     gp, gs = None, 0
     if gate is not None:
         if gate.dim() == 2:
             gp, gs = _rows_need(what, "gate", gate, yt, shape, dev)
         else:
-            gp = _need(what, "gate", gate, yt, (H,), dev)
-    _check(lib.tq_residual_norm(
-        TQ_F32 if y is None else _act_dtype(y), _act_dtype(res), TQ_F32 if x is None else _act_dtype(x), M, H,
+            gp = _need(what, "gate", gate, yt, row, dev)
+    rc = lib.tq_residual_norm(
+        TQ_F32 if y is None else T.acts.get(yt, -1), T.acts.get(rt, -1), TQ_F32 if x is None else T.acts.get(x.dtype, -1), M, H,
         None if y is None else _need(what, "y", y, yt, shape, dev),
-        None if post_w is None else _need(what, "post_w", post_w, f32, (H,), dev), gp, gs, res_scale,
-        _need(what, "res", res, res.dtype, shape, dev),
-        None if res_out is None else _need(what, "res_out", res_out, res.dtype, shape, dev),
-        None if pre_w is None else _need(what, "pre_w", pre_w, f32, (H,), dev), eps,
+        None if post_w is None else _need(what, "post_w", post_w, f32, row, dev), gp, gs, res_scale,
+        _need(what, "res", res, rt, shape, dev),
+        None if res_out is None else _need(what, "res_out", res_out, rt, shape, dev),
+        None if pre_w is None else _need(what, "pre_w", pre_w, f32, row, dev), eps,
         None if x is None else _need(what, "x", x, x.dtype, shape, dev),
-        None if q is None else _need(what, "q", q, torch.int8, shape, dev),
-        None if a_scale is None else _need(what, "a_scale", a_scale, f32, (M,), dev), st), what)
+        None if q is None else _need(what, "q", q, T.i8, shape, dev),
+        None if a_scale is None else _need(what, "a_scale", a_scale, f32, (M,), dev), st)
+    if rc:
+        raise TQError(rc, what)
 
 
 def tq_debug_kv_read(pages, k_cache, v_cache, k_scale, v_scale, values, stream=None) -> None:
     """values (fp16 / fp32 [2][n][kv_heads][64][head_dim]) of the cache pages named by pages (int32 [n])."""
-    import torch
-    what = "tq_debug_kv_read"
-    dev, st = _current(stream, k_cache)
+    what, T = "tq_debug_kv_read", _Torch.get()
+    dev, st = _current(T, stream, k_cache)
     if k_cache.dim() != 4 or pages.dim() != 1:
         raise ValueError(f"{what}: k_cache must have four dimensions, pages one")
     num, heads, _, dim = k_cache.shape
-    n, u8, f32 = pages.shape[0], torch.uint8, torch.float32
-    _check(lib.tq_debug_kv_read(
-        _act_dtype(values), n, heads, dim, _need(what, "pages", pages, torch.int32, (n,), dev),
-        _need(what, "k_cache", k_cache, u8, (num, heads, KV_PAGE, dim), dev),
-        _need(what, "v_cache", v_cache, u8, (num, heads, dim, KV_PAGE), dev),
-        _need(what, "k_scale", k_scale, f32, (num, heads), dev), _need(what, "v_scale", v_scale, f32, (num, heads), dev), num,
-        _need(what, "values", values, values.dtype, (2, n, heads, KV_PAGE, dim), dev), st), what)
+    n, per = pages.shape[0], (num, heads)
+    rc = lib.tq_debug_kv_read(
+        T.acts.get(values.dtype, -1), n, heads, dim, _need(what, "pages", pages, T.i32, (n,), dev),
+        _need(what, "k_cache", k_cache, T.u8, (num, heads, KV_PAGE, dim), dev),
+        _need(what, "v_cache", v_cache, T.u8, (num, heads, dim, KV_PAGE), dev),
+        _need(what, "k_scale", k_scale, T.f32, per, dev), _need(what, "v_scale", v_scale, T.f32, per, dev), num,
+        _need(what, "values", values, values.dtype, (2, n, heads, KV_PAGE, dim), dev), st)
+    if rc:
+        raise TQError(rc, what)
 
 
 def stack_timeouts(ws) -> int:
