@@ -371,7 +371,7 @@ class _Torch:
             import torch
             cls.f32, cls.i32, cls.u8, cls.i8 = torch.float32, torch.int32, torch.uint8, torch.int8
             cls.acts = {torch.float16: TQ_F16, torch.float32: TQ_F32}
-            cls.device = torch.cuda.current_device
+            cls.device, cls.available = torch.cuda.current_device, torch.cuda.is_available
             # the stream's handle without a Stream object, where torch has it
             cls.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
             cls.f16 = torch.float16
@@ -427,9 +427,9 @@ def _cache_need(what, T, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale,
 
 def _current(T, stream, t):
     """(index of the current GPU, the call's stream as an integer) for a call on t and others."""
-    if t.get_device() < 0:
-        return -1, 0  # the checks still run; the library reports that there is no GPU memory
-    dev = T.device()
+    if t.get_device() < 0 and not T.available():
+        return -1, 0  # nothing can run: the checks do, and the library reports the launch
+    dev = T.device()  # (host memory is refused against it: a kernel must not be given its address)
     if stream is None:
         return dev, T.stream(dev)
     return dev, stream if isinstance(stream, int) else stream.cuda_stream

@@ -132,6 +132,30 @@ def test_binding_refuses_wrong_tensors():
             tq.tq_residual_norm(**{**dict(y=r, res=r, res_out=r), **bad})
 
 
+def test_binding_refuses_host_memory_where_there_is_a_gpu(monkeypatch):
+    """Before any call into the library: a kernel given a host address would fault."""
+    torch = pytest.importorskip("torch")
+    T = tq._Torch.get()
+    monkeypatch.setattr(T, "available", lambda: True)
+    monkeypatch.setattr(T, "device", lambda: 0)
+    monkeypatch.setattr(T, "stream", lambda d: 0)
+
+    def called(*a):
+        raise AssertionError("the library was called")
+    monkeypatch.setattr(tq, "lib", type("Lib", (), dict.fromkeys(("tq_kv_append", "tq_kv_attn", "tq_residual_norm", "tq_debug_kv_read"),
+                                                                 staticmethod(called))))
+    i32 = torch.int32
+    k, v = torch.zeros((3, 2, 64, 128), dtype=torch.uint8), torch.zeros((3, 2, 128, 64), dtype=torch.uint8)
+    s, cu, kv, tb = torch.zeros((3, 2)), torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros((2, 4), dtype=i32)
+    q, r = torch.zeros((4, 8, 128), dtype=torch.float16), torch.zeros((2, 640))
+    for call in (lambda: tq.tq_kv_append(torch.zeros((4, 12 * 128)), None, cu, kv, tb, k, v, s, s, q),
+                 lambda: tq.tq_kv_attn(q, cu, kv, tb, k, v, s, s, q, 64),
+                 lambda: tq.tq_residual_norm(r, r, r, x=r),
+                 lambda: tq.tq_debug_kv_read(kv, k, v, s, s, torch.zeros((2, 2, 2, 64, 128)))):
+        with pytest.raises(ValueError, match="current GPU"):
+            call()
+
+
 def test_references():
     """The references on cases worked by hand."""
     assert [scale_for(m) for m in (0.0, 1.0, 127.9, 128.0, 2.0 ** -130)] == [0.0, 2.0 ** -6, 1.0, 2.0, 2.0 ** -126]
