@@ -425,8 +425,10 @@ int tq_gemm(int fmt, int64_t M, int64_t N, int64_t K, const void *W, const int8_
  * seen, and a query row at such a position is written as zeros by
  * tq_kv_append.
  *
- * Heads: head_dim 64 or 128 (else TQ_ERR_SHAPE), q_heads a multiple of
- * kv_heads, rows * q_heads below 2^30; query head h reads KV head h / (q_heads / kv_heads). */
+ * Heads: head_dim 64 or 128, q_heads a multiple of kv_heads; 1 <= rows <= 2^24,
+ * rows * q_heads below 2^30, and a call's workgroups few enough for one launch
+ * (below 2^32 threads); else TQ_ERR_SHAPE.  Query head h reads KV head
+ * h / (q_heads / kv_heads). */
 
 /* Host: table[positions][rot] of fp32, cos(p base^(-2i/rot)) for i < rot / 2,
  * then the sines, from angles in double.  rot a multiple of 8, 8..128;
@@ -499,7 +501,8 @@ int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
  * multiple of 4 when H is).  y, res and outputs [M][H] contiguous, y and
  * gate of y_dtype, res and res_out of res_dtype; post_w, pre_w fp32 [H].
  * res_out may be res, and may be NULL when y is (else TQ_ERR_NULL, as is
- * post_w or gate without y, or no output at all).  1 <= H <= 32768, any M.
+ * post_w or gate without y, or no output at all).  1 <= H <= 32768,
+ * 1 <= M < 2^22.
  * eps >= 0 (TQ_ERR_VALUE).  All arrays 16-byte aligned, a_scale 4-byte. */
 int tq_residual_norm(int y_dtype, int res_dtype, int x_dtype, int64_t M, int64_t H, const void *y,
                      const float *post_w, const void *gate, int64_t gate_stride, double res_scale,

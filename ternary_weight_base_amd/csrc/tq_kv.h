@@ -72,4 +72,7 @@ inline int shape_check(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_h
   return TQ_OK;
 }
 
+// A launch counts its threads in 32 bits.
+inline bool grid_ok(int64_t wgs, int64_t threads) { return wgs <= 0xffffffffll / threads; }
+
 }  // namespace tqkv

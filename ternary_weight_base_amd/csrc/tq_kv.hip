@@ -472,7 +472,7 @@ extern "C" int tq_kv_append(int dtype, int64_t rows, int64_t seqs, int64_t q_hea
   const int64_t per_wg = few ? 64 : 4 * kThreads;
   A.q_chunks = (int)((q_heads * head_dim / 8 + per_wg - 1) / per_wg);
   const int64_t page_wgs = (A.by_row ? rows : slots) * kv_heads * 2, wgs = page_wgs + (q_out ? rows * A.q_chunks : 0);
-  if (wgs > 0x7fffffff) return TQ_ERR_SHAPE;
+  if (!grid_ok(wgs, few ? 64 : kThreads)) return TQ_ERR_SHAPE;
   A.page_wgs = (int)page_wgs;
   const dim3 grid((unsigned)wgs), block(few ? 64 : kThreads);
   hipStream_t st = (hipStream_t)stream;
@@ -497,7 +497,7 @@ extern "C" int tq_debug_kv_read(int dtype, int64_t n, int64_t kv_heads, int64_t 
   if (dtype != TQ_F16 && dtype != TQ_F32) return TQ_ERR_DTYPE;
   const int rc = shape_check(n, 1, kv_heads, kv_heads, head_dim, 1, num_pages);
   if (rc != TQ_OK) return rc;
-  if (n * kv_heads > ((int64_t)1 << 29)) return TQ_ERR_SHAPE;
+  if (!grid_ok(2 * n * kv_heads, kThreads)) return TQ_ERR_SHAPE;
   if (!aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(k_scale, 4) || !aligned_to(v_scale, 4) ||
       !aligned_to(pages, 4) || !aligned_to(values, 16))
     return TQ_ERR_ALIGN;

@@ -254,7 +254,8 @@ extern "C" int tq_residual_norm(int y_dtype, int res_dtype, int x_dtype, int64_t
   if (!res || (q && !a_scale) || (!x && !q && !res_out) || (y && !res_out) || (!y && (post_w || gate)))
     return TQ_ERR_NULL;
   if (!is_act(res_dtype) || (y && !is_act(y_dtype)) || (x && !is_act(x_dtype))) return TQ_ERR_DTYPE;
-  if (M < 1 || M > ((int64_t)1 << 30) || H < 1 || H > 32768 ||
+  // a launch counts its threads, up to 1024 a row, in 32 bits
+  if (M < 1 || M >= ((int64_t)1 << 22) || H < 1 || H > 32768 ||
       (gate && gate_stride != 0 && (gate_stride < H || gate_stride > ((int64_t)1 << 31) || (H % 4 == 0 && gate_stride % 4 != 0))))
     return TQ_ERR_SHAPE;
   if (!(eps >= 0.0) || !(eps < 1e30) || !(res_scale > -1e30 && res_scale < 1e30)) return TQ_ERR_VALUE;

@@ -108,6 +108,14 @@ def test_kv_read_validates_on_host():
         assert f(**{name: ODD}) == ALIGN, name
 
 
+def test_more_threads_than_a_launch_counts():
+    assert _append(rows=(1 << 24) - 1, seqs=1) == SHAPE      # a workgroup of 256 threads a row
+    assert _append(rows=(1 << 24) - 1, seqs=1 << 20, hq=32, hkv=32, stride=96 * 128) == SHAPE
+    assert _attn(rows=1 << 20, seqs=1 << 20, hq=64, hkv=64, qs=8192, os=8192) == SHAPE  # a workgroup of 256 a row and head
+    assert _norm(m=1 << 22) == SHAPE
+    assert L.tq_debug_kv_read(0, 1 << 20, 8, 128, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 21, FAKE, None) == SHAPE
+
+
 def test_binding_refuses_wrong_tensors():
     torch = pytest.importorskip("torch")
     if torch.cuda.is_available():
