@@ -473,8 +473,10 @@ size_t tq_kv_attn_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, i
  * window or j < sinks (the first tokens, visible from everywhere).  A row
  * that sees no key gives zeros.  q and out fp16, rows q_stride and
  * out_stride elements apart (multiples of 8), 16-byte aligned; out may be
- * q itself (same stride).  Scales of the cache may be any finite
- * non-negative fp32.  Sums, maxima and outputs are held in fp32.
+ * q itself (same stride).  Scales of the cache need not be powers of two;
+ * value scales up to 2^50 (values below 2^-33 in a page are worth nothing to
+ * an fp16 output and may be dropped), key scales that keep the scores finite
+ * in fp32.  Sums, maxima and outputs are held in fp32.
  * max_kv_len: the largest kv_len of the call, which sets how the keys are
  * split over workgroups (a larger kv_len gives the same results more
  * slowly).  softmax_scale > 0 and finite, window and sinks >= 0

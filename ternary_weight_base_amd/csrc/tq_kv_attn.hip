@@ -166,6 +166,12 @@ __device__ __forceinline__ void load_values(const AttnArgs &A, int h, int id, Ra
   for (int i = 0; i < D / 16; i++) t.v[i] = tqdev::ld_stream16(vp + 16 * i * kPage);
 }
 
+// A page with a smaller value scale counts as zeros: its values are below
+// 2^-33, nothing to an fp16 output (half its least step is 2^-25).  So the
+// state's unit (below) never falls by more than the largest scale's 2^50 over
+// this, and 2^90 times what the products can sum up to stays within fp32.
+constexpr float kLeastScale = 0x1p-40f;
+
 // Running state of a lane's query row.  The output is held as
 //   unit * (o + corr / 2), corr = sum of the weights that o's products took,
 // where `unit` (one for the wave) is a value scale: pages whose scale is
@@ -709,11 +715,11 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
       if (ks >= 0.0f) {  // wave-uniform, as all of this page's scales
         // a page of zeros has scale 0: its (zero) scores stay finite, masked ones -inf
         const float sc = fmaxf(ks * A.scale_log2, 1e-37f);
-        const bool has_v = vs > 0.0f;  // a page of zeros adds to the sum only
+        const bool has_v = vs >= kLeastScale;  // a page of zeros adds to the sum only
         const float over = has_v ? __builtin_amdgcn_logf(vs) - unit : 0.0f;
         const bool far = !(fabsf(over) < 4.0f);
         const float shift = far ? 0.0f : over;
-        const float moves = far ? fminf(__builtin_amdgcn_exp2f(-over), 3.0e38f) : 1.0f;
+        const float moves = far ? __builtin_amdgcn_exp2f(-over) : 1.0f;
         if (far) unit += over;
         h8 hi16[RT][2], lo16[RT][2];
 #pragma unroll
@@ -853,7 +859,7 @@ __device__ __forceinline__ void put_keys(const Half<D, NT> &t, Lds<D> &l) {
     d[1] = codes8(t.r[i].z, t.r[i].w);
   }
 }
-// (live: the page's scale is not 0; else its bytes, whatever they are, stand for zeros)
+// (live: the page's scale counts; else its bytes, whatever they are, stand for zeros)
 template <int D, int NT>
 __device__ __forceinline__ void put_values(const Half<D, NT> &t, bool live, Lds<D> &l) {
   const uint32_t zero = 0x80808080u;
@@ -897,9 +903,10 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
     qf[j] = x;
   }
   qsum = 0.5f * half_sum(qsum);
-  // the wave's own rows: positions wmin .. wmax (none: wmax = -1)
+  // the wave's own rows: positions wmin .. wmax (none: wmax = -1); not below 0,
+  // from where a window of 2^31 - 1 could not be taken off
   const int r0 = wave * kWaveRows, r1 = min(r0 + kWaveRows, P.nrows) - 1;
-  const int wmin = P.p0 + (uint32_t)(P.f0 + r0) / (uint32_t)A.group;
+  const int wmin = max(P.p0 + (int)((uint32_t)(P.f0 + r0) / (uint32_t)A.group), 0);
   const int wmax = r1 < r0 ? -1 : P.p0 + (int)((uint32_t)(P.f0 + r1) / (uint32_t)A.group);
 
   f16x o[D / 32];
@@ -925,7 +932,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
     const float ks = A.ks[ph], vs = A.vs[ph];
     t.there = t.there && ks >= 0.0f;
     t.sc = fmaxf(ks * A.scale_log2, 1e-37f);
-    t.live = vs > 0.0f;
+    t.live = vs >= kLeastScale;
     t.lv = __builtin_amdgcn_logf(vs);
     return t;
   };
@@ -964,7 +971,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
       m = mn;
       l *= alpha;
       if (far) {
-        alpha *= fminf(__builtin_amdgcn_exp2f(-over), 3.0e38f);
+        alpha *= __builtin_amdgcn_exp2f(-over);
         unit += over;
       }
       corr *= alpha;

@@ -134,6 +134,21 @@ def test_scales_apart_and_zero_pages():
         _check(d, _run(d))
 
 
+def test_value_scales_from_one_end_to_the_other():
+    """Pages whose values are below all that fp16 holds, before, behind and
+    between pages of large ones (dropped, they are worth less than 2^-33)."""
+    say("attention value scales 2^-126 .. 2^8")
+    rng = np.random.default_rng(53)
+    for lens in ([(1, 900)], [(1, 9000)], [(5, 1500)], [(60, 900)]):
+        d = _inputs(rng, 4, 1, 128, lens)
+        ids = d["table"][0, :-(-lens[0][1] // PAGE)]
+        place = np.arange(len(ids))
+        for small in (place * 2 >= len(ids), place * 2 < len(ids), place % 16 < 8, place % 2 == 0, place >= 0):
+            for tiny in (2.0 ** -110, 2.0 ** -126):
+                d["vs"][ids, 0] = np.where(small, tiny, 2.0 ** 8)
+                _check(d, _run(d))
+
+
 def test_unused_places_do_not_matter():
     """NaN and infinite scales in pages that no sequence holds, and other
     bytes behind the last token: the same output bits."""
@@ -184,6 +199,16 @@ def test_rows_out_of_order_touch_nothing_else():
         for cu in ([0, rows, 0, rows], [5, -3, rows + 9, 1 << 30], [rows, 1, 1, 0], [-1 << 30, rows, rows, rows], [1, 1, 1, 1]):
             _run({**d, "cu": np.array(cu, np.int32)}, ws=ws)
         assert np.array_equal(_run(d, ws=ws).view(np.uint16), good.view(np.uint16))
+
+
+def test_largest_window_and_rows_before_the_start():
+    """A window and sinks as large as their type holds, with rows at negative positions."""
+    say("attention largest window")
+    rng = np.random.default_rng(76)
+    for lens in ([(80, 60), (3, 2)], [(3, 2), (1, 40)], [(200, 190)]):
+        d = _inputs(rng, 4, 1, 64, lens)
+        for window, sinks in ((0x7fffffff, 0), (0x7fffffff, 0x7fffff00), (0x7ffffff0, 1)):
+            _check(d, _run(d, window, sinks), window, sinks)
 
 
 def test_cache_beyond_32_bits():
