@@ -449,12 +449,12 @@ int tq_rope_table(int64_t positions, int64_t rot, double base, float *table);
  * a larger scale the page's earlier codes are shifted to it, so the cache
  * holds the same bytes however its tokens were cut into calls.  Bytes of
  * slots behind the sequence's last token keep what they held.
- * Two sequences of a call must not append to the same page (its contents
- * are then unspecified); full pages may be shared.  A token at a page's
+ * Two sequences of a call, or two places of one, must not append to the same
+ * page (its contents are then unspecified); full pages may be shared.  A token at a page's
  * start begins the page anew: rewriting a sequence from such a position (or,
  * with the page's scale kept at least as large, from any) is allowed.
  * Non-finite keys or values leave that page and head unspecified.  qkv,
- * rope, the caches and q_out 16-byte aligned. */
+ * rope, the caches and q_out 16-byte aligned; q_out does not overlap qkv. */
 int tq_kv_append(int dtype, int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
                  int64_t head_dim, const void *qkv, int64_t row_stride, const float *rope,
                  int64_t rope_rows, int64_t rot, int rope_mode, const int32_t *cu_rows,
@@ -498,10 +498,12 @@ int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
  * x (x_dtype TQ_F16 or TQ_F32), and q, a_scale: fp32 x quantised per row by
  * a = max |x| to a_scale = a / 127 and q = clamp(rint(x * (127 * (1 / a))),
  * -127, 127), zeros for a = 0 (tq_quant_act but for the reciprocal: its code
- * is the same or, for x at a rounding border, one step away).  gate (y_dtype; NULL: ones) has one row of H values
- * for all rows (gate_stride 0) or rows gate_stride >= H elements apart (a
- * multiple of 4 when H is).  y, res and outputs [M][H] contiguous, y and
- * gate of y_dtype, res and res_out of res_dtype; post_w, pre_w fp32 [H].
+ * is the same or, for x at a rounding border, one step away; for a < 2^-100
+ * both are moved up by 2^100 first).  Codes of a row that is not finite are
+ * unspecified.  gate (y_dtype; NULL: ones) has one row of H values for all
+ * rows (gate_stride 0) or rows gate_stride >= H elements apart (a multiple of
+ * 4 when H is).  y, res and outputs [M][H] contiguous, y and gate of y_dtype,
+ * res and res_out of res_dtype; post_w, pre_w fp32 [H].
  * res_out may be res, and may be NULL when y is (else TQ_ERR_NULL, as is
  * post_w or gate without y, or no output at all).  1 <= H <= 32768,
  * 1 <= M < 2^22.

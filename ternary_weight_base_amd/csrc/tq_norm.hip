@@ -189,7 +189,10 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(const NormArgs A) {
 #pragma unroll
   for (int w = 0; w < NT / 64; w++) amax = fmaxf(amax, wmax[w]);
   const bool zero = amax == 0.0f;
-  const float qi = zero ? 0.0f : 127.0f * (1.0f / amax);  // two IEEE roundings
+  // a maximum whose reciprocal would overflow is moved up first, and so are
+  // the values (exact: powers of two)
+  const float up = amax < 0x1p-100f ? 0x1p100f : 1.0f;
+  const float qi = zero ? 0.0f : 127.0f * (1.0f / (amax * up));  // two IEEE roundings
   int8_t *q = A.q + row * H;
 #pragma unroll
   for (int i = 0; i < ITEMS; i++) {
@@ -198,7 +201,7 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(const NormArgs A) {
       uint32_t pk = 0;
 #pragma unroll
       for (int j = 0; j < V; j++) {
-        const float t = fminf(fmaxf(rintf(r[i][j] * qi), -127.0f), 127.0f);
+        const float t = fminf(fmaxf(rintf(r[i][j] * up * qi), -127.0f), 127.0f);
         pk |= (uint32_t)(uint8_t)(int8_t)(zero ? 0 : (int)t) << (8 * j);
       }
       if constexpr (V == 4)

@@ -157,3 +157,27 @@ def test_graph_replay():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(x, want[0]) and torch.equal(out, want[1])
+
+
+@pytest.mark.parametrize("M,H", [(3, 256), (2, 1001), (300, 2048)])
+def test_smallest_values(M, H):
+    """Rows whose largest element's reciprocal is past fp32, zeros among them."""
+    import ternary_weight_base_amd as tq
+    say(f"norm of tiny rows {M}x{H}")
+    rng = np.random.default_rng(M)
+    top = (2.0 ** rng.integers(-148, -95, (M, 1)))
+    res = (rng.uniform(-1, 1, (M, H)) * top).astype(np.float32)
+    res[:, ::5] = 0
+    res[:, 1] = top[:, 0]
+    x, q, a = torch.empty((M, H), device="cuda"), torch.empty((M, H), dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    tq.tq_residual_norm(None, dev(res), None, x=x, q=q, a_scale=a, eps=1.0)
+    got = x.cpu().numpy()
+    assert np.array_equal(got, res)  # rms = 1 but for 2^-190
+    up = got * np.float32(2.0 ** 100)
+    inv = np.float32(127) * (np.float32(1) / np.abs(up).max(1))
+    big = np.abs(got).max(1) >= 2.0 ** -100
+    inv[big] = np.float32(127) * (np.float32(1) / np.abs(got[big]).max(1))
+    up[big] = got[big]
+    want = np.clip(np.rint(up * inv[:, None]), -127, 127).astype(np.int8)
+    assert np.array_equal(q.cpu().numpy(), want) and np.all(want[:, ::5] == 0)
+    assert np.array_equal(a.cpu().numpy(), np.abs(got).max(1) / np.float32(127))
