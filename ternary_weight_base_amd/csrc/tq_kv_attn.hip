@@ -277,19 +277,23 @@ __device__ __forceinline__ float inverse(float l) { return l > 0.0f || l != l ? 
 // for the next call, whatever its shape.
 template <int R, int D, int NT, int MAXP, typename At, typename Out>
 __device__ __forceinline__ void join(int tid, Rsrc part, int pieces, int nrows, float *lds, const At &at, const Out &out) {
-  // 8 loads of 16 bytes in flight a thread: of 8 pieces, or (many rows, few
-  // pieces) of 2 pieces for each of 4 outputs
-  constexpr int kPer16 = (MAXP + 15) / 16, kQ = R > 32 ? 4 : 1, kBatch = 8 / kQ;
+  // loads of 16 bytes in flight a thread: of 8 pieces (32 rows: for each of two
+  // outputs), or (many rows, few pieces) of 2 pieces for each of 4 outputs
+  constexpr int kPer16 = (MAXP + 15) / 16, kQ = R > 32 ? 4 : R > 16 ? 2 : 1, kBatch = R > 32 ? 2 : 8;
   const int quads = nrows * (D / 4);
   const int parts = quads * 4 <= NT ? 4 : quads * 2 <= NT ? 2 : 1;
   const int per = NT / parts, p = tid / per, q0 = tid - p * per;
   f4 v[kQ][kBatch];
   auto fetch = [&](int k0, int q) {
+    auto some = [&](int b0) {
 #pragma unroll
-    for (int a = 0; a < kQ; a++)
+      for (int a = 0; a < kQ; a++)
 #pragma unroll
-      for (int b = 0; b < kBatch; b++)
-        v[a][b] = load_dev(part, at(min(k0 + b * parts, pieces - 1)) + 4 * min(q + a * per, quads - 1));
+        for (int b = b0; b < b0 + kBatch / 2; b++)
+          v[a][b] = load_dev(part, at(min(k0 + b * parts, pieces - 1)) + 4 * min(q + a * per, quads - 1));
+    };
+    some(0);
+    if (pieces > kBatch / 2 * parts) some(kBatch / 2);
   };
   if (q0 < quads) fetch(p, q0);
   float *wt = lds;  // the pieces' weights, [MAXP][R]
