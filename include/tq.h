@@ -306,9 +306,9 @@ size_t tq_decode_stack_workspace_bytes(int fmt, int64_t layers, int64_t hidden, 
  *   y_out[l] = down . quant(h[l])
  * Every quant is tq_quant_act's per-row absmax int8 quantisation (done
  * inside the projection that consumes it, bit-exact with tq_quant_act);
- * every product is tq_gemv's.  x_in and a_in are the layer inputs that the
- * attention and normalisation steps (not part of this library) would
- * produce.  Outputs are fp32, [layers][N]; y_o, h and the workspace must be
+ * every product is tq_gemv's.  x_in and a_in stand for the layer inputs
+ * that the steps between the projections produce (tq_residual_norm,
+ * tq_kv_append and tq_kv_attn below; not part of this call).  Outputs are fp32, [layers][N]; y_o, h and the workspace must be
  * 16-byte aligned, hidden and inter multiples of 128.  The projections run
  * one after another, QKV, O, gate/up, down of layer 0, then layer 1, ...:
  * each starts on its input only once the one before it is complete, as the
