@@ -470,8 +470,11 @@ extern "C" int tq_kv_append(int dtype, int64_t rows, int64_t seqs, int64_t q_hea
   A.row_stride = row_stride; A.max_pages = max_pages; A.num_pages = num_pages; A.rope_rows = rope_rows;
   A.rows = (int)rows; A.seqs = (int)seqs; A.hq = (int)q_heads; A.hkv = (int)kv_heads; A.rot = (int)rot;
   A.pairs = rope_mode == TQ_ROPE_PAIRS;
-  // up to four rows a sequence: a row's worth of lanes has work in a wave, not in 256 threads
-  const bool few = rows <= 4 * seqs;
+  // a row's worth of lanes has work in a wave, not in 256 threads: one row a
+  // sequence (64 of them: 14.1 against 14.4 us with a read-back; 1: 7.05, 7.2), or a
+  // few in each of many (64 x 2: 15.2, 16.8; 64 x 4: 16.8, 17.5).  In fewer sequences
+  // the wave's second trip costs more (8 x 4: 8.35, 7.75; 32 x 4: 13.3, 12.1)
+  const bool few = rows <= seqs || (rows <= 4 * seqs && seqs >= 64);
   const int64_t slots = rows / kPage + 2 * seqs;
   A.by_row = rows < slots;
   const int64_t per_wg = few ? 64 : 4 * kThreads;
