@@ -58,7 +58,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 constexpr int kRows = 16;  // (token, query head) rows of a decode workgroup
 constexpr int kWaves = 8;  // of a decode workgroup
 constexpr int kDecPieces = 128;  // pieces of a unit at most (and one or two more)
-constexpr int kSnap = 4, kLeast = 8, kWhole = 16;  // pages: see "few rows"
+constexpr int kSnap = 4, kLeast = 4, kWhole = 16;  // pages: see "few rows"
 constexpr float kNone = -1e30f;  // running maximum before the first visible key
 
 struct AttnArgs {
@@ -1230,6 +1230,8 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
   }
 }
 
+constexpr int kCus = 256;
+
 // The launch of a call: which kernel, its workgroups, how the keys are split,
 // and the workspace that needs.
 struct Plan {
@@ -1241,12 +1243,20 @@ struct Plan {
   size_t counter_bytes, bytes;
 };
 
-constexpr int kCus = 256;
-
 Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_kv) {
   Plan P;
   const int64_t group = q_heads / kv_heads, flat = rows * group;
-  const bool prefill = flat > 32 * seqs;
+  // The decode kernel converts a page for each 32 rows, the prefill kernel for
+  // 128, but it starts and ends sooner and cuts the keys finer.  It takes up to 32
+  // rows a sequence, up to half a tile of 32 a CU (64 query and 8 KV heads, 16
+  // tokens on 600: 12.4 against 28.2 us, on 6001 25.0 against 56.5; 64 tokens on
+  // 30000 121 against 139), and up to a tile a CU with contexts of up to 12 K (96
+  // tokens on 12000 91 against 99 us, on 30000 211 against 148).  More is a second
+  // round of workgroups, which still pays on up to 1024 tokens (256 on 600 23 against
+  // 31 us; 180 on 4000 81 against 62); a third does not (64 sequences of 16 on 1000
+  // 98 against 58).  (The tiles as of sequences of the same length.)
+  const int64_t each = (flat + seqs - 1) / seqs, tiles32 = (each + 31) / 32 * seqs * kv_heads;
+  const bool prefill = each > 32 && tiles32 > (max_kv <= 1024 ? 2 * kCus : max_kv <= 12288 ? kCus : kCus / 2);
   const int R = prefill ? kTileRows : flat > kRows * seqs ? 2 * kRows : kRows;
   P.tile_rows = R;
   const int64_t tiles = (max_kv + kPage - 1) / kPage;
@@ -1292,7 +1302,7 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
   // one workgroup a CU: a second one's start and end cost more than its
   // waves bring (131001 tokens: 58 against 82 us with two a CU)
   P.whole = kWhole;
-  P.wgs = (units * tiles + kLeast - 1) / kLeast;
+  P.wgs = units * ((tiles + kLeast - 1) / kLeast);
   if (P.wgs > kCus) P.wgs = kCus;
   P.counter_bytes = ((size_t)P.wgs * 4 + 15) / 16 * 16;
   P.bytes = P.counter_bytes + (size_t)P.wgs * 2 * partial_floats(R, (int)head_dim) * 4;

@@ -34,7 +34,8 @@ def _run(d, window=0, sinks=0, scale=None, max_kv=None, ws=None, out=None):
     g = {k: dev(v) for k, v in d.items()}
     if out is None:
         out = torch.full((rows, hq, dim), float("nan"), dtype=torch.float16, device="cuda")
-    most = max_kv or max(1, int(d["kv"].max()))
+    # (a large max_kv_len: the kernel for many rows takes these sizes already)
+    most = max_kv or (20000 if rows > 1000 else max(1, int(d["kv"].max())))
     if ws is None:
         ws = tq.kv_attn_workspace(rows, len(d["kv"]), hq, d["ks"].shape[1], dim, most)
     tq.tq_kv_attn(g["q"], g["cu"], g["kv"], g["table"], g["k"], g["v"], g["ks"], g["vs"], out, most, softmax_scale=scale,
@@ -89,6 +90,35 @@ def test_attention(i):
     _check(d, _run(d, window, sinks), window, sinks)
 
 
+# as above, and max_kv_len: sizes that the kernel for many rows takes (more than
+# 128 tiles of 32 (token, query head) rows times KV heads, 256 for up to 12288 tokens, 512 for up to 1024)
+MANY = [
+    (8, 8, 128, [(520, 520)], 0, 0, 0, 20000),
+    (16, 16, 64, [(1100, 1100)], 0, 0, 0, None),
+    (8, 4, 64, [(700, 900), (0, 3), (333, 333)], 0, 0, 3, 20000),
+    (16, 2, 128, [(300, 500)], 77, 130, 0, 20000),
+    (40, 8, 128, [(131, 700)], 0, 0, 1, 20000),
+    (7, 1, 128, [(700, 790), (90, 2000), (0, 5), (12, 12)], 0, 0, 2, 20000),
+    (4, 2, 64, [(1400, 1000)], 1, 0, 0, 20000),             # rows before position 0, each row sees itself
+    (8, 8, 64, [(530, 600), (530, 20)], 2000, 5, 0, 20000),
+    (8, 8, 128, [(530, 900), (70, 130)], 200, 70, 3, 20000),
+    (32, 8, 128, [(300, 9001)], 0, 0, 0, None),             # keys in pieces
+    (24, 4, 64, [(260, 7000), (400, 4001)], 0, 0, 5, None),
+    (32, 8, 128, [(300, 5000), (10, 70)], 3001, 64, 0, None),
+    (4, 1, 128, [(4100, 4160)], 64, 4, 0, 20000),
+]
+
+
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_many_rows(i):
+    hq, hkv, dim, lens, window, sinks, pad, most = MANY[i]
+    say(f"attention of many rows, case {i}: {MANY[i]}")
+    d = _inputs(np.random.default_rng(300 + i), hq, hkv, dim, lens, pad)
+    got = _run(d, window, sinks, max_kv=most)
+    _check(d, got, window, sinks)
+    assert np.array_equal(got.view(np.uint16), _run(d, window, sinks, max_kv=most).view(np.uint16))
+
+
 @pytest.mark.parametrize("rows", [1, 3, 40])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_split_keys(rows, dim):
@@ -122,7 +152,7 @@ def test_scales_apart_and_zero_pages():
     """Value scales of neighbouring pages far apart, pages of zeros (scale 0), any positive scale."""
     say("attention scales")
     rng = np.random.default_rng(51)
-    for lens in ([(1, 600), (2, 64)], [(60, 640)]):
+    for lens in ([(1, 600), (2, 64)], [(60, 640)], [(1040, 1100)]):
         d = _inputs(rng, 4, 2, 128, lens)
         n = d["vs"].shape[0]
         d["vs"] = (2.0 ** rng.integers(-24, 4, d["vs"].shape)).astype(np.float32)
@@ -139,7 +169,7 @@ def test_value_scales_from_one_end_to_the_other():
     between pages of large ones (dropped, they are worth less than 2^-33)."""
     say("attention value scales 2^-126 .. 2^8")
     rng = np.random.default_rng(53)
-    for lens in ([(1, 900)], [(1, 9000)], [(5, 1500)], [(60, 900)]):
+    for lens in ([(1, 900)], [(1, 9000)], [(5, 1500)], [(60, 900)], [(1100, 1200)]):
         d = _inputs(rng, 4, 1, 128, lens)
         ids = d["table"][0, :-(-lens[0][1] // PAGE)]
         place = np.arange(len(ids))
@@ -154,7 +184,7 @@ def test_unused_places_do_not_matter():
     bytes behind the last token: the same output bits."""
     say("attention garbage")
     rng = np.random.default_rng(61)
-    for lens in ([(1, 70), (1, 1)], [(50, 100)]):
+    for lens in ([(1, 70), (1, 1)], [(50, 100)], [(1040, 1100)]):
         d = _inputs(rng, 4, 1, 64, lens)
         a = _run(d)
         held = set()
@@ -175,7 +205,7 @@ def test_unused_places_do_not_matter():
 def test_holes_and_lengths_beyond_the_table():
     say("attention holes")
     rng = np.random.default_rng(71)
-    for lens in ([(1, 400), (2, 300), (1, 64)], [(70, 400), (33, 290), (1, 1)]):
+    for lens in ([(1, 400), (2, 300), (1, 64)], [(70, 400), (33, 290), (1, 1)], [(1040, 1200), (300, 400), (1, 1)]):
         d = _inputs(rng, 4, 2, 128, lens)
         d["table"][0, 1], d["table"][0, 4], d["table"][1, 0] = -1, 1 << 20, -9
         d["table"][2, 0] = len(d["ks"])  # all that this sequence has
@@ -191,10 +221,10 @@ def test_rows_out_of_order_touch_nothing_else():
     import ternary_weight_base_amd as tq
     say("attention with bad cu_rows")
     rng = np.random.default_rng(75)
-    for lens in ([(1, 2000), (2, 300), (1, 64)], [(70, 400), (33, 290), (1, 1)], [(1, 90)] * 3):
+    for lens in ([(1, 2000), (2, 300), (1, 64)], [(70, 400), (33, 290), (1, 1)], [(1, 90)] * 3, [(1000, 1100), (33, 290), (1, 1)]):
         d = _inputs(rng, 4, 2, 128, lens)
         rows = d["q"].shape[0]
-        ws = torch.zeros(tq.tq_kv_attn_workspace_bytes(rows, 3, 4, 2, 128, int(d["kv"].max())) // 4 + 4, dtype=torch.int32, device="cuda")
+        ws = torch.zeros(tq.tq_kv_attn_workspace_bytes(rows, 3, 4, 2, 128, 20000 if rows > 1000 else int(d["kv"].max())) // 4 + 4, dtype=torch.int32, device="cuda")
         good = _run(d, ws=ws)
         for cu in ([0, rows, 0, rows], [5, -3, rows + 9, 1 << 30], [rows, 1, 1, 0], [-1 << 30, rows, rows, rows], [1, 1, 1, 1]):
             _run({**d, "cu": np.array(cu, np.int32)}, ws=ws)
@@ -205,7 +235,7 @@ def test_largest_window_and_rows_before_the_start():
     """A window and sinks as large as their type holds, with rows at negative positions."""
     say("attention largest window")
     rng = np.random.default_rng(76)
-    for lens in ([(80, 60), (3, 2)], [(3, 2), (1, 40)], [(200, 190)]):
+    for lens in ([(80, 60), (3, 2)], [(3, 2), (1, 40)], [(200, 190)], [(1100, 1070)]):
         d = _inputs(rng, 4, 1, 64, lens)
         for window, sinks in ((0x7fffffff, 0), (0x7fffffff, 0x7fffff00), (0x7ffffff0, 1)):
             _check(d, _run(d, window, sinks), window, sinks)
@@ -249,7 +279,7 @@ def test_sharp_scores_and_large_queries():
     running maximum moves in every tile)."""
     say("attention sharp")
     rng = np.random.default_rng(81)
-    for lens in ([(1, 900)], [(64, 900)]):
+    for lens in ([(1, 900)], [(64, 900)], [(1040, 1100)]):
         d = _inputs(rng, 4, 1, 128, lens, spread=30.0)
         _check(d, _run(d))
         d["q"][:] = np.abs(d["q"]) / 8
@@ -264,7 +294,7 @@ def test_sharp_scores_and_large_queries():
 def test_infinite_and_nan_queries_stay_in_their_row():
     say("attention nan")
     rng = np.random.default_rng(91)
-    for lens in ([(2, 200), (1, 90)], [(80, 200)]):
+    for lens in ([(2, 200), (1, 90)], [(80, 200)], [(1040, 1100)]):
         d = _inputs(rng, 4, 2, 64, lens)
         clean = _run(d)
         d["q"][1, 2, 5] = np.nan
@@ -278,7 +308,7 @@ def test_strided_and_in_place():
     import ternary_weight_base_amd as tq
     say("attention strides")
     rng = np.random.default_rng(95)
-    for lens in ([(1, 300), (1, 50)], [(50, 300)]):
+    for lens in ([(1, 300), (1, 50)], [(50, 300)], [(1040, 1100)]):
         d = _inputs(rng, 4, 2, 128, lens)
         want = _run(d)
         rows = d["q"].shape[0]
@@ -286,8 +316,9 @@ def test_strided_and_in_place():
         qs = wide[:, 32:32 + 512].unflatten(1, (4, 128))
         qs.copy_(dev(d["q"]))
         g = {k: dev(v) for k, v in d.items()}
-        ws = tq.kv_attn_workspace(rows, len(d["kv"]), 4, 2, 128, 300)
-        tq.tq_kv_attn(qs, g["cu"], g["kv"], g["table"], g["k"], g["v"], g["ks"], g["vs"], qs, 300, ws=ws)
+        most = 20000 if rows > 1000 else 300
+        ws = tq.kv_attn_workspace(rows, len(d["kv"]), 4, 2, 128, most)
+        tq.tq_kv_attn(qs, g["cu"], g["kv"], g["table"], g["k"], g["v"], g["ks"], g["vs"], qs, most, ws=ws)
         assert np.array_equal(qs.cpu().numpy().view(np.uint16), want.view(np.uint16))
         assert torch.isnan(wide[:, :32]).all() and torch.isnan(wide[:, 544:]).all()
 
