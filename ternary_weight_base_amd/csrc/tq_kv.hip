@@ -36,6 +36,7 @@
 #include "tq.h"
 #include "tq_device.h"
 #include "tq_kv.h"
+#include "tq_wave.h"
 
 namespace {
 

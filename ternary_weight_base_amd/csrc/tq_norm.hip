@@ -22,6 +22,7 @@
 
 #include "tq.h"
 #include "tq_device.h"
+#include "tq_wave.h"
 
 namespace {
 
