@@ -371,8 +371,10 @@ class _Torch:
             import torch
             cls.f32, cls.i32, cls.u8, cls.i8 = torch.float32, torch.int32, torch.uint8, torch.int8
             cls.acts = {torch.float16: TQ_F16, torch.float32: TQ_F32}
-            cls.device, cls.available = torch.cuda.current_device, torch.cuda.is_available
-            # the stream's handle without a Stream object, where torch has it
+            cls.available = torch.cuda.is_available
+            # the current device without the check that torch is initialised, and the
+            # stream's handle without a Stream object, where torch has them
+            cls.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
             cls.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
             cls.f16 = torch.float16
         return cls
@@ -414,15 +416,26 @@ def _cache_need(what, T, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale,
     i32, f32 = T.i32, T.f32
     if k_cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError(f"{what}: k_cache must have shape [pages][kv_heads][{KV_PAGE}][head_dim], page_table two dimensions")
-    pages, heads, _, dim = k_cache.shape
+    pages, heads, page, dim = k_cache.shape
     seqs, width = page_table.shape
     per = (pages, heads)
-    return seqs, heads, dim, (
-        _need(what, "cu_rows", cu_rows, i32, (seqs + 1,), dev), _need(what, "kv_len", kv_len, i32, (seqs,), dev),
-        _need(what, "page_table", page_table, i32, (seqs, width), dev), width,
-        _need(what, "k_cache", k_cache, T.u8, (pages, heads, KV_PAGE, dim), dev),
-        _need(what, "v_cache", v_cache, T.u8, (pages, heads, dim, KV_PAGE), dev),
-        _need(what, "k_scale", k_scale, f32, per, dev), _need(what, "v_scale", v_scale, f32, per, dev), pages)
+    # one expression where all is well: seven calls of _need would be most of a call's host time
+    if not (cu_rows.dtype is kv_len.dtype is page_table.dtype is i32 and k_cache.dtype is v_cache.dtype is T.u8
+            and k_scale.dtype is v_scale.dtype is f32
+            and cu_rows.get_device() == kv_len.get_device() == page_table.get_device() == k_cache.get_device()
+            == v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == dev
+            and cu_rows.shape == (seqs + 1,) and kv_len.shape == (seqs,) and page == KV_PAGE
+            and v_cache.shape == (pages, heads, dim, KV_PAGE) and k_scale.shape == per and v_scale.shape == per
+            and cu_rows.is_contiguous() and kv_len.is_contiguous() and page_table.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        for name, t, dtype, shape in (("cu_rows", cu_rows, i32, (seqs + 1,)), ("kv_len", kv_len, i32, (seqs,)),
+                                      ("page_table", page_table, i32, (seqs, width)),
+                                      ("k_cache", k_cache, T.u8, (pages, heads, KV_PAGE, dim)),
+                                      ("v_cache", v_cache, T.u8, (pages, heads, dim, KV_PAGE)),
+                                      ("k_scale", k_scale, f32, per), ("v_scale", v_scale, f32, per)):
+            _need(what, name, t, dtype, shape, dev)
+    return seqs, heads, dim, (cu_rows.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width, k_cache.data_ptr(),
+                              v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages)
 
 
 def _current(T, stream, t):
@@ -448,7 +461,7 @@ def tq_kv_append(qkv, rope, cu_rows, kv_len, page_table, k_cache, v_cache, k_sca
         raise ValueError(f"{what}: qkv must have two dimensions")
     rows, width = qkv.shape
     if q_heads is None:
-        q_heads = width // dim - 2 * heads
+        q_heads = width // max(dim, 1) - 2 * heads
     x, stride = _rows_need(what, "qkv", qkv, qkv.dtype, (rows, (q_heads + 2 * heads) * dim), dev)
     q = None if q_out is None else _need(what, "q_out", q_out, T.f16, (rows, q_heads, dim), dev)
     r, rope_rows, rot = None, 0, 0
@@ -519,16 +532,32 @@ def tq_residual_norm(y, res, res_out, pre_w=None, x=None, q=None, a_scale=None, 
             gp, gs = _rows_need(what, "gate", gate, yt, shape, dev)
         else:
             gp = _need(what, "gate", gate, yt, row, dev)
+    # (one expression where all is well, as for the cache's tensors)
+    if not (res.get_device() == dev and res.is_contiguous()
+            and (y is None or y.get_device() == dev and y.shape == shape and y.is_contiguous())
+            and (res_out is None or res_out.dtype is rt and res_out.get_device() == dev and res_out.shape == shape
+                 and res_out.is_contiguous())
+            and (post_w is None or post_w.dtype is f32 and post_w.get_device() == dev and post_w.shape == row
+                 and post_w.is_contiguous())
+            and (pre_w is None or pre_w.dtype is f32 and pre_w.get_device() == dev and pre_w.shape == row
+                 and pre_w.is_contiguous())
+            and (x is None or x.get_device() == dev and x.shape == shape and x.is_contiguous())
+            and (q is None or q.dtype is T.i8 and q.get_device() == dev and q.shape == shape and q.is_contiguous())
+            and (a_scale is None or a_scale.dtype is f32 and a_scale.get_device() == dev and a_scale.shape == (M,)
+                 and a_scale.is_contiguous())):
+        for name, t, dtype, size in (("res", res, rt, shape), ("y", y, yt, shape), ("res_out", res_out, rt, shape),
+                                     ("post_w", post_w, f32, row), ("pre_w", pre_w, f32, row),
+                                     ("x", x, None if x is None else x.dtype, shape), ("q", q, T.i8, shape),
+                                     ("a_scale", a_scale, f32, (M,))):
+            if t is not None:
+                _need(what, name, t, dtype, size, dev)
+    acts = T.acts
     rc = lib.tq_residual_norm(
-        TQ_F32 if y is None else T.acts.get(yt, -1), T.acts.get(rt, -1), TQ_F32 if x is None else T.acts.get(x.dtype, -1), M, H,
-        None if y is None else _need(what, "y", y, yt, shape, dev),
-        None if post_w is None else _need(what, "post_w", post_w, f32, row, dev), gp, gs, res_scale,
-        _need(what, "res", res, rt, shape, dev),
-        None if res_out is None else _need(what, "res_out", res_out, rt, shape, dev),
-        None if pre_w is None else _need(what, "pre_w", pre_w, f32, row, dev), eps,
-        None if x is None else _need(what, "x", x, x.dtype, shape, dev),
-        None if q is None else _need(what, "q", q, T.i8, shape, dev),
-        None if a_scale is None else _need(what, "a_scale", a_scale, f32, (M,), dev), st)
+        TQ_F32 if y is None else acts.get(yt, -1), acts.get(rt, -1), TQ_F32 if x is None else acts.get(x.dtype, -1), M, H,
+        None if y is None else y.data_ptr(), None if post_w is None else post_w.data_ptr(), gp, gs, res_scale, res.data_ptr(),
+        None if res_out is None else res_out.data_ptr(), None if pre_w is None else pre_w.data_ptr(), eps,
+        None if x is None else x.data_ptr(), None if q is None else q.data_ptr(),
+        None if a_scale is None else a_scale.data_ptr(), st)
     if rc:
         raise TQError(rc, what)
 
@@ -539,14 +568,21 @@ def tq_debug_kv_read(pages, k_cache, v_cache, k_scale, v_scale, values, stream=N
     dev, st = _current(T, stream, k_cache)
     if k_cache.dim() != 4 or pages.dim() != 1:
         raise ValueError(f"{what}: k_cache must have four dimensions, pages one")
-    num, heads, _, dim = k_cache.shape
+    num, heads, page, dim = k_cache.shape
     n, per = pages.shape[0], (num, heads)
-    rc = lib.tq_debug_kv_read(
-        T.acts.get(values.dtype, -1), n, heads, dim, _need(what, "pages", pages, T.i32, (n,), dev),
-        _need(what, "k_cache", k_cache, T.u8, (num, heads, KV_PAGE, dim), dev),
-        _need(what, "v_cache", v_cache, T.u8, (num, heads, dim, KV_PAGE), dev),
-        _need(what, "k_scale", k_scale, T.f32, per, dev), _need(what, "v_scale", v_scale, T.f32, per, dev), num,
-        _need(what, "values", values, values.dtype, (2, n, heads, KV_PAGE, dim), dev), st)
+    shape = (2, n, heads, KV_PAGE, dim)
+    if not (pages.dtype is T.i32 and k_cache.dtype is v_cache.dtype is T.u8 and k_scale.dtype is v_scale.dtype is T.f32
+            and pages.get_device() == k_cache.get_device() == v_cache.get_device() == k_scale.get_device()
+            == v_scale.get_device() == values.get_device() == dev
+            and page == KV_PAGE and v_cache.shape == (num, heads, dim, KV_PAGE) and k_scale.shape == per and v_scale.shape == per
+            and values.shape == shape and pages.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous() and values.is_contiguous()):
+        for name, t, dtype, size in (("pages", pages, T.i32, (n,)), ("k_cache", k_cache, T.u8, (num, heads, KV_PAGE, dim)),
+                                     ("v_cache", v_cache, T.u8, (num, heads, dim, KV_PAGE)), ("k_scale", k_scale, T.f32, per),
+                                     ("v_scale", v_scale, T.f32, per), ("values", values, values.dtype, shape)):
+            _need(what, name, t, dtype, size, dev)
+    rc = lib.tq_debug_kv_read(T.acts.get(values.dtype, -1), n, heads, dim, pages.data_ptr(), k_cache.data_ptr(),
+                              v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), num, values.data_ptr(), st)
     if rc:
         raise TQError(rc, what)
 

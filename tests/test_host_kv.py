@@ -138,6 +138,15 @@ def test_binding_refuses_wrong_tensors():
                 {"q": r, "a_scale": r[0, :2]}, {"a_scale": r[0]}):
         with pytest.raises(ValueError):
             tq.tq_residual_norm(**{**dict(y=r, res=r, res_out=r), **bad})
+    for bad in ({"post_w": r}, {"post_w": r[0].half()}, {"q": r.char(), "a_scale": r[:, 0]}, {"res": r.t().contiguous().t()},
+                {"res_out": r.t().contiguous().t()}, {"y": r.half().t()}, {"x": r[:, :8]}):
+        with pytest.raises(ValueError):
+            tq.tq_residual_norm(**{**dict(y=r, res=r, res_out=r), **bad})
+    rd = dict(pages=kv, k_cache=k, v_cache=v, k_scale=s, v_scale=s, values=torch.zeros((2, 2, 2, 64, 128)))
+    for bad in ({"pages": kv.long()}, {"pages": tb}, {"k_cache": v}, {"v_cache": k}, {"k_scale": s.half()}, {"v_scale": s[:2]},
+                {"values": torch.zeros((2, 2, 2, 64, 64))}, {"values": torch.zeros((2, 2, 2, 128, 64)).transpose(3, 4)}):
+        with pytest.raises(ValueError):
+            tq.tq_debug_kv_read(**{**rd, **bad})
 
 
 def test_binding_refuses_host_memory_where_there_is_a_gpu(monkeypatch):
