@@ -83,7 +83,12 @@ CASES = [
     (2, 2, 64, 8, True, np.float16, [(9, 4)], 1),     # more rows than tokens: the first rows have no position
     (2, 1, 128, 128, False, np.float32, [(3, 0), (4, 4)], 0),
     (4, 2, 128, 64, True, np.float32, [(21, 70)] + [(0, 5)] * 7 + [(1, 65)], 0),   # few rows a sequence, but many in one
-] + [(4, 2, 64, 64, False, np.float32, [(1 + i % 3, 1 + i % 3) for i in range(150)], 2)]
+] + [
+    (4, 2, 64, 64, False, np.float32, [(1 + i % 3, 1 + i % 3) for i in range(150)], 2),
+    (4, 2, 128, 64, True, np.float32, [(21, 70)] + [(0, 5)] * 70 + [(1, 65)], 0),  # the kernel for few rows, with many in one sequence
+    (4, 2, 128, 128, False, np.float16, [(4, 66 + i) for i in range(70)], 1),
+    (4, 2, 64, 32, True, np.float16, [(130, 131)] + [(0, 9)] * 140, 3),
+]
 
 
 @pytest.mark.parametrize("i", range(len(CASES)))
