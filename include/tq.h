@@ -477,9 +477,10 @@ size_t tq_kv_attn_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, i
  * value scales up to 2^50 (values below 2^-33 in a page are worth nothing to
  * an fp16 output and may be dropped), key scales that keep the scores finite
  * in fp32.  Sums, maxima and outputs are held in fp32.
- * max_kv_len: the largest kv_len of the call, which sets how the keys are
- * split over workgroups (a larger kv_len gives the same results more
- * slowly).  softmax_scale > 0 and finite, window and sinks >= 0
+ * max_kv_len: the largest kv_len of the call, which sets the kernel and how
+ * the keys are split over workgroups (a larger kv_len is right too, only
+ * slower; results for other max_kv_len differ by the rounding of weights and
+ * sums).  softmax_scale > 0 and finite, window and sinks >= 0
  * (TQ_ERR_VALUE).  The result does not depend on the order in which
  * workgroups finish.  One launch. */
 int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim,

@@ -374,3 +374,64 @@ def test_graph_replay_with_new_lengths():
         _check(d, got)
         assert np.array_equal(got.view(np.uint16), _run(d, max_kv=3000).view(np.uint16))
         assert int(torch.count_nonzero(ws)) == 0
+
+
+def test_two_graphs_share_a_workspace():
+    """A prompt's piece whose keys are cut, and one token over a long context,
+    captured apart with one workspace, replayed in turn."""
+    import ternary_weight_base_amd as tq
+    say("attention, two graphs")
+    rng = np.random.default_rng(103)
+    sets = [_inputs(rng, 32, 8, 128, [(300, 5000)]), _inputs(rng, 16, 2, 128, [(1, 9000)]), _inputs(rng, 8, 1, 64, [(9, 4000)])]
+    want = [_run(d) for d in sets]
+    shapes = [(d["q"].shape[0], 1, d["q"].shape[1], d["ks"].shape[1], d["q"].shape[2], int(d["kv"][0])) for d in sets]
+    need = [tq.tq_kv_attn_workspace_bytes(*s) for s in shapes]
+    assert min(need) > 0
+    ws = torch.zeros(max(need) // 4, dtype=torch.int32, device="cuda")
+    g = [{k: dev(v) for k, v in d.items()} for d in sets]
+    outs = [torch.empty(d["q"].shape, dtype=torch.float16, device="cuda") for d in sets]
+    graphs = []
+    s = torch.cuda.Stream()
+    for x, out, shape in zip(g, outs, shapes):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                tq.tq_kv_attn(x["q"], x["cu"], x["kv"], x["table"], x["k"], x["v"], x["ks"], x["vs"], out, shape[5], ws=ws)
+        graphs.append(graph)
+    for order in ((0, 1, 2), (2, 0, 1, 1), (1, 2, 2, 0)):
+        for i in order:
+            outs[i].fill_(float("nan"))
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert np.array_equal(outs[i].cpu().numpy().view(np.uint16), want[i].view(np.uint16)), i
+        assert int(torch.count_nonzero(ws)) == 0
+
+
+def test_long_prompt_against_its_own_last_rows():
+    """12000 rows at once, and rows of it asked for alone: the kernels for many
+    and for few rows, each within its distance from exact, agree."""
+    import ternary_weight_base_amd as tq
+    say("attention of 12000 rows")
+    hq, hkv, dim, n, t = 16, 2, 128, 12000, 16000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    pages = t // PAGE
+    q = torch.randn((n, hq, dim), generator=gen, device="cuda").half()
+    k, v = (torch.randint(0, 256, (pages, hkv) + s, generator=gen, device="cuda", dtype=torch.uint8) for s in ((PAGE, dim), (dim, PAGE)))
+    ks, vs = (torch.full((pages, hkv), 2.0 ** -6, device="cuda") for _ in range(2))
+    table = torch.randperm(pages, generator=gen, device="cuda").int()[None]
+    out = torch.empty_like(q)
+    cu = dev(np.array([0, n], np.int32))
+
+    def call(qq, o, cu, last):
+        kv = dev(np.array([last], np.int32))
+        tq.tq_kv_attn(qq, cu, kv, table, k, v, ks, vs, o, last, ws=tq.kv_attn_workspace(qq.shape[0], 1, hq, hkv, dim, last))
+
+    call(q, out, cu, t)
+    for first in (0, 1, 4000, 7777, n - 3):
+        few = torch.empty((3, hq, dim), dtype=torch.float16, device="cuda")
+        call(q[first:first + 3], few, dev(np.array([0, 3], np.int32)), t - n + first + 3)
+        # weights off by 2^-11 and little else, values up to 2 (2^7 codes of 2^-6), two outputs rounded to fp16
+        err = (out[first:first + 3].double() - few.double()).abs().max()
+        assert float(err) <= 2 * 2 * 2.0 ** -11 + 2 * 2.0 ** -11, first
