@@ -463,7 +463,8 @@ int tq_kv_append(int dtype, int64_t rows, int64_t seqs, int64_t q_heads, int64_t
                  int64_t num_pages, void *q_out, void *stream);
 
 /* Workspace bytes of tq_kv_attn (0 when the keys are not split, or on a bad
- * shape); same zero-fill rule as tq_gemv_workspace_bytes. */
+ * shape); same zero-fill rule as tq_gemv_workspace_bytes.  Not monotonic in
+ * the shape; never above 2^27 bytes. */
 size_t tq_kv_attn_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
                                   int64_t head_dim, int64_t max_kv_len);
 

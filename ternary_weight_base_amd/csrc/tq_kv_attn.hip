@@ -1279,6 +1279,8 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
     const int64_t idle = all - units, real = rest > idle ? rest - idle : rest;  // some tiles may hold no row
     int64_t nsplit = rest ? round / real : 1;
     if (nsplit > kPreSplits) nsplit = kPreSplits;
+    // (where most of the rest holds no row, what is launched and kept for it is bounded)
+    if (rest && nsplit > 2 * round / rest) nsplit = 2 * round / rest;
     if (nsplit > tiles / 4) nsplit = tiles / 4;
     P.wgs = P.solo = all;
     if (nsplit > 1) {

@@ -73,6 +73,14 @@ def test_kv_attn_validates_on_host():
         assert tq.tq_kv_attn_workspace_bytes(*bad) == 0
 
 
+def test_kv_attn_workspace_is_bounded():
+    most = max(tq.tq_kv_attn_workspace_bytes(rows, seqs, hq, hkv, dim, kv) for rows in (1, 7, 33, 130, 1040, 1041, 4096, 9000, 70000)
+               for seqs in (1, 2, 20, 33, 64, 300) for hq, hkv in ((8, 8), (64, 8), (16, 2), (5, 1), (32, 32)) for dim in (64, 128)
+               for kv in (1, 1024, 1025, 5000, 12288, 12289, 131072, 1 << 30))
+    assert 0 < most <= 1 << 27
+    assert tq.tq_kv_attn_workspace_bytes(1040, 33, 64, 8, 128, 13000) <= 1 << 27  # few rows left over among many places
+
+
 def _norm(yt=1, rt=1, xt=1, m=2, h=640, y=FAKE, pw=FAKE, g=FAKE, gs=0, rs=1.0, r=FAKE, ro=FAKE, w=FAKE, eps=1e-6, x=FAKE, q=FAKE, a=FAKE):
     return L.tq_residual_norm(yt, rt, xt, m, h, y, pw, g, gs, rs, r, ro, w, eps, x, q, a, None)
 
