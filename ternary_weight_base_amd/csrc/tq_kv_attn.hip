@@ -1248,16 +1248,22 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
   Plan P;
   const int64_t group = q_heads / kv_heads, flat = rows * group;
   // The decode kernel converts a page for each 32 rows, the prefill kernel for
-  // 128, but it starts and ends sooner and cuts the keys finer.  It takes up to 32
-  // rows a sequence, up to half a tile of 32 a CU (64 query and 8 KV heads, 16
-  // tokens on 600: 12.4 against 28.2 us, on 6001 25.0 against 56.5; 64 tokens on
-  // 30000 121 against 139), and up to a tile a CU with contexts of up to 12 K (96
-  // tokens on 12000 91 against 99 us, on 30000 211 against 148).  More is a second
-  // round of workgroups, which still pays on up to 1024 tokens (256 on 600 23 against
-  // 31 us; 180 on 4000 81 against 62); a third does not (64 sequences of 16 on 1000
-  // 98 against 58).  (The tiles as of sequences of the same length.)
+  // 128, but it starts and ends sooner, cuts the keys finer and shares them out
+  // by the lengths there are.  It takes (us of decode against prefill; 64 query
+  // and 8 KV heads of 128, sequences x rows on up to so many tokens)
+  //  - up to 32 (row, query head) rows a sequence;
+  //  - up to half a tile of 32 a CU (1 x 16 on 600 12.4 against 28.2, on 6001 25.0
+  //    against 56.5; 1 x 64 on 30000 116 against 136), up to a tile a CU on up to
+  //    12 K tokens (1 x 96 on 12000 91 against 99, on 30000 211 against 148), up to
+  //    two on up to 1024 (1 x 256 on 600 23 against 31; 1 x 180 on 4000 81 against 62);
+  //  - up to two tiles a CU of up to 64 rows a sequence, which fill half of a tile of
+  //    128, on more than 3500 tokens (32 x 8 on 4000 87 against 126, on 8000 146
+  //    against 179; 24 x 8 on 2000 56 against 47; 24 x 12, three tiles each, on 8000
+  //    161 against 143; 64 x 8, four a CU, on 4000 167 against 146).
+  // The tiles are counted as of sequences with the same number of rows.
   const int64_t each = (flat + seqs - 1) / seqs, tiles32 = (each + 31) / 32 * seqs * kv_heads;
-  const bool prefill = each > 32 && tiles32 > (max_kv <= 1024 ? 2 * kCus : max_kv <= 12288 ? kCus : kCus / 2);
+  const int64_t most = max_kv <= 1024 || (each <= 64 && max_kv > 3500) ? 2 * kCus : max_kv <= 12288 ? kCus : kCus / 2;
+  const bool prefill = each > 32 && tiles32 > most;
   const int R = prefill ? kTileRows : flat > kRows * seqs ? 2 * kRows : kRows;
   P.tile_rows = R;
   const int64_t tiles = (max_kv + kPage - 1) / kPage;

@@ -90,8 +90,7 @@ def test_attention(i):
     _check(d, _run(d, window, sinks), window, sinks)
 
 
-# as above, and max_kv_len: sizes that the kernel for many rows takes (more than
-# 128 tiles of 32 (token, query head) rows times KV heads, 256 for up to 12288 tokens, 512 for up to 1024)
+# as above, and max_kv_len: sizes that the kernel for many rows takes
 MANY = [
     (8, 8, 128, [(520, 520)], 0, 0, 0, 20000),
     (16, 16, 64, [(1100, 1100)], 0, 0, 0, None),
