@@ -481,8 +481,9 @@ size_t tq_kv_attn_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, i
  * max_kv_len: the largest kv_len of the call, which sets the kernel and how
  * the keys are split over workgroups (a larger kv_len is right too, only
  * slower; results for other max_kv_len differ by the rounding of weights and
- * sums).  softmax_scale > 0 and finite, window and sinks >= 0
- * (TQ_ERR_VALUE).  The result does not depend on the order in which
+ * sums).  Prompts and single tokens may share a call; where a step has many
+ * of the latter, a call for each kind takes less time.  softmax_scale > 0 and
+ * finite, window and sinks >= 0 (TQ_ERR_VALUE).  The result does not depend on the order in which
  * workgroups finish.  One launch. */
 int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                const void *q, int64_t q_stride, const int32_t *cu_rows, const int32_t *kv_len,
