@@ -42,8 +42,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "tq.h"
 #include "tq_device.h"
 #include "tq_kv.h"
@@ -59,7 +57,12 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 constexpr int kRows = 16;  // (token, query head) rows of a decode workgroup
 constexpr int kWaves = 8;  // of a decode workgroup
 constexpr int kDecPieces = 128;  // pieces of a unit at most (and one or two more)
-constexpr int kSnap = 4, kLeast = 4, kWhole = 16;  // pages: see "few rows"
+// Pages, see "few rows".  A piece has kLeast at least: one token of 1100 10.8 us, of
+// 4096 12.0 (8: 13.7, 13.0; 3: 10.9, 13.1).  Units of up to kWhole stay whole: 64
+// sequences of up to 700 tokens 17.6 us (8: 35; 32: 17.5).  A cut leaves kSnap at
+// least on both sides (the workspace's two results a workgroup rest on per >= kSnap).
+constexpr int kSnap = 4, kLeast = 4, kWhole = 16;
+static_assert(kSnap <= kLeast, "a share's two borders must not meet in one unit's end");
 constexpr float kNone = -1e30f;  // running maximum before the first visible key
 
 struct AttnArgs {
@@ -851,7 +854,7 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
 // (fp16 weights reach 2^8, times 2^4 for the page's value scale).
 constexpr int kWaveRows = 32;
 constexpr int kPreWaves = 4, kTileRows = kPreWaves * kWaveRows;
-constexpr int kPreSplits = 16;
+constexpr int kPreSplits = 16;  // pieces of a tile at most
 typedef float f16x __attribute__((ext_vector_type(16)));
 
 // The token of a 32-token group that row r of the score product takes.
