@@ -1279,10 +1279,8 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
   P.counter_bytes = P.bytes = 0;
   if (prefill) {
     // Two workgroups a CU run together.  Full rounds of them take whole units;
-    // the rest of a last round is cut into pieces for all CUs (a piece costs a
-    // tile's partial outputs written and read, 66 KB, so not more than the
-    // rest is cut).  With many rounds the longest-first order levels the load
-    // by itself.
+    // the rest of a last round is cut into pieces for all CUs.  With many rounds
+    // the longest-first order levels the load by itself.
     const int64_t slots = flat / R + seqs, all = slots * kv_heads, round = 2 * kCus;
     const int64_t rest = all < 4 * round ? all % round : 0;
     const int64_t idle = all - units, real = rest > idle ? rest - idle : rest;  // some tiles may hold no row
@@ -1291,6 +1289,24 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
     // (where most of the rest holds no row, what is launched and kept for it is bounded)
     if (rest && nsplit > 2 * round / rest) nsplit = 2 * round / rest;
     if (nsplit > tiles / 4) nsplit = tiles / 4;
+    if (rest == all && tiles <= 32 && each >= R) {
+      // One round of full tiles and few pages: the number of pieces that should take least, in 10
+      // ns.  A page takes a workgroup 1.25 us alone on its CU and 2.34 (64 elements:
+      // 1.17) beside another; pieces cost 12 us and the time of their partial
+      // results, 66 (33) KB each, written and read.  (1 x 256 rows on 2000, 64 and 8
+      // heads: one piece 49 us, two 47, four 60; 3 x 300 on 1000, 24 and 4 heads of
+      // 64: 22, three 30.  More pages: 1 x 180 on 4000 one 92, two 64, five 62; 3 x
+      // 200 on 3000, 32 and 8 heads, two 73, four 63.  Tiles half empty: 30 x 13 on
+      // 2000, 40 and 8 heads, one 63, two 51.)
+      const int64_t pages = tiles - rows / seqs / (2 * kPage);
+      int64_t least = 0, best = 1;
+      for (int64_t n = 1; n <= nsplit; n++) {
+        const int64_t wgs = real * n, page = wgs <= kCus ? 125 : 234 * head_dim / 128;
+        const int64_t t = (pages + n - 1) / n * page + (n > 1 ? 1200 + wgs * head_dim * 27 / 1280 : 0);
+        if (n == 1 || t < least) least = t, best = n;
+      }
+      nsplit = best;
+    }
     P.wgs = P.solo = all;
     if (nsplit > 1) {
       P.nsplit = (int)nsplit;
