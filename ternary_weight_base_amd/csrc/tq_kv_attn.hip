@@ -950,7 +950,8 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
 
   // A page's scales: the score's factor (finite for a page of zeros, so that a
   // masked score stays -inf), log2 of the value scale (a page of zeros adds to
-  // the sum only: its values are put into LDS as zeros).
+  // the sum only: its values are put into LDS as zeros).  A page that is not
+  // there is read as page 0, whose scales may be anything: none of them counts.
   struct Scales {
     float sc, lv;
     bool there, live;
@@ -961,8 +962,8 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
     const int64_t ph = (int64_t)(t.there ? id : 0) * A.hkv + P.h;
     const float ks = A.ks[ph], vs = A.vs[ph];
     t.there = t.there && ks >= 0.0f;
-    t.sc = fmaxf(ks * A.scale_log2, 1e-37f);
-    t.live = vs >= kLeastScale;
+    t.sc = t.there ? fmaxf(ks * A.scale_log2, 1e-37f) : 1e-37f;
+    t.live = t.there && vs >= kLeastScale;
     t.lv = __builtin_amdgcn_logf(vs);
     return t;
   };
