@@ -20,10 +20,15 @@
 // next within a lane: no LDS, no lane exchange, and every softmax quantity is
 // lane-local but for two exchanges of the running maximum.
 //
-// The weights are rounded to fp16 for the second product.  The kernel for up
-// to 16 rows adds the rounding error back as a second fp16 term (its matrix
-// units are idle anyway), so there only the output's own rounding to fp16 is
-// left; with more rows the term would cost 10 % and more.
+// The weights are rounded to fp16 for the second product, half a step of 2^-11
+// each; their sum is of the fp32 weights.  The kernel for up to 16 rows adds the
+// rounding error back as a second fp16 term (its matrix units are idle anyway);
+// with more rows the term would cost 10 % and more.  fp16 ends at 2^-24, so the
+// largest weight of a row is put at 2^11 to 2^15, not at 1: a weight keeps its
+// eleven bits down to 2^-25 of the largest one, and what is lost of a smaller one
+// is at most 2^-36 of that.  (With the largest at 1 the 2^17 keys of a long
+// context 2^-24 below a first token that draws all attention were rounded to a
+// single bit, all the same way.)
 //
 // Bound: few rows (decode) read 2 head_dim bytes a token and KV head and are
 // bound by HBM; the work along the keys is split over workgroups, whose
@@ -133,6 +138,9 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// A value that all lanes have alike, in a scalar register.
+__device__ __forceinline__ float uniform(float v) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v))); }
+
 // Over the four lanes lane % 16 + 16 g.
 __device__ __forceinline__ float quarter_max(float v) {
   const uint32_t b = __float_as_uint(v);
@@ -181,18 +189,28 @@ __device__ __forceinline__ void load_values(const AttnArgs &A, int h, int id, Ra
 }
 
 // A page with a smaller value scale counts as zeros: its values are below
-// 2^-33, nothing to an fp16 output (half its least step is 2^-25).  So the
+// 2^-30, nothing to an fp16 output (half its least step is 2^-25).  So the
 // state's unit (below) never falls by more than the largest scale's 2^50 over
-// this, and 2^90 times what the products can sum up to stays within fp32.
-constexpr float kLeastScale = 0x1p-40f;
+// this, and 2^87 times what the products can sum up to stays within fp32.
+constexpr float kLeastScale = 0x1p-37f;
 
 // Running state of a lane's query row.  The output is held as
 //   unit * (o + corr / 2), corr = sum of the weights that o's products took,
-// where `unit` (one for the wave) is a value scale: pages whose scale is
-// within 2^4 of it have the ratio folded into their weights, others move the
-// state to their own.  m is a reference for the weights' exponents: it moves
-// only when a score exceeds it by 8 (weights reach 2^8, times 2^4 for the
-// scale, in fp16), so the outputs are hardly ever rescaled.
+// where `unit` (one for the wave) is a value scale: pages with 2^-7 to 1 of it
+// have the ratio folded into their weights, larger and smaller ones move the
+// state to their own.  (A ratio below one takes bits from weights of values that
+// are as much smaller; room for ratios above one would take them from all.)
+// m is a reference for the weights' exponents: kLift below the score it was set
+// by, moved only when a score exceeds it by kTop, so the outputs are hardly ever
+// rescaled and weights reach 2^15 in fp16, which ends at 2^16.  (kLift 9 or 7, for
+// scores that rise further, measured the same.)
+constexpr float kLift = 11.0f, kTop = 15.0f;
+constexpr float kNoUnit = -1000.0f;  // log2 of the unit before the first page with values
+
+// Whether the state moves to the scale of a page, whose log2 is `over` above
+// the unit's: outside -7.75 .. 0.25 (weights stay below 2^15.25).
+__device__ __forceinline__ bool unit_moves(float over) { return !(fabsf(over + 3.75f) < 4.0f); }
+
 template <int D>
 struct State {
   f4 o[D / 16];
@@ -221,7 +239,7 @@ __device__ __forceinline__ void scores(const Raw<D> &t, const h8 (&qf)[RT][D / 3
 
 // The weights of one row tile: hi (+ lo, if LO) fp16 terms of w * 2^shift.
 template <int D, bool LO>
-__device__ __forceinline__ void weights(const AttnArgs &A, f4 (&x)[4], float qsum, float sc, float shift, float unit_moves,
+__device__ __forceinline__ void weights(const AttnArgs &A, f4 (&x)[4], float qsum, float sc, float shift, float moves,
                                         bool masked, int j0, int pos, bool has_v, State<D> &st, h8 (&hi)[2], h8 (&lo)[2]) {
   if (masked) {
 #pragma unroll
@@ -235,12 +253,12 @@ __device__ __forceinline__ void weights(const AttnArgs &A, f4 (&x)[4], float qsu
 #pragma unroll
   for (int i = 1; i < 16; i++) mx = fmaxf(mx, x[i >> 2][i & 3]);
   mx = (quarter_max(mx) + qsum) * sc;
-  if (unit_moves != 1.0f || __any(mx > st.m + 8.0f)) {
-    const float mn = mx > st.m + 8.0f ? mx : st.m;
+  if (moves != 1.0f || __any(mx > st.m + kTop)) {
+    const float mn = mx > st.m + kTop ? mx - kLift : st.m;
     float alpha = __builtin_amdgcn_exp2f(st.m - mn);
     st.m = mn;
     st.l *= alpha;
-    alpha *= unit_moves;
+    alpha *= moves;
     st.corr *= alpha;
 #pragma unroll
     for (int i = 0; i < D / 16; i++) st.o[i] *= alpha;
@@ -710,7 +728,7 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
     const Tiles T = u.T;
     int i = u.i, id;
     State<D> st[RT];
-    float qsum[RT], unit = 0.0f;  // log2 of the outputs' unit
+    float qsum[RT], unit = kNoUnit;  // log2 of the outputs' unit
 #pragma unroll
     for (int a = 0; a < RT; a++) {
       qsum[a] = 0.0f;
@@ -741,11 +759,11 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
         // a page of zeros has scale 0: its (zero) scores stay finite, masked ones -inf
         const float sc = fmaxf(ks * A.scale_log2, 1e-37f);
         const bool has_v = vs >= kLeastScale;  // a page of zeros adds to the sum only
-        const float over = has_v ? __builtin_amdgcn_logf(vs) - unit : 0.0f;
-        const bool far = !(fabsf(over) < 4.0f);
+        const float lv = uniform(__builtin_amdgcn_logf(vs)), over = has_v ? lv - unit : 0.0f;
+        const bool far = unit_moves(over);
         const float shift = far ? 0.0f : over;
         const float moves = far ? __builtin_amdgcn_exp2f(-over) : 1.0f;
-        if (far) unit += over;
+        if (far) unit = lv;
         h8 hi16[RT][2], lo16[RT][2];
 #pragma unroll
         for (int a = 0; a < RT; a++)
@@ -849,9 +867,8 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
 // rows 139 against 119); 64 rows a wave, which halves the LDS reads but leaves
 // one wave a SIMD (374 against 309, 173 against 115).
 //
-// The running maximum is a reference, not the maximum: it moves only when a
-// score exceeds it by 2^8 in weight, so the output is hardly ever rescaled
-// (fp16 weights reach 2^8, times 2^4 for the page's value scale).
+// The running maximum is a reference, not the maximum, as in the decode kernel
+// (kLift, kTop), and so is the output's unit.
 constexpr int kWaveRows = 32;
 constexpr int kPreWaves = 4, kTileRows = kPreWaves * kWaveRows;
 constexpr int kPreSplits = 16;  // pieces of a tile at most
@@ -946,7 +963,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
     for (int r = 0; r < 16; r++) o[i][r] = 0.0f;
   // keys up to `lowest` are outside the row's window (no window: none are)
   const int lowest = A.window ? pos - A.window : -1;
-  float m = kNone, l = 0.0f, corr = 0.0f, unit = 0.0f;  // unit: its log2
+  float m = kNone, l = 0.0f, corr = 0.0f, unit = kNoUnit;  // unit: its log2
 
   // A page's scales: the score's factor (finite for a page of zeros, so that a
   // masked score stays -inf), log2 of the value scale (a page of zeros adds to
@@ -999,15 +1016,15 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
   auto refer = [&](const Scales &t, float mx) {
     mx = t.there ? (half_max(mx) + qsum) * t.sc : -__builtin_inff();
     const float over = t.live ? t.lv - unit : 0.0f;
-    const bool far = !(fabsf(over) < 4.0f);
-    if (far || __any(mx > m + 8.0f)) {
-      const float mn = mx > m + 8.0f ? mx : m;
+    const bool far = unit_moves(over);
+    if (far || __any(mx > m + kTop)) {
+      const float mn = mx > m + kTop ? mx - kLift : m;
       float alpha = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= alpha;
       if (far) {
         alpha *= __builtin_amdgcn_exp2f(-over);
-        unit += over;
+        unit = t.lv;
       }
       corr *= alpha;
 #pragma unroll

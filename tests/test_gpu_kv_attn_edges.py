@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 from gpu_util import say
+from kv_util import attention, attention_tolerance
 from test_gpu_kv_attn import _check, _inputs, _run
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +39,36 @@ def test_missing_pages_beside_a_page_that_was_never_written(i):
                    (np.nan, np.nan), (2.0 ** -6, np.nan), (-1.0, 2.0 ** 122), (0.0, 0.0), (2.0 ** -6, 2.0 ** -126)):
         d["ks"][0], d["vs"][0] = ks, vs
         assert np.array_equal(_run(d).view(np.uint16), clean.view(np.uint16)), (ks, vs)
+
+
+# sequences' rows and lengths, max_kv_len: 16 rows whole and cut, 32 rows whole and cut, 128 rows
+WEAK = [([(1, 900)], None), ([(1, 12000)], None), ([(5, 900)], None), ([(5, 12000)], None), ([(1040, 4096)], 20000)]
+
+
+@pytest.mark.parametrize("first_page", [2.0 ** -4, 2.0 ** -14])
+@pytest.mark.parametrize("gap", [16.0, 18.5])
+@pytest.mark.parametrize("i", range(len(WEAK)))
+def test_many_weak_keys_under_a_strong_one(i, gap, first_page):
+    """A first token that draws all attention and has next to no value, under it
+    keys of one sign that differ little: each weighs exp(-gap) of it, together
+    they are the output.  Beside attention_tolerance's terms a weight below
+    2^-25 of the row's largest may be off by 2^-36 of that (half of fp16's
+    least step, the largest weight at 2^11 or above), times its value."""
+    lens, most = WEAK[i]
+    say(f"attention of weak keys, {lens}, gap {gap}, first page's scale {first_page}")
+    rng = np.random.default_rng(500 + i)
+    d = _inputs(rng, 4, 2, 128, lens)
+    d["q"] = (1 + 0.02 * rng.standard_normal(d["q"].shape)).astype(np.float16)
+    d["k"] = rng.integers(118, 138, d["k"].shape, dtype=np.uint8)
+    d["v"] = rng.integers(160, 256, d["v"].shape, dtype=np.uint8)
+    d["ks"][:], d["vs"][:] = 2.0 ** -6, 2.0 ** -4
+    first = d["table"][0, 0]
+    # score of code c against ones: 2^-6 (c - 127.5) 128 / sqrt(128)
+    d["k"][first, :, 0] = round(127.5 + gap / (2.0 ** -6 * 128 ** 0.5))
+    d["v"][first, :, :, 0] = rng.integers(127, 129, d["v"][first, :, :, 0].shape)
+    d["vs"][first] = first_page
+    ref, mag, dot = attention(d["q"], d["cu"], d["kv"], d["table"], d["k"], d["v"], d["ks"], d["vs"], 128 ** -0.5, 0, 0)
+    keys = lens[0][1]
+    tol = attention_tolerance(ref, mag, dot, keys, 128) + keys * 2.0 ** -36 * 128 * 2.0 ** -4
+    err = np.abs(_run(d, max_kv=most).astype(np.float64) - ref)
+    assert np.all(err <= tol), f"{np.max(err / tol)} of the tolerance, output {np.median(np.abs(ref))}"
