@@ -476,12 +476,15 @@ size_t tq_kv_attn_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, i
  * out_stride elements apart (multiples of 8), 16-byte aligned; out may be
  * q itself (same stride).  Scales of the cache need not be powers of two;
  * value scales up to 2^50 (values below 2^-30 in a page are worth nothing to
- * an fp16 output and may be dropped), key scales that keep the scores finite
- * in fp32.  Sums, maxima and outputs are held in fp32.  For the product with the
- * values a weight is rounded to fp16, half a step of 2^-11 of it; in calls with
- * rows * q_heads / kv_heads <= 16 seqs (single tokens) that rounding is added
- * back.  What a key that weighs less than 2^-25 of the row's largest weight adds
- * is off by up to 2^-36 of that weight times 128 of the largest value scale.
+ * an fp16 output and may be dropped).  For every row and key that it sees,
+ * softmax_scale sum |q||k| must be at most 2^20: scores are fp32 sums, one of
+ * magnitude 2^n is off by up to some 2^(n - 16), and from 2^21 on a weight may
+ * pass the end of fp16 (the output is then not finite).  Sums, maxima and outputs
+ * are held in fp32.  For the product with the values a weight is rounded to fp16,
+ * half a step of 2^-11 of it; in calls with rows * q_heads / kv_heads <= 16 seqs
+ * (single tokens) that rounding is added back.  What a key that weighs less than
+ * 2^-25 of the row's largest weight adds is off by up to 2^-36 of that weight
+ * times 128 of the largest value scale.
  * max_kv_len: the largest kv_len of the call, which sets the kernel and how
  * the keys are split over workgroups (a larger kv_len is right too, only
  * slower; results for other max_kv_len differ by the rounding of weights and

@@ -204,8 +204,10 @@ constexpr float kLeastScale = 0x1p-37f;
 // are as much smaller; room for ratios above one would take them from all.)
 // m is a reference for the weights' exponents: kLift below the score it was set
 // by, moved only when a score exceeds it by kTop, so the outputs are hardly ever
-// rescaled and weights reach 2^15 in fp16, which ends at 2^16.  (kLift 9 or 7, for
-// scores that rise further, measured the same.)
+// rescaled and weights reach 2^15.25 in fp16, which ends at 2^16.  (kLift 9 or 7, for
+// scores that rise further, measured the same.)  The 0.75 between are for the
+// exponent's roundings: those of the reference, of the half-code term and of their
+// difference, together 8 of 2^-24 of 2^20.5, 0.71, at scores of 2^20.
 constexpr float kLift = 11.0f, kTop = 15.0f;
 constexpr float kNoUnit = -1000.0f;  // log2 of the unit before the first page with values
 

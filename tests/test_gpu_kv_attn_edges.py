@@ -72,3 +72,31 @@ def test_many_weak_keys_under_a_strong_one(i, gap, first_page):
     tol = attention_tolerance(ref, mag, dot, keys, 128) + keys * 2.0 ** -36 * 128 * 2.0 ** -4
     err = np.abs(_run(d, max_kv=most).astype(np.float64) - ref)
     assert np.all(err <= tol), f"{np.max(err / tol)} of the tolerance, output {np.median(np.abs(ref))}"
+
+
+@pytest.mark.parametrize("i", range(len(WEAK)))
+def test_largest_scores(i):
+    """The largest softmax_scale sum |q||k| that is taken, 2^20: such scores are
+    off by several units, but the output stays a mean of values: within their
+    range, off by the roundings of weights (2^-11, on both sums), of the sums
+    (keys and keys / 64 rescalings, 2^-24 each, on both) and of the output (2^-11)."""
+    lens, most = WEAK[i]
+    say(f"attention of the largest scores, {lens}")
+    rng = np.random.default_rng(600 + i)
+    d = _inputs(rng, 4, 2, 128, lens)
+    d["vs"][:] = 2.0 ** -7
+    _, _, dot = attention(d["q"], d["cu"], d["kv"], d["table"], d["k"], d["v"], d["ks"], d["vs"], 1.0, 0, 0)
+    bound = 127.5 * 2.0 ** -7 * (1 + 3 * 2.0 ** -11 + 2 * (lens[0][1] * 65 / 64 + 8) * 2.0 ** -24)
+    for scale in (2.0 ** 20 / dot.max(), 2.0 ** 14 / dot.max()):
+        got = _run(d, max_kv=most, scale=float(np.float32(scale * (1 - 2.0 ** -20)))).astype(np.float64)
+        assert np.all(np.abs(got) <= bound), scale
+        # and one key's score far above the rest: its value alone
+        one = {**d, "k": d["k"].copy(), "q": np.abs(d["q"])}
+        one["k"][d["table"][0, 0], :, 0] = 255
+        one["k"][one["k"] > 200] = 200
+        one["k"][d["table"][0, 0], :, 0] = 255
+        one["ks"] = np.full_like(d["ks"], 2.0 ** -6)
+        ref, mag, dot1 = attention(one["q"], d["cu"], d["kv"], d["table"], one["k"], d["v"], one["ks"], d["vs"], 1.0, 0, 0)
+        s1 = float(np.float32(scale * dot.max() / dot1.max() * (1 - 2.0 ** -20)))
+        ref, mag, _ = attention(one["q"], d["cu"], d["kv"], d["table"], one["k"], d["v"], one["ks"], d["vs"], s1, 0, 0)
+        assert np.all(np.abs(_run(one, max_kv=most, scale=s1) - ref) <= 2.0 ** -9 * np.abs(ref) + 2.0 ** -25)
