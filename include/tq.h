@@ -489,9 +489,13 @@ size_t tq_kv_attn_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, i
  * the keys are split over workgroups (a larger kv_len is right too, only
  * slower; results for other max_kv_len differ by the rounding of weights and
  * sums).  Prompts and single tokens may share a call; where a step has many
- * of the latter, a call for each kind takes less time.  softmax_scale > 0 and
- * finite, window and sinks >= 0 (TQ_ERR_VALUE).  The result does not depend on the order in which
- * workgroups finish.  One launch. */
+ * of the latter, a call for each kind takes less time.  Where the keys of a few
+ * rows are split, the pages of all row tiles are counted in 32 bits: with tiles
+ * of T = 16 rows, or 32 from rows * q_heads / kv_heads > 16 seqs on,
+ * (rows * q_heads / kv_heads / T + seqs) * kv_heads * max_pages must be below
+ * 2^31 (TQ_ERR_SHAPE).  softmax_scale > 0 and finite, window and sinks >= 0
+ * (TQ_ERR_VALUE).  The result does not depend on the order in which workgroups
+ * finish.  One launch. */
 int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                const void *q, int64_t q_stride, const int32_t *cu_rows, const int32_t *kv_len,
                const int32_t *page_table, int64_t max_pages, const uint8_t *k_cache,

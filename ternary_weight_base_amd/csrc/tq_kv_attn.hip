@@ -1399,9 +1399,9 @@ extern "C" int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t k
   const Plan P = make_plan(rows, seqs, q_heads, kv_heads, head_dim, max_kv_len);
   if (P.bytes && !ws) return TQ_ERR_NULL;
   if (ws_bytes < P.bytes) return TQ_ERR_SIZE;
-  // the kernels count pages of all sequences and heads in 32 bits
+  // where units are cut their list counts the pages of all of them in 32 bits
   const int64_t units = (rows * (q_heads / kv_heads) / P.tile_rows + seqs) * kv_heads;
-  if (!grid_ok(P.wgs, P.waves * 64) || units > 0x7fffffff / max_pages) return TQ_ERR_SHAPE;
+  if (!grid_ok(P.wgs, P.waves * 64) || (P.whole && units > 0x7fffffff / max_pages)) return TQ_ERR_SHAPE;
   AttnArgs A;
   A.q = (const _Float16 *)q; A.out = (_Float16 *)out;
   A.cu = cu_rows; A.kv_len = kv_len; A.table = page_table;

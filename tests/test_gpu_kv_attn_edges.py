@@ -3,7 +3,7 @@ there, weights far apart, the launch plans of each shape."""
 import numpy as np
 import pytest
 
-from gpu_util import say
+from gpu_util import dev, say
 from kv_util import attention, attention_tolerance
 from test_gpu_kv_attn import _check, _inputs, _run
 
@@ -100,3 +100,22 @@ def test_largest_scores(i):
         s1 = float(np.float32(scale * dot.max() / dot1.max() * (1 - 2.0 ** -20)))
         ref, mag, _ = attention(one["q"], d["cu"], d["kv"], d["table"], one["k"], d["v"], one["ks"], d["vs"], s1, 0, 0)
         assert np.all(np.abs(_run(one, max_kv=most, scale=s1) - ref) <= 2.0 ** -9 * np.abs(ref) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("rows,kv", [(1, 500), (200, 300)])
+def test_page_table_of_any_width(rows, kv):
+    """A table whose width times the row tiles passes 32 bits, in calls that
+    keep no list of pages: as with a table of the pages that are used."""
+    import ternary_weight_base_amd as tq
+    say(f"attention with a wide page table, {rows} rows")
+    d = _inputs(np.random.default_rng(700 + rows), 64, 64, 64, [(rows, kv), (rows, kv - 70)])
+    want = _run(d)
+    assert tq.tq_kv_attn_workspace_bytes(2 * rows, 2, 64, 64, 64, kv) == 0
+    g = {k: dev(v) for k, v in d.items()}
+    wide = torch.full((2, 1 << 25), -1, dtype=torch.int32, device="cuda")
+    wide[:, :d["table"].shape[1]] = g["table"]
+    out = torch.empty_like(g["q"])
+    tq.tq_kv_attn(g["q"], g["cu"], g["kv"], wide, g["k"], g["v"], g["ks"], g["vs"], out, kv)
+    assert np.array_equal(out.cpu().numpy().view(np.uint16), want.view(np.uint16))
+    del wide
+    torch.cuda.empty_cache()

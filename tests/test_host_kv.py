@@ -207,3 +207,12 @@ def test_references():
     assert np.all(out[1] == 2.5) and np.all(out[2] == 0.5)
     out, _, _ = attention(q, [0, 3], np.array([3]), np.array([[0]], np.int32), k, v, one, one, 1.0, 1, 1)
     assert np.all(out[1] == 1.5) and np.all(out[2] == 0.5)
+
+
+def test_pages_of_all_units_are_counted_in_32_bits():
+    """Where a few rows' keys are cut, the pages of all row tiles and KV heads,
+    as many as the table is wide, must be fewer than 2^31 (128 units here)."""
+    wide = dict(rows=4, seqs=2, hq=64, hkv=64, qs=8192, os=8192)
+    assert tq.tq_kv_attn_workspace_bytes(4, 2, 64, 64, 128, 100000) > 0
+    assert _attn(**wide, mk=100000, mp=1 << 24) == SHAPE
+    assert _attn(rows=4, seqs=2, hq=64, hkv=32, qs=8192, os=8192, mk=100000, mp=1 << 25) == SHAPE
