@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 
 from gpu_util import dev, say
-from kv_util import attention, attention_tolerance
+from kv_plans import PLANS
+from kv_util import PAGE, attention, attention_tolerance
 from test_gpu_kv_attn import _check, _inputs, _run
 
 pytestmark = pytest.mark.gpu
@@ -119,3 +120,54 @@ def test_page_table_of_any_width(rows, kv):
     assert np.array_equal(out.cpu().numpy().view(np.uint16), want.view(np.uint16))
     del wide
     torch.cuda.empty_cache()
+
+
+def _reference(d, window, sinks):
+    """kv_util.attention's three results for tables without holes, by float64
+    products of whole heads on the CPU."""
+    rows, hq, dim = d["q"].shape
+    hkv, scale = d["ks"].shape[1], dim ** -0.5
+    group = hq // hkv
+    out, mag, dot = np.full((rows, hq, dim), np.nan), np.zeros((rows, hq, dim)), np.zeros((rows, hq))
+    T = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.float64))
+    for s, t in enumerate(d["kv"].tolist()):
+        a, b = int(d["cu"][s]), int(d["cu"][s + 1])
+        n = b - a
+        if n == 0:
+            continue
+        ids = d["table"][s, :-(-t // PAGE)]
+        pos, j = torch.arange(t - n, t)[:, None], torch.arange(t)[None]
+        see = j <= pos
+        if window:
+            see = see & ((j > pos - window) | (j < sinks))
+        see = see.repeat_interleave(group, 0)  # rows (token, head)
+        for h in range(hkv):
+            k = T((d["k"][ids, h].astype(np.float64) - 127.5) * d["ks"][ids, h][:, None, None]).reshape(-1, dim)[:t]
+            v = T(((d["v"][ids, h].astype(np.float64) - 127.5) * d["vs"][ids, h][:, None, None]).transpose(0, 2, 1)).reshape(-1, dim)[:t]
+            q = T(d["q"][a:b, h * group:(h + 1) * group]).reshape(-1, dim)
+            z = torch.where(see, q @ k.T * scale, -torch.inf)
+            w = torch.exp(z - z.amax(1, keepdim=True).clamp(min=-1e300)) if t else z
+            w = torch.nan_to_num(w / w.sum(1, keepdim=True))  # a row that sees nothing: zeros
+            put = lambda x: x.reshape(n, group, dim).numpy()
+            out[a:b, h * group:(h + 1) * group] = put(w @ v)
+            mag[a:b, h * group:(h + 1) * group] = put(w @ v.abs())
+            if t:
+                dot[a:b, h * group:(h + 1) * group] = (q.abs() @ k.abs().T * scale * see).amax(1).reshape(n, group).numpy()
+    return out, mag, dot
+
+
+@pytest.mark.parametrize("name", PLANS)
+def test_every_launch_plan(name):
+    """Each plan against the 64-bit result, twice with the same bits, the
+    workspace left zero."""
+    import ternary_weight_base_amd as tq
+    hq, hkv, dim, lens, window, sinks, most, need = PLANS[name]
+    say(f"attention plan {name}: {hq}/{hkv} heads of {dim}, {len(lens)} sequences, {lens[:3]}, window {window}, sinks {sinks}")
+    d = _inputs(np.random.default_rng(sum(map(ord, name))), hq, hkv, dim, lens)
+    assert tq.tq_kv_attn_workspace_bytes(d["q"].shape[0], len(lens), hq, hkv, dim, most) == need
+    got = _run(d, window, sinks, max_kv=most)
+    assert np.array_equal(got.view(np.uint16), _run(d, window, sinks, max_kv=most).view(np.uint16))
+    ref, mag, dot = _reference(d, window, sinks)
+    tol = attention_tolerance(ref, mag, dot, most, dim)
+    off = ~(np.abs(got.astype(np.float64) - ref) <= tol)
+    assert not off.any(), f"{off.sum()} off, first at {np.argwhere(off)[0]}"

@@ -4,6 +4,7 @@ own pins."""
 import numpy as np
 import pytest
 
+import kv_plans
 import ternary_weight_base_amd as tq
 from kv_util import Cache, attention, rotate, scale_for
 from test_host_abi import FAKE, MIS, ODD
@@ -216,3 +217,12 @@ def test_pages_of_all_units_are_counted_in_32_bits():
     assert tq.tq_kv_attn_workspace_bytes(4, 2, 64, 64, 128, 100000) > 0
     assert _attn(**wide, mk=100000, mp=1 << 24) == SHAPE
     assert _attn(rows=4, seqs=2, hq=64, hkv=32, qs=8192, os=8192, mk=100000, mp=1 << 25) == SHAPE
+
+
+@pytest.mark.parametrize("name", kv_plans.PLANS)
+def test_attention_plans(name):
+    """The workspace of each call that tests/test_gpu_kv_attn_edges.py makes to
+    take a plan."""
+    hq, hkv, dim, lens, _, _, most, need = kv_plans.PLANS[name]
+    assert tq.tq_kv_attn_workspace_bytes(sum(n for n, _ in lens), len(lens), hq, hkv, dim, most) == need
+    assert max(t for _, t in lens) == most
