@@ -171,3 +171,22 @@ def test_every_launch_plan(name):
     tol = attention_tolerance(ref, mag, dot, most, dim)
     off = ~(np.abs(got.astype(np.float64) - ref) <= tol)
     assert not off.any(), f"{off.sum()} off, first at {np.argwhere(off)[0]}"
+
+
+def test_infinite_queries_stay_in_their_row():
+    """+inf, -inf, both and NaN in a query: every other row and head keeps its
+    bits, also of other sequences."""
+    say("attention of infinite queries")
+    for i, (lens, most) in enumerate([([(2, 200), (1, 90)], None), ([(1, 5000), (3, 2000)], None), ([(80, 200)], None),
+                                      ([(1040, 1100)], 20000), ([(300, 5000), (700, 900)], 20000)]):
+        d = _inputs(np.random.default_rng(800 + i), 4, 2, 64, lens)
+        clean = _run(d, max_kv=most)
+        for at, bad in (((1, 2, 5), np.inf), ((0, 0, 63), -np.inf), ((len(d["q"]) - 1, 3, 0), np.nan)):
+            d["q"][at] = bad
+        d["q"][2, 1, :2] = np.inf, -np.inf
+        got = _run(d, max_kv=most)
+        hit = ((1, 2), (0, 0), (len(d["q"]) - 1, 3), (2, 1))
+        assert np.isnan(got[hit[2]]).all() and np.isnan(got[hit[3]]).all()
+        for at in hit:
+            got[at] = clean[at]
+        assert np.array_equal(got.view(np.uint16), clean.view(np.uint16)), lens
