@@ -3,7 +3,7 @@ there, weights far apart, the launch plans of each shape."""
 import numpy as np
 import pytest
 
-from gpu_util import dev, say
+from gpu_util import B3, dev, say, upload_blob, weights
 from kv_plans import PLANS
 from kv_util import PAGE, attention, attention_tolerance
 from test_gpu_kv_attn import _check, _inputs, _run
@@ -190,3 +190,65 @@ def test_infinite_queries_stay_in_their_row():
         for at in hit:
             got[at] = clean[at]
         assert np.array_equal(got.view(np.uint16), clean.view(np.uint16)), lens
+
+
+def test_workspace_shared_with_the_projections():
+    """One buffer for attention whose keys are cut (few rows, a prompt), tq_gemv
+    and tq_gemm in turn, eager and from a graph: the bits of calls with
+    workspaces of their own."""
+    import ternary_weight_base_amd as tq
+    say("one workspace for attention and projections")
+    rng = np.random.default_rng(900)
+    sets = [_inputs(rng, 16, 2, 128, [(1, 5000), (2, 3000)]), _inputs(rng, 32, 8, 128, [(300, 5000)])]
+    most = [5000, 5000]
+    want = [_run(d, max_kv=m) for d, m in zip(sets, most)]
+    shape = {1: (640, 5120), 16: (640, 5120), 100: (640, 5120)}
+    blob = {m: upload_blob(B3, *weights(*nk, 40 + m)) for m, nk in shape.items()}
+    acts = {m: (torch.randint(-127, 128, (m, nk[1]), dtype=torch.int8, device="cuda"), torch.rand(m, device="cuda")) for m, nk in shape.items()}
+    need = [tq.tq_kv_attn_workspace_bytes(len(d["q"]), len(d["kv"]), d["q"].shape[1], d["ks"].shape[1], 128, m) for d, m in zip(sets, most)]
+    proj = [tq.tq_gemv_workspace_bytes(B3, m, *shape[m]) for m in (1, 16)] + [tq.tq_gemm_workspace_bytes(B3, 100, *shape[100])]
+    assert min(need) > 0 and max(proj) > 0, (need, proj)
+    ws = torch.zeros(max(need + proj) // 4 + 4, dtype=torch.int32, device="cuda")
+    y = {m: torch.empty((m, shape[m][0]), device="cuda") for m in shape}
+    g = [{k: dev(v) for k, v in d.items()} for d in sets]
+    outs = [torch.empty_like(x["q"]) for x in g]
+
+    def product(m, w):
+        (tq.tq_gemv if m <= 16 else tq.tq_gemm)(B3, m, *shape[m], blob[m], *acts[m], y[m], w)
+
+    def attend(i):
+        x = g[i]
+        tq.tq_kv_attn(x["q"], x["cu"], x["kv"], x["table"], x["k"], x["v"], x["ks"], x["vs"], outs[i], most[i], ws=ws)
+
+    def all_calls():
+        for m, i in ((1, 0), (100, 1), (16, 0), (1, 1), (100, 0)):
+            product(m, ws)
+            attend(i)
+
+    plain = {}
+    for m in shape:
+        own = torch.zeros(max(proj) // 4 + 4, dtype=torch.int32, device="cuda")
+        product(m, own)
+        plain[m] = y[m].clone()
+
+    def check():
+        torch.cuda.synchronize()
+        assert int(torch.count_nonzero(ws)) == 0
+        for m in shape:
+            assert torch.equal(y[m], plain[m]), m
+        for o, w in zip(outs, want):
+            assert np.array_equal(o.cpu().numpy().view(np.uint16), w.view(np.uint16))
+        for t in (*y.values(), *outs):
+            t.fill_(float("nan"))
+
+    all_calls()
+    check()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            all_calls()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        graph.replay()
+        check()

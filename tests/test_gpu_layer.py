@@ -181,3 +181,34 @@ def test_layer_token_from_a_graph():
         assert np.array_equal(x0.view(np.uint16), x1.view(np.uint16)) and np.array_equal(a0.view(np.uint16), a1.view(np.uint16))
     for p, q in zip(results[0][1], results[1][1]):
         assert np.array_equal(p, q)
+
+
+def test_layer_tokens_with_cut_keys_share_the_workspace():
+    """Tokens on contexts long enough that attention's keys are cut: it and the
+    projections take one workspace in turn, eager and replayed."""
+    import ternary_weight_base_amd as tq
+    say("decoder layer, attention in pieces")
+    rng = np.random.default_rng(13)
+    width = 20
+    L = Layer(700, 2 * width, 2, width)
+    assert tq.tq_kv_attn_workspace_bytes(2, 2, HQ, HKV, D, width * PAGE) > 0
+    cache = Cache(2 * width, HKV, D)
+    lens = _prompt(L, cache, rng)
+    b, cu, kv = L.buffers(2), np.array([0, 1, 2], np.int32), dev(np.array(lens, np.int32))
+    call = lambda: (kv.add_(1), L.token(b, dev_cu, kv, width * PAGE))
+    dev_cu = dev(cu)
+    graph = None
+    for step in range(6):
+        lens = [x + 1 for x in lens]
+        b["res"].copy_(torch.from_numpy(rng.standard_normal((2, H)).astype(np.float32)))
+        if step == 3:
+            s = torch.cuda.Stream()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(s):
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=s):
+                    call()
+        torch.cuda.synchronize()
+        graph.replay() if graph else call()
+        L.check(b, cache, cu, lens, True)
+        assert int(torch.count_nonzero(L.ws)) == 0
