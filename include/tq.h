@@ -422,8 +422,9 @@ int tq_gemm(int fmt, int64_t M, int64_t N, int64_t K, const void *W, const int8_
  * lengths.  A bad entry (a page outside 0..num_pages-1, a position below 0,
  * behind the page table or behind the rope table, cu_rows out of order)
  * leads to no access outside the arrays: such tokens are not stored and not
- * seen, and a query row at such a position is written as zeros by
- * tq_kv_append.
+ * seen.  tq_kv_append writes a query row as zeros at a position below 0 and,
+ * where it rotates, behind the rope table; elsewhere (behind the page table, on a
+ * page outside the cache) the rotated query is written as for any other row.
  *
  * Heads: head_dim 64 or 128, q_heads a multiple of kv_heads; 1 <= rows <= 2^24,
  * rows * q_heads below 2^30, and a call's workgroups few enough for one launch
