@@ -448,8 +448,10 @@ int tq_rope_table(int64_t positions, int64_t rot, double base, float *table);
  * A page's scale becomes the smallest power of two with max |x| < 128 scale
  * over its tokens and codes are floor(x / scale) + 128; where a token needs
  * a larger scale the page's earlier codes are shifted to it, so the cache
- * holds the same bytes however its tokens were cut into calls.  Bytes of
- * slots behind the sequence's last token keep what they held.
+ * holds the same bytes however its tokens were cut into calls.  (So tokens may
+ * only join a page whose scales are powers of two or 0, as this call leaves them;
+ * beside another scale the earlier codes are not adapted.)  Bytes of slots
+ * behind the sequence's last token keep what they held.
  * Two sequences of a call, or two places of one, must not append to the same
  * page (its contents are then unspecified); full pages may be shared.  A token at a page's
  * start begins the page anew: rewriting a sequence from such a position (or,
