@@ -184,7 +184,10 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(const NormArgs A) {
     }
   }
   if (!A.q) return;
-  // int8 by absmax as tq_quant_act, the factor by a reciprocal: 127 (1 / a)
+  // int8 by absmax as tq_quant_act, the factor by a reciprocal: 127 (1 / a).  That is
+  // what x * (127 / a) comes to for a tensor a in torch, and what the header says:
+  // a plain evaluation there gives the same codes.  (tq_quant_act divides once, 127 / a;
+  // at most one code in 2^15 differs, by one step, as the factors differ by 2^-23.)
   m = tqdev::wave_max64(m);
   if ((tid & 63) == 0) wmax[tid >> 6] = m;
   __syncthreads();
