@@ -252,3 +252,69 @@ def test_workspace_shared_with_the_projections():
         torch.cuda.synchronize()
         graph.replay()
         check()
+
+
+@pytest.mark.parametrize("rows,seqs,most", [(40, 40, 3000), (60, 12, 5000), (40, 40, 1000), (1040, 3, 20000), (700, 3, 20000)])
+def test_graph_with_rows_dealt_anew(rows, seqs, most):
+    """Captured once; then cu_rows and kv_len give the rows to other sequences:
+    one row each, all rows to one sequence, rows of padding, sequences without
+    any, contexts shorter and longer than they were."""
+    import ternary_weight_base_amd as tq
+    say(f"attention in a graph, {rows} rows of {seqs} sequences dealt anew")
+    rng = np.random.default_rng(rows + seqs)
+    hq, hkv, dim, longest = (16, 8, 64, most) if rows <= 60 else (4, 2, 128, 1500)
+    d = _inputs(rng, hq, hkv, dim, [(rows // seqs + (s < rows % seqs), longest) for s in range(seqs)])
+    g = {k: dev(v) for k, v in d.items()}
+    out = torch.empty(d["q"].shape, dtype=torch.float16, device="cuda")
+    ws = tq.kv_attn_workspace(rows, seqs, hq, hkv, dim, most)
+
+    def call():
+        tq.tq_kv_attn(g["q"], g["cu"], g["kv"], g["table"], g["k"], g["v"], g["ks"], g["vs"], out, most, ws=ws)
+
+    call()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call()
+    even = d["cu"].copy()
+    first, last = np.full(seqs + 1, rows), np.zeros(seqs + 1)
+    first[0] = 0
+    last[-1] = rows
+    some = np.minimum(np.arange(seqs + 1) // 2 * 2, rows - 5)  # every other one without rows, padding behind
+    for cu in (even, first, last, some, np.sort(np.concatenate(([0], rng.integers(0, rows + 1, seqs - 1), [rows]))), even):
+        d["cu"] = cu.astype(np.int32)
+        d["kv"] = np.minimum(rng.integers(0, longest + 1, seqs) + np.diff(d["cu"]) // 2, longest).astype(np.int32)
+        g["cu"].copy_(dev(d["cu"]))
+        g["kv"].copy_(dev(d["kv"]))
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.cpu().numpy()
+        _check(d, got)
+        assert np.array_equal(got.view(np.uint16), _run(d, max_kv=most).view(np.uint16))
+        assert ws is None or int(torch.count_nonzero(ws)) == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls with workspaces of their own beside each other on two streams."""
+    import ternary_weight_base_amd as tq
+    say("attention on two streams at once")
+    rng = np.random.default_rng(950)
+    sets = [_inputs(rng, 16, 2, 128, [(1, 9000), (3, 4000)]), _inputs(rng, 32, 8, 128, [(300, 5000)])]
+    want = [_run(d, max_kv=9000) for d in sets]
+    g = [{k: dev(v) for k, v in d.items()} for d in sets]
+    outs = [[torch.empty_like(x["q"]) for _ in range(20)] for x in g]
+    spaces = [tq.kv_attn_workspace(len(d["q"]), len(d["kv"]), d["q"].shape[1], d["ks"].shape[1], 128, 9000) for d in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for n in range(20):
+        for x, o, w, s in zip(g, outs, spaces, streams):
+            tq.tq_kv_attn(x["q"], x["cu"], x["kv"], x["table"], x["k"], x["v"], x["ks"], x["vs"], o[n], 9000, ws=w, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for x in o:
+            assert np.array_equal(x.cpu().numpy().view(np.uint16), w.view(np.uint16))
+    assert all(int(torch.count_nonzero(w)) == 0 for w in spaces)
