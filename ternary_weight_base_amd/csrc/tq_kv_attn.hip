@@ -41,11 +41,12 @@
 // Measured, 64 query and 8 KV heads of 128 (a plain streaming read reaches 6.9
 // TB/s, a large fp16 matrix product 1202 TFLOP/s):
 //   one token over 517 tokens            9 us
-//   one token over 131001 tokens        53 us   5.1 TB/s
-//   64 sequences of up to 8190 tokens  123 us   5.5 TB/s
+//   one token over 131001 tokens        53 us   5.0 TB/s
+//   64 sequences of up to 8190 tokens  125 us   5.4 TB/s
 //   64 sequences of up to 32 K tokens  436 us   6.2 TB/s
 //   8 sequences of up to 6001, 4 rows   27 us   2.6 TB/s
-//   a prompt of 4096 tokens            309 us   890 TFLOP/s
+//   a prompt of 4096 tokens            315 us   870 TFLOP/s
+// decode_kernel<128, 2, false> takes 256 registers and spills 11 more.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -64,8 +65,8 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 constexpr int kRows = 16;  // (token, query head) rows of a decode workgroup
 constexpr int kWaves = 8;  // of a decode workgroup
 constexpr int kDecPieces = 128;  // pieces of a unit at most (and one or two more)
-// Pages, see "few rows".  A piece has kLeast at least: one token of 1100 10.8 us, of
-// 4096 12.0 (8: 13.7, 13.0; 3: 10.9, 13.1).  Units of up to kWhole stay whole: 64
+// Pages, see "few rows".  A piece has kLeast at least: one token of 1100 10.9 us, of
+// 4096 12.1 (8: 13.7, 13.0; 3: 10.9, 13.1).  Units of up to kWhole stay whole: 64
 // sequences of up to 700 tokens 17.6 us (8: 35; 32: 17.5).  A cut leaves kSnap at
 // least on both sides (the workspace's two results a workgroup rest on per >= kSnap).
 constexpr int kSnap = 4, kLeast = 4, kWhole = 16;
@@ -1281,14 +1282,15 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
   // by the lengths there are.  It takes (us of decode against prefill; 64 query
   // and 8 KV heads of 128, sequences x rows on up to so many tokens)
   //  - up to 32 (row, query head) rows a sequence;
-  //  - up to half a tile of 32 a CU (1 x 16 on 600 12.4 against 28.2, on 6001 25.0
-  //    against 56.5; 1 x 64 on 30000 116 against 136), up to a tile a CU on up to
-  //    12 K tokens (1 x 96 on 12000 91 against 99, on 30000 211 against 148), up to
-  //    two on up to 1024 (1 x 256 on 600 23 against 31; 1 x 180 on 4000 81 against 62);
+  //  - up to half a tile of 32 a CU (1 x 16 on 600 12.5 against 21.7, on 6001 25.3
+  //    against 56.9; 1 x 64 on 30000 118 against 139), up to a tile a CU on up to
+  //    12 K tokens (1 x 96 on 12000 92 against 96, on 30000 213 against 152), up to
+  //    two on up to 1024 (1 x 180 on 1000 28.8 against 30.2, on 4000 82 against 62;
+  //    1 x 256 on 600 23.5 against 22.7);
   //  - up to two tiles a CU of up to 64 rows a sequence, which fill half of a tile of
-  //    128, on more than 3500 tokens (32 x 8 on 4000 87 against 126, on 8000 146
-  //    against 179; 24 x 8 on 2000 56 against 47; 24 x 12, three tiles each, on 8000
-  //    161 against 143; 64 x 8, four a CU, on 4000 167 against 146).
+  //    128, on more than 3500 tokens (32 x 8 on 4000 87 against 128, on 8000 147
+  //    against 183; 24 x 8 on 2000 56 against 47; 24 x 12, three tiles each, on 8000
+  //    163 against 146; 64 x 8, four a CU, on 4000 170 against 149).
   // The tiles are counted as of sequences with the same number of rows.
   const int64_t each = (flat + seqs - 1) / seqs, tiles32 = (each + 31) / 32 * seqs * kv_heads;
   const int64_t most = max_kv <= 1024 || (each <= 64 && max_kv > 3500) ? 2 * kCus : max_kv <= 12288 ? kCus : kCus / 2;
