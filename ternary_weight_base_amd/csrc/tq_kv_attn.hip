@@ -1318,23 +1318,24 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
     if (rest && nsplit > 2 * round / rest) nsplit = 2 * round / rest;
     if (nsplit > tiles / 4) nsplit = tiles / 4;
     if (rest == all && tiles <= 32 && each >= R) {
-      // One round of full tiles and few pages: the number of pieces that should take least, in 10
-      // ns.  A page takes a workgroup 1.25 us alone on its CU and 2.34 beside another
-      // (64 elements: 0.98 and 1.37, slopes of 1 x 264 and 3 x 264 rows); pieces cost
-      // 12 us (64 elements: 6, and 1 each) and the time of their partial results, 66 (33)
-      // KB each, written and read.  (1 x 256 rows on 2000, 64 and 8 heads: one piece 49
-      // us, two 47, four 60; 1 x 300, 32 and 8 heads: one 50, two 45, three 42, four 48.  Of
-      // 64: 1 x 256 on 2000, 64 and 8 heads, one 38, two 33, four 37; 1 x 300, 32 and 8,
-      // one 38, three 29, four 32; 3 x 300, 24 and 4, one 40, two 43; on 1000 one 23,
-      // three 30.  More pages: 1 x 180 on 4000 one 92, two 64, five 62; 3 x 200 on 3000,
-      // 32 and 8 heads, two 73, four 63.  Tiles half empty: 30 x 13 on 2000, 40 and 8
-      // heads, one 63, two 51.)
+      // One round of full tiles and few pages: the number of pieces that should take
+      // least, in 10 ns.  A page takes a workgroup 1.25 us alone on its CU and 2.34
+      // beside another (64 elements: 0.98 and 1.37, slopes of 1 x 264 and 3 x 264 rows);
+      // pieces cost 12 us (64 elements: 3.5, and 0.5 each) and the time of their partial
+      // results, 66 (33) KB each, written and read.  (1 x 256 rows on 2000, 64 and 8
+      // heads: one piece 49 us, two 47, four 60; 1 x 300, 32 and 8 heads: one 50, two
+      // 45, three 42, four 48.  Heads of 64: 1 x 256 on 2000, 64 and 8 heads, one 38, two
+      // 33, four 37; 1 x 300, 32 and 8, one 38, three 29, four 32; 1 x 1200, 16 and 4,
+      // one 36, three 34; 3 x 300, 24 and 4, one 40, two 43, on 1000 one 23, two 30.
+      // More pages: 1 x 180 on 4000 one 92, two 64, five 62; 3 x 200 on 3000, 32 and 8
+      // heads, two 73, four 63.  Tiles half empty: 30 x 13 on 2000, 40 and 8 heads, one
+      // 63, two 51.)
       const bool wide = head_dim == 128;
       const int64_t pages = tiles - rows / seqs / (2 * kPage);
       int64_t least = 0, best = 1;
       for (int64_t n = 1; n <= nsplit; n++) {
         const int64_t wgs = real * n, page = wgs <= kCus ? (wide ? 125 : 98) : (wide ? 234 : 137);
-        const int64_t cut = (wide ? 1200 : 600 + 100 * n) + wgs * head_dim * 27 / 1280;
+        const int64_t cut = (wide ? 1200 : 350 + 50 * n) + wgs * head_dim * 27 / 1280;
         const int64_t t = (pages + n - 1) / n * page + (n > 1 ? cut : 0);
         if (n == 1 || t < least) least = t, best = n;
       }
