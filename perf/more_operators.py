@@ -310,9 +310,9 @@ def run(st):
         return {"linear": _linear_plain, "shared": _shared_plain, "sample": _sample_plain}[case["op"]](st)
     import ternary_weight_base_amd as tq
     if case["op"] == "linear":
-        if "ws" not in st:  # a server keeps one workspace
-            st["ws"] = tq.linear_attn_workspace(st["total"], case["seqs"], case["q_heads"], case["kv_heads"], case["dim"])
-        tq.tq_linear_attn(st["qkv"], st["decay"], st["cu"], st["from"], st["to"], st["states"], st["out"], ws=st["ws"])
+        if "scratch" not in st:  # a server keeps one
+            st["scratch"] = tq.linear_attn_scratch(st["total"], case["seqs"], case["q_heads"], case["kv_heads"], case["dim"])
+        tq.tq_linear_attn(st["qkv"], st["decay"], st["cu"], st["from"], st["to"], st["states"], st["out"], scratch=st["scratch"])
         return {"out": st["out"], "states": st["states"]}
     if case["op"] == "shared":
         if "ws" not in st:
