@@ -507,6 +507,45 @@ int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
                int64_t sinks, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
                void *stream);
 
+/* Scratch bytes of tq_linear_attn (0 when it needs none, or on a bad shape).
+ * Scratch is device memory that needs no contents and is left with any: it
+ * must not be a workspace of the other calls, which have to find theirs zero.
+ * At most 2^27 bytes and a state for each KV head, or what 128 rows of all KV
+ * heads take (6 kv_heads head_dim^2 bytes) where that is more; not monotonic. */
+size_t tq_linear_attn_scratch_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                                    int64_t head_dim);
+
+/* Linear attention with a decay for each head and a recurrent state (the
+ * pages' model keeps one beside its KV cache, "Ternary Bonsai 2 27B：8GB 显卡硬塞
+ * 27B 三元模型…"): for each KV head, over a sequence's rows t in order,
+ *   S_t = exp(log_decay[t]) S_{t-1} + k_t v_t^T,  out_t = scale q_t^T S_t
+ * with S fp32 [head_dim][head_dim], key index first.  Rows, heads and cu_rows as
+ * above; a row of qkv (dtype, row_stride a multiple of 8) as in tq_kv_append.
+ *   log_decay: fp32, [kv_heads] for all rows (decay_stride 0) or rows
+ *     decay_stride >= kv_heads elements apart.  Above 0 (growth) counts as 0,
+ *     very low (-inf too) as a factor of 0.
+ *   states: fp32 [num_states][kv_heads][head_dim][head_dim].  Sequence s starts
+ *     from state state_from[s] and leaves state_to[s] behind; an index outside
+ *     0..num_states-1 stands for zeros, or nowhere.  Both may be the same (in
+ *     place).  Sequences may start from the same state, but one that another
+ *     sequence of the call writes must be no other's start, and no two write
+ *     the same (those states and outputs are then unspecified).  A sequence
+ *     without rows neither reads nor writes a state.
+ *   out: fp16, rows out_stride elements apart (a multiple of 8).
+ * Up to 16 rows a sequence, on average, the recurrence runs row by row in fp32
+ * (one launch, no scratch); more run in chunks of 128 rows (three launches for
+ * up to 2^27 bytes of scratch), where states keep fp32's accuracy and the
+ * factors of an output's products are rounded to fp16.  A sequence of many rows
+ * beside many single tokens is better a call of its own.  Non-finite inputs make
+ * their sequence's outputs and state for that KV head (from the chunk on that
+ * holds them) unspecified, those of no other.  qkv, states, out and scratch
+ * 16-byte aligned; out does not overlap qkv. */
+int tq_linear_attn(int dtype, int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                   int64_t head_dim, const void *qkv, int64_t row_stride, const float *log_decay,
+                   int64_t decay_stride, const int32_t *cu_rows, const int32_t *state_from,
+                   const int32_t *state_to, float *states, int64_t num_states, float scale, void *out,
+                   int64_t out_stride, void *scratch, size_t scratch_bytes, void *stream);
+
 /* The step from one block to the next, rms(v) = sqrt(mean v^2 + eps):
  *   u  = y / rms(y) * post_w         (post_w NULL: u = y; y NULL: no block, r' = res)
  *   r' = res + res_scale * gate * u  rounded to fp32, then to res_dtype, to res_out

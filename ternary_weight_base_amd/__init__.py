@@ -46,7 +46,7 @@ EXPORTS = ("tq_status_str", "tq_packed_bytes", "tq_pack", "tq_unpack", "tq_quant
            "tq_decode_stack_batch_workspace_bytes", "tq_decode_stack_batch",
            "tq_debug_gemv_quant_rows_sums", "tq_workspace_clear", "tq_workspace_check",
            "tq_rope_table", "tq_kv_append", "tq_kv_attn_workspace_bytes", "tq_kv_attn",
-           "tq_residual_norm", "tq_debug_kv_read")
+           "tq_residual_norm", "tq_debug_kv_read", "tq_linear_attn_scratch_bytes", "tq_linear_attn")
 
 
 class TqLayer(ctypes.Structure):
@@ -104,6 +104,8 @@ def _load():
         "tq_kv_attn": ([I64, I64, I64, I64, I64, P, I64, P, P, P, I64, P, P, P, P, I64, I64, F, I64, I64, P, I64,
                         P, SZ, P], I),
         "tq_residual_norm": ([I, I, I, I64, I64, P, P, P, I64, F64, P, P, P, F64, P, P, P, P], I),
+        "tq_linear_attn_scratch_bytes": ([I64, I64, I64, I64, I64], SZ),
+        "tq_linear_attn": ([I, I64, I64, I64, I64, I64, P, I64, P, I64, P, P, P, P, I64, F, P, I64, P, SZ, P], I),
         "tq_debug_kv_read": ([I, I64, I64, I64, P, P, P, P, P, I64, P, P], I),
     }
     for name, (args, res) in sig.items():
@@ -510,6 +512,58 @@ def tq_kv_attn(q, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scal
         wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
     rc = lib.tq_kv_attn(rows, seqs, q_heads, heads, dim, qp, qs, *cache, max_kv_len,
                         dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, op, os_, wp, wb, st)
+    if rc:
+        raise TQError(rc, what)
+
+
+def tq_linear_attn_scratch_bytes(rows, seqs, q_heads, kv_heads, head_dim) -> int:
+    return int(lib.tq_linear_attn_scratch_bytes(rows, seqs, q_heads, kv_heads, head_dim))
+
+
+def linear_attn_scratch(rows, seqs, q_heads, kv_heads, head_dim, device="cuda"):
+    """A scratch tensor for tq_linear_attn (None when it needs none); not a workspace: it need not be zero."""
+    import torch
+    nbytes = tq_linear_attn_scratch_bytes(rows, seqs, q_heads, kv_heads, head_dim)
+    return torch.empty((nbytes + 15) // 16 * 4, dtype=torch.int32, device=device) if nbytes else None
+
+
+def tq_linear_attn(qkv, log_decay, cu_rows, state_from, state_to, states, out, scale=None, scratch=None, stream=None) -> None:
+    """out fp16 [rows][q_heads][head_dim] = linear attention of the rows of qkv
+    [rows][(q_heads + 2 kv_heads) head_dim] (fp16 or fp32), from the states
+    state_from[seq] (outside the pool: zeros), whose successors go to
+    state_to[seq] (outside: nowhere).  states fp32 [num][kv_heads][head_dim][head_dim]
+    (key index first); log_decay fp32 [kv_heads] or [rows][kv_heads].  Rows of
+    qkv, log_decay and out may be strided.  scale defaults to head_dim ** -0.5."""
+    what, T = "tq_linear_attn", _Torch.get()
+    dev, st = _current(T, stream, states)
+    if states.dim() != 4 or out.dim() != 3 or qkv.dim() != 2:
+        raise ValueError(f"{what}: states must have shape [num][kv_heads][head_dim][head_dim], out three dimensions, qkv two")
+    num, heads, dim, _ = states.shape
+    rows, q_heads, _ = out.shape
+    i32, f32 = T.i32, T.f32
+    seqs = state_from.shape[0] if state_from.dim() else 0
+    if not (states.dtype is f32 and states.shape == (num, heads, dim, dim) and states.is_contiguous()
+            and cu_rows.dtype is state_from.dtype is state_to.dtype is i32 and cu_rows.shape == (seqs + 1,)
+            and state_from.shape == state_to.shape == (seqs,) and cu_rows.is_contiguous() and state_from.is_contiguous()
+            and state_to.is_contiguous() and states.get_device() == cu_rows.get_device() == state_from.get_device()
+            == state_to.get_device() == dev):
+        for name, t, dtype, shape in (("states", states, f32, (num, heads, dim, dim)), ("state_from", state_from, i32, (seqs,)),
+                                      ("cu_rows", cu_rows, i32, (seqs + 1,)), ("state_to", state_to, i32, (seqs,))):
+            _need(what, name, t, dtype, shape, dev)
+    x, xs = _rows_need(what, "qkv", qkv, qkv.dtype, (rows, (q_heads + 2 * heads) * dim), dev)
+    if log_decay.dim() == 1:
+        g, gs = _need(what, "log_decay", log_decay, f32, (heads,), dev), 0
+    else:
+        g, gs = _rows_need(what, "log_decay", log_decay, f32, (rows, heads), dev)
+    op, os_ = _rows_need(what, "out", out, T.f16, (rows, q_heads, dim), dev)
+    wp, wb = None, 0
+    if scratch is not None:
+        if scratch.get_device() != dev or not scratch.is_contiguous():
+            raise ValueError(f"{what}: scratch must be contiguous and on the current GPU")
+        wp, wb = scratch.data_ptr(), scratch.numel() * scratch.element_size()
+    rc = lib.tq_linear_attn(T.acts.get(qkv.dtype, -1), rows, seqs, q_heads, heads, dim, x, xs, g, gs, cu_rows.data_ptr(),
+                            state_from.data_ptr(), state_to.data_ptr(), states.data_ptr(), num,
+                            dim ** -0.5 if scale is None else scale, op, os_, wp, wb, st)
     if rc:
         raise TQError(rc, what)
 

@@ -1,0 +1,704 @@
+// tq_linear.hip -- linear attention with a decay for each head.
+//
+//   S_t = a_t S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t,   a_t = exp(log_decay_t)
+//
+// with an fp32 state S [head_dim][head_dim] (key index first) a sequence and
+// KV head.  Two forms:
+//
+// Few rows a sequence: the recurrence itself, in fp32.  A workgroup holds 64
+// columns of a state in registers, a wave a quarter of their rows.  Bound: the
+// states' bytes, read and written once.
+//
+// Prompts, in chunks of 128 rows (G: the chunk's running sum of log2 a):
+//   o_i = scale (2^G_i q_i S + sum_{j <= i} 2^(G_i - G_j) (q_i . k_j) v_j)
+//   S'  = 2^G_n S + U,   U = sum_j 2^(G_n - G_j) k_j v_j^T
+// in three launches: every chunk's U; the states before each chunk, element by
+// element along the chunks; every chunk's outputs.
+//
+// Products run on v_mfma_f32_32x32x16_f16, sums in fp32.  fp16 operands are
+// scaled by powers of two into its range, so no size of input overflows it.
+// U is of two fp16 terms a factor (fp16 inputs: the keys with their weights
+// two, the values are exact), so the state keeps fp32's accuracy.  For the
+// outputs, which are fp16, every factor is rounded to fp16 once.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "tq.h"
+#include "tq_device.h"
+#include "tq_kv.h"
+#include "tq_wave.h"
+
+namespace {
+
+using namespace tqkv;
+
+constexpr int kChunk = 128;     // rows of a chunk
+constexpr int kStep = 64;       // ... of them that U's kernel takes at once
+constexpr int kFewRows = 16;    // up to so many rows a sequence (on average): the recurrence
+constexpr size_t kPassBytes = (size_t)1 << 27;  // scratch of a pass over the chunks
+constexpr int kNoState = -100000;  // exponent of a snapshot that is zero
+
+typedef float f16x __attribute__((ext_vector_type(16)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4 lds_s4;
+
+struct Meta {
+  float decay, most_u, most_s;  // log2 of the chunk's decay; max |U|; max |S| before the pass's first chunk
+  int e;                        // the snapshot holds S * 2^-e
+};
+
+struct LinArgs {
+  const void *qkv;
+  const float *log_decay;
+  const int *cu, *from, *to;
+  float *states;
+  _Float16 *out;
+  int64_t row_stride, decay_stride, out_stride, num_states;
+  float scale;
+  int rows, seqs, hq, hkv, group;
+  // a pass over the chunks: slots slot0 .. slot0 + slots - 1
+  float *u, *carry;
+  _Float16 *snap;
+  Meta *meta;
+  int slot0, slots, parts;
+};
+
+__device__ __forceinline__ bool state_ok(const LinArgs &A, int id) { return id >= 0 && id < A.num_states; }
+
+// log2 of a row's decay: above 0 (growth) counts as 0, below -2000 as -2000 (a factor of 0).
+__device__ __forceinline__ double log2_decay(const LinArgs &A, int row, int h) {
+  const double g = (double)A.log_decay[row * A.decay_stride + h] * 1.4426950408889634;
+  return fmin(fmax(g, -2000.0), 0.0);
+}
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const f4 a = *reinterpret_cast<const f4 *>(p), b = *reinterpret_cast<const f4 *>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
+}
+__device__ __forceinline__ void load8(const _Float16 *p, float (&v)[8]) {
+  const h8 a = *reinterpret_cast<const h8 *>(p);
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = (float)a[i];
+}
+
+// ---- few rows a sequence ---------------------------------------------------
+
+constexpr int kHeads = 8;  // query heads taken together
+
+template <int D, typename T>
+__global__ __launch_bounds__(256) void recur_kernel(const LinArgs A) {
+  constexpr int kOwn = D / 4;  // rows of the state a wave
+  __shared__ __attribute__((aligned(16))) float ks[D], qs[kHeads][D], red[4][kHeads][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t blk = blockIdx.x % (uint32_t)(D / 64), sh = blockIdx.x / (uint32_t)(D / 64);
+  const int h = sh % (uint32_t)A.hkv, s = sh / (uint32_t)A.hkv;
+  const int begin = cu_at(A.cu, s, A.rows), n = cu_at(A.cu, s + 1, A.rows) - begin;
+  if (n <= 0) return;
+  const int from = A.from[s], to = A.to[s], col = blk * 64 + lane;
+  float S[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; i++) S[i] = 0.0f;
+  if (state_ok(A, from)) {
+    const float *p = A.states + ((int64_t)from * A.hkv + h) * (D * D) + wave * kOwn * D + col;
+#pragma unroll
+    for (int i = 0; i < kOwn; i++) S[i] = p[i * D];
+  }
+  for (int r = 0; r < n; r++) {
+    const T *x = (const T *)A.qkv + (int64_t)(begin + r) * A.row_stride;
+    const float v = (float)x[(A.hq + A.hkv + h) * D + col];
+    const float a = __builtin_amdgcn_exp2f((float)log2_decay(A, begin + r, h));
+    for (int g0 = 0; g0 < A.group; g0 += kHeads) {
+      const int heads = min(kHeads, A.group - g0);
+      __syncthreads();
+      if (g0 == 0)
+        for (int i = tid; i < D; i += 256) ks[i] = (float)x[(A.hq + h) * D + i];
+      for (int i = tid; i < heads * D; i += 256) qs[i / D][i % D] = (float)x[(h * A.group + g0) * D + i] * A.scale;
+      __syncthreads();
+      if (g0 == 0) {
+#pragma unroll
+        for (int i = 0; i < kOwn; i++) S[i] = a * S[i] + ks[wave * kOwn + i] * v;
+      }
+      for (int g = 0; g < heads; g++) {
+        float o = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kOwn; i++) o += qs[g][wave * kOwn + i] * S[i];
+        red[wave][g][lane] = o;
+      }
+      __syncthreads();
+      for (int i = tid; i < heads * 64; i += 256) {
+        const int g = i / 64, c = i % 64;
+        const float o = (red[0][g][c] + red[1][g][c]) + (red[2][g][c] + red[3][g][c]);
+        A.out[(int64_t)(begin + r) * A.out_stride + (h * A.group + g0 + g) * D + blk * 64 + c] = (_Float16)o;
+      }
+    }
+  }
+  if (state_ok(A, to)) {
+    float *p = A.states + ((int64_t)to * A.hkv + h) * (D * D) + wave * kOwn * D + col;
+#pragma unroll
+    for (int i = 0; i < kOwn; i++) p[i * D] = S[i];
+  }
+}
+
+// ---- prompts ---------------------------------------------------------------
+
+// A chunk: n rows from `begin` on, the `local`-th of sequence s.
+struct Chunk {
+  int s, begin, n, local;
+};
+__device__ __forceinline__ bool find_chunk(const LinArgs &A, int slot, Chunk &c) {
+  c.s = find_seq<kChunk, 1>(A.cu, A.seqs, A.rows, slot, 1);
+  const int first = cu_at(A.cu, c.s, A.rows), end = cu_at(A.cu, c.s + 1, A.rows);
+  c.local = slot - slot_base<kChunk, 1>(first, c.s, 1);
+  if (c.local < 0 || c.local >= (end - first + kChunk - 1) / kChunk || end <= first) return false;
+  c.begin = first + c.local * kChunk;
+  c.n = min(kChunk, end - c.begin);
+  return true;
+}
+
+// Running sums of the chunk's log2 decays, by one wave: lane l's are of rows
+// 2 l and 2 l + 1; rows behind the chunk do not decay.
+__device__ __forceinline__ void decay_sums(const LinArgs &A, const Chunk &c, int h, double &g0, double &g1) {
+  const int lane = threadIdx.x & 63;
+  const double d0 = 2 * lane < c.n ? log2_decay(A, c.begin + 2 * lane, h) : 0.0;
+  const double d1 = 2 * lane + 1 < c.n ? log2_decay(A, c.begin + 2 * lane + 1, h) : 0.0;
+  double sum = d0 + d1;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const double o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
+  }
+  g1 = sum;
+  g0 = sum - d1;
+}
+
+// A tile of fp16 rows in LDS whose operands are read transposed (below):
+// 64-byte blocks of a row in an order that puts the same block of four
+// consecutive rows into different banks.  -> byte offset of a block
+template <int D>
+__device__ __forceinline__ int block_at(int row, int blk) {
+  return row * 2 * D + ((blk ^ (D == 128 ? row & 3 : (row >> 1) & 1)) << 6);
+}
+template <int D>
+__device__ __forceinline__ int piece_at(int row, int piece) {  // 8 elements
+  return block_at<D>(row, piece >> 2) + (piece & 3) * 16;
+}
+
+// A matrix operand from such a tile: lane l takes column 32 blk + l % 32 of rows
+// row0 + 8 (l / 32) + 0 .. 7.  ds_read_b64_tr_b16 turns 4 rows x 16 columns
+// among 16 lanes.
+template <int D>
+struct Turned {
+  int at;  // this lane's byte offset in rows 0 .. 15, block 0 but for the order
+  int sw;
+  __device__ __forceinline__ Turned() {
+    const int lane = threadIdx.x & 63, row = 8 * (lane >> 5) + ((lane & 15) >> 2);
+    sw = D == 128 ? row & 3 : (row >> 1) & 1;
+    at = row * 2 * D + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+  }
+  __device__ __forceinline__ h8 operator()(const uint8_t *tile, int row0, int blk) const {
+    const uint8_t *p = tile + at + ((blk ^ sw) << 6) + row0 * 2 * D;
+    const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p);
+    const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 8 * D));
+    const h4 x = __builtin_bit_cast(h4, a), y = __builtin_bit_cast(h4, b);
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+// e with |v| < 2^e, at least -100 (so that scaling by 2^(14 - e) stays finite)
+__device__ __forceinline__ int exponent(float v) { return max(__builtin_amdgcn_frexp_expf(v), -100); }
+
+template <int D, typename T>
+__global__ __launch_bounds__(256) void chunk_state_kernel(const LinArgs A) {
+  constexpr bool kWide = std::is_same<T, float>::value;
+  constexpr int kPer = kStep * (D / 8) / 256;     // pieces of 8 elements a thread
+  constexpr int kNb = D == 128 ? 4 : 1;           // column blocks of 32 a wave
+  constexpr int kTile = kStep * 2 * D;
+  __shared__ __attribute__((aligned(16))) uint8_t kh[kTile], kl[kTile], vh[kTile], vl[kWide ? kTile : 16];
+  __shared__ float w[kChunk], red[2][4], most[4], most0[4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = blockIdx.x % (uint32_t)A.hkv, rel = blockIdx.x / (uint32_t)A.hkv;
+  Chunk c;
+  if (!find_chunk(A, A.slot0 + rel, c)) return;
+  Meta *meta = A.meta + (int64_t)rel * A.hkv + h;
+  if (wave == 0) {
+    double g0, g1;
+    decay_sums(A, c, h, g0, g1);
+    const double all = __shfl(g1, 63);
+    w[2 * lane] = __builtin_amdgcn_exp2f((float)(all - g0));
+    w[2 * lane + 1] = __builtin_amdgcn_exp2f((float)(all - g1));
+    if (lane == 0) meta->decay = (float)all;
+  }
+  // the largest element of the state that the pass starts from
+  if (c.local == 0 || rel == 0) {
+    const int from = A.from[c.s];
+    const float *p = c.local ? A.carry + (int64_t)h * (D * D) : state_ok(A, from) ? A.states + ((int64_t)from * A.hkv + h) * (D * D) : nullptr;
+    float m = 0.0f;
+    if (p) {
+#pragma unroll 4
+      for (int i = tid * 4; i < D * D; i += 1024) {
+        const f4 x = *reinterpret_cast<const f4 *>(p + i);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+      }
+    }
+    m = tqdev::wave_max64(m);
+    if (lane == 0) most0[wave] = m;
+  }
+  const int mb = D == 128 ? wave : wave & 1, nb0 = D == 128 ? 0 : wave >> 1;
+  const Turned<D> turned;
+  f16x acc[kNb];
+#pragma unroll
+  for (int b = 0; b < kNb; b++) acc[b] = (f16x)(0.0f);
+  int unit = kNoState;  // acc holds U * 2^(28 - unit)
+  const T *kp = (const T *)A.qkv + (int64_t)c.begin * A.row_stride + (A.hq + h) * D;
+  const T *vp = kp + A.hkv * D;
+  for (int t0 = 0; t0 < c.n; t0 += kStep) {
+    float k[kPer][8], v[kPer][8], mk = 0.0f, mv = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      const int p = i * 256 + tid, row = t0 + p / (D / 8), at = p % (D / 8) * 8;
+      if (row < c.n) {
+        load8(kp + row * A.row_stride + at, k[i]);
+        load8(vp + row * A.row_stride + at, v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) k[i][j] = v[i][j] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        mk = fmaxf(mk, fabsf(k[i][j]));
+        mv = fmaxf(mv, fabsf(v[i][j]));
+      }
+    }
+    mk = tqdev::wave_max64(mk);
+    mv = tqdev::wave_max64(mv);
+    if (lane == 0) {
+      red[0][wave] = mk;
+      red[1][wave] = mv;
+    }
+    __syncthreads();  // (and the last step's operands are read)
+    mk = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    mv = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+    const int ek = exponent(mk), ev = exponent(mv), now = max(unit, ek + ev);
+    if (now != unit) {
+#pragma unroll
+      for (int b = 0; b < kNb; b++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) acc[b][r] = ldexpf(acc[b][r], max(unit - now, -200));
+    }
+    unit = now;
+    const int shift = 14 - ek + max(ek + ev - now, -300);
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      const int p = i * 256 + tid, row = p / (D / 8), at = piece_at<D>(row, p % (D / 8));
+      const float f = ldexpf(w[t0 + row], shift);
+      h8 a, b, x, y;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        // (held as fp32: the product may not be made again in one rounding to
+        // fp16 for one of its two uses, which would differ now and then)
+        float kw = k[i][j] * f;
+        asm("" : "+v"(kw));
+        const float vs = ldexpf(v[i][j], 14 - ev);
+        a[j] = (_Float16)kw;
+        b[j] = (_Float16)(kw - (float)a[j]);
+        x[j] = (_Float16)vs;
+        y[j] = (_Float16)(vs - (float)x[j]);
+      }
+      *reinterpret_cast<h8 *>(kh + at) = a;
+      *reinterpret_cast<h8 *>(kl + at) = b;
+      *reinterpret_cast<h8 *>(vh + at) = x;
+      if constexpr (kWide) *reinterpret_cast<h8 *>(vl + at) = y;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kStep; t += 16) {
+      const h8 a = turned(kh, t, mb), b = turned(kl, t, mb);
+#pragma unroll
+      for (int nb = 0; nb < kNb; nb++) {
+        const h8 x = turned(vh, t, nb0 + nb);
+        acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, x, acc[nb], 0, 0, 0);
+        acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, x, acc[nb], 0, 0, 0);
+        if constexpr (kWide) acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, turned(vl, t, nb0 + nb), acc[nb], 0, 0, 0);
+      }
+    }
+  }
+  // acc[b][r] is row 32 mb + 8 (r / 4) + 4 (lane / 32) + r % 4, column 32 (nb0 + b) + lane % 32
+  float *u = A.u + ((int64_t)rel * A.hkv + h) * (D * D) + (32 * mb + 4 * (lane >> 5)) * D + 32 * nb0 + (lane & 31);
+  float m = 0.0f;
+#pragma unroll
+  for (int b = 0; b < kNb; b++)
+#pragma unroll
+    for (int r = 0; r < 16; r++) {
+      const float x = ldexpf(acc[b][r], unit - 28);
+      u[(8 * (r >> 2) + (r & 3)) * D + 32 * b] = x;
+      m = fmaxf(m, fabsf(x));
+    }
+  m = tqdev::wave_max64(m);
+  if (lane == 0) most[wave] = m;
+  __syncthreads();
+  if (tid == 0) {
+    meta->most_u = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    meta->most_s = c.local == 0 || rel == 0 ? fmaxf(fmaxf(most0[0], most0[1]), fmaxf(most0[2], most0[3])) : 0.0f;
+  }
+}
+
+// The states before each chunk (fp16, scaled), and the last one: a thread has
+// four elements of a state.
+template <int D>
+__global__ __launch_bounds__(64) void scan_kernel(const LinArgs A) {
+  constexpr uint32_t kBlocks = D * D / 256;
+  constexpr int kAhead = 4;
+  const uint32_t blk = blockIdx.x % kBlocks, sh = blockIdx.x / kBlocks;
+  const int h = sh % (uint32_t)A.hkv, s = sh / (uint32_t)A.hkv, at = blk * 256 + threadIdx.x * 4;
+  const int begin = cu_at(A.cu, s, A.rows), n = cu_at(A.cu, s + 1, A.rows) - begin;
+  if (n <= 0) return;
+  const int base = slot_base<kChunk, 1>(begin, s, 1), end = base + (n + kChunk - 1) / kChunk;
+  const int lo = max(base, A.slot0), hi = min(end, A.slot0 + A.slots);
+  if (lo >= hi) return;
+  const int from = A.from[s], to = A.to[s];
+  float *carry = A.carry + (int64_t)h * (D * D) + at;
+  f4 S = {0, 0, 0, 0};
+  if (lo > base) S = *reinterpret_cast<const f4 *>(carry);
+  else if (state_ok(A, from)) S = *reinterpret_cast<const f4 *>(A.states + ((int64_t)from * A.hkv + h) * (D * D) + at);
+  const int64_t r0 = (int64_t)(lo - A.slot0) * A.hkv + h;
+  const float *u = A.u + r0 * (D * D) + at;
+  _Float16 *snap = A.snap + r0 * (D * D) + at;
+  Meta *meta = A.meta + r0;
+  const int count = hi - lo;
+  const int64_t step = (int64_t)A.hkv * (D * D);
+  float bound = meta->most_s;  // of |S|, from the chunks' largest elements
+  for (int c0 = 0; c0 < count; c0 += kAhead) {
+    f4 x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) x[i] = *reinterpret_cast<const f4 *>(u + min(c0 + i, count - 1) * step);
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) {
+      if (c0 + i >= count) break;
+      Meta *m = meta + (int64_t)(c0 + i) * A.hkv;
+      const int e = bound > 0.0f ? exponent(bound) - 15 : kNoState;
+      const int sh16 = bound > 0.0f ? -e : 0;
+      h4 o;
+#pragma unroll
+      for (int j = 0; j < 4; j++) o[j] = (_Float16)ldexpf(S[j], sh16);
+      *reinterpret_cast<h4 *>(snap + (c0 + i) * step) = o;
+      if (blk == 0 && threadIdx.x == 0) m->e = e;
+      const float a = __builtin_amdgcn_exp2f(m->decay);
+      S = S * a + x[i];
+      bound = bound * a + m->most_u;
+    }
+  }
+  if (hi < end) *reinterpret_cast<f4 *>(carry) = S;
+  else if (state_ok(A, to)) *reinterpret_cast<f4 *>(A.states + ((int64_t)to * A.hkv + h) * (D * D) + at) = S;
+}
+
+// The token of a 32-token group that row r of the score product takes: a lane
+// then holds 8 consecutive tokens per 16, as the second product wants them.
+__device__ __forceinline__ int row_token(int r) { return (r & 16) + ((r >> 2) & 1) * 8 + ((r >> 3) & 1) * 4 + (r & 3); }
+
+__device__ __forceinline__ float half_max(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Outputs of a chunk: keys, values and the state in LDS, 32 rows a wave, the
+// query heads that share them one after the other (NW = 8: two at a time).
+template <int D, typename T, int NW>
+__global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
+  constexpr bool kWide = std::is_same<T, float>::value;
+  constexpr int NT = NW * 64, kPer = kChunk * (D / 8) / NT, kTogether = NW / 4;
+  __shared__ __attribute__((aligned(16))) _Float16 kt[kChunk][D + 8];
+  __shared__ __attribute__((aligned(16))) uint8_t vt[kChunk * 2 * D], stt[D * 2 * D];
+  __shared__ __attribute__((aligned(16))) float ghi[kChunk], glo[kChunk];
+  __shared__ float red[2][NW];
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t part = blockIdx.x % (uint32_t)A.parts, rh = blockIdx.x / (uint32_t)A.parts;
+  const int h = rh % (uint32_t)A.hkv, rel = rh / (uint32_t)A.hkv;
+  Chunk c;
+  if (!find_chunk(A, A.slot0 + rel, c)) return;
+  const int64_t rs = (int64_t)rel * A.hkv + h;
+  const int es = A.meta[rs].e;
+  const T *kp = (const T *)A.qkv + (int64_t)c.begin * A.row_stride + (A.hq + h) * D;
+  const T *vp = kp + A.hkv * D;
+  int ek = 14, ev = 14;  // kt holds k * 2^(14 - ek); fp16 inputs are taken as they are
+  {
+    float k[kPer][8], v[kPer][8], mk = 0.0f, mv = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      const int p = i * NT + tid, row = p / (D / 8), at = p % (D / 8) * 8;
+      if (row < c.n) {
+        load8(kp + row * A.row_stride + at, k[i]);
+        load8(vp + row * A.row_stride + at, v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) k[i][j] = v[i][j] = 0.0f;
+      }
+      if constexpr (kWide) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          mk = fmaxf(mk, fabsf(k[i][j]));
+          mv = fmaxf(mv, fabsf(v[i][j]));
+        }
+      }
+    }
+    if (es != kNoState) {
+      const _Float16 *sp = A.snap + rs * (D * D);
+#pragma unroll
+      for (int i = 0; i < D * (D / 8) / NT; i++) {
+        const int p = i * NT + tid;
+        *reinterpret_cast<uint4 *>(stt + piece_at<D>(p / (D / 8), p % (D / 8))) = *reinterpret_cast<const uint4 *>(sp + 8 * p);
+      }
+    }
+    if (wave == 0) {
+      double g0, g1;
+      decay_sums(A, c, h, g0, g1);
+      ghi[2 * lane] = (float)g0;
+      glo[2 * lane] = (float)(g0 - (double)(float)g0);
+      ghi[2 * lane + 1] = (float)g1;
+      glo[2 * lane + 1] = (float)(g1 - (double)(float)g1);
+    }
+    if constexpr (kWide) {
+      mk = tqdev::wave_max64(mk);
+      mv = tqdev::wave_max64(mv);
+      if (lane == 0) {
+        red[0][wave] = mk;
+        red[1][wave] = mv;
+      }
+      __syncthreads();
+      mk = mv = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NW; i++) {
+        mk = fmaxf(mk, red[0][i]);
+        mv = fmaxf(mv, red[1][i]);
+      }
+      ek = exponent(mk);
+      ev = exponent(mv);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      const int p = i * NT + tid, row = p / (D / 8), at = p % (D / 8);
+      h8 a, b;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        a[j] = (_Float16)(kWide ? ldexpf(k[i][j], 14 - ek) : k[i][j]);
+        b[j] = (_Float16)(kWide ? ldexpf(v[i][j], 14 - ev) : v[i][j]);
+      }
+      *reinterpret_cast<h8 *>(&kt[row][8 * at]) = a;
+      *reinterpret_cast<h8 *>(vt + piece_at<D>(row, at)) = b;
+    }
+  }
+  __syncthreads();
+  // the two waves of a SIMD take a row block with few earlier tokens and one with many
+  const int rb = wave < 4 ? wave : 7 - wave;
+  if (32 * rb >= c.n) return;
+  const int row = 32 * rb + n;
+  const bool valid = row < c.n;
+  const Turned<D> turned;
+  const float gh = ghi[row], gl = glo[row];
+  const int per = (A.group + A.parts - 1) / A.parts, end = min((int)(part + 1) * per, A.group);
+  for (int g = part * per + wave / 4; g < end; g += kTogether) {
+    const int head = h * A.group + g;
+    const T *qp = (const T *)A.qkv + (int64_t)(c.begin + (valid ? row : c.n - 1)) * A.row_stride + head * D;
+    h8 qf[D / 16];
+    int eq = 14;
+    {
+      float q[D / 16][8], m = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 16; j++) load8(qp + 16 * j + 8 * half, q[j]);
+      if constexpr (kWide) {
+#pragma unroll
+        for (int j = 0; j < D / 16; j++)
+#pragma unroll
+          for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(q[j][i]));
+        eq = exponent(half_max(m));
+      }
+#pragma unroll
+      for (int j = 0; j < D / 16; j++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) qf[j][i] = (_Float16)(kWide ? ldexpf(q[j][i], 14 - eq) : q[j][i]);
+    }
+    // scores S^T = K Q^T: sc[t][r] is token 32 t + 16 (r / 8) + 8 half + r % 8
+    f16x sc[4];
+    float mp = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+      sc[t] = (f16x)(0.0f);
+      if (t > rb) continue;
+      const _Float16 *kr = &kt[32 * t + row_token(n)][8 * half];
+#pragma unroll
+      for (int j = 0; j < D / 16; j++)
+        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8 *>(kr + 16 * j), qf[j], sc[t], 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < 16; r++) {
+        const int j = 32 * t + 16 * (r >> 3) + 8 * half + (r & 7);
+        const float wgt = __builtin_amdgcn_exp2f((gh - ghi[j]) + (gl - glo[j]));
+        sc[t][r] = t < rb || j <= row ? sc[t][r] * wgt : 0.0f;
+        mp = fmaxf(mp, fabsf(sc[t][r]));
+      }
+    }
+    // o^T: o[d][r] is element 32 d + 8 (r / 4) + 4 half + r % 4 of the row, in
+    // units of 2^x: of the weights, whose largest is put at 2^15, or of the
+    // state's part where that is larger by 2^60
+    f16x o[D / 32];
+#pragma unroll
+    for (int d = 0; d < D / 32; d++) o[d] = (f16x)(0.0f);
+    mp = half_max(mp);
+    int x = mp > 0.0f ? (eq - 14) + (ek - 14) + __builtin_amdgcn_frexp_expf(mp) - 15 + (ev - 14) : kNoState;
+    if (es != kNoState) {
+#pragma unroll
+      for (int j = 0; j < D / 16; j++)
+#pragma unroll
+        for (int d = 0; d < D / 32; d++)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(turned(stt, 16 * j, d), qf[j], o[d], 0, 0, 0);
+      const int xs = (eq - 14) + es;
+      x = max(x, xs - 60);
+      const float f = ldexpf(__builtin_amdgcn_exp2f(gh + gl), max(xs - x, -300));
+#pragma unroll
+      for (int d = 0; d < D / 32; d++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) o[d][r] *= f;
+    }
+    if (mp == 0.0f && es == kNoState) x = 0;
+    const int xp = max((eq - 14) + (ek - 14) + (ev - 14) - x, -300);
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+      if (t > rb) continue;
+      h8 p[2];
+#pragma unroll
+      for (int r = 0; r < 16; r++) p[r >> 3][r & 7] = (_Float16)ldexpf(sc[t][r], xp);
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int d = 0; d < D / 32; d++)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(turned(vt, 32 * t + 16 * u, d), p[u], o[d], 0, 0, 0);
+    }
+    if (valid) {
+      _Float16 *dst = A.out + (int64_t)(c.begin + row) * A.out_stride + head * D;
+#pragma unroll
+      for (int d = 0; d < D / 32; d++)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          h4 y;
+#pragma unroll
+          for (int i = 0; i < 4; i++) y[i] = (_Float16)(ldexpf(o[d][r + i], x) * A.scale);
+          *reinterpret_cast<h4 *>(dst + 32 * d + 2 * r + 4 * half) = y;
+        }
+    }
+  }
+}
+
+constexpr int kCus = 256;
+
+struct Plan {
+  bool chunked;
+  int64_t slots, pass;  // chunks, and those of a pass
+  size_t carry_bytes, meta_bytes, u_bytes, bytes;
+};
+
+Plan make_plan(int64_t rows, int64_t seqs, int64_t kv_heads, int64_t head_dim) {
+  Plan P = {};
+  P.chunked = rows > kFewRows * seqs;
+  if (!P.chunked) return P;
+  P.slots = rows / kChunk + seqs;
+  const size_t state = (size_t)(kv_heads * head_dim * head_dim);
+  const size_t each = state * 6 + (size_t)kv_heads * sizeof(Meta);
+  P.pass = (int64_t)(kPassBytes / each);
+  if (P.pass < 1) P.pass = 1;
+  if (P.pass > P.slots) P.pass = P.slots;
+  P.carry_bytes = P.pass < P.slots ? state * 4 : 0;
+  P.meta_bytes = (size_t)(P.pass * kv_heads) * sizeof(Meta);
+  P.u_bytes = (size_t)P.pass * state * 4;
+  P.bytes = P.carry_bytes + P.meta_bytes + P.u_bytes + P.u_bytes / 2;
+  return P;
+}
+
+int check_shape(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+  const int rc = shape_check(rows, seqs, q_heads, kv_heads, head_dim, 1, 1);
+  if (rc != TQ_OK) return rc;
+  const Plan P = make_plan(rows, seqs, kv_heads, head_dim);
+  const int64_t blocks = head_dim * head_dim / 256;
+  const bool ok = P.chunked ? grid_ok(P.pass * q_heads, 512) && grid_ok(seqs * kv_heads * blocks, 64)
+                            : grid_ok(seqs * kv_heads * (head_dim / 64), 256);
+  return ok ? TQ_OK : TQ_ERR_SHAPE;
+}
+
+bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+template <int D, typename T>
+void launch_passes(LinArgs A, const Plan &P, hipStream_t st) {
+  for (int64_t s0 = 0; s0 < P.slots; s0 += P.pass) {
+    A.slot0 = (int)s0;
+    A.slots = (int)(P.slots - s0 < P.pass ? P.slots - s0 : P.pass);
+    const int64_t units = (int64_t)A.slots * A.hkv;
+    hipLaunchKernelGGL((chunk_state_kernel<D, T>), dim3((unsigned)units), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((scan_kernel<D>), dim3((unsigned)((int64_t)A.seqs * A.hkv * (D * D / 256))), dim3(64), 0, st, A);
+    // the query heads of a KV head over as many workgroups as fill the CUs
+    const int most = A.group >= 2 ? A.group / 2 : 1;
+    int64_t parts = kCus / units;
+    A.parts = (int)(parts < 1 ? 1 : parts > most ? most : parts);
+    const dim3 grid((unsigned)(units * A.parts));
+    if (A.group >= 2) hipLaunchKernelGGL((chunk_out_kernel<D, T, 8>), grid, dim3(512), 0, st, A);
+    else hipLaunchKernelGGL((chunk_out_kernel<D, T, 4>), grid, dim3(256), 0, st, A);
+  }
+}
+
+}  // namespace
+
+extern "C" size_t tq_linear_attn_scratch_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                                               int64_t head_dim) {
+  if (check_shape(rows, seqs, q_heads, kv_heads, head_dim) != TQ_OK) return 0;
+  return make_plan(rows, seqs, kv_heads, head_dim).bytes;
+}
+
+extern "C" int tq_linear_attn(int dtype, int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                              int64_t head_dim, const void *qkv, int64_t row_stride, const float *log_decay,
+                              int64_t decay_stride, const int32_t *cu_rows, const int32_t *state_from,
+                              const int32_t *state_to, float *states, int64_t num_states, float scale, void *out,
+                              int64_t out_stride, void *scratch, size_t scratch_bytes, void *stream) {
+  if (!qkv || !log_decay || !cu_rows || !state_from || !state_to || !states || !out) return TQ_ERR_NULL;
+  if (dtype != TQ_F16 && dtype != TQ_F32) return TQ_ERR_DTYPE;
+  const int rc = check_shape(rows, seqs, q_heads, kv_heads, head_dim);
+  if (rc != TQ_OK) return rc;
+  if (row_stride < (q_heads + 2 * kv_heads) * head_dim || row_stride % 8 != 0 || row_stride > ((int64_t)1 << 31) ||
+      (decay_stride != 0 && decay_stride < kv_heads) || decay_stride > ((int64_t)1 << 31) || num_states < 1 ||
+      num_states > 0x7fffffff || out_stride < q_heads * head_dim || out_stride % 8 != 0 ||
+      out_stride > ((int64_t)1 << 31))
+    return TQ_ERR_SHAPE;
+  if (!(scale > -3.0e38f && scale < 3.0e38f)) return TQ_ERR_VALUE;
+  if (!aligned_to(qkv, 16) || !aligned_to(states, 16) || !aligned_to(out, 16) || !aligned_to(scratch, 16) ||
+      !aligned_to(log_decay, 4) || !aligned_to(cu_rows, 4) || !aligned_to(state_from, 4) || !aligned_to(state_to, 4))
+    return TQ_ERR_ALIGN;
+  const Plan P = make_plan(rows, seqs, kv_heads, head_dim);
+  if (P.bytes && !scratch) return TQ_ERR_NULL;
+  if (scratch_bytes < P.bytes) return TQ_ERR_SIZE;
+  LinArgs A = {};
+  A.qkv = qkv; A.log_decay = log_decay; A.cu = cu_rows; A.from = state_from; A.to = state_to;
+  A.states = states; A.out = (_Float16 *)out;
+  A.row_stride = row_stride; A.decay_stride = decay_stride; A.out_stride = out_stride; A.num_states = num_states;
+  A.scale = scale;
+  A.rows = (int)rows; A.seqs = (int)seqs; A.hq = (int)q_heads; A.hkv = (int)kv_heads; A.group = (int)(q_heads / kv_heads);
+  char *p = (char *)scratch;
+  A.carry = (float *)p;
+  A.meta = (Meta *)(p + P.carry_bytes);
+  A.u = (float *)(p + P.carry_bytes + P.meta_bytes);
+  A.snap = (_Float16 *)(p + P.carry_bytes + P.meta_bytes + P.u_bytes);
+  hipStream_t st = (hipStream_t)stream;
+#define TQ_LINEAR(D, T)                                                                                       \
+  {                                                                                                           \
+    if (P.chunked) launch_passes<D, T>(A, P, st);                                                             \
+    else hipLaunchKernelGGL((recur_kernel<D, T>), dim3((unsigned)(seqs * kv_heads * (D / 64))), dim3(256), 0, st, A); \
+  }
+  if (head_dim == 128) {
+    if (dtype == TQ_F16) TQ_LINEAR(128, _Float16) else TQ_LINEAR(128, float)
+  } else {
+    if (dtype == TQ_F16) TQ_LINEAR(64, _Float16) else TQ_LINEAR(64, float)
+  }
+#undef TQ_LINEAR
+  return hipGetLastError() == hipSuccess ? TQ_OK : TQ_ERR_HIP;
+}
