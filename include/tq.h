@@ -534,8 +534,8 @@ size_t tq_linear_attn_scratch_bytes(int64_t rows, int64_t seqs, int64_t q_heads,
  *   out: fp16, rows out_stride elements apart (a multiple of 8).
  * Up to 16 rows a sequence, on average, the recurrence runs row by row in fp32
  * (one launch, no scratch); more run in chunks of 128 rows (three launches for
- * up to 2^27 bytes of scratch), where states keep fp32's accuracy and the
- * factors of an output's products are rounded to fp16.  A sequence of many rows
+ * up to 2^27 bytes of scratch), where states keep fp32's accuracy; for the
+ * outputs fp32 values and the states before each chunk are rounded to fp16.  A sequence of many rows
  * beside many single tokens is better a call of its own.  Non-finite inputs make
  * their sequence's outputs and state for that KV head (from the chunk on that
  * holds them) unspecified, those of no other.  qkv, states, out and scratch

@@ -19,7 +19,8 @@
 // scaled by powers of two into its range, so no size of input overflows it.
 // U is of two fp16 terms a factor (fp16 inputs: the keys with their weights
 // two, the values are exact), so the state keeps fp32's accuracy.  For the
-// outputs, which are fp16, every factor is rounded to fp16 once.
+// outputs, which are fp16, queries, keys and weights have two terms each; fp32
+// values and the states before a chunk are rounded to fp16 once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -41,6 +42,7 @@ constexpr size_t kPassBytes = (size_t)1 << 27;  // scratch of a pass over the ch
 constexpr int kNoState = -100000;  // exponent of a snapshot that is zero
 
 typedef float f16x __attribute__((ext_vector_type(16)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
@@ -208,23 +210,85 @@ struct Turned {
   }
 };
 
+// x as two fp16 terms, together within 2^-21 of it (or the least fp16 step):
+// the first cut off, two elements an instruction.
+__device__ __forceinline__ void two_terms(const float (&x)[8], h8 &hi, h8 &lo) {
+  typedef __fp16 c2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const c2 a = __builtin_amdgcn_cvt_pkrtz(x[i], x[i + 1]);
+    const c2 b = __builtin_amdgcn_cvt_pkrtz(x[i] - (float)a[0], x[i + 1] - (float)a[1]);
+    hi[i] = (_Float16)a[0], hi[i + 1] = (_Float16)a[1];
+    lo[i] = (_Float16)b[0], lo[i + 1] = (_Float16)b[1];
+  }
+}
+
+// 2^e as a factor, e within fp32's exponents
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+
 // e with |v| < 2^e, at least -100 (so that scaling by 2^(14 - e) stays finite)
 __device__ __forceinline__ int exponent(float v) { return max(__builtin_amdgcn_frexp_expf(v), -100); }
 
+// U of a chunk and KV head, 64 rows at a time; further workgroups take the
+// largest element of the state that each sequence starts the pass from.
 template <int D, typename T>
-__global__ __launch_bounds__(256) void chunk_state_kernel(const LinArgs A) {
+__global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
   constexpr bool kWide = std::is_same<T, float>::value;
-  constexpr int kPer = kStep * (D / 8) / 256;     // pieces of 8 elements a thread
-  constexpr int kNb = D == 128 ? 4 : 1;           // column blocks of 32 a wave
+  constexpr int kSteps = kChunk / kStep, kPer = kStep * (D / 8) / 512;  // pieces of 8 elements a thread and step
+  constexpr int kNb = D == 128 ? 2 : 1;  // column blocks of 32 a wave
   constexpr int kTile = kStep * 2 * D;
   __shared__ __attribute__((aligned(16))) uint8_t kh[kTile], kl[kTile], vh[kTile], vl[kWide ? kTile : 16];
-  __shared__ float w[kChunk], red[2][4], most[4], most0[4];
+  __shared__ float w[kChunk], red[2][8];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = blockIdx.x % (uint32_t)A.hkv, rel = blockIdx.x / (uint32_t)A.hkv;
+  auto most_of = [&](float m) {  // over the workgroup, in thread 0
+    m = tqdev::wave_max64(m);
+    if (lane == 0) red[0][wave] = m;
+    __syncthreads();
+    float r = red[0][0];
+#pragma unroll
+    for (int i = 1; i < 8; i++) r = fmaxf(r, red[0][i]);
+    return r;
+  };
+  if (rel >= A.slots) {
+    const int s = rel - A.slots, first = cu_at(A.cu, s, A.rows), n = cu_at(A.cu, s + 1, A.rows) - first;
+    const int base = slot_base<kChunk, 1>(first, s, 1), slot = max(base, A.slot0);
+    if (n <= 0 || slot >= min(base + (n + kChunk - 1) / kChunk, A.slot0 + A.slots)) return;
+    const int from = A.from[s];
+    const float *p = base < slot ? A.carry + (int64_t)h * (D * D) : A.states + ((int64_t)from * A.hkv + h) * (D * D);
+    float m = 0.0f;
+    if (base < slot || state_ok(A, from)) {
+#pragma unroll
+      for (int i = 0; i < D * D / 2048; i++) {
+        const f4 x = *reinterpret_cast<const f4 *>(p + (i * 512 + tid) * 4);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+      }
+    }
+    m = most_of(m);
+    if (tid == 0) A.meta[(int64_t)(slot - A.slot0) * A.hkv + h].most_s = m;
+    return;
+  }
   Chunk c;
   if (!find_chunk(A, A.slot0 + rel, c)) return;
   Meta *meta = A.meta + (int64_t)rel * A.hkv + h;
+  const T *kp = (const T *)A.qkv + (int64_t)c.begin * A.row_stride + (A.hq + h) * D;
+  const T *vp = kp + A.hkv * D;
+  // all rows are sent for at once
+  float k[kSteps][kPer][8], v[kSteps][kPer][8];
+#pragma unroll
+  for (int t = 0; t < kSteps; t++)
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      const int p = i * 512 + tid, row = t * kStep + p / (D / 8), at = p % (D / 8) * 8;
+      if (row < c.n) {
+        load8(kp + row * A.row_stride + at, k[t][i]);
+        load8(vp + row * A.row_stride + at, v[t][i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) k[t][i][j] = v[t][i][j] = 0.0f;
+      }
+    }
   if (wave == 0) {
     double g0, g1;
     decay_sums(A, c, h, g0, g1);
@@ -233,47 +297,23 @@ __global__ __launch_bounds__(256) void chunk_state_kernel(const LinArgs A) {
     w[2 * lane + 1] = __builtin_amdgcn_exp2f((float)(all - g1));
     if (lane == 0) meta->decay = (float)all;
   }
-  // the largest element of the state that the pass starts from
-  if (c.local == 0 || rel == 0) {
-    const int from = A.from[c.s];
-    const float *p = c.local ? A.carry + (int64_t)h * (D * D) : state_ok(A, from) ? A.states + ((int64_t)from * A.hkv + h) * (D * D) : nullptr;
-    float m = 0.0f;
-    if (p) {
-#pragma unroll 4
-      for (int i = tid * 4; i < D * D; i += 1024) {
-        const f4 x = *reinterpret_cast<const f4 *>(p + i);
-        m = fmaxf(m, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-      }
-    }
-    m = tqdev::wave_max64(m);
-    if (lane == 0) most0[wave] = m;
-  }
-  const int mb = D == 128 ? wave : wave & 1, nb0 = D == 128 ? 0 : wave >> 1;
+  const int mb = D == 128 ? wave & 3 : wave & 1, nb0 = D == 128 ? 2 * (wave >> 2) : (wave >> 1) & 1;
   const Turned<D> turned;
   f16x acc[kNb];
 #pragma unroll
   for (int b = 0; b < kNb; b++) acc[b] = (f16x)(0.0f);
   int unit = kNoState;  // acc holds U * 2^(28 - unit)
-  const T *kp = (const T *)A.qkv + (int64_t)c.begin * A.row_stride + (A.hq + h) * D;
-  const T *vp = kp + A.hkv * D;
-  for (int t0 = 0; t0 < c.n; t0 += kStep) {
-    float k[kPer][8], v[kPer][8], mk = 0.0f, mv = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; i++) {
-      const int p = i * 256 + tid, row = t0 + p / (D / 8), at = p % (D / 8) * 8;
-      if (row < c.n) {
-        load8(kp + row * A.row_stride + at, k[i]);
-        load8(vp + row * A.row_stride + at, v[i]);
-      } else {
+  for (int t = 0; t < kSteps; t++) {
+    if (t * kStep >= c.n) break;
+    float mk = 0.0f, mv = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; j++) k[i][j] = v[i][j] = 0.0f;
-      }
+    for (int i = 0; i < kPer; i++)
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        mk = fmaxf(mk, fabsf(k[i][j]));
-        mv = fmaxf(mv, fabsf(v[i][j]));
+        mk = fmaxf(mk, fabsf(k[t][i][j]));
+        mv = fmaxf(mv, fabsf(v[t][i][j]));
       }
-    }
     mk = tqdev::wave_max64(mk);
     mv = tqdev::wave_max64(mv);
     if (lane == 0) {
@@ -281,8 +321,12 @@ __global__ __launch_bounds__(256) void chunk_state_kernel(const LinArgs A) {
       red[1][wave] = mv;
     }
     __syncthreads();  // (and the last step's operands are read)
-    mk = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    mv = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+    mk = mv = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      mk = fmaxf(mk, red[0][i]);
+      mv = fmaxf(mv, red[1][i]);
+    }
     const int ek = exponent(mk), ev = exponent(mv), now = max(unit, ek + ev);
     if (now != unit) {
 #pragma unroll
@@ -292,22 +336,24 @@ __global__ __launch_bounds__(256) void chunk_state_kernel(const LinArgs A) {
     }
     unit = now;
     const int shift = 14 - ek + max(ek + ev - now, -300);
+    const float fv = power(14 - ev);
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
-      const int p = i * 256 + tid, row = p / (D / 8), at = piece_at<D>(row, p % (D / 8));
-      const float f = ldexpf(w[t0 + row], shift);
-      h8 a, b, x, y;
+      const int p = i * 512 + tid, row = p / (D / 8), at = piece_at<D>(row, p % (D / 8));
+      const float f = ldexpf(w[t * kStep + row], shift);
+      float kw[8], vs[8];
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        // (held as fp32: the product may not be made again in one rounding to
-        // fp16 for one of its two uses, which would differ now and then)
-        float kw = k[i][j] * f;
-        asm("" : "+v"(kw));
-        const float vs = ldexpf(v[i][j], 14 - ev);
-        a[j] = (_Float16)kw;
-        b[j] = (_Float16)(kw - (float)a[j]);
-        x[j] = (_Float16)vs;
-        y[j] = (_Float16)(vs - (float)x[j]);
+        kw[j] = k[t][i][j] * f;
+        vs[j] = v[t][i][j] * fv;
+      }
+      h8 a, b, x, y;
+      two_terms(kw, a, b);
+      if constexpr (kWide) {
+        two_terms(vs, x, y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] = (_Float16)vs[j];  // exact
       }
       *reinterpret_cast<h8 *>(kh + at) = a;
       *reinterpret_cast<h8 *>(kl + at) = b;
@@ -315,81 +361,101 @@ __global__ __launch_bounds__(256) void chunk_state_kernel(const LinArgs A) {
       if constexpr (kWide) *reinterpret_cast<h8 *>(vl + at) = y;
     }
     __syncthreads();
+    // (head_dim 64: the upper four waves take the other half of the rows)
+    constexpr int kRows = D == 128 ? kStep : kStep / 2;
+    const int r0 = D == 128 ? 0 : (wave >> 2) * kRows;
 #pragma unroll
-    for (int t = 0; t < kStep; t += 16) {
-      const h8 a = turned(kh, t, mb), b = turned(kl, t, mb);
+    for (int r = 0; r < kRows; r += 16) {
+      const h8 a = turned(kh, r0 + r, mb), b = turned(kl, r0 + r, mb);
 #pragma unroll
       for (int nb = 0; nb < kNb; nb++) {
-        const h8 x = turned(vh, t, nb0 + nb);
+        const h8 x = turned(vh, r0 + r, nb0 + nb);
         acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, x, acc[nb], 0, 0, 0);
         acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, x, acc[nb], 0, 0, 0);
-        if constexpr (kWide) acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, turned(vl, t, nb0 + nb), acc[nb], 0, 0, 0);
+        if constexpr (kWide) acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, turned(vl, r0 + r, nb0 + nb), acc[nb], 0, 0, 0);
       }
+    }
+  }
+  __syncthreads();
+  if constexpr (D == 64) {  // the halves' sums meet
+    float *half = reinterpret_cast<float *>(kh);  // [4 waves][16][64], over kh and kl
+    static_assert(sizeof(kh) + sizeof(kl) >= 4 * 16 * 64 * 4, "room for the sums of four waves");
+    if (wave >= 4) {
+#pragma unroll
+      for (int r = 0; r < 16; r++) half[((wave - 4) * 16 + r) * 64 + lane] = acc[0][r];
+    }
+    __syncthreads();
+    if (wave < 4) {
+#pragma unroll
+      for (int r = 0; r < 16; r++) acc[0][r] += half[(wave * 16 + r) * 64 + lane];
     }
   }
   // acc[b][r] is row 32 mb + 8 (r / 4) + 4 (lane / 32) + r % 4, column 32 (nb0 + b) + lane % 32
   float *u = A.u + ((int64_t)rel * A.hkv + h) * (D * D) + (32 * mb + 4 * (lane >> 5)) * D + 32 * nb0 + (lane & 31);
   float m = 0.0f;
+  if (D == 128 || wave < 4) {
 #pragma unroll
-  for (int b = 0; b < kNb; b++)
+    for (int b = 0; b < kNb; b++)
 #pragma unroll
-    for (int r = 0; r < 16; r++) {
-      const float x = ldexpf(acc[b][r], unit - 28);
-      u[(8 * (r >> 2) + (r & 3)) * D + 32 * b] = x;
-      m = fmaxf(m, fabsf(x));
-    }
-  m = tqdev::wave_max64(m);
-  if (lane == 0) most[wave] = m;
-  __syncthreads();
-  if (tid == 0) {
-    meta->most_u = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-    meta->most_s = c.local == 0 || rel == 0 ? fmaxf(fmaxf(most0[0], most0[1]), fmaxf(most0[2], most0[3])) : 0.0f;
+      for (int r = 0; r < 16; r++) {
+        const float x = ldexpf(acc[b][r], unit - 28);
+        u[(8 * (r >> 2) + (r & 3)) * D + 32 * b] = x;
+        m = fmaxf(m, fabsf(x));
+      }
   }
+  m = most_of(m);
+  if (tid == 0) meta->most_u = m;
 }
 
 // The states before each chunk (fp16, scaled), and the last one: a thread has
-// four elements of a state.
+// four elements of a state, its next chunks' on their way.
 template <int D>
 __global__ __launch_bounds__(64) void scan_kernel(const LinArgs A) {
   constexpr uint32_t kBlocks = D * D / 256;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   const uint32_t blk = blockIdx.x % kBlocks, sh = blockIdx.x / kBlocks;
-  const int h = sh % (uint32_t)A.hkv, s = sh / (uint32_t)A.hkv, at = blk * 256 + threadIdx.x * 4;
+  const int h = sh % (uint32_t)A.hkv, s = sh / (uint32_t)A.hkv, lane = threadIdx.x, at = blk * 256 + lane * 4;
   const int begin = cu_at(A.cu, s, A.rows), n = cu_at(A.cu, s + 1, A.rows) - begin;
   if (n <= 0) return;
   const int base = slot_base<kChunk, 1>(begin, s, 1), end = base + (n + kChunk - 1) / kChunk;
   const int lo = max(base, A.slot0), hi = min(end, A.slot0 + A.slots);
   if (lo >= hi) return;
-  const int from = A.from[s], to = A.to[s];
+  const int from = A.from[s], to = A.to[s], count = hi - lo;
+  const int64_t r0 = (int64_t)(lo - A.slot0) * A.hkv + h;
+  const float *u = A.u + r0 * (D * D) + at;
+  const int64_t step = (int64_t)A.hkv * (D * D);
+  f4 x[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; i++) x[i] = *reinterpret_cast<const f4 *>(u + min(i, count - 1) * step);
   float *carry = A.carry + (int64_t)h * (D * D) + at;
   f4 S = {0, 0, 0, 0};
   if (lo > base) S = *reinterpret_cast<const f4 *>(carry);
   else if (state_ok(A, from)) S = *reinterpret_cast<const f4 *>(A.states + ((int64_t)from * A.hkv + h) * (D * D) + at);
-  const int64_t r0 = (int64_t)(lo - A.slot0) * A.hkv + h;
-  const float *u = A.u + r0 * (D * D) + at;
   _Float16 *snap = A.snap + r0 * (D * D) + at;
   Meta *meta = A.meta + r0;
-  const int count = hi - lo;
-  const int64_t step = (int64_t)A.hkv * (D * D);
   float bound = meta->most_s;  // of |S|, from the chunks' largest elements
+  float decay = 0.0f, most = 0.0f;  // of chunk c0 + lane
   for (int c0 = 0; c0 < count; c0 += kAhead) {
-    f4 x[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; i++) x[i] = *reinterpret_cast<const f4 *>(u + min(c0 + i, count - 1) * step);
+    if ((c0 & 63) == 0) {
+      const Meta m = meta[(int64_t)min(c0 + lane, count - 1) * A.hkv];
+      decay = __builtin_amdgcn_exp2f(m.decay);
+      most = m.most_u;
+    }
 #pragma unroll
     for (int i = 0; i < kAhead; i++) {
-      if (c0 + i >= count) break;
-      Meta *m = meta + (int64_t)(c0 + i) * A.hkv;
+      const int c = c0 + i;
+      if (c >= count) break;
       const int e = bound > 0.0f ? exponent(bound) - 15 : kNoState;
       const int sh16 = bound > 0.0f ? -e : 0;
       h4 o;
 #pragma unroll
       for (int j = 0; j < 4; j++) o[j] = (_Float16)ldexpf(S[j], sh16);
-      *reinterpret_cast<h4 *>(snap + (c0 + i) * step) = o;
-      if (blk == 0 && threadIdx.x == 0) m->e = e;
-      const float a = __builtin_amdgcn_exp2f(m->decay);
+      *reinterpret_cast<h4 *>(snap + c * step) = o;
+      if (blk == 0 && lane == 0) meta[(int64_t)c * A.hkv].e = e;
+      const float a = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(decay), c & 63));
+      bound = bound * a + __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(most), c & 63));
       S = S * a + x[i];
-      bound = bound * a + m->most_u;
+      x[i] = *reinterpret_cast<const f4 *>(u + min(c + kAhead, count - 1) * step);
     }
   }
   if (hi < end) *reinterpret_cast<f4 *>(carry) = S;
@@ -406,15 +472,23 @@ __device__ __forceinline__ float half_max(float v) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// Outputs of a chunk: keys, values and the state in LDS, 32 rows a wave, the
-// query heads that share them one after the other (NW = 8: two at a time).
+// Outputs of a chunk: keys, values and the state in LDS; a wave takes 32 rows
+// of a query head, then of another one (NW = 8: two heads at a time), its next
+// queries on their way meanwhile.  The block of 32 rows changes from head to
+// head, so that the waves' shares of the causal triangle come out even.
+//
+// A weight 2^(G_i - G_j) is a factor of the row and one of the token, both at
+// most 1, with the sum up to the end of the token's 32 between them; among the
+// row's own 32 tokens it is made as it stands.  Weights are put into fp16's
+// range by what their scores can reach, head_dim max |q| max |k|.
 template <int D, typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   constexpr bool kWide = std::is_same<T, float>::value;
-  constexpr int NT = NW * 64, kPer = kChunk * (D / 8) / NT, kTogether = NW / 4;
-  __shared__ __attribute__((aligned(16))) _Float16 kt[kChunk][D + 8];
+  constexpr int NT = NW * 64, kPer = kChunk * (D / 8) / NT, kTogether = NW / 4, kTerms = kWide ? 2 : 1;
+  constexpr int kLogD = D == 128 ? 7 : 6;
+  __shared__ __attribute__((aligned(16))) _Float16 kt[kTerms][kChunk][D + 8];
   __shared__ __attribute__((aligned(16))) uint8_t vt[kChunk * 2 * D], stt[D * 2 * D];
-  __shared__ __attribute__((aligned(16))) float ghi[kChunk], glo[kChunk];
+  __shared__ __attribute__((aligned(16))) float ghi[kChunk], glo[kChunk], wt[kChunk];
   __shared__ float red[2][NW];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -422,11 +496,27 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   const int h = rh % (uint32_t)A.hkv, rel = rh / (uint32_t)A.hkv;
   Chunk c;
   if (!find_chunk(A, A.slot0 + rel, c)) return;
+  // this wave's head and row block of round i
+  const int per = (A.group + A.parts - 1) / A.parts, g0 = part * per, heads = min(per, A.group - g0);
+  const int rounds = (heads + kTogether - 1) / kTogether;
+  auto head_of = [&](int i) { return i * kTogether + (wave >> 2); };
+  auto block_of = [&](int i) { return wave < 4 ? (wave + i) & 3 : 3 - ((wave + i) & 3); };
+  typedef typename std::conditional<kWide, f4, h8>::type Piece;
+  constexpr int kPieces = D / 16 * (kWide ? 2 : 1);
+  Piece raw[kPieces];
+  auto send_for = [&](int i) {
+    const int row = 32 * block_of(i) + n, head = h * A.group + g0 + min(head_of(i), heads - 1);
+    const T *qp = (const T *)A.qkv + (int64_t)(c.begin + min(row, c.n - 1)) * A.row_stride + head * D + 8 * half;
+#pragma unroll
+    for (int j = 0; j < kPieces; j++)
+      raw[j] = *reinterpret_cast<const Piece *>(qp + (kWide ? 16 * (j >> 1) + 4 * (j & 1) : 16 * j));
+  };
+  if (heads > 0) send_for(0);
   const int64_t rs = (int64_t)rel * A.hkv + h;
   const int es = A.meta[rs].e;
   const T *kp = (const T *)A.qkv + (int64_t)c.begin * A.row_stride + (A.hq + h) * D;
   const T *vp = kp + A.hkv * D;
-  int ek = 14, ev = 14;  // kt holds k * 2^(14 - ek); fp16 inputs are taken as they are
+  int bk, ek = 14, ev = 14;  // |k| < 2^bk; kt holds k * 2^(14 - ek), vt v * 2^(14 - ev): fp16 inputs are taken as they are
   {
     float k[kPer][8], v[kPer][8], mk = 0.0f, mv = 0.0f;
 #pragma unroll
@@ -439,156 +529,206 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
 #pragma unroll
         for (int j = 0; j < 8; j++) k[i][j] = v[i][j] = 0.0f;
       }
-      if constexpr (kWide) {
+    }
+    u4 sp[D * (D / 8) / NT];
+    if (es != kNoState) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          mk = fmaxf(mk, fabsf(k[i][j]));
-          mv = fmaxf(mv, fabsf(v[i][j]));
-        }
+      for (int i = 0; i < D * (D / 8) / NT; i++) sp[i] = reinterpret_cast<const u4 *>(A.snap + rs * (D * D))[i * NT + tid];
+    }
+    if (wave == 0) {
+      double d0, d1;
+      decay_sums(A, c, h, d0, d1);
+      const double last = __shfl(d1, lane | 15);  // up to the end of the row's 32
+      ghi[2 * lane] = (float)d0;
+      glo[2 * lane] = (float)(d0 - (double)(float)d0);
+      wt[2 * lane] = __builtin_amdgcn_exp2f((float)(last - d0));
+      ghi[2 * lane + 1] = (float)d1;
+      glo[2 * lane + 1] = (float)(d1 - (double)(float)d1);
+      wt[2 * lane + 1] = __builtin_amdgcn_exp2f((float)(last - d1));
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; i++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        mk = fmaxf(mk, fabsf(k[i][j]));
+        mv = fmaxf(mv, fabsf(v[i][j]));
       }
+    mk = tqdev::wave_max64(mk);
+    mv = tqdev::wave_max64(mv);
+    if (lane == 0) {
+      red[0][wave] = mk;
+      red[1][wave] = mv;
     }
     if (es != kNoState) {
-      const _Float16 *sp = A.snap + rs * (D * D);
 #pragma unroll
       for (int i = 0; i < D * (D / 8) / NT; i++) {
         const int p = i * NT + tid;
-        *reinterpret_cast<uint4 *>(stt + piece_at<D>(p / (D / 8), p % (D / 8))) = *reinterpret_cast<const uint4 *>(sp + 8 * p);
+        *reinterpret_cast<u4 *>(stt + piece_at<D>(p / (D / 8), p % (D / 8))) = sp[i];
       }
     }
-    if (wave == 0) {
-      double g0, g1;
-      decay_sums(A, c, h, g0, g1);
-      ghi[2 * lane] = (float)g0;
-      glo[2 * lane] = (float)(g0 - (double)(float)g0);
-      ghi[2 * lane + 1] = (float)g1;
-      glo[2 * lane + 1] = (float)(g1 - (double)(float)g1);
-    }
-    if constexpr (kWide) {
-      mk = tqdev::wave_max64(mk);
-      mv = tqdev::wave_max64(mv);
-      if (lane == 0) {
-        red[0][wave] = mk;
-        red[1][wave] = mv;
-      }
-      __syncthreads();
-      mk = mv = 0.0f;
+    __syncthreads();
+    mk = mv = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NW; i++) {
-        mk = fmaxf(mk, red[0][i]);
-        mv = fmaxf(mv, red[1][i]);
-      }
-      ek = exponent(mk);
+    for (int i = 0; i < NW; i++) {
+      mk = fmaxf(mk, red[0][i]);
+      mv = fmaxf(mv, red[1][i]);
+    }
+    bk = exponent(mk);
+    if (kWide) {
+      ek = bk;
       ev = exponent(mv);
     }
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
       const int p = i * NT + tid, row = p / (D / 8), at = p % (D / 8);
-      h8 a, b;
+      h8 a, l, b;
+      if constexpr (kWide) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) k[i][j] *= power(14 - ek);
+        two_terms(k[i], a, l);
+      }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        a[j] = (_Float16)(kWide ? ldexpf(k[i][j], 14 - ek) : k[i][j]);
-        b[j] = (_Float16)(kWide ? ldexpf(v[i][j], 14 - ev) : v[i][j]);
+        if (!kWide) a[j] = (_Float16)k[i][j];
+        b[j] = (_Float16)(kWide ? v[i][j] * power(14 - ev) : v[i][j]);
       }
-      *reinterpret_cast<h8 *>(&kt[row][8 * at]) = a;
+      *reinterpret_cast<h8 *>(&kt[0][row][8 * at]) = a;
+      if constexpr (kWide) *reinterpret_cast<h8 *>(&kt[1][row][8 * at]) = l;
       *reinterpret_cast<h8 *>(vt + piece_at<D>(row, at)) = b;
     }
   }
   __syncthreads();
-  // the two waves of a SIMD take a row block with few earlier tokens and one with many
-  const int rb = wave < 4 ? wave : 7 - wave;
-  if (32 * rb >= c.n) return;
-  const int row = 32 * rb + n;
-  const bool valid = row < c.n;
+  int scale_e;
+  const float scale_m = frexpf(A.scale, &scale_e);
   const Turned<D> turned;
-  const float gh = ghi[row], gl = glo[row];
-  const int per = (A.group + A.parts - 1) / A.parts, end = min((int)(part + 1) * per, A.group);
-  for (int g = part * per + wave / 4; g < end; g += kTogether) {
-    const int head = h * A.group + g;
-    const T *qp = (const T *)A.qkv + (int64_t)(c.begin + (valid ? row : c.n - 1)) * A.row_stride + head * D;
-    h8 qf[D / 16];
-    int eq = 14;
-    {
-      float q[D / 16][8], m = 0.0f;
+
+  // one round: rows 32 RB + n of a head
+  auto rows = [&](auto block, int i) {
+    constexpr int RB = decltype(block)::value;
+    const int row = 32 * RB + n, head = h * A.group + g0 + head_of(i);
+    h8 qf[kTerms][D / 16];
+    float mq = 0.0f;
 #pragma unroll
-      for (int j = 0; j < D / 16; j++) load8(qp + 16 * j + 8 * half, q[j]);
-      if constexpr (kWide) {
+    for (int j = 0; j < kPieces; j++)
 #pragma unroll
-        for (int j = 0; j < D / 16; j++)
+      for (int r = 0; r < (kWide ? 4 : 8); r++) mq = fmaxf(mq, fabsf((float)raw[j][r]));
+    const int bq = exponent(half_max(mq)), eq = kWide ? bq : 14;
+    if constexpr (kWide) {
+      const float f = power(14 - eq);
 #pragma unroll
-          for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(q[j][i]));
-        eq = exponent(half_max(m));
+      for (int j = 0; j < D / 16; j++) {
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 8; r++) x[r] = (float)raw[kPieces / (D / 16) * j + (r >> 2)][r & 3] * f;
+        two_terms(x, qf[0][j], qf[kTerms - 1][j]);
       }
+    } else {
 #pragma unroll
-      for (int j = 0; j < D / 16; j++)
+      for (int j = 0; j < kPieces; j++)
 #pragma unroll
-        for (int i = 0; i < 8; i++) qf[j][i] = (_Float16)(kWide ? ldexpf(q[j][i], 14 - eq) : q[j][i]);
+        for (int r = 0; r < 8; r++) qf[0][j][r] = (_Float16)raw[j][r];
     }
-    // scores S^T = K Q^T: sc[t][r] is token 32 t + 16 (r / 8) + 8 half + r % 8
-    f16x sc[4];
-    float mp = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 4; t++) {
-      sc[t] = (f16x)(0.0f);
-      if (t > rb) continue;
-      const _Float16 *kr = &kt[32 * t + row_token(n)][8 * half];
-#pragma unroll
-      for (int j = 0; j < D / 16; j++)
-        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8 *>(kr + 16 * j), qf[j], sc[t], 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 16; r++) {
-        const int j = 32 * t + 16 * (r >> 3) + 8 * half + (r & 7);
-        const float wgt = __builtin_amdgcn_exp2f((gh - ghi[j]) + (gl - glo[j]));
-        sc[t][r] = t < rb || j <= row ? sc[t][r] * wgt : 0.0f;
-        mp = fmaxf(mp, fabsf(sc[t][r]));
-      }
-    }
+    if (i + 1 < rounds) send_for(i + 1);
+    if (32 * RB >= c.n || head_of(i) >= heads) return;
     // o^T: o[d][r] is element 32 d + 8 (r / 4) + 4 half + r % 4 of the row, in
-    // units of 2^x: of the weights, whose largest is put at 2^15, or of the
-    // state's part where that is larger by 2^60
+    // units of 2^x: weights are below 2^15 in it, the state's part below 2^97
+    const int xs = eq - 14 + es;
+    int x = bq + bk + kLogD + ev - 29;
+    if (es != kNoState) x = max(x, xs - 60);
+    const float gh = ghi[row], gl = glo[row];
     f16x o[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; d++) o[d] = (f16x)(0.0f);
-    mp = half_max(mp);
-    int x = mp > 0.0f ? (eq - 14) + (ek - 14) + __builtin_amdgcn_frexp_expf(mp) - 15 + (ev - 14) : kNoState;
     if (es != kNoState) {
 #pragma unroll
       for (int j = 0; j < D / 16; j++)
 #pragma unroll
-        for (int d = 0; d < D / 32; d++)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(turned(stt, 16 * j, d), qf[j], o[d], 0, 0, 0);
-      const int xs = (eq - 14) + es;
-      x = max(x, xs - 60);
+        for (int d = 0; d < D / 32; d++) {
+          const h8 a = turned(stt, 16 * j, d);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qf[0][j], o[d], 0, 0, 0);
+          if constexpr (kWide) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qf[1][j], o[d], 0, 0, 0);
+        }
       const float f = ldexpf(__builtin_amdgcn_exp2f(gh + gl), max(xs - x, -300));
 #pragma unroll
       for (int d = 0; d < D / 32; d++)
 #pragma unroll
         for (int r = 0; r < 16; r++) o[d][r] *= f;
     }
-    if (mp == 0.0f && es == kNoState) x = 0;
     const int xp = max((eq - 14) + (ek - 14) + (ev - 14) - x, -300);
 #pragma unroll
-    for (int t = 0; t < 4; t++) {
-      if (t > rb) continue;
-      h8 p[2];
+    for (int t = 0; t <= RB; t++) {
+      // scores S^T = K Q^T: sc[r] is token 32 t + 16 (r / 8) + 8 half + r % 8
+      f16x sc = (f16x)(0.0f);
+      const int key = 32 * t + row_token(n);
+      // (a wave in its products goes first, so that the SIMD's two waves do not
+      // stay side by side in them: a prompt of 4096 rows 92.8 against 95.3 us)
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int r = 0; r < 16; r++) p[r >> 3][r & 7] = (_Float16)ldexpf(sc[t][r], xp);
+      for (int j = 0; j < D / 16; j++) {
+        const h8 a = *reinterpret_cast<const h8 *>(&kt[0][key][16 * j + 8 * half]);
+        sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qf[0][j], sc, 0, 0, 0);
+        if constexpr (kWide) {
+          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qf[1][j], sc, 0, 0, 0);
+          const h8 b = *reinterpret_cast<const h8 *>(&kt[1][key][16 * j + 8 * half]);
+          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, qf[0][j], sc, 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_s_setprio(0);
+      // weights: two fp16 terms, so that they lose nothing to the outputs' rounding
+      const int j0 = 32 * t + 8 * half;
+      h8 p[2], pl[2];
+      const float f = t == RB ? 0.0f : ldexpf(__builtin_amdgcn_exp2f((gh - ghi[32 * t + 31]) + (gl - glo[32 * t + 31])), xp);
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        float w[8];
+#pragma unroll
+        for (int r = 0; r < 8; r++) {
+          const int j = j0 + 16 * u + r;
+          if (t == RB) {
+            w[r] = sc[8 * u + r] * ldexpf(__builtin_amdgcn_exp2f((gh - ghi[j]) + (gl - glo[j])), xp);
+            w[r] = j <= row ? w[r] : 0.0f;
+          } else {
+            w[r] = sc[8 * u + r] * (wt[j] * f);
+          }
+        }
+        two_terms(w, p[u], pl[u]);
+      }
 #pragma unroll
       for (int u = 0; u < 2; u++)
 #pragma unroll
-        for (int d = 0; d < D / 32; d++)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(turned(vt, 32 * t + 16 * u, d), p[u], o[d], 0, 0, 0);
-    }
-    if (valid) {
-      _Float16 *dst = A.out + (int64_t)(c.begin + row) * A.out_stride + head * D;
-#pragma unroll
-      for (int d = 0; d < D / 32; d++)
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          h4 y;
-#pragma unroll
-          for (int i = 0; i < 4; i++) y[i] = (_Float16)(ldexpf(o[d][r + i], x) * A.scale);
-          *reinterpret_cast<h4 *>(dst + 32 * d + 2 * r + 4 * half) = y;
+        for (int d = 0; d < D / 32; d++) {
+          const h8 a = turned(vt, 32 * t + 16 * u, d);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, p[u], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, pl[u], o[d], 0, 0, 0);
         }
+    }
+    // (held within fp32's exponents: sums are 0 or 2^-48 to 2^98, so a result
+    // that fp16 holds is not changed)
+    const float last = scale_m * power(x + scale_e);
+    // two quads' halves change places between the halves of the wave: 16 bytes a lane
+    _Float16 *dst = A.out + (int64_t)(c.begin + row) * A.out_stride + head * D + 8 * half;
+#pragma unroll
+    for (int d = 0; d < D / 32; d++)
+#pragma unroll
+      for (int r = 0; r < 16; r += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i2 = 0; i2 < 4; i2++) {
+          const h2 y = {(_Float16)(o[d][r + 2 * i2] * last), (_Float16)(o[d][r + 2 * i2 + 1] * last)};
+          w[i2] = __builtin_bit_cast(uint32_t, y);
+        }
+        const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+        if (row < c.n) *reinterpret_cast<u4 *>(dst + 32 * d + 2 * r) = (u4){a[0], b[0], a[1], b[1]};
+      }
+  };
+#pragma unroll 1
+  for (int i = 0; i < rounds; i++) {
+    switch (block_of(i)) {
+      case 0: rows(std::integral_constant<int, 0>(), i); break;
+      case 1: rows(std::integral_constant<int, 1>(), i); break;
+      case 2: rows(std::integral_constant<int, 2>(), i); break;
+      default: rows(std::integral_constant<int, 3>(), i); break;
     }
   }
 }
@@ -623,7 +763,7 @@ int check_shape(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, i
   if (rc != TQ_OK) return rc;
   const Plan P = make_plan(rows, seqs, kv_heads, head_dim);
   const int64_t blocks = head_dim * head_dim / 256;
-  const bool ok = P.chunked ? grid_ok(P.pass * q_heads, 512) && grid_ok(seqs * kv_heads * blocks, 64)
+  const bool ok = P.chunked ? grid_ok(P.pass * q_heads + seqs * kv_heads, 512) && grid_ok(seqs * kv_heads * blocks, 64)
                             : grid_ok(seqs * kv_heads * (head_dim / 64), 256);
   return ok ? TQ_OK : TQ_ERR_SHAPE;
 }
@@ -636,7 +776,7 @@ void launch_passes(LinArgs A, const Plan &P, hipStream_t st) {
     A.slot0 = (int)s0;
     A.slots = (int)(P.slots - s0 < P.pass ? P.slots - s0 : P.pass);
     const int64_t units = (int64_t)A.slots * A.hkv;
-    hipLaunchKernelGGL((chunk_state_kernel<D, T>), dim3((unsigned)units), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((chunk_state_kernel<D, T>), dim3((unsigned)(units + (int64_t)A.seqs * A.hkv)), dim3(512), 0, st, A);
     hipLaunchKernelGGL((scan_kernel<D>), dim3((unsigned)((int64_t)A.seqs * A.hkv * (D * D / 256))), dim3(64), 0, st, A);
     // the query heads of a KV head over as many workgroups as fill the CUs
     const int most = A.group >= 2 ? A.group / 2 : 1;
