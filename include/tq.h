@@ -569,6 +569,38 @@ int tq_residual_norm(int y_dtype, int res_dtype, int x_dtype, int64_t M, int64_t
                      const void *res, void *res_out, const float *pre_w, double eps, void *x,
                      int8_t *q, float *a_scale, void *stream);
 
+/* ---- device: behind the last layer -------------------------------------
+ *
+ * The choice of the next token from the logits (the pages run their model with
+ * temperature, top-k, top-p and min-p; "为什么PTQ1_0能让27B模型在4090上活得很好"). */
+
+/* Workspace bytes of tq_sample; same zero-fill rule as
+ * tq_gemv_workspace_bytes. */
+size_t tq_sample_workspace_bytes(int64_t rows, int64_t vocab);
+
+/* The next token of each row of logits (dtype TQ_F16 or TQ_F32, rows row_stride
+ * >= vocab elements apart), from the row's uniform number u in [0, 1):
+ *   w_i = exp((x_i - max x) / temperature);
+ *   of the tokens by descending logit (equal ones: the lower index first) the
+ *   first top_k are kept, of these the fewest, at least one, whose sum of w
+ *   reaches top_p times theirs, of these the ones with w >= min_p;
+ *   token = the first, in index order, at which the running sum of the kept
+ *   tokens' w exceeds u times their sum (u outside: as 0, or the last kept one).
+ * temperature, top_p, min_p (fp32) and top_k (int32) have a value a row, or are
+ * NULL: 1, and no limit.  A temperature that is not above 0 takes the largest
+ * logit (the lowest index of equal ones); top_k <= 0 or >= vocab, top_p not
+ * below 1 and min_p not above 0 set no limit; min_p above 1 counts as 1.
+ * A NaN logit counts as -inf; -inf is never taken: a row of nothing else gives
+ * token -1 and logprob -inf.  Where a logit is +inf, those weigh 1 and all others 0.
+ * logprob (fp32, may be NULL): ln of the token's w over the kept tokens' sum (0
+ * where the largest logit is taken).
+ * Weights and sums are in double; a row's token does not depend on the other
+ * rows.  1 <= rows <= 2^20, 1 <= vocab <= 2^20.  logits 16-byte aligned (its
+ * rows need not be). */
+int tq_sample(int dtype, int64_t rows, int64_t vocab, const void *logits, int64_t row_stride,
+              const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+              const float *u, int32_t *token, float *logprob, void *ws, size_t ws_bytes, void *stream);
+
 /* ---- device: parity hooks (same decode / integer core as above) ------- */
 
 /* What `n` pages of the cache stand for: values[2][n][kv_heads][64][head_dim]

@@ -46,7 +46,8 @@ EXPORTS = ("tq_status_str", "tq_packed_bytes", "tq_pack", "tq_unpack", "tq_quant
            "tq_decode_stack_batch_workspace_bytes", "tq_decode_stack_batch",
            "tq_debug_gemv_quant_rows_sums", "tq_workspace_clear", "tq_workspace_check",
            "tq_rope_table", "tq_kv_append", "tq_kv_attn_workspace_bytes", "tq_kv_attn",
-           "tq_residual_norm", "tq_debug_kv_read", "tq_linear_attn_scratch_bytes", "tq_linear_attn")
+           "tq_residual_norm", "tq_debug_kv_read", "tq_linear_attn_scratch_bytes", "tq_linear_attn",
+           "tq_sample_workspace_bytes", "tq_sample")
 
 
 class TqLayer(ctypes.Structure):
@@ -106,6 +107,8 @@ def _load():
         "tq_residual_norm": ([I, I, I, I64, I64, P, P, P, I64, F64, P, P, P, F64, P, P, P, P], I),
         "tq_linear_attn_scratch_bytes": ([I64, I64, I64, I64, I64], SZ),
         "tq_linear_attn": ([I, I64, I64, I64, I64, I64, P, I64, P, I64, P, P, P, P, I64, F, P, I64, P, SZ, P], I),
+        "tq_sample_workspace_bytes": ([I64, I64], SZ),
+        "tq_sample": ([I, I64, I64, P, I64, P, P, P, P, P, P, P, P, SZ, P], I),
         "tq_debug_kv_read": ([I, I64, I64, I64, P, P, P, P, P, I64, P, P], I),
     }
     for name, (args, res) in sig.items():
@@ -612,6 +615,58 @@ def tq_residual_norm(y, res, res_out, pre_w=None, x=None, q=None, a_scale=None, 
         None if res_out is None else res_out.data_ptr(), None if pre_w is None else pre_w.data_ptr(), eps,
         None if x is None else x.data_ptr(), None if q is None else q.data_ptr(),
         None if a_scale is None else a_scale.data_ptr(), st)
+    if rc:
+        raise TQError(rc, what)
+
+
+# ---- device: behind the last layer ----------------------------------------
+
+def tq_sample_workspace_bytes(rows, vocab) -> int:
+    return int(lib.tq_sample_workspace_bytes(rows, vocab))
+
+
+def sample_workspace(rows, vocab, device="cuda"):
+    """A zero-filled workspace tensor for tq_sample (None when it needs none)."""
+    import torch
+    nbytes = tq_sample_workspace_bytes(rows, vocab)
+    return torch.zeros((nbytes + 15) // 16 * 4, dtype=torch.int32, device=device) if nbytes else None
+
+
+def tq_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, ws=None, stream=None) -> None:
+    """token int32 [rows] = the next token of each row of logits [rows][vocab]
+    (fp16 or fp32; rows may be strided) for the uniform numbers u fp32 [rows] in
+    [0, 1), by each row's temperature, top_p and min_p (fp32 [rows]) and top_k
+    (int32 [rows]); None: 1, or no such limit.  logprob fp32 [rows]: the token's
+    log probability among the kept ones."""
+    what, T = "tq_sample", _Torch.get()
+    dev, st = _current(T, stream, logits)
+    if logits.dim() != 2:
+        raise ValueError(f"{what}: logits must have two dimensions")
+    rows, vocab = shape = logits.shape
+    x, xs = _rows_need(what, "logits", logits, logits.dtype, shape, dev)
+    f32, i32, each = T.f32, T.i32, (rows,)
+    if not (u.dtype is f32 and token.dtype is i32 and u.get_device() == token.get_device() == dev and u.shape == token.shape == each
+            and u.is_contiguous() and token.is_contiguous()
+            and (temperature is None or temperature.dtype is f32 and temperature.get_device() == dev and temperature.shape == each
+                 and temperature.is_contiguous())
+            and (top_k is None or top_k.dtype is i32 and top_k.get_device() == dev and top_k.shape == each and top_k.is_contiguous())
+            and (top_p is None or top_p.dtype is f32 and top_p.get_device() == dev and top_p.shape == each and top_p.is_contiguous())
+            and (min_p is None or min_p.dtype is f32 and min_p.get_device() == dev and min_p.shape == each and min_p.is_contiguous())
+            and (logprob is None or logprob.dtype is f32 and logprob.get_device() == dev and logprob.shape == each
+                 and logprob.is_contiguous())):
+        for name, t, dtype in (("u", u, f32), ("token", token, i32), ("temperature", temperature, f32), ("top_k", top_k, i32),
+                               ("top_p", top_p, f32), ("min_p", min_p, f32), ("logprob", logprob, f32)):
+            if t is not None:
+                _need(what, name, t, dtype, each, dev)
+    wp, wb = None, 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"{what}: ws must be contiguous and on the current GPU")
+        wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
+    rc = lib.tq_sample(T.acts.get(logits.dtype, -1), rows, vocab, x, xs, None if temperature is None else temperature.data_ptr(),
+                       None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+                       None if min_p is None else min_p.data_ptr(), u.data_ptr(), token.data_ptr(),
+                       None if logprob is None else logprob.data_ptr(), wp, wb, st)
     if rc:
         raise TQError(rc, what)
 

@@ -210,7 +210,7 @@ struct Turned {
   }
 };
 
-// x as two fp16 terms, together within 2^-21 of it (or the least fp16 step):
+// x as two fp16 terms, together within 2^-20 of it (or the least fp16 step):
 // the first cut off, two elements an instruction.
 __device__ __forceinline__ void two_terms(const float (&x)[8], h8 &hi, h8 &lo) {
   typedef __fp16 c2 __attribute__((ext_vector_type(2)));

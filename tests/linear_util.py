@@ -51,28 +51,30 @@ def state_tolerance(M, n, fall, chunks_form):
     (U of it), its product and the sum one rounding each: n (5 U) and U times the
     log2 decays' sum (times ln 2 < 1).
     In chunks: a weight is an exp2 of a rounded sum and a product (4 U and the
-    sums' U); two fp16 terms a factor leave 2^-22 of it, the product of the
-    second terms is 2^-22 (together 12 U for both factors and that); 3 x 128
+    sums' U); two fp16 terms a factor, both cut off, leave 2^-20 of it, and the
+    product of the second terms is 2^-20 (48 U for both factors and that); 3 x 128
     terms are added in fp32 (384 U), each chunk's state with two roundings and a
     decay of 2 U: 4 U a chunk.  fp16's least step, half of 2^-24 under a largest
     element of at least 2^13, is 2^-38 of a tile's largest key times a value
     (and the reverse), in up to 64 terms a tile: 2^-30 of the largest M."""
     if not chunks_form:
         return (5 * n + fall + 4) * U * M
-    return (400 + 4 * math.ceil(n / 128) + 2 * fall) * U * M + 2.0 ** -30 * M.amax((1, 2), keepdim=True)
+    return (440 + 4 * math.ceil(n / 128) + 2 * fall) * U * M + 2.0 ** -30 * M.amax((1, 2), keepdim=True)
 
 
-def out_tolerance(ref, mag, most, n, fall, dim, wide, chunks_form):
+def out_tolerance(ref, mag, most, n, fall, dim, chunks_form):
     """Row by row: the state's error, the query's scaling and dim products and
     sums in fp32, then fp16 (half a step, 2^-11, or half of the least one).
-    In chunks: of the factors of a term, fp16 inputs round the weight or the state
-    once to fp16 (2^-11); fp32 inputs also query, key and value: four at most
-    (second orders: less than 2^-11 of these in all, counted as 1 %).  Small parts of a tile as for
+    In chunks: of the factors of a term, the state (of a term with it) or the fp32
+    value (of the others) is rounded once to fp16 (2^-11); query, key and weight
+    have two terms and lose 2^-20 each, 2^-20 more for a product of second
+    terms (64 U), dim products and sums of a score and up to 500 of an output
+    are in fp32, three terms each.  Small parts of a tile as for
     states: 2^-30 of the largest magnitude `most` of the sequence and head."""
     t = 2.0 ** -11 * ref.abs() + 2.0 ** -25
     if not chunks_form:
         return t + (5 * n + fall + dim + 8) * U * mag
-    return t + (1.01 * (4 if wide else 1) * 2.0 ** -11 + (2 * dim + 500 + 2 * fall) * U) * mag + 2.0 ** -30 * most
+    return t + (2.0 ** -11 + (3 * dim + 64 + 2 * 500 + 2 * fall) * U) * mag + 2.0 ** -30 * most
 
 
 def check(got_out, got_states, qkv, log_decay, cu, start, to, states, scale, hq, hkv, dim):
@@ -87,7 +89,7 @@ def check(got_out, got_states, qkv, log_decay, cu, start, to, states, scale, hq,
         f = fall[s].reshape(1, hkv, 1, 1)
         sh = (b - a, hkv, hq // hkv, dim)
         ref, m = out[a:b].reshape(sh), mag[a:b].reshape(sh)
-        tol = out_tolerance(ref, m, m.amax((0, 2, 3), keepdim=True), b - a, f, dim, qkv.dtype == torch.float32, form)
+        tol = out_tolerance(ref, m, m.amax((0, 2, 3), keepdim=True), b - a, f, dim, form)
         got = got_out[a:b].to(F8).reshape(sh)
         err = (got - ref).abs()
         # from 65520 on fp16 rounds to infinity
