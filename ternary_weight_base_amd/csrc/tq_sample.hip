@@ -32,6 +32,8 @@ struct SampleArgs {
   float *logprob;
   int64_t row_stride;
   int rows, vocab;
+  int row0, segs;  // a pass over the rows: its first; segments of a row
+  bool wide;       // every row aligned to 16 bytes
 };
 
 // A row's settings.
@@ -208,11 +210,7 @@ template <typename T, int NT>
 __device__ int pick(const T *x, int vocab, int seg, const Weigher &weigh, const Cut &cut, double min_p, double before,
                     double target, double *room, double &weight) {
   constexpr int kEach = kSeg / NT;
-  __shared__ int first, end;
-  if (threadIdx.x == 0) {
-    first = 0x7fffffff;
-    end = -1;
-  }
+  __shared__ int first[NT / 64], end[NT / 64];
   double w[kEach], sum = 0.0;
   const int i0 = seg * kSeg + threadIdx.x * kEach;
 #pragma unroll
@@ -226,32 +224,77 @@ __device__ int pick(const T *x, int vocab, int seg, const Weigher &weigh, const 
     sum += w[j];
   }
   double c = before + block_before<NT>(sum, room);
+  int above = 0x7fffffff, some = -1;
 #pragma unroll
   for (int j = 0; j < kEach; j++) {
     c += w[j];
     if (w[j] > 0.0) {
-      if (c > target) atomicMin(&first, i0 + j);
-      atomicMax(&end, i0 + j);
+      if (c > target) above = min(above, i0 + j);
+      some = i0 + j;
     }
   }
+  // (a wave's lanes are in index order)
+  const uint64_t has_above = __ballot(above < 0x7fffffff), has_some = __ballot(some >= 0);
+  if ((threadIdx.x & 63) == 0) {
+    first[threadIdx.x >> 6] = 0x7fffffff;
+    end[threadIdx.x >> 6] = -1;
+  }
   __syncthreads();
-  const int i = first < 0x7fffffff ? first : end;
+  if (has_above && (int)(threadIdx.x & 63) == __builtin_ctzll(has_above)) first[threadIdx.x >> 6] = above;
+  if (has_some && (int)(threadIdx.x & 63) == 63 - __builtin_clzll(has_some)) end[threadIdx.x >> 6] = some;
+  __syncthreads();
+  int i = 0x7fffffff, last = -1;
+#pragma unroll
+  for (int j = 0; j < NT / 64; j++) {
+    i = min(i, first[j]);
+    last = max(last, end[j]);
+  }
+  if (i == 0x7fffffff) i = last;
   weight = i >= 0 ? weigh(clean((float)x[i])) : 0.0;
   return i;
 }
 
+__device__ __forceinline__ void answer(const SampleArgs &A, int row, int token, double weight, double total) {
+  A.token[row] = token;
+  if (A.logprob) A.logprob[row] = token < 0 ? -__builtin_inff() : weight == total ? 0.0f : (float)log(weight / total);
+}
+
+// The token from the segments' sums of kept weights.
 template <typename T, int NT>
-__global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
+__device__ void choose(const SampleArgs &A, int row, int segs, const double *seg_sum, const Weigher &weigh, const Cut &cut,
+                       double min_p, double *room) {
+  double total = 0.0;
+  for (int s = 0; s < segs; s++) total += seg_sum[s];
+  const float u = A.u[row];
+  const double target = (u > 0.0f ? (double)u : 0.0) * total;
+  double before = 0.0;
+  int seg = 0;
+  for (int s = 0, some = -1; s < segs; s++) {
+    if (!(seg_sum[s] > 0.0)) continue;
+    if (some >= 0) before += seg_sum[some];
+    seg = some = s;
+    if (before + seg_sum[s] > target) break;
+  }
+  double weight;
+  const int i = pick<T, NT>((const T *)A.logits + row * A.row_stride, A.vocab, seg, weigh, cut, min_p, before, target, room, weight);
+  if (threadIdx.x == 0) answer(A, row, i, weight, total);
+}
+
+// A row's token by one workgroup: where the segments' way (below) does not lead
+// on, and for vocabularies of one segment.
+template <typename T, int NT>
+__device__ void whole_row(const SampleArgs &A, int row) {
   __shared__ uint64_t hist[256];
   __shared__ double room[NT / 64], seg_sum[kMaxSegs];
   __shared__ float wave_most[NT / 64];
   __shared__ int where;
-  const int row = blockIdx.x, tid = threadIdx.x, vocab = A.vocab;
+  const int tid = threadIdx.x, vocab = A.vocab;
   const T *x = (const T *)A.logits + row * A.row_stride;
   const Rule rule = rule_of(A, row);
   float most = -__builtin_inff();
   for (int i = tid; i < vocab; i += NT) most = fmaxf(most, clean((float)x[i]));
   most = tqdev::wave_max64(most);
+  __syncthreads();
   if ((tid & 63) == 0) wave_most[tid >> 6] = most;
   if (tid == 0) where = 0x7fffffff;
   __syncthreads();
@@ -264,15 +307,11 @@ __global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
         break;
       }
     __syncthreads();
-    if (tid == 0) {
-      const bool none = most == -__builtin_inff();
-      A.token[row] = none ? -1 : where;
-      if (A.logprob) A.logprob[row] = none ? -__builtin_inff() : 0.0f;
-    }
+    if (tid == 0) answer(A, row, most == -__builtin_inff() ? -1 : where, 1.0, 1.0);
     return;
   }
   const Weigher weigh = {most, rule.per};
-  Cut cut = {key_of(-__builtin_inff()), -1};
+  Cut cut = {0, -1};
   if (rule.top_k < vocab) narrow<T, NT>(x, vocab, weigh, false, (double)rule.top_k, cut, hist, room);
   if (rule.top_p < 1.0) {
     double sum = 0.0;
@@ -281,7 +320,7 @@ __global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
       if (cut.keeps(key_of(v), i)) sum += weigh(v);
     }
     sum = block_sum<NT>(sum, room);
-    narrow<T, NT>(x, vocab, weigh, true, fmax(rule.top_p, 0.0) * sum, cut, hist, room);
+    narrow<T, NT>(x, vocab, weigh, true, rule.top_p * sum, cut, hist, room);
   }
   const int segs = (vocab + kSeg - 1) / kSeg;
   for (int s = 0; s < segs; s++) {
@@ -295,24 +334,464 @@ __global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
     if (tid == 0) seg_sum[s] = sum;
   }
   __syncthreads();
-  double total = 0.0;
-  for (int s = 0; s < segs; s++) total += seg_sum[s];
-  const float u = A.u[row];
-  const double target = (u > 0.0f ? (double)u : 0.0) * total;
-  double before = 0.0;
-  int seg = -1;
-  for (int s = 0; s < segs; s++) {
-    if (!(seg_sum[s] > 0.0)) continue;
-    if (seg >= 0) before += seg_sum[seg];
-    seg = s;
-    if (before + seg_sum[s] > target) break;
+  choose<T, NT>(A, row, segs, seg_sum, weigh, cut, rule.min_p, room);
+}
+
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
+  whole_row<T, NT>(A, blockIdx.x);
+}
+
+// ---- a workgroup a segment -----------------------------------------------------
+//
+// Two launches.  In the first each segment's largest logit and, in units of its
+// weight, either the sum of its weights or how many tokens (and what weight) fall
+// into each of 255 steps of the logits; the row's last workgroup joins them.
+// Without limits it takes the token at once; else it finds the step in which the
+// limit falls.  In the second the tokens of that step (top-k up to kFewK: of all
+// steps down to it) are gathered, and sums made of the steps above; the row's last
+// workgroup narrows them down by a finer step, sorts what is left, cuts and takes
+// the token.  A row that gathers more than kGather tokens or has more than kSort
+// left (flat logits), or has a larger top_k and top_p too, is done by its last
+// workgroup alone, as above.
+
+constexpr int kThreads = 256, kOwn = kSeg / kThreads;
+constexpr int kSteps = 256;    // the last one: everything below the others
+constexpr int kGather = 16384;  // tokens of a row
+constexpr int kSort = kSeg;     // ... of them sorted
+constexpr int kFewK = 1024;
+constexpr double kFixed = 0x1p48;  // weights as integers: kGather of them stay in 62 bits
+
+enum Mode { kDone = 0, kTopK, kManyK, kTopP, kMinP, kAlone };
+
+struct SegInfo {
+  float most;
+  int index;   // of the largest logit, where that is the answer
+  double sum;  // of the segment's weights, in units of its largest one's
+};
+
+// What the second launch has to know of a row.
+struct RowInfo {
+  int mode;
+  float most;
+  int step;     // the gathered step
+  int top_step; // of the largest logit
+  double left;  // top_k's tokens, or top_p's sum, to be found in that step
+};
+
+// The workspace: all zero between calls.
+struct SampleWs {
+  uint32_t *counters;  // a row: segments done in the first launch, in the second, tokens gathered
+  RowInfo *info;
+  SegInfo *seg;
+  double *seg_sum;
+  uint32_t *count;     // [row][segment][step]
+  uint64_t *weight;
+  uint64_t *gathered;  // [row][kGather]: key, then the index's complement
+};
+
+template <typename V>
+__device__ __forceinline__ void put(V *p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+__device__ __forceinline__ V get(const V *p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Whether this workgroup is the last of a row's `segs`, whose words (put) it may
+// then get; the counter is left zero.
+__device__ __forceinline__ bool last_one(uint32_t *counter, int segs) {
+  __shared__ int last;
+  __builtin_amdgcn_s_waitcnt(0);  // this thread's words have reached device scope
+  __syncthreads();                // ... and so have every other thread's
+  if (threadIdx.x == 0) {
+    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(segs - 1);
+    if (last) put(counter, 0u);
   }
-  double weight;
-  const int i = pick<T, NT>(x, vocab, seg, weigh, cut, rule.min_p, before, target, room, weight);
+  __syncthreads();
+  return last;
+}
+
+// A segment's logits, kOwn a thread; `wide`: 16 bytes a load (rows aligned to them).
+template <typename T>
+struct Own {
+  static constexpr int kV = 16 / sizeof(T);
+  float x[kOwn];
+  bool wide;
+  int first;
+  __device__ __forceinline__ int index(int j) const {
+    return wide ? first + (j / kV * kThreads + (int)threadIdx.x) * kV + j % kV : first + j * kThreads + (int)threadIdx.x;
+  }
+  __device__ __forceinline__ void load(const SampleArgs &A, const T *row, int seg) {
+    wide = A.wide;
+    first = seg * kSeg;
+    typedef T Wide __attribute__((ext_vector_type(kV)));
+    if (wide && first + kSeg <= A.vocab) {
+      Wide v[kOwn / kV];
+#pragma unroll
+      for (int i = 0; i < kOwn / kV; i++) v[i] = *reinterpret_cast<const Wide *>(row + first + (i * kThreads + threadIdx.x) * kV);
+#pragma unroll
+      for (int j = 0; j < kOwn; j++) x[j] = clean((float)v[j / kV][j % kV]);
+    } else {
+      T v[kOwn];
+#pragma unroll
+      for (int j = 0; j < kOwn; j++) v[j] = index(j) < A.vocab ? row[index(j)] : (T)-__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < kOwn; j++) x[j] = clean((float)v[j]);
+    }
+  }
+};
+
+// The steps are of an eighth of a logit (for top-p of the temperature, where that
+// is below 1): the 255 reach 32 logits, or weights of 2^-46, down.  Rounding keeps
+// the order, and segments count from steps of the same grid.
+struct Steps {
+  float per;
+  __device__ __forceinline__ Steps(const Rule &r, int mode)
+      : per(mode == kTopP ? fminf(8.0f * fmaxf((float)(r.per * 0.6931471805599453), 1.0f), 1e30f) : 8.0f) {}
+  __device__ __forceinline__ int operator()(float x) const { return (int)floorf(fminf(fmaxf(x * per, -1e9f), 1e9f)); }
+  // the 256th of step `at` (of the grid) that x lies in, from its upper end; below the step: the last
+  __device__ __forceinline__ int part(float x, int at) const {
+    const float f = (fminf(fmaxf(x * per, -1e9f), 1e9f) - (float)at) * 256.0f;
+    return 255 - (int)fminf(fmaxf(f, 0.0f), 255.0f);
+  }
+};
+
+__device__ __forceinline__ float block_most(float v, float *room) {
+  v = tqdev::wave_max64(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(room[0], room[1]), fmaxf(room[2], room[3]));
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, const SampleWs W) {
+  __shared__ uint32_t count[kSteps];
+  __shared__ unsigned long long weight[kSteps];
+  __shared__ double room[4], seg_sum[kMaxSegs], share[kMaxSegs];
+  __shared__ float froom[4];
+  __shared__ int seg_step[kMaxSegs], where;
+  const int tid = threadIdx.x, segs = A.segs;
+  const int rel = blockIdx.x / (uint32_t)segs, seg = blockIdx.x % (uint32_t)segs, row = A.row0 + rel;
+  const T *x = (const T *)A.logits + row * A.row_stride;
+  Own<T> own;
+  own.load(A, x, seg);
+  const Rule rule = rule_of(A, row);
+  const bool by_k = rule.top_k < A.vocab, by_p = rule.top_p < 1.0;
+  const int mode = rule.greedy ? kDone : by_k ? (rule.top_k <= kFewK ? kTopK : by_p ? kAlone : kManyK) : by_p ? kTopP : rule.min_p > 0.0 ? kMinP : kDone;
+  const Steps step(rule, mode);
+  float most = own.x[0];
+#pragma unroll
+  for (int j = 1; j < kOwn; j++) most = fmaxf(most, own.x[j]);
+  if (tid == 0) where = 0x7fffffff;
+  count[tid] = 0;
+  weight[tid] = 0;
+  most = block_most(most, froom);
+  const Weigher in_seg = {most, rule.per};
+  SegInfo mine = {most, 0, 0.0};
+  const int64_t at = (int64_t)rel * segs + seg;
+  if (rule.greedy) {
+#pragma unroll
+    for (int j = kOwn - 1; j >= 0; j--)
+      if (own.x[j] == most) atomicMin(&where, own.index(j));
+    __syncthreads();
+    mine.index = where;
+  } else if (mode == kDone) {
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < kOwn; j++) sum += in_seg(own.x[j]);
+    mine.sum = block_sum<kThreads>(sum, room);
+  } else if (mode == kTopK || mode == kManyK || mode == kTopP) {
+    // (a thread's run of the same step is added at once: equal logits would queue)
+    const int top = step(most);
+    int run = -1;
+    uint32_t n = 0;
+    unsigned long long sum = 0;
+    auto add = [&]() {
+      if (run < 0) return;
+      atomicAdd(&count[run], n);
+      if (mode == kTopP) atomicAdd(&weight[run], sum);
+    };
+#pragma unroll
+    for (int j = 0; j < kOwn; j++)
+      if (own.x[j] > -__builtin_inff()) {
+        const int b = min(top - step(own.x[j]), kSteps - 1);
+        if (b != run) {
+          add();
+          run = b;
+          n = 0;
+          sum = 0;
+        }
+        n++;
+        if (mode == kTopP) sum += (unsigned long long)rint(in_seg(own.x[j]) * kFixed);
+      }
+    add();
+    __syncthreads();
+    put(W.count + at * kSteps + tid, count[tid]);
+    if (mode == kTopP) {
+      put(W.weight + at * kSteps + tid, (uint64_t)weight[tid]);
+      mine.sum = block_sum<kThreads>((double)weight[tid] / kFixed, room);
+    }
+  }
   if (tid == 0) {
-    A.token[row] = i;
-    if (A.logprob) A.logprob[row] = (float)log(weight / total);
+    put(&W.seg[at].most, mine.most);
+    put(&W.seg[at].index, mine.index);
+    put(&W.seg[at].sum, mine.sum);
   }
+  if (!last_one(W.counters + 4 * rel, segs)) return;
+
+  // the row's last workgroup
+  const SegInfo *all = W.seg + (int64_t)rel * segs;
+  const float seg_most = tid < segs ? get(&all[tid].most) : -__builtin_inff();
+  most = block_most(seg_most, froom);
+  const bool none = most == -__builtin_inff();
+  const Weigher weigh = {most, rule.per};
+  const int top = step(most);
+  if (tid < segs) {
+    share[tid] = weigh(seg_most);  // of a segment's unit
+    seg_sum[tid] = get(&all[tid].sum) * share[tid];
+    // (a segment without a token that may come counts from far below)
+    seg_step[tid] = seg_most == -__builtin_inff() ? 2 * kSteps : min(top - step(seg_most), 2 * kSteps);
+  }
+  if (none || mode == kDone) {
+    if (rule.greedy && !none) {
+      if (tid == 0) where = 0x7fffffff;
+      __syncthreads();
+      if (tid < segs && seg_most == most) atomicMin(&where, get(&all[tid].index));
+    }
+    __syncthreads();
+    if (none || rule.greedy) {
+      if (tid == 0) answer(A, row, none ? -1 : where, 1.0, 1.0);
+    } else {
+      choose<T, kThreads>(A, row, segs, seg_sum, weigh, Cut{0, -1}, 0.0, room);
+    }
+    for (int i = tid; i < segs; i += kThreads) W.seg[(int64_t)rel * segs + i] = SegInfo{0.0f, 0, 0.0};
+    return;
+  }
+  RowInfo info = {mode, most, 0, top, 0.0};
+  if (mode == kTopK || mode == kManyK || mode == kTopP) {
+    __syncthreads();
+    // thread t's step: t below the largest logit's
+    double have = 0.0;
+    const uint32_t *c = W.count + (int64_t)rel * segs * kSteps;
+    const uint64_t *w = W.weight + (int64_t)rel * segs * kSteps;
+    if (mode == kTopP) {
+#pragma unroll 8
+      for (int i = 0; i < segs; i++) {
+        const int b = tid - seg_step[i];
+        const uint64_t v = get(w + i * kSteps + max(b, 0));
+        have += b >= 0 ? (double)v / kFixed * share[i] : 0.0;
+      }
+    } else {
+#pragma unroll 8
+      for (int i = 0; i < segs; i++) {
+        const int b = tid - seg_step[i];
+        const uint32_t v = get(c + i * kSteps + max(b, 0));
+        have += b >= 0 ? (double)v : 0.0;
+      }
+    }
+    if (tid == kSteps - 1) have = 0.0;  // (not whole: other segments' last steps belong to it too)
+    double target = (double)rule.top_k;
+    if (mode == kTopP) {
+      double sum = 0.0;
+      for (int i = 0; i < segs; i++) sum += seg_sum[i];
+      target = rule.top_p * sum;
+    }
+    const double before = block_before<kThreads>(have, room);
+    // the first step that reaches the target; nothing does: the last one
+    if (tid == 0) where = kSteps - 1;
+    __syncthreads();
+    if (tid < kSteps - 1 && before + have >= target && have > 0.0) atomicMin(&where, tid);
+    __syncthreads();
+    info.step = where;
+    if (tid == info.step) {
+      info.left = target - before;
+      W.info[rel] = info;
+    }
+  } else if (tid == 0) {
+    W.info[rel] = info;
+  }
+}
+
+// Sorts n <= kGather words in descending order (room behind them for the next
+// power of two).
+__device__ __forceinline__ void sort_down(uint64_t *v, int n) {
+  int size = 64;
+  while (size < n) size *= 2;
+  for (int i = n + threadIdx.x; i < size; i += kThreads) v[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= size; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+        const int a = 2 * t - (t & (j - 1)), b = a + j;  // the bit of j clear, set
+        const uint64_t x = v[a], y = v[b];
+        if ((x < y) == ((a & k) == 0)) {
+          v[a] = y;
+          v[b] = x;
+        }
+      }
+      __syncthreads();
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, const SampleWs W) {
+  __shared__ uint64_t list[kSort];
+  __shared__ double room[4], seg_sum[kMaxSegs];
+  __shared__ unsigned long long extra[kMaxSegs], fine[kSteps];
+  __shared__ int found, base, kept;
+  const int tid = threadIdx.x, segs = A.segs;
+  const int rel = blockIdx.x / (uint32_t)segs, seg = blockIdx.x % (uint32_t)segs, row = A.row0 + rel;
+  const RowInfo info = W.info[rel];
+  if (info.mode == kDone) return;
+  const T *x = (const T *)A.logits + row * A.row_stride;
+  const int64_t at = (int64_t)rel * segs + seg;
+  const Rule rule = rule_of(A, row);
+  const Weigher weigh = {info.most, rule.per};
+  uint32_t *counters = W.counters + 4 * rel;
+  uint64_t *gathered = W.gathered + (int64_t)rel * kGather;
+  if (info.mode != kAlone) {
+    Own<T> own;
+    own.load(A, x, seg);
+    if (info.mode != kMinP) {
+      W.count[at * kSteps + tid] = 0;
+      if (info.mode == kTopP) W.weight[at * kSteps + tid] = 0;
+    }
+    if (tid == 0) found = 0;
+    __syncthreads();
+    const Steps step(rule, info.mode);
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < kOwn; j++) {
+      const float v = own.x[j];
+      const int b = info.mode == kMinP ? -1 : min(info.top_step - step(v), kSteps - 1);
+      if (!(v > -__builtin_inff()) || b > info.step) continue;
+      if (b == info.step || info.mode == kTopK) {
+        const int i = atomicAdd(&found, 1);
+        list[i] = (uint64_t)key_of(v) << 32 | (uint32_t)~own.index(j);
+      } else {
+        const double w = weigh(v);
+        if (w >= rule.min_p) sum += w;
+      }
+    }
+    sum = block_sum<kThreads>(sum, room);
+    if (tid == 0) {
+      put(W.seg_sum + at, sum);
+      base = found ? (int)__hip_atomic_fetch_add(counters + 2, (uint32_t)found, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < found && base + i < kGather; i += kThreads) put(gathered + base + i, list[i]);
+  }
+  if (!last_one(counters + 1, segs)) return;
+
+  // the row's last workgroup
+  const int n = (int)get(counters + 2);
+  if (tid == 0) counters[2] = 0;
+  for (int i = tid; i < segs; i += kThreads) {
+    seg_sum[i] = get(W.seg_sum + (int64_t)rel * segs + i);
+    extra[i] = 0;
+    W.seg_sum[(int64_t)rel * segs + i] = 0.0;
+    W.seg[(int64_t)rel * segs + i] = SegInfo{0.0f, 0, 0.0};
+  }
+  if (tid == 0) {
+    W.info[rel] = RowInfo{0, 0.0f, 0, 0, 0.0};
+    kept = 0;
+  }
+  fine[tid] = 0;
+  __syncthreads();
+  auto value = [&](uint64_t entry) {
+    const uint32_t k = (uint32_t)(entry >> 32);
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+  };
+  auto keep = [&](uint64_t entry) {
+    const double w = weigh(value(entry));
+    if (w >= rule.min_p) atomicAdd(&extra[(int)~(uint32_t)entry / kSeg], (unsigned long long)rint(w * kFixed));
+  };
+  double left = info.left;
+  bool alone = info.mode == kAlone || n > kGather;
+  int m = n;  // tokens to be sorted
+  if (!alone && (info.mode == kTopK || n <= kThreads)) {
+    alone = n > kSort;
+    for (int i = tid; i < min(n, kSort); i += kThreads) list[i] = get(gathered + i);
+  } else if (!alone) {
+    // by 256ths of the step: those above the one in which the limit falls are kept
+    const Steps step(rule, info.mode);
+    auto part = [&](uint64_t entry) { return step.part(value(entry), info.top_step - info.step); };
+    const bool weights = info.mode == kTopP;
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t e = get(gathered + i);
+      atomicAdd(&fine[part(e)], weights ? (unsigned long long)rint(weigh(value(e)) * kFixed) : 1ull);
+    }
+    __syncthreads();
+    const double have = (double)fine[tid] / (weights ? kFixed : 1.0), before = block_before<kThreads>(have, room);
+    // (where roundings of the sums leave the limit unreached: the last one there is)
+    if (tid == 0) {
+      base = kSteps;
+      found = 0;
+    }
+    __syncthreads();
+    if (have > 0.0) {
+      if (before + have >= left) atomicMin(&base, tid);
+      atomicMax(&found, tid);
+    }
+    __syncthreads();
+    const int at_part = base < kSteps ? base : found;
+    __syncthreads();
+    if (tid == 0) found = 0;
+    if (tid == at_part) room[0] = left - before;
+    __syncthreads();
+    left = room[0];
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t e = get(gathered + i);
+      const int q = part(e);
+      if (q < at_part) keep(e);
+      if (q == at_part) {
+        const int k = atomicAdd(&found, 1);
+        if (k < kSort) list[k] = e;
+      }
+    }
+    __syncthreads();
+    m = found;
+    alone = m > kSort;
+  }
+  for (int i = tid; i < min(n, kGather); i += kThreads) gathered[i] = 0;
+  __syncthreads();
+  if (alone) {
+    whole_row<T, kThreads>(A, row);
+    return;
+  }
+  Cut cut = {0, -1};
+  if (info.mode != kMinP) {
+    sort_down(list, m);
+    // thread t has the sorted tokens from t * each on
+    const int each = (m + kThreads - 1) / kThreads, i0 = tid * each;
+    const int top = info.mode == kTopK ? min(rule.top_k, m) : info.mode == kManyK ? min((int)left, m) : m;
+    int mine = 0;
+    if (rule.top_p < 1.0) {
+      double sum = 0.0;
+      for (int i = i0; i < min(i0 + each, top); i++) sum += weigh(value(list[i]));
+      double c = block_before<kThreads>(sum, room);
+      const double target = info.mode == kTopP ? left : rule.top_p * block_sum<kThreads>(sum, room);
+      for (int i = i0; i < min(i0 + each, top); i++) {
+        mine += i == 0 || c < target;
+        c += weigh(value(list[i]));
+      }
+    } else {
+      mine = max(min(i0 + each, top) - i0, 0);
+    }
+    if (mine) atomicAdd(&kept, mine);
+    __syncthreads();
+    // (nothing is there where the limit falls behind the last token: all are kept)
+    const uint64_t lowest = kept ? list[kept - 1] : 0xffffffffull;
+    cut = Cut{(uint32_t)(lowest >> 32), (int)~(uint32_t)lowest};
+    for (int i = i0; i < min(i0 + each, kept); i++) keep(list[i]);
+    __syncthreads();
+    for (int i = tid; i < segs; i += kThreads) seg_sum[i] += (double)extra[i] / kFixed;
+    __syncthreads();
+  }
+  choose<T, kThreads>(A, row, segs, seg_sum, weigh, cut, rule.min_p, room);
 }
 
 bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -321,12 +800,28 @@ int check_shape(int64_t rows, int64_t vocab) {
   return rows < 1 || rows > (1 << 20) || vocab < 1 || vocab > kMaxVocab ? TQ_ERR_SHAPE : TQ_OK;
 }
 
+// A call's rows in passes whose words fit kWsBytes.
+constexpr size_t kWsBytes = (size_t)1 << 27;
+
+struct Plan {
+  int64_t segs, pass;  // pass 0: a workgroup a row, no workspace
+  size_t bytes;
+};
+
+Plan make_plan(int64_t rows, int64_t vocab) {
+  Plan P = {(vocab + kSeg - 1) / kSeg, 0, 0};
+  if (P.segs == 1) return P;
+  const size_t each = sizeof(RowInfo) + kGather * 8 + 16 + (size_t)P.segs * (sizeof(SegInfo) + 8 + kSteps * 12);
+  P.pass = (int64_t)(kWsBytes / each);
+  if (P.pass > rows) P.pass = rows;
+  P.bytes = (size_t)P.pass * each;
+  return P;
+}
+
 }  // namespace
 
 extern "C" size_t tq_sample_workspace_bytes(int64_t rows, int64_t vocab) {
-  (void)rows;
-  (void)vocab;
-  return 0;
+  return check_shape(rows, vocab) == TQ_OK ? make_plan(rows, vocab).bytes : 0;
 }
 
 extern "C" int tq_sample(int dtype, int64_t rows, int64_t vocab, const void *logits, int64_t row_stride,
@@ -341,12 +836,38 @@ extern "C" int tq_sample(int dtype, int64_t rows, int64_t vocab, const void *log
       !aligned_to(top_p, 4) || !aligned_to(min_p, 4) || !aligned_to(u, 4) || !aligned_to(token, 4) ||
       !aligned_to(logprob, 4))
     return TQ_ERR_ALIGN;
-  const size_t need = tq_sample_workspace_bytes(rows, vocab);
-  if (need && !ws) return TQ_ERR_NULL;
-  if (ws_bytes < need) return TQ_ERR_SIZE;
-  const SampleArgs A = {logits, temperature, top_p, min_p, u, top_k, token, logprob, row_stride, (int)rows, (int)vocab};
+  const Plan P = make_plan(rows, vocab);
+  if (P.bytes && !ws) return TQ_ERR_NULL;
+  if (ws_bytes < P.bytes) return TQ_ERR_SIZE;
+  const int64_t unit = dtype == TQ_F16 ? 8 : 4;
+  SampleArgs A = {logits, temperature, top_p, min_p, u, top_k, token, logprob, row_stride, (int)rows, (int)vocab,
+                  0, (int)P.segs, rows == 1 || row_stride % unit == 0};
   hipStream_t st = (hipStream_t)stream;
-  if (dtype == TQ_F16) hipLaunchKernelGGL((row_kernel<_Float16, 1024>), dim3((unsigned)rows), dim3(1024), 0, st, A);
-  else hipLaunchKernelGGL((row_kernel<float, 1024>), dim3((unsigned)rows), dim3(1024), 0, st, A);
+  if (P.pass == 0) {
+    if (dtype == TQ_F16) hipLaunchKernelGGL((row_kernel<_Float16, 1024>), dim3((unsigned)rows), dim3(1024), 0, st, A);
+    else hipLaunchKernelGGL((row_kernel<float, 1024>), dim3((unsigned)rows), dim3(1024), 0, st, A);
+    return hipGetLastError() == hipSuccess ? TQ_OK : TQ_ERR_HIP;
+  }
+  char *p = (char *)ws;
+  const size_t n = (size_t)P.pass, ns = n * (size_t)P.segs;
+  SampleWs W;
+  W.info = (RowInfo *)p;
+  W.seg = (SegInfo *)(p += n * sizeof(RowInfo));
+  W.gathered = (uint64_t *)(p += ns * sizeof(SegInfo));
+  W.weight = (uint64_t *)(p += n * kGather * 8);
+  W.seg_sum = (double *)(p += ns * kSteps * 8);
+  W.count = (uint32_t *)(p += ns * 8);
+  W.counters = (uint32_t *)(p += ns * kSteps * 4);
+  for (int64_t r = 0; r < rows; r += P.pass) {
+    A.row0 = (int)r;
+    const dim3 grid((unsigned)((rows - r < P.pass ? rows - r : P.pass) * P.segs)), block(kThreads);
+    if (dtype == TQ_F16) {
+      hipLaunchKernelGGL((first_kernel<_Float16>), grid, block, 0, st, A, W);
+      hipLaunchKernelGGL((second_kernel<_Float16>), grid, block, 0, st, A, W);
+    } else {
+      hipLaunchKernelGGL((first_kernel<float>), grid, block, 0, st, A, W);
+      hipLaunchKernelGGL((second_kernel<float>), grid, block, 0, st, A, W);
+    }
+  }
   return hipGetLastError() == hipSuccess ? TQ_OK : TQ_ERR_HIP;
 }

@@ -101,6 +101,51 @@ def test_largest_vocabulary():
 
 
 @pytest.mark.parametrize("dtype", ["float16", "float32"])
+def test_large_k(dtype):
+    """More tokens than are sorted: by their count, with top-p, and where fewer may come than k."""
+    rng = np.random.default_rng(14)
+    for kind, vocab in (("usual", 60000), ("masked", 60000), ("steps", 9000), ("flat", 9000)):
+        x = logits(rng, 6, vocab, kind, dtype)
+        k = [1024, 1025, 3000, 8000, vocab - 1, 5000]
+        u = rng.random(6)
+        assert verify(x, u, k=k) >= 5 or kind in ("steps", "flat")
+        verify(x, u, k=k, m=[1e-3] * 6)
+        verify(x, u, k=k, p=[0.3, 0.5, 0.9, 0.99, 0.7, 0.999], t=[0.3, 0.5, 1.0, 2.0, 5.0, 100.0])
+
+
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
+def test_steep_and_flat_temperatures(dtype):
+    """The place of top-p from the first token to the bulk, in steps of few and of very many tokens."""
+    rng = np.random.default_rng(15)
+    x = logits(rng, 12, 70001, "usual", dtype)
+    t = [0.01, 0.1, 0.3, 0.6, 1.0, 1.3, 2.0, 3.0, 5.0, 10.0, 100.0, 1e6]
+    for p in (0.05, 0.5, 0.9, 0.99, 0.9999):
+        assert verify(x, rng.random(12), t=t, p=[p] * 12) >= 11
+        verify(x, rng.random(12), t=t, p=[p] * 12, m=[1e-4] * 12)
+    for k in (1, 64, 1000):
+        assert verify(x, rng.random(12), t=t, k=[k] * 12, p=[0.9] * 12) >= 11
+
+
+def test_many_rows_of_more_than_one_segment():
+    """More rows than a pass holds."""
+    import ternary_weight_base_amd as tq
+    rng = np.random.default_rng(16)
+    rows, vocab = 1500, 4100
+    assert tq.tq_sample_workspace_bytes(rows, vocab) < rows * 150000
+    x = logits(rng, rows, vocab, "usual", "float16")
+    u = rng.random(rows)
+    token, lp = call(x, u, **settings(rng, "mixed", rows))
+    assert token.min() >= 0
+    pick = np.arange(0, rows, 37)
+    rng = np.random.default_rng(17)
+    s = settings(rng, "all", rows)
+    token, _ = call(x, u, **s)
+    for r in pick:
+        want, _, margin = sample(x[r], float(np.float32(u[r])), *(float(np.float32(s[n][r])) if n != "k" else int(s[n][r]) for n in "tkpm"))
+        assert margin <= NEAR or token[r] == want
+
+
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
 def test_strided_rows(dtype):
     rng = np.random.default_rng(4)
     for vocab, stride in ((5001, 5001), (5000, 5003), (4096, 5000), (10007, 10009)):
