@@ -71,22 +71,21 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ double power2(double t) {
   if (!(t > -1000.0)) return 0.0;
   const double n = rint(t), f = (t - n) * 0.6931471805599453;
-  // exp's series: |f| <= 0.3466, its 14th term is below 2^-57
-  double s = 1.0 / 6227020800.0;
-  s = fma(s, f, 1.0 / 479001600.0);
-  s = fma(s, f, 1.0 / 39916800.0);
-  s = fma(s, f, 1.0 / 3628800.0);
-  s = fma(s, f, 1.0 / 362880.0);
-  s = fma(s, f, 1.0 / 40320.0);
-  s = fma(s, f, 1.0 / 5040.0);
-  s = fma(s, f, 1.0 / 720.0);
-  s = fma(s, f, 1.0 / 120.0);
-  s = fma(s, f, 1.0 / 24.0);
-  s = fma(s, f, 1.0 / 6.0);
-  s = fma(s, f, 0.5);
-  s = fma(s, f, 1.0);
-  s = fma(s, f, 1.0);
+  // exp's series: |f| <= 0.3466, its 14th term is below 2^-57; in pairs, fours
+  // and eights, since a chain of fourteen products would be waited for
+  const double f2 = f * f, f4 = f2 * f2;
+  const double a = fma(fma(1.0 / 6.0, f, 0.5), f2, 1.0 + f);
+  const double b = fma(fma(1.0 / 5040.0, f, 1.0 / 720.0), f2, fma(1.0 / 120.0, f, 1.0 / 24.0));
+  const double c = fma(fma(1.0 / 39916800.0, f, 1.0 / 3628800.0), f2, fma(1.0 / 362880.0, f, 1.0 / 40320.0));
+  const double d = fma(1.0 / 6227020800.0, f, 1.0 / 479001600.0);
+  const double s = fma(fma(fma(d, f4, c), f4, b), f4, a);
   return ldexp(s, (int)n);
+}
+
+// A weight (at most 1) in steps of 1 / steps, a power of two up to 2^48, to the
+// nearest: the sum with 2^52 has it in its low bits.
+__device__ __forceinline__ uint64_t fixed(double w, double steps) {
+  return __builtin_bit_cast(uint64_t, fma(w, steps, 0x1p52)) - __builtin_bit_cast(uint64_t, 0x1p52);
 }
 
 // The row's logits as its weights are taken from them: where one is +inf those
@@ -119,21 +118,44 @@ __device__ __forceinline__ double block_sum(double v, double *room) {
   for (int i = 1; i < NT / 64; i++) s += room[i];
   return s;
 }
-// ... of the threads before this one.
+// Sums of the lanes up to this one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double from_below(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_upto(double v) {
+  v += from_below<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v += from_below<0x112, 0xF>(v);
+  v += from_below<0x114, 0xF>(v);
+  v += from_below<0x118, 0xF>(v);
+  v += from_below<0x142, 0xA>(v);  // lane 15 of rows 0, 2 to rows 1, 3
+  v += from_below<0x143, 0xC>(v);  // lane 31 to rows 2, 3
+  return v;
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)b, lane), hi = __builtin_amdgcn_readlane((int)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// ... of the threads before this one (`all`: of all threads).
 template <int NT>
-__device__ __forceinline__ double block_before(double v, double *room) {
+__device__ __forceinline__ double block_before(double v, double *room, double *all = nullptr) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  double sum = v;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double o = __shfl_up(sum, d);
-    if (lane >= d) sum += o;
-  }
+  const double sum = wave_upto(v);
   __syncthreads();
   if (lane == 63) room[wave] = sum;
   __syncthreads();
-  double s = 0.0;
-  for (int i = 0; i < wave; i++) s += room[i];
+  double s = 0.0, t = 0.0;
+#pragma unroll
+  for (int i = 0; i < NT / 64; i++) {
+    s = i == wave ? t : s;
+    t += room[i];
+  }
+  if (all) *all = t;
   return s + (sum - v);
 }
 
@@ -151,7 +173,7 @@ __device__ void narrow(const T *x, int vocab, const Weigher &weigh, bool weights
   __shared__ int last;
   uint32_t prefix = 0;
   double rest = target;
-  const int bits = 62 - (32 - __builtin_clz(vocab));
+  const int bits = min(62 - (32 - __builtin_clz(vocab)), 48);
   const double steps = weights ? ldexp(1.0, bits) : 1.0, unit = weights ? ldexp(1.0, -bits) : 1.0;
   for (int shift = 24; shift >= 0; shift -= 8) {
     for (int i = threadIdx.x; i < 256; i += NT) hist[i] = 0;
@@ -161,7 +183,7 @@ __device__ void narrow(const T *x, int vocab, const Weigher &weigh, bool weights
       const float v = clean((float)x[i]);
       const uint32_t k = key_of(v);
       if (v > -__builtin_inff() && (k & mask) == prefix && cut.keeps(k, i))
-        atomicAdd((unsigned long long *)&hist[k >> shift & 255], weights ? (unsigned long long)rint(weigh(v) * steps) : 1ull);
+        atomicAdd((unsigned long long *)&hist[k >> shift & 255], weights ? (unsigned long long)fixed(weigh(v), steps) : 1ull);
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -204,54 +226,69 @@ __device__ void narrow(const T *x, int vocab, const Weigher &weigh, bool weights
   __syncthreads();
 }
 
-// The token of a segment at which the running sum from `before` on exceeds
-// `target`: the first one, or the last that is kept; its weight.
+// A segment's logits into LDS, -inf behind the vocabulary; `wide`: rows aligned to
+// 16 bytes.
 template <typename T, int NT>
-__device__ int pick(const T *x, int vocab, int seg, const Weigher &weigh, const Cut &cut, double min_p, double before,
-                    double target, double *room, double &weight) {
-  constexpr int kEach = kSeg / NT;
-  __shared__ int first[NT / 64], end[NT / 64];
-  double w[kEach], sum = 0.0;
-  const int i0 = seg * kSeg + threadIdx.x * kEach;
+__device__ __forceinline__ void stage(const T *x, bool wide, int vocab, int seg, float *xs) {
+  constexpr int kV = (int)(16 / sizeof(T)) < kSeg / NT ? 16 / sizeof(T) : kSeg / NT;
+  typedef T Wide __attribute__((ext_vector_type(kV)));
+  const int tid = threadIdx.x;
+  x += seg * kSeg;
+  if (wide && (seg + 1) * kSeg <= vocab) {
+    Wide v[kSeg / NT / kV];
 #pragma unroll
-  for (int j = 0; j < kEach; j++) {
-    w[j] = 0.0;
-    if (i0 + j < vocab) {
-      const float v = clean((float)x[i0 + j]);
-      const double e = weigh(v);
-      if (cut.keeps(key_of(v), i0 + j) && e >= min_p) w[j] = e;
-    }
-    sum += w[j];
-  }
-  double c = before + block_before<NT>(sum, room);
-  int above = 0x7fffffff, some = -1;
+    for (int i = 0; i < kSeg / NT / kV; i++) v[i] = reinterpret_cast<const Wide *>(x)[i * NT + tid];
 #pragma unroll
-  for (int j = 0; j < kEach; j++) {
-    c += w[j];
-    if (w[j] > 0.0) {
-      if (c > target) above = min(above, i0 + j);
-      some = i0 + j;
-    }
+    for (int i = 0; i < kSeg / NT / kV; i++)
+#pragma unroll
+      for (int j = 0; j < kV; j++) xs[(i * NT + tid) * kV + j] = clean((float)v[i][j]);
+  } else {
+    const int n = vocab - seg * kSeg;
+    T v[kSeg / NT];
+#pragma unroll
+    for (int i = 0; i < kSeg / NT; i++) v[i] = i * NT + tid < n ? x[i * NT + tid] : (T)-__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < kSeg / NT; i++) xs[i * NT + tid] = clean((float)v[i]);
   }
-  // (a wave's lanes are in index order)
-  const uint64_t has_above = __ballot(above < 0x7fffffff), has_some = __ballot(some >= 0);
-  if ((threadIdx.x & 63) == 0) {
-    first[threadIdx.x >> 6] = 0x7fffffff;
-    end[threadIdx.x >> 6] = -1;
+}
+
+// The token of a segment (its logits in LDS) at which the running sum from
+// `before` on exceeds `target`: the first one, or the last that weighs something;
+// its weight.  A wave has 64 consecutive tokens of each NT.
+template <int NT>
+__device__ int pick(const float *xs, int seg, const Weigher &weigh, const Cut &cut, double min_p, double before, double target,
+                    double &weight) {
+  constexpr int kCells = kSeg / 64;
+  __shared__ double cell[kCells];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto weight_of = [&](int i) {
+    const float c = xs[i];
+    double w = 0.0;
+    if (cut.keeps(key_of(c), seg * kSeg + i)) {
+      w = weigh(c);
+      if (!(w >= min_p)) w = 0.0;
+    }
+    return w;
+  };
+  __syncthreads();
+#pragma unroll 4
+  for (int j = 0; j < kCells / (NT / 64); j++) {
+    const int i = j * (NT / 64) + wave;
+    const double sum = tqdev::wave_sum64(weight_of(i * 64 + lane));
+    if (lane == 0) cell[i] = sum;
   }
   __syncthreads();
-  if (has_above && (int)(threadIdx.x & 63) == __builtin_ctzll(has_above)) first[threadIdx.x >> 6] = above;
-  if (has_some && (int)(threadIdx.x & 63) == 63 - __builtin_clzll(has_some)) end[threadIdx.x >> 6] = some;
-  __syncthreads();
-  int i = 0x7fffffff, last = -1;
-#pragma unroll
-  for (int j = 0; j < NT / 64; j++) {
-    i = min(i, first[j]);
-    last = max(last, end[j]);
-  }
-  if (i == 0x7fffffff) i = last;
-  weight = i >= 0 ? weigh(clean((float)x[i])) : 0.0;
-  return i;
+  // the cell that crosses the target, or the last with a sum: every wave finds it
+  static_assert(kCells == 64, "a cell a lane");
+  const double own = cell[lane], upto = before + wave_upto(own);
+  const uint64_t some = __ballot(own > 0.0), above = __ballot(own > 0.0 && upto > target);
+  const int at = above ? __builtin_ctzll(above) : some ? 63 - __builtin_clzll(some) : 0;
+  const double from = lane_value(upto - own, at);
+  const double w = weight_of(at * 64 + lane), r = from + wave_upto(w);
+  const uint64_t some1 = __ballot(w > 0.0), above1 = __ballot(w > 0.0 && r > target);
+  const int l = above1 ? __builtin_ctzll(above1) : some1 ? 63 - __builtin_clzll(some1) : 0;
+  weight = lane_value(w, l);
+  return seg * kSeg + at * 64 + l;
 }
 
 __device__ __forceinline__ void answer(const SampleArgs &A, int row, int token, double weight, double total) {
@@ -259,31 +296,51 @@ __device__ __forceinline__ void answer(const SampleArgs &A, int row, int token, 
   if (A.logprob) A.logprob[row] = token < 0 ? -__builtin_inff() : weight == total ? 0.0f : (float)log(weight / total);
 }
 
-// The token from the segments' sums of kept weights.
+// The token from the segments' sums of kept weights (in LDS); xs: room for a
+// segment's logits.
 template <typename T, int NT>
 __device__ void choose(const SampleArgs &A, int row, int segs, const double *seg_sum, const Weigher &weigh, const Cut &cut,
-                       double min_p, double *room) {
-  double total = 0.0;
-  for (int s = 0; s < segs; s++) total += seg_sum[s];
+                       double min_p, float *xs) {
+  // every wave finds the segment by itself: a lane has four of them
+  static_assert(kMaxSegs <= 256, "four segments a lane");
+  const int lane = threadIdx.x & 63;
+  double mine[4], own = 0.0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    mine[j] = 4 * lane + j < segs ? seg_sum[4 * lane + j] : 0.0;
+    own += mine[j];
+  }
+  const double upto = wave_upto(own), total = lane_value(upto, 63);
   const float u = A.u[row];
   const double target = (u > 0.0f ? (double)u : 0.0) * total;
-  double before = 0.0;
-  int seg = 0;
-  for (int s = 0, some = -1; s < segs; s++) {
-    if (!(seg_sum[s] > 0.0)) continue;
-    if (some >= 0) before += seg_sum[some];
-    seg = some = s;
-    if (before + seg_sum[s] > target) break;
+  double r = upto - own, before_above = 0.0, before_some = 0.0;
+  int above = -1, some = -1;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    if (mine[j] > 0.0) {
+      if (above < 0 && r + mine[j] > target) {
+        above = j;
+        before_above = r;
+      }
+      some = j;
+      before_some = r;
+    }
+    r += mine[j];
   }
+  const uint64_t has_above = __ballot(above >= 0), has_some = __ballot(some >= 0);
+  const int l = has_above ? __builtin_ctzll(has_above) : has_some ? 63 - __builtin_clzll(has_some) : 0;
+  const int seg = 4 * l + max(__builtin_amdgcn_readlane(has_above ? above : some, l), 0);
+  const double from = lane_value(has_above ? before_above : before_some, l);
+  stage<T, NT>((const T *)A.logits + row * A.row_stride, A.wide, A.vocab, seg, xs);
   double weight;
-  const int i = pick<T, NT>((const T *)A.logits + row * A.row_stride, A.vocab, seg, weigh, cut, min_p, before, target, room, weight);
+  const int i = pick<NT>(xs, seg, weigh, cut, min_p, from, target, weight);
   if (threadIdx.x == 0) answer(A, row, i, weight, total);
 }
 
 // A row's token by one workgroup: where the segments' way (below) does not lead
 // on, and for vocabularies of one segment.
 template <typename T, int NT>
-__device__ void whole_row(const SampleArgs &A, int row) {
+__device__ void whole_row(const SampleArgs &A, int row, float *xs) {
   __shared__ uint64_t hist[256];
   __shared__ double room[NT / 64], seg_sum[kMaxSegs];
   __shared__ float wave_most[NT / 64];
@@ -334,12 +391,13 @@ __device__ void whole_row(const SampleArgs &A, int row) {
     if (tid == 0) seg_sum[s] = sum;
   }
   __syncthreads();
-  choose<T, NT>(A, row, segs, seg_sum, weigh, cut, rule.min_p, room);
+  choose<T, NT>(A, row, segs, seg_sum, weigh, cut, rule.min_p, xs);
 }
 
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
-  whole_row<T, NT>(A, blockIdx.x);
+  __shared__ __attribute__((aligned(16))) float xs[kSeg];
+  whole_row<T, NT>(A, blockIdx.x, xs);
 }
 
 // ---- a workgroup a segment -----------------------------------------------------
@@ -399,6 +457,18 @@ __device__ __forceinline__ V get(const V *p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// Such words by the dozen: loads that need not wait for each other.
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr int kDevScope = 16;  // the sc1 bit of the cache policy
+__device__ __forceinline__ Rsrc rsrc_of(const void *p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7fffffff, 0x00027000);
+}
+__device__ __forceinline__ uint32_t get4(Rsrc r, int i) { return __builtin_amdgcn_raw_buffer_load_b32(r, 4 * i, 0, kDevScope); }
+__device__ __forceinline__ uint64_t get8(Rsrc r, int i) {
+  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, 8 * i, 0, kDevScope));
+}
+
 // Whether this workgroup is the last of a row's `segs`, whose words (put) it may
 // then get; the counter is left zero.
 __device__ __forceinline__ bool last_one(uint32_t *counter, int segs) {
@@ -412,36 +482,6 @@ __device__ __forceinline__ bool last_one(uint32_t *counter, int segs) {
   __syncthreads();
   return last;
 }
-
-// A segment's logits, kOwn a thread; `wide`: 16 bytes a load (rows aligned to them).
-template <typename T>
-struct Own {
-  static constexpr int kV = 16 / sizeof(T);
-  float x[kOwn];
-  bool wide;
-  int first;
-  __device__ __forceinline__ int index(int j) const {
-    return wide ? first + (j / kV * kThreads + (int)threadIdx.x) * kV + j % kV : first + j * kThreads + (int)threadIdx.x;
-  }
-  __device__ __forceinline__ void load(const SampleArgs &A, const T *row, int seg) {
-    wide = A.wide;
-    first = seg * kSeg;
-    typedef T Wide __attribute__((ext_vector_type(kV)));
-    if (wide && first + kSeg <= A.vocab) {
-      Wide v[kOwn / kV];
-#pragma unroll
-      for (int i = 0; i < kOwn / kV; i++) v[i] = *reinterpret_cast<const Wide *>(row + first + (i * kThreads + threadIdx.x) * kV);
-#pragma unroll
-      for (int j = 0; j < kOwn; j++) x[j] = clean((float)v[j / kV][j % kV]);
-    } else {
-      T v[kOwn];
-#pragma unroll
-      for (int j = 0; j < kOwn; j++) v[j] = index(j) < A.vocab ? row[index(j)] : (T)-__builtin_inff();
-#pragma unroll
-      for (int j = 0; j < kOwn; j++) x[j] = clean((float)v[j]);
-    }
-  }
-};
 
 // The steps are of an eighth of a logit (for top-p of the temperature, where that
 // is below 1): the 255 reach 32 logits, or weights of 2^-46, down.  Rounding keeps
@@ -470,21 +510,23 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, const SampleWs W) {
   __shared__ uint32_t count[kSteps];
   __shared__ unsigned long long weight[kSteps];
+  __shared__ __attribute__((aligned(16))) float xs[kSeg];
   __shared__ double room[4], seg_sum[kMaxSegs], share[kMaxSegs];
+  __shared__ double part[4][64];
   __shared__ float froom[4];
   __shared__ int seg_step[kMaxSegs], where;
   const int tid = threadIdx.x, segs = A.segs;
   const int rel = blockIdx.x / (uint32_t)segs, seg = blockIdx.x % (uint32_t)segs, row = A.row0 + rel;
   const T *x = (const T *)A.logits + row * A.row_stride;
-  Own<T> own;
-  own.load(A, x, seg);
+  stage<T, kThreads>(x, A.wide, A.vocab, seg, xs);
   const Rule rule = rule_of(A, row);
   const bool by_k = rule.top_k < A.vocab, by_p = rule.top_p < 1.0;
   const int mode = rule.greedy ? kDone : by_k ? (rule.top_k <= kFewK ? kTopK : by_p ? kAlone : kManyK) : by_p ? kTopP : rule.min_p > 0.0 ? kMinP : kDone;
   const Steps step(rule, mode);
-  float most = own.x[0];
+  __syncthreads();
+  float most = xs[tid];
 #pragma unroll
-  for (int j = 1; j < kOwn; j++) most = fmaxf(most, own.x[j]);
+  for (int j = 1; j < kOwn; j++) most = fmaxf(most, xs[j * kThreads + tid]);
   if (tid == 0) where = 0x7fffffff;
   count[tid] = 0;
   weight[tid] = 0;
@@ -493,15 +535,15 @@ __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, con
   SegInfo mine = {most, 0, 0.0};
   const int64_t at = (int64_t)rel * segs + seg;
   if (rule.greedy) {
-#pragma unroll
-    for (int j = kOwn - 1; j >= 0; j--)
-      if (own.x[j] == most) atomicMin(&where, own.index(j));
+#pragma unroll 1
+    for (int j = 0; j < kOwn; j++)
+      if (xs[j * kThreads + tid] == most) atomicMin(&where, seg * kSeg + j * kThreads + tid);
     __syncthreads();
     mine.index = where;
   } else if (mode == kDone) {
     double sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < kOwn; j++) sum += in_seg(own.x[j]);
+#pragma unroll 4
+    for (int j = 0; j < kOwn; j++) sum += in_seg(xs[j * kThreads + tid]);
     mine.sum = block_sum<kThreads>(sum, room);
   } else if (mode == kTopK || mode == kManyK || mode == kTopP) {
     // (a thread's run of the same step is added at once: equal logits would queue)
@@ -514,10 +556,11 @@ __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, con
       atomicAdd(&count[run], n);
       if (mode == kTopP) atomicAdd(&weight[run], sum);
     };
-#pragma unroll
-    for (int j = 0; j < kOwn; j++)
-      if (own.x[j] > -__builtin_inff()) {
-        const int b = min(top - step(own.x[j]), kSteps - 1);
+#pragma unroll 4
+    for (int j = 0; j < kOwn; j++) {
+      const float v = xs[j * kThreads + tid];
+      if (v > -__builtin_inff()) {
+        const int b = min(top - step(v), kSteps - 1);
         if (b != run) {
           add();
           run = b;
@@ -525,8 +568,9 @@ __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, con
           sum = 0;
         }
         n++;
-        if (mode == kTopP) sum += (unsigned long long)rint(in_seg(own.x[j]) * kFixed);
+        if (mode == kTopP) sum += fixed(in_seg(v), kFixed);
       }
+    }
     add();
     __syncthreads();
     put(W.count + at * kSteps + tid, count[tid]);
@@ -565,7 +609,7 @@ __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, con
     if (none || rule.greedy) {
       if (tid == 0) answer(A, row, none ? -1 : where, 1.0, 1.0);
     } else {
-      choose<T, kThreads>(A, row, segs, seg_sum, weigh, Cut{0, -1}, 0.0, room);
+      choose<T, kThreads>(A, row, segs, seg_sum, weigh, Cut{0, -1}, 0.0, xs);
     }
     for (int i = tid; i < segs; i += kThreads) W.seg[(int64_t)rel * segs + i] = SegInfo{0.0f, 0, 0.0};
     return;
@@ -573,40 +617,48 @@ __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, con
   RowInfo info = {mode, most, 0, top, 0.0};
   if (mode == kTopK || mode == kManyK || mode == kTopP) {
     __syncthreads();
-    // thread t's step: t below the largest logit's
-    double have = 0.0;
-    const uint32_t *c = W.count + (int64_t)rel * segs * kSteps;
-    const uint64_t *w = W.weight + (int64_t)rel * segs * kSteps;
-    if (mode == kTopP) {
+    // 64 steps at a time (mostly the first ones are enough), a lane each: the
+    // segments' contents are summed by the waves in turn
+    const Rsrc c = rsrc_of(W.count + (int64_t)rel * segs * kSteps), w = rsrc_of(W.weight + (int64_t)rel * segs * kSteps);
+    const int lane = tid & 63, wave = tid >> 6;
+    double target = (double)rule.top_k, before = 0.0;
+    if (mode == kTopP) target = rule.top_p * block_sum<kThreads>(tid < segs ? seg_sum[tid] : 0.0, room);
+    info.step = kSteps - 1;  // (where nothing above reaches the target)
+#pragma unroll 1
+    for (int s0 = 0; s0 < kSteps; s0 += 64) {
+      const int t = s0 + lane;
+      double have = 0.0;
+      if (mode == kTopP) {
 #pragma unroll 8
-      for (int i = 0; i < segs; i++) {
-        const int b = tid - seg_step[i];
-        const uint64_t v = get(w + i * kSteps + max(b, 0));
-        have += b >= 0 ? (double)v / kFixed * share[i] : 0.0;
-      }
-    } else {
+        for (int i = wave; i < segs; i += 4) {
+          const int b = t - seg_step[i];
+          const uint64_t v = get8(w, i * kSteps + max(b, 0));
+          have += b >= 0 ? (double)v / kFixed * share[i] : 0.0;
+        }
+      } else {
 #pragma unroll 8
-      for (int i = 0; i < segs; i++) {
-        const int b = tid - seg_step[i];
-        const uint32_t v = get(c + i * kSteps + max(b, 0));
-        have += b >= 0 ? (double)v : 0.0;
+        for (int i = wave; i < segs; i += 4) {
+          const int b = t - seg_step[i];
+          const uint32_t v = get4(c, i * kSteps + max(b, 0));
+          have += b >= 0 ? (double)v : 0.0;
+        }
       }
+      part[wave][lane] = have;
+      __syncthreads();
+      have = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+      __syncthreads();
+      if (t == kSteps - 1) have = 0.0;  // (not whole: other segments' last steps belong to it too)
+      const double upto = before + wave_upto(have);
+      const uint64_t there = __ballot(have > 0.0 && upto >= target);
+      if (there) {
+        const int l = __builtin_ctzll(there);
+        info.step = s0 + l;
+        before = lane_value(upto - have, l);
+        break;
+      }
+      before = lane_value(upto, 63);
     }
-    if (tid == kSteps - 1) have = 0.0;  // (not whole: other segments' last steps belong to it too)
-    double target = (double)rule.top_k;
-    if (mode == kTopP) {
-      double sum = 0.0;
-      for (int i = 0; i < segs; i++) sum += seg_sum[i];
-      target = rule.top_p * sum;
-    }
-    const double before = block_before<kThreads>(have, room);
-    // the first step that reaches the target; nothing does: the last one
-    if (tid == 0) where = kSteps - 1;
-    __syncthreads();
-    if (tid < kSteps - 1 && before + have >= target && have > 0.0) atomicMin(&where, tid);
-    __syncthreads();
-    info.step = where;
-    if (tid == info.step) {
+    if (tid == 0) {
       info.left = target - before;
       W.info[rel] = info;
     }
@@ -615,9 +667,14 @@ __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, con
   }
 }
 
-// Sorts n <= kGather words in descending order (room behind them for the next
+__device__ __forceinline__ float logit_of(uint64_t entry) {  // of a key and index
+  const uint32_t k = (uint32_t)(entry >> 32);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// Sorts n <= kSort words in descending order (room behind them for the next
 // power of two).
-__device__ __forceinline__ void sort_down(uint64_t *v, int n) {
+__device__ __forceinline__ void sort_equal(uint64_t *v, int n) {
   int size = 64;
   while (size < n) size *= 2;
   for (int i = n + threadIdx.x; i < size; i += kThreads) v[i] = 0;
@@ -636,10 +693,60 @@ __device__ __forceinline__ void sort_down(uint64_t *v, int n) {
     }
 }
 
+// The same for up to kSort / 2 words, `other` with room for as many: by 256 equal
+// parts of the range between the least and the largest logit, and within a part by
+// counting larger ones; where a part holds many (nearly equal logits) as above.
+__device__ __forceinline__ void sort_down(uint64_t *v, uint64_t *other, int n, float *froom, double *room) {
+  constexpr int kCrowd = 64;
+  __shared__ int count[kThreads], next[kThreads];
+  const int tid = threadIdx.x;
+  float lo = __builtin_inff(), hi = -__builtin_inff();
+  for (int i = tid; i < n; i += kThreads) {
+    lo = fminf(lo, logit_of(v[i]));
+    hi = fmaxf(hi, logit_of(v[i]));
+  }
+  count[tid] = 0;
+  hi = block_most(hi, froom);
+  lo = -block_most(-lo, froom);
+  const float per = hi > lo ? 256.0f / (hi - lo) : 0.0f;
+  auto part = [&](uint64_t e) { return (int)fminf(fmaxf((hi - logit_of(e)) * per, 0.0f), 255.0f); };
+  for (int i = tid; i < n; i += kThreads) atomicAdd(&count[part(v[i])], 1);
+  __syncthreads();
+  const int mine = count[tid];
+  next[tid] = (int)block_before<kThreads>((double)mine, room);
+  if (block_most((float)mine, froom) > (float)kCrowd) {
+    sort_equal(v, n);
+    return;
+  }
+  for (int i = tid; i < n; i += kThreads) other[atomicAdd(&next[part(v[i])], 1)] = v[i];
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t e = other[i];
+    const int p = part(e), end = next[p], first = end - count[p];
+    int at = first;
+    for (int k = first; k < end; k++) at += other[k] > e;
+    v[at] = e;
+  }
+  __syncthreads();
+}
+
+// The same for up to a word a thread: its place is the number of larger ones.
+__device__ __forceinline__ void sort_few(uint64_t *v, int n) {
+  const uint64_t a = (int)threadIdx.x < n ? v[threadIdx.x] : 0;
+  int at = 0;
+#pragma unroll 8
+  for (int i = 0; i < n; i++) at += v[i] > a;
+  __syncthreads();
+  if ((int)threadIdx.x < n) v[at] = a;
+  __syncthreads();
+}
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, const SampleWs W) {
-  __shared__ uint64_t list[kSort];
+  __shared__ __attribute__((aligned(16))) uint64_t list[kSort];
+  float *xs = reinterpret_cast<float *>(list + kSort / 2);  // a segment's logits, while few are gathered from it
   __shared__ double room[4], seg_sum[kMaxSegs];
+  __shared__ float froom[4];
   __shared__ unsigned long long extra[kMaxSegs], fine[kSteps];
   __shared__ int found, base, kept;
   const int tid = threadIdx.x, segs = A.segs;
@@ -653,36 +760,41 @@ __global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, co
   uint32_t *counters = W.counters + 4 * rel;
   uint64_t *gathered = W.gathered + (int64_t)rel * kGather;
   if (info.mode != kAlone) {
-    Own<T> own;
-    own.load(A, x, seg);
+    stage<T, kThreads>(x, A.wide, A.vocab, seg, xs);
     if (info.mode != kMinP) {
       W.count[at * kSteps + tid] = 0;
       if (info.mode == kTopP) W.weight[at * kSteps + tid] = 0;
     }
-    if (tid == 0) found = 0;
-    __syncthreads();
     const Steps step(rule, info.mode);
     double sum = 0.0;
-#pragma unroll
+    uint32_t mine = 0;  // this thread's tokens that are gathered
+    __syncthreads();
+#pragma unroll 4
     for (int j = 0; j < kOwn; j++) {
-      const float v = own.x[j];
+      const float v = xs[j * kThreads + tid];
       const int b = info.mode == kMinP ? -1 : min(info.top_step - step(v), kSteps - 1);
       if (!(v > -__builtin_inff()) || b > info.step) continue;
       if (b == info.step || info.mode == kTopK) {
-        const int i = atomicAdd(&found, 1);
-        list[i] = (uint64_t)key_of(v) << 32 | (uint32_t)~own.index(j);
+        mine |= 1u << j;
       } else {
         const double w = weigh(v);
         if (w >= rule.min_p) sum += w;
       }
     }
     sum = block_sum<kThreads>(sum, room);
+    double all;
+    int to = (int)block_before<kThreads>((double)__popc(mine), room, &all);
     if (tid == 0) {
       put(W.seg_sum + at, sum);
-      base = found ? (int)__hip_atomic_fetch_add(counters + 2, (uint32_t)found, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+      base = all > 0.0 ? (int)__hip_atomic_fetch_add(counters + 2, (uint32_t)all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
     }
     __syncthreads();
-    for (int i = tid; i < found && base + i < kGather; i += kThreads) put(gathered + base + i, list[i]);
+    to += base;
+#pragma unroll 1
+    for (; mine; mine &= mine - 1, to++) {
+      const int i = __builtin_ctz(mine) * kThreads + tid;
+      if (to < kGather) put(gathered + to, (uint64_t)key_of(xs[i]) << 32 | (uint32_t)~(seg * kSeg + i));
+    }
   }
   if (!last_one(counters + 1, segs)) return;
 
@@ -697,32 +809,30 @@ __global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, co
   }
   if (tid == 0) {
     W.info[rel] = RowInfo{0, 0.0f, 0, 0, 0.0};
-    kept = 0;
+    kept = kGather;
   }
   fine[tid] = 0;
   __syncthreads();
-  auto value = [&](uint64_t entry) {
-    const uint32_t k = (uint32_t)(entry >> 32);
-    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-  };
+  const Rsrc words = rsrc_of(gathered);
   auto keep = [&](uint64_t entry) {
-    const double w = weigh(value(entry));
-    if (w >= rule.min_p) atomicAdd(&extra[(int)~(uint32_t)entry / kSeg], (unsigned long long)rint(w * kFixed));
+    const double w = weigh(logit_of(entry));
+    if (w >= rule.min_p) atomicAdd(&extra[(int)~(uint32_t)entry / kSeg], (unsigned long long)fixed(w, kFixed));
   };
   double left = info.left;
   bool alone = info.mode == kAlone || n > kGather;
   int m = n;  // tokens to be sorted
   if (!alone && (info.mode == kTopK || n <= kThreads)) {
     alone = n > kSort;
-    for (int i = tid; i < min(n, kSort); i += kThreads) list[i] = get(gathered + i);
+    for (int i = tid; i < min(n, kSort); i += kThreads) list[i] = get8(words, i);
   } else if (!alone) {
     // by 256ths of the step: those above the one in which the limit falls are kept
     const Steps step(rule, info.mode);
-    auto part = [&](uint64_t entry) { return step.part(value(entry), info.top_step - info.step); };
+    auto part = [&](uint64_t entry) { return step.part(logit_of(entry), info.top_step - info.step); };
     const bool weights = info.mode == kTopP;
+#pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
-      const uint64_t e = get(gathered + i);
-      atomicAdd(&fine[part(e)], weights ? (unsigned long long)rint(weigh(value(e)) * kFixed) : 1ull);
+      const uint64_t e = get8(words, i);
+      atomicAdd(&fine[part(e)], weights ? (unsigned long long)fixed(weigh(logit_of(e)), kFixed) : 1ull);
     }
     __syncthreads();
     const double have = (double)fine[tid] / (weights ? kFixed : 1.0), before = block_before<kThreads>(have, room);
@@ -744,7 +854,7 @@ __global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, co
     __syncthreads();
     left = room[0];
     for (int i = tid; i < n; i += kThreads) {
-      const uint64_t e = get(gathered + i);
+      const uint64_t e = get8(words, i);
       const int q = part(e);
       if (q < at_part) keep(e);
       if (q == at_part) {
@@ -759,39 +869,47 @@ __global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, co
   for (int i = tid; i < min(n, kGather); i += kThreads) gathered[i] = 0;
   __syncthreads();
   if (alone) {
-    whole_row<T, kThreads>(A, row);
+    whole_row<T, kThreads>(A, row, reinterpret_cast<float *>(list));
     return;
   }
   Cut cut = {0, -1};
   if (info.mode != kMinP) {
-    sort_down(list, m);
-    // thread t has the sorted tokens from t * each on
-    const int each = (m + kThreads - 1) / kThreads, i0 = tid * each;
+    if (m > kSort / 2) sort_equal(list, m);
+    else if (m > kThreads / 2) sort_down(list, list + kSort / 2, m, froom, room);
+    else sort_few(list, m);
+    // the limits, kThreads sorted tokens at a time (a second time for top-p of top-k)
     const int top = info.mode == kTopK ? min(rule.top_k, m) : info.mode == kManyK ? min((int)left, m) : m;
-    int mine = 0;
+    int keeps = top;
     if (rule.top_p < 1.0) {
-      double sum = 0.0;
-      for (int i = i0; i < min(i0 + each, top); i++) sum += weigh(value(list[i]));
-      double c = block_before<kThreads>(sum, room);
-      const double target = info.mode == kTopP ? left : rule.top_p * block_sum<kThreads>(sum, room);
-      for (int i = i0; i < min(i0 + each, top); i++) {
-        mine += i == 0 || c < target;
-        c += weigh(value(list[i]));
+      double target = left;
+      if (info.mode == kTopK) {
+        double sum = 0.0;
+        for (int i = tid; i < top; i += kThreads) sum += weigh(logit_of(list[i]));
+        target = rule.top_p * block_sum<kThreads>(sum, room);
       }
-    } else {
-      mine = max(min(i0 + each, top) - i0, 0);
+      double before = 0.0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < top; i0 += kThreads) {
+        const int i = i0 + tid;
+        const double w = i < top ? weigh(logit_of(list[i])) : 0.0;
+        double all;
+        const double c = before + block_before<kThreads>(w, room, &all);
+        if (i < top && i > 0 && c >= target) atomicMin(&kept, i);  // the first that is not needed
+        __syncthreads();
+        if (kept < top) break;
+        before += all;
+      }
+      keeps = min(kept, top);
     }
-    if (mine) atomicAdd(&kept, mine);
-    __syncthreads();
     // (nothing is there where the limit falls behind the last token: all are kept)
-    const uint64_t lowest = kept ? list[kept - 1] : 0xffffffffull;
+    const uint64_t lowest = keeps ? list[keeps - 1] : 0xffffffffull;
     cut = Cut{(uint32_t)(lowest >> 32), (int)~(uint32_t)lowest};
-    for (int i = i0; i < min(i0 + each, kept); i++) keep(list[i]);
+    for (int i = tid; i < keeps; i += kThreads) keep(list[i]);
     __syncthreads();
     for (int i = tid; i < segs; i += kThreads) seg_sum[i] += (double)extra[i] / kFixed;
     __syncthreads();
   }
-  choose<T, kThreads>(A, row, segs, seg_sum, weigh, cut, rule.min_p, room);
+  choose<T, kThreads>(A, row, segs, seg_sum, weigh, cut, rule.min_p, reinterpret_cast<float *>(list));
 }
 
 bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
