@@ -67,19 +67,28 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// 2^t for t <= 0, to some 2^-51 of it; 0 from 2^-1000 on (and for -inf, NaN).
-__device__ __forceinline__ double power2(double t) {
+// 2^t for t <= 0, to some 2^-51 of it; 0 from 2^-1000 on (and for -inf, NaN): a
+// power of two, a 64th of one from a table in LDS and exp's series up to its fifth
+// power for the rest, |r| <= 0.0055 (the next term is below 2^-54).
+constexpr int kParts = 64;
+__device__ __forceinline__ double power2(double t, const double *table) {
   if (!(t > -1000.0)) return 0.0;
-  const double n = rint(t), f = (t - n) * 0.6931471805599453;
-  // exp's series: |f| <= 0.3466, its 14th term is below 2^-57; in pairs, fours
-  // and eights, since a chain of fourteen products would be waited for
-  const double f2 = f * f, f4 = f2 * f2;
-  const double a = fma(fma(1.0 / 6.0, f, 0.5), f2, 1.0 + f);
-  const double b = fma(fma(1.0 / 5040.0, f, 1.0 / 720.0), f2, fma(1.0 / 120.0, f, 1.0 / 24.0));
-  const double c = fma(fma(1.0 / 39916800.0, f, 1.0 / 3628800.0), f2, fma(1.0 / 362880.0, f, 1.0 / 40320.0));
-  const double d = fma(1.0 / 6227020800.0, f, 1.0 / 479001600.0);
-  const double s = fma(fma(fma(d, f4, c), f4, b), f4, a);
-  return ldexp(s, (int)n);
+  const double n = rint(t * kParts), r = (t - n * (1.0 / kParts)) * 0.6931471805599453;
+  const int k = (int)n;
+  const double r2 = r * r;
+  const double s = fma(fma(fma(1.0 / 120.0, r, 1.0 / 24.0), r2, fma(1.0 / 6.0, r, 0.5)), r2, 1.0 + r);
+  return ldexp(s * table[k & (kParts - 1)], k >> 6);
+}
+
+// The table, 2^(i / 64), by 64 threads: exp's series at up to 0.3466, whose 14th
+// term is below 2^-57.  (A barrier before its use.)
+__device__ __forceinline__ void fill_table(double *table) {
+  const int i = threadIdx.x;
+  if (i >= kParts) return;
+  const double f = (i < kParts / 2 ? i : i - kParts) * (0.6931471805599453 / kParts);
+  double s = 1.0;
+  for (int k = 13; k > 0; k--) s = fma(s, f / k, 1.0);
+  table[i] = i < kParts / 2 ? s : 2.0 * s;
 }
 
 // A weight (at most 1) in steps of 1 / steps, a power of two up to 2^48, to the
@@ -93,9 +102,10 @@ __device__ __forceinline__ uint64_t fixed(double w, double steps) {
 struct Weigher {
   float most;
   double per;
+  const double *table;
   __device__ __forceinline__ double operator()(float x) const {
     if (most == __builtin_inff()) return x == most ? 1.0 : 0.0;
-    return x == -__builtin_inff() ? 0.0 : power2(((double)x - (double)most) * per);
+    return x == -__builtin_inff() ? 0.0 : power2(((double)x - (double)most) * per, table);
   }
 };
 
@@ -340,7 +350,7 @@ __device__ void choose(const SampleArgs &A, int row, int segs, const double *seg
 // A row's token by one workgroup: where the segments' way (below) does not lead
 // on, and for vocabularies of one segment.
 template <typename T, int NT>
-__device__ void whole_row(const SampleArgs &A, int row, float *xs) {
+__device__ void whole_row(const SampleArgs &A, int row, const double *table, float *xs) {
   __shared__ uint64_t hist[256];
   __shared__ double room[NT / 64], seg_sum[kMaxSegs];
   __shared__ float wave_most[NT / 64];
@@ -367,7 +377,7 @@ __device__ void whole_row(const SampleArgs &A, int row, float *xs) {
     if (tid == 0) answer(A, row, most == -__builtin_inff() ? -1 : where, 1.0, 1.0);
     return;
   }
-  const Weigher weigh = {most, rule.per};
+  const Weigher weigh = {most, rule.per, table};
   Cut cut = {0, -1};
   if (rule.top_k < vocab) narrow<T, NT>(x, vocab, weigh, false, (double)rule.top_k, cut, hist, room);
   if (rule.top_p < 1.0) {
@@ -397,30 +407,46 @@ __device__ void whole_row(const SampleArgs &A, int row, float *xs) {
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
   __shared__ __attribute__((aligned(16))) float xs[kSeg];
-  whole_row<T, NT>(A, blockIdx.x, xs);
+  __shared__ double table[kParts];
+  fill_table(table);  // (whole_row has barriers before its first use)
+  whole_row<T, NT>(A, blockIdx.x, table, xs);
 }
 
 // ---- a workgroup a segment -----------------------------------------------------
 //
-// Two launches.  In the first each segment's largest logit and, in units of its
-// weight, either the sum of its weights or how many tokens (and what weight) fall
-// into each of 255 steps of the logits; the row's last workgroup joins them.
-// Without limits it takes the token at once; else it finds the step in which the
-// limit falls.  In the second the tokens of that step (top-k up to kFewK: of all
-// steps down to it) are gathered, and sums made of the steps above; the row's last
-// workgroup narrows them down by a finer step, sorts what is left, cuts and takes
-// the token.  A row that gathers more than kGather tokens or has more than kSort
-// left (flat logits), or has a larger top_k and top_p too, is done by its last
-// workgroup alone, as above.
+// Four launches, two with a workgroup a segment and two with one a row behind them:
+//  - each segment's largest logit and, in units of its weight, either the sum of
+//    its weights or how many tokens (and what weight) fall into each of 255 steps
+//    of the logits;
+//  - a row without limits gets its token; else the step is found in which the
+//    limit falls;
+//  - the tokens of that step (top-k up to kFewK: of all steps down to it) are
+//    gathered, and each segment's weights in the steps above summed;
+//  - the gathered ones are narrowed down by a finer step, what is left is sorted and
+//    cut, and the token taken.
+// A row that gathers more than kGather tokens or has more than kSort left (flat
+// logits), or has a larger top_k and top_p too, is done by the last launch's
+// workgroup alone, as above.  (Instead of the launches for a row, the last of its
+// segments' workgroups did their work at first: 64 against 51 us for 64 rows, since
+// what it meets in had to be written past the caches and its room in LDS was
+// every workgroup's.)
 
 constexpr int kThreads = 256, kOwn = kSeg / kThreads;
-constexpr int kSteps = 256;    // the last one: everything below the others
+constexpr int kLast = 1024;     // threads of the last launch
+constexpr int kSteps = 256;     // the last one: everything below the others
 constexpr int kGather = 16384;  // tokens of a row
-constexpr int kSort = kSeg;     // ... of them sorted
+constexpr int kSort = 4096;     // ... of them sorted
 constexpr int kFewK = 1024;
 constexpr double kFixed = 0x1p48;  // weights as integers: kGather of them stay in 62 bits
 
 enum Mode { kDone = 0, kTopK, kManyK, kTopP, kMinP, kAlone };
+
+__device__ __forceinline__ int mode_of(const SampleArgs &A, const Rule &r) {
+  const bool by_k = r.top_k < A.vocab, by_p = r.top_p < 1.0;
+  if (r.greedy) return kDone;
+  if (by_k) return r.top_k <= kFewK ? kTopK : by_p ? kAlone : kManyK;
+  return by_p ? kTopP : r.min_p > 0.0 ? kMinP : kDone;
+}
 
 struct SegInfo {
   float most;
@@ -428,60 +454,25 @@ struct SegInfo {
   double sum;  // of the segment's weights, in units of its largest one's
 };
 
-// What the second launch has to know of a row.
+// What the later launches have to know of a row.
 struct RowInfo {
   int mode;
   float most;
-  int step;     // the gathered step
-  int top_step; // of the largest logit
-  double left;  // top_k's tokens, or top_p's sum, to be found in that step
+  int step;      // the gathered step
+  int top_step;  // of the largest logit
+  double left;   // top_k's tokens, or top_p's sum, to be found in that step
 };
 
 // The workspace: all zero between calls.
 struct SampleWs {
-  uint32_t *counters;  // a row: segments done in the first launch, in the second, tokens gathered
   RowInfo *info;
   SegInfo *seg;
   double *seg_sum;
+  uint32_t *found;     // a row's gathered tokens
   uint32_t *count;     // [row][segment][step]
   uint64_t *weight;
   uint64_t *gathered;  // [row][kGather]: key, then the index's complement
 };
-
-template <typename V>
-__device__ __forceinline__ void put(V *p, V v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-template <typename V>
-__device__ __forceinline__ V get(const V *p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// Such words by the dozen: loads that need not wait for each other.
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-constexpr int kDevScope = 16;  // the sc1 bit of the cache policy
-__device__ __forceinline__ Rsrc rsrc_of(const void *p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7fffffff, 0x00027000);
-}
-__device__ __forceinline__ uint32_t get4(Rsrc r, int i) { return __builtin_amdgcn_raw_buffer_load_b32(r, 4 * i, 0, kDevScope); }
-__device__ __forceinline__ uint64_t get8(Rsrc r, int i) {
-  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, 8 * i, 0, kDevScope));
-}
-
-// Whether this workgroup is the last of a row's `segs`, whose words (put) it may
-// then get; the counter is left zero.
-__device__ __forceinline__ bool last_one(uint32_t *counter, int segs) {
-  __shared__ int last;
-  __builtin_amdgcn_s_waitcnt(0);  // this thread's words have reached device scope
-  __syncthreads();                // ... and so have every other thread's
-  if (threadIdx.x == 0) {
-    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(segs - 1);
-    if (last) put(counter, 0u);
-  }
-  __syncthreads();
-  return last;
-}
 
 // The steps are of an eighth of a logit (for top-p of the temperature, where that
 // is below 1): the 255 reach 32 logits, or weights of 2^-46, down.  Rounding keeps
@@ -498,52 +489,57 @@ struct Steps {
   }
 };
 
+template <int NT>
 __device__ __forceinline__ float block_most(float v, float *room) {
   v = tqdev::wave_max64(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
   __syncthreads();
-  return fmaxf(fmaxf(room[0], room[1]), fmaxf(room[2], room[3]));
+  v = room[0];
+#pragma unroll
+  for (int i = 1; i < NT / 64; i++) v = fmaxf(v, room[i]);
+  return v;
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, const SampleWs W) {
+__global__ __launch_bounds__(kThreads) void segment_kernel(const SampleArgs A, const SampleWs W) {
+  __shared__ __attribute__((aligned(16))) float xs[kSeg];
   __shared__ uint32_t count[kSteps];
   __shared__ unsigned long long weight[kSteps];
-  __shared__ __attribute__((aligned(16))) float xs[kSeg];
-  __shared__ double room[4], seg_sum[kMaxSegs], share[kMaxSegs];
-  __shared__ double part[4][64];
-  __shared__ float froom[4];
-  __shared__ int seg_step[kMaxSegs], where;
+  __shared__ double room[kThreads / 64], table[kParts];
+  __shared__ float froom[kThreads / 64];
+  __shared__ int where;
   const int tid = threadIdx.x, segs = A.segs;
   const int rel = blockIdx.x / (uint32_t)segs, seg = blockIdx.x % (uint32_t)segs, row = A.row0 + rel;
-  const T *x = (const T *)A.logits + row * A.row_stride;
-  stage<T, kThreads>(x, A.wide, A.vocab, seg, xs);
+  stage<T, kThreads>((const T *)A.logits + row * A.row_stride, A.wide, A.vocab, seg, xs);
   const Rule rule = rule_of(A, row);
-  const bool by_k = rule.top_k < A.vocab, by_p = rule.top_p < 1.0;
-  const int mode = rule.greedy ? kDone : by_k ? (rule.top_k <= kFewK ? kTopK : by_p ? kAlone : kManyK) : by_p ? kTopP : rule.min_p > 0.0 ? kMinP : kDone;
+  const int mode = mode_of(A, rule);
   const Steps step(rule, mode);
+  if (mode == kDone || mode == kTopP) fill_table(table);
+  if (tid == 0) where = 0x7fffffff;
+  count[tid] = 0;
+  weight[tid] = 0;
   __syncthreads();
   float most = xs[tid];
 #pragma unroll
   for (int j = 1; j < kOwn; j++) most = fmaxf(most, xs[j * kThreads + tid]);
-  if (tid == 0) where = 0x7fffffff;
-  count[tid] = 0;
-  weight[tid] = 0;
-  most = block_most(most, froom);
-  const Weigher in_seg = {most, rule.per};
+  most = block_most<kThreads>(most, froom);
+  const Weigher weigh = {most, rule.per, table};
   SegInfo mine = {most, 0, 0.0};
   const int64_t at = (int64_t)rel * segs + seg;
   if (rule.greedy) {
 #pragma unroll 1
     for (int j = 0; j < kOwn; j++)
-      if (xs[j * kThreads + tid] == most) atomicMin(&where, seg * kSeg + j * kThreads + tid);
+      if (xs[j * kThreads + tid] == most) {
+        atomicMin(&where, seg * kSeg + j * kThreads + tid);
+        break;
+      }
     __syncthreads();
     mine.index = where;
   } else if (mode == kDone) {
     double sum = 0.0;
 #pragma unroll 4
-    for (int j = 0; j < kOwn; j++) sum += in_seg(xs[j * kThreads + tid]);
+    for (int j = 0; j < kOwn; j++) sum += weigh(xs[j * kThreads + tid]);
     mine.sum = block_sum<kThreads>(sum, room);
   } else if (mode == kTopK || mode == kManyK || mode == kTopP) {
     // (a thread's run of the same step is added at once: equal logits would queue)
@@ -568,78 +564,80 @@ __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, con
           sum = 0;
         }
         n++;
-        if (mode == kTopP) sum += fixed(in_seg(v), kFixed);
+        if (mode == kTopP) sum += fixed(weigh(v), kFixed);
       }
     }
     add();
     __syncthreads();
-    put(W.count + at * kSteps + tid, count[tid]);
+    W.count[at * kSteps + tid] = count[tid];
     if (mode == kTopP) {
-      put(W.weight + at * kSteps + tid, (uint64_t)weight[tid]);
+      W.weight[at * kSteps + tid] = weight[tid];
       mine.sum = block_sum<kThreads>((double)weight[tid] / kFixed, room);
     }
   }
-  if (tid == 0) {
-    put(&W.seg[at].most, mine.most);
-    put(&W.seg[at].index, mine.index);
-    put(&W.seg[at].sum, mine.sum);
-  }
-  if (!last_one(W.counters + 4 * rel, segs)) return;
+  if (tid == 0) W.seg[at] = mine;
+}
 
-  // the row's last workgroup
-  const SegInfo *all = W.seg + (int64_t)rel * segs;
-  const float seg_most = tid < segs ? get(&all[tid].most) : -__builtin_inff();
-  most = block_most(seg_most, froom);
+template <typename T>
+__global__ __launch_bounds__(kThreads) void limit_kernel(const SampleArgs A, const SampleWs W) {
+  __shared__ __attribute__((aligned(16))) float xs[kSeg];
+  __shared__ double room[kThreads / 64], seg_sum[kMaxSegs], share[kMaxSegs], part[kThreads / 64][64], table[kParts];
+  __shared__ float froom[kThreads / 64];
+  __shared__ int seg_step[kMaxSegs], where;
+  const int tid = threadIdx.x, segs = A.segs, rel = blockIdx.x, row = A.row0 + rel;
+  SegInfo mine = {-__builtin_inff(), 0, 0.0};
+  if (tid < segs) mine = W.seg[(int64_t)rel * segs + tid];
+  const Rule rule = rule_of(A, row);
+  const int mode = mode_of(A, rule);
+  const Steps step(rule, mode);
+  fill_table(table);
+  if (tid == 0) where = 0x7fffffff;
+  const float most = block_most<kThreads>(mine.most, froom);
   const bool none = most == -__builtin_inff();
-  const Weigher weigh = {most, rule.per};
+  const Weigher weigh = {most, rule.per, table};
   const int top = step(most);
   if (tid < segs) {
-    share[tid] = weigh(seg_most);  // of a segment's unit
-    seg_sum[tid] = get(&all[tid].sum) * share[tid];
+    W.seg[(int64_t)rel * segs + tid] = SegInfo{0.0f, 0, 0.0};
+    share[tid] = weigh(mine.most);  // of a segment's unit
+    seg_sum[tid] = mine.sum * share[tid];
     // (a segment without a token that may come counts from far below)
-    seg_step[tid] = seg_most == -__builtin_inff() ? 2 * kSteps : min(top - step(seg_most), 2 * kSteps);
+    seg_step[tid] = mine.most == -__builtin_inff() ? 2 * kSteps : min(top - step(mine.most), 2 * kSteps);
+    if (mine.most == most) atomicMin(&where, mine.index);
   }
-  if (none || mode == kDone) {
-    if (rule.greedy && !none) {
-      if (tid == 0) where = 0x7fffffff;
-      __syncthreads();
-      if (tid < segs && seg_most == most) atomicMin(&where, get(&all[tid].index));
-    }
-    __syncthreads();
-    if (none || rule.greedy) {
-      if (tid == 0) answer(A, row, none ? -1 : where, 1.0, 1.0);
-    } else {
-      choose<T, kThreads>(A, row, segs, seg_sum, weigh, Cut{0, -1}, 0.0, xs);
-    }
-    for (int i = tid; i < segs; i += kThreads) W.seg[(int64_t)rel * segs + i] = SegInfo{0.0f, 0, 0.0};
+  __syncthreads();
+  if (none || rule.greedy) {
+    if (tid == 0) answer(A, row, none ? -1 : where, 1.0, 1.0);
     return;
   }
-  RowInfo info = {mode, most, 0, top, 0.0};
+  if (mode == kDone) {
+    choose<T, kThreads>(A, row, segs, seg_sum, weigh, Cut{0, -1}, 0.0, xs);
+    return;
+  }
+  RowInfo info = {mode, most, kSteps - 1, top, 0.0};
   if (mode == kTopK || mode == kManyK || mode == kTopP) {
-    __syncthreads();
     // 64 steps at a time (mostly the first ones are enough), a lane each: the
     // segments' contents are summed by the waves in turn
-    const Rsrc c = rsrc_of(W.count + (int64_t)rel * segs * kSteps), w = rsrc_of(W.weight + (int64_t)rel * segs * kSteps);
+    const uint32_t *c = W.count + (int64_t)rel * segs * kSteps;
+    const uint64_t *w = W.weight + (int64_t)rel * segs * kSteps;
     const int lane = tid & 63, wave = tid >> 6;
     double target = (double)rule.top_k, before = 0.0;
     if (mode == kTopP) target = rule.top_p * block_sum<kThreads>(tid < segs ? seg_sum[tid] : 0.0, room);
-    info.step = kSteps - 1;  // (where nothing above reaches the target)
 #pragma unroll 1
     for (int s0 = 0; s0 < kSteps; s0 += 64) {
       const int t = s0 + lane;
       double have = 0.0;
       if (mode == kTopP) {
 #pragma unroll 8
-        for (int i = wave; i < segs; i += 4) {
+        for (int i = wave; i < segs; i += kThreads / 64) {
           const int b = t - seg_step[i];
-          const uint64_t v = get8(w, i * kSteps + max(b, 0));
+          const uint64_t v = w[i * kSteps + max(b, 0)];
           have += b >= 0 ? (double)v / kFixed * share[i] : 0.0;
         }
       } else {
 #pragma unroll 8
-        for (int i = wave; i < segs; i += 4) {
+        for (int i = wave; i < segs; i += kThreads / 64) {
           const int b = t - seg_step[i];
-          const uint32_t v = get4(c, i * kSteps + max(b, 0));
+          const uint32_t v = c[i * kSteps + max(b, 0)];
           have += b >= 0 ? (double)v : 0.0;
         }
       }
@@ -656,15 +654,11 @@ __global__ __launch_bounds__(kThreads) void first_kernel(const SampleArgs A, con
         before = lane_value(upto - have, l);
         break;
       }
-      before = lane_value(upto, 63);
+      before = lane_value(upto, 63);  // (nothing above reaches the target: the last step)
     }
-    if (tid == 0) {
-      info.left = target - before;
-      W.info[rel] = info;
-    }
-  } else if (tid == 0) {
-    W.info[rel] = info;
+    info.left = target - before;
   }
+  if (tid == 0) W.info[rel] = info;
 }
 
 __device__ __forceinline__ float logit_of(uint64_t entry) {  // of a key and index
@@ -672,16 +666,68 @@ __device__ __forceinline__ float logit_of(uint64_t entry) {  // of a key and ind
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+template <typename T>
+__global__ __launch_bounds__(kThreads) void gather_kernel(const SampleArgs A, const SampleWs W) {
+  __shared__ __attribute__((aligned(16))) float xs[kSeg];
+  __shared__ double room[kThreads / 64], table[kParts];
+  __shared__ int base;
+  const int tid = threadIdx.x, segs = A.segs;
+  const int rel = blockIdx.x / (uint32_t)segs, seg = blockIdx.x % (uint32_t)segs, row = A.row0 + rel;
+  const RowInfo info = W.info[rel];
+  if (info.mode == kDone || info.mode == kAlone) return;
+  const int64_t at = (int64_t)rel * segs + seg;
+  stage<T, kThreads>((const T *)A.logits + row * A.row_stride, A.wide, A.vocab, seg, xs);
+  const Rule rule = rule_of(A, row);
+  const Steps step(rule, info.mode);
+  const Weigher weigh = {info.most, rule.per, table};
+  if (info.mode != kMinP) {
+    W.count[at * kSteps + tid] = 0;
+    if (info.mode == kTopP) W.weight[at * kSteps + tid] = 0;
+  }
+  if (info.mode != kTopK) fill_table(table);
+  __syncthreads();
+  double sum = 0.0;
+  uint32_t mine = 0;  // this thread's tokens that are gathered
+#pragma unroll 4
+  for (int j = 0; j < kOwn; j++) {
+    const float v = xs[j * kThreads + tid];
+    const int b = info.mode == kMinP ? -1 : min(info.top_step - step(v), kSteps - 1);
+    if (!(v > -__builtin_inff()) || b > info.step) continue;
+    if (b == info.step || info.mode == kTopK) {
+      mine |= 1u << j;
+    } else {
+      const double w = weigh(v);
+      if (w >= rule.min_p) sum += w;
+    }
+  }
+  if (info.mode != kTopK) {
+    sum = block_sum<kThreads>(sum, room);
+    if (tid == 0) W.seg_sum[at] = sum;
+  }
+  double all;
+  int to = (int)block_before<kThreads>((double)__popc(mine), room, &all);
+  if (all == 0.0) return;
+  if (tid == 0) base = (int)atomicAdd(W.found + rel, (uint32_t)all);
+  __syncthreads();
+  to += base;
+  uint64_t *gathered = W.gathered + (int64_t)rel * kGather;
+#pragma unroll 1
+  for (; mine; mine &= mine - 1, to++) {
+    const int i = __builtin_ctz(mine) * kThreads + tid;
+    if (to < kGather) gathered[to] = (uint64_t)key_of(xs[i]) << 32 | (uint32_t)~(seg * kSeg + i);
+  }
+}
+
 // Sorts n <= kSort words in descending order (room behind them for the next
 // power of two).
 __device__ __forceinline__ void sort_equal(uint64_t *v, int n) {
   int size = 64;
   while (size < n) size *= 2;
-  for (int i = n + threadIdx.x; i < size; i += kThreads) v[i] = 0;
+  for (int i = n + threadIdx.x; i < size; i += kLast) v[i] = 0;
   __syncthreads();
   for (int k = 2; k <= size; k *= 2)
     for (int j = k / 2; j > 0; j /= 2) {
-      for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+      for (int t = threadIdx.x; t < size / 2; t += kLast) {
         const int a = 2 * t - (t & (j - 1)), b = a + j;  // the bit of j clear, set
         const uint64_t x = v[a], y = v[b];
         if ((x < y) == ((a & k) == 0)) {
@@ -693,34 +739,34 @@ __device__ __forceinline__ void sort_equal(uint64_t *v, int n) {
     }
 }
 
-// The same for up to kSort / 2 words, `other` with room for as many: by 256 equal
+// The same for up to kSort / 2 words, `other` with room for as many: by kLast equal
 // parts of the range between the least and the largest logit, and within a part by
 // counting larger ones; where a part holds many (nearly equal logits) as above.
 __device__ __forceinline__ void sort_down(uint64_t *v, uint64_t *other, int n, float *froom, double *room) {
   constexpr int kCrowd = 64;
-  __shared__ int count[kThreads], next[kThreads];
+  __shared__ int count[kLast], next[kLast];
   const int tid = threadIdx.x;
   float lo = __builtin_inff(), hi = -__builtin_inff();
-  for (int i = tid; i < n; i += kThreads) {
+  for (int i = tid; i < n; i += kLast) {
     lo = fminf(lo, logit_of(v[i]));
     hi = fmaxf(hi, logit_of(v[i]));
   }
   count[tid] = 0;
-  hi = block_most(hi, froom);
-  lo = -block_most(-lo, froom);
-  const float per = hi > lo ? 256.0f / (hi - lo) : 0.0f;
-  auto part = [&](uint64_t e) { return (int)fminf(fmaxf((hi - logit_of(e)) * per, 0.0f), 255.0f); };
-  for (int i = tid; i < n; i += kThreads) atomicAdd(&count[part(v[i])], 1);
+  hi = block_most<kLast>(hi, froom);
+  lo = -block_most<kLast>(-lo, froom);
+  const float per = hi > lo ? (float)kLast / (hi - lo) : 0.0f;
+  auto part = [&](uint64_t e) { return (int)fminf(fmaxf((hi - logit_of(e)) * per, 0.0f), (float)(kLast - 1)); };
+  for (int i = tid; i < n; i += kLast) atomicAdd(&count[part(v[i])], 1);
   __syncthreads();
   const int mine = count[tid];
-  next[tid] = (int)block_before<kThreads>((double)mine, room);
-  if (block_most((float)mine, froom) > (float)kCrowd) {
+  next[tid] = (int)block_before<kLast>((double)mine, room);
+  if (block_most<kLast>((float)mine, froom) > (float)kCrowd) {
     sort_equal(v, n);
     return;
   }
-  for (int i = tid; i < n; i += kThreads) other[atomicAdd(&next[part(v[i])], 1)] = v[i];
+  for (int i = tid; i < n; i += kLast) other[atomicAdd(&next[part(v[i])], 1)] = v[i];
   __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
+  for (int i = tid; i < n; i += kLast) {
     const uint64_t e = other[i];
     const int p = part(e), end = next[p], first = end - count[p];
     int at = first;
@@ -730,90 +776,51 @@ __device__ __forceinline__ void sort_down(uint64_t *v, uint64_t *other, int n, f
   __syncthreads();
 }
 
-// The same for up to a word a thread: its place is the number of larger ones.
+// The same for few words, by a wave: a word's place is the number of larger ones.
 __device__ __forceinline__ void sort_few(uint64_t *v, int n) {
-  const uint64_t a = (int)threadIdx.x < n ? v[threadIdx.x] : 0;
+  const int tid = threadIdx.x;
+  const uint64_t a = tid < n ? v[tid] : 0;
   int at = 0;
+  if (tid < 64) {
 #pragma unroll 8
-  for (int i = 0; i < n; i++) at += v[i] > a;
+    for (int i = 0; i < n; i++) at += v[i] > a;
+  }
   __syncthreads();
-  if ((int)threadIdx.x < n) v[at] = a;
+  if (tid < n) v[at] = a;
   __syncthreads();
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, const SampleWs W) {
+__global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const SampleWs W) {
   __shared__ __attribute__((aligned(16))) uint64_t list[kSort];
-  float *xs = reinterpret_cast<float *>(list + kSort / 2);  // a segment's logits, while few are gathered from it
-  __shared__ double room[4], seg_sum[kMaxSegs];
-  __shared__ float froom[4];
+  __shared__ double room[kLast / 64], seg_sum[kMaxSegs], table[kParts], left_of;
+  __shared__ float froom[kLast / 64];
   __shared__ unsigned long long extra[kMaxSegs], fine[kSteps];
-  __shared__ int found, base, kept;
-  const int tid = threadIdx.x, segs = A.segs;
-  const int rel = blockIdx.x / (uint32_t)segs, seg = blockIdx.x % (uint32_t)segs, row = A.row0 + rel;
+  __shared__ int found, base, last, kept;
+  const int tid = threadIdx.x, segs = A.segs, rel = blockIdx.x, row = A.row0 + rel;
   const RowInfo info = W.info[rel];
   if (info.mode == kDone) return;
-  const T *x = (const T *)A.logits + row * A.row_stride;
-  const int64_t at = (int64_t)rel * segs + seg;
+  const int n = (int)W.found[rel];
   const Rule rule = rule_of(A, row);
-  const Weigher weigh = {info.most, rule.per};
-  uint32_t *counters = W.counters + 4 * rel;
+  const Weigher weigh = {info.most, rule.per, table};
   uint64_t *gathered = W.gathered + (int64_t)rel * kGather;
-  if (info.mode != kAlone) {
-    stage<T, kThreads>(x, A.wide, A.vocab, seg, xs);
-    if (info.mode != kMinP) {
-      W.count[at * kSteps + tid] = 0;
-      if (info.mode == kTopP) W.weight[at * kSteps + tid] = 0;
-    }
-    const Steps step(rule, info.mode);
-    double sum = 0.0;
-    uint32_t mine = 0;  // this thread's tokens that are gathered
-    __syncthreads();
-#pragma unroll 4
-    for (int j = 0; j < kOwn; j++) {
-      const float v = xs[j * kThreads + tid];
-      const int b = info.mode == kMinP ? -1 : min(info.top_step - step(v), kSteps - 1);
-      if (!(v > -__builtin_inff()) || b > info.step) continue;
-      if (b == info.step || info.mode == kTopK) {
-        mine |= 1u << j;
-      } else {
-        const double w = weigh(v);
-        if (w >= rule.min_p) sum += w;
-      }
-    }
-    sum = block_sum<kThreads>(sum, room);
-    double all;
-    int to = (int)block_before<kThreads>((double)__popc(mine), room, &all);
-    if (tid == 0) {
-      put(W.seg_sum + at, sum);
-      base = all > 0.0 ? (int)__hip_atomic_fetch_add(counters + 2, (uint32_t)all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-    }
-    __syncthreads();
-    to += base;
-#pragma unroll 1
-    for (; mine; mine &= mine - 1, to++) {
-      const int i = __builtin_ctz(mine) * kThreads + tid;
-      if (to < kGather) put(gathered + to, (uint64_t)key_of(xs[i]) << 32 | (uint32_t)~(seg * kSeg + i));
-    }
+  fill_table(table);
+  if (tid < segs) {
+    seg_sum[tid] = W.seg_sum[(int64_t)rel * segs + tid];
+    W.seg_sum[(int64_t)rel * segs + tid] = 0.0;
+    extra[tid] = 0;
   }
-  if (!last_one(counters + 1, segs)) return;
-
-  // the row's last workgroup
-  const int n = (int)get(counters + 2);
-  if (tid == 0) counters[2] = 0;
-  for (int i = tid; i < segs; i += kThreads) {
-    seg_sum[i] = get(W.seg_sum + (int64_t)rel * segs + i);
-    extra[i] = 0;
-    W.seg_sum[(int64_t)rel * segs + i] = 0.0;
-    W.seg[(int64_t)rel * segs + i] = SegInfo{0.0f, 0, 0.0};
+  if (tid < kSteps) fine[tid] = 0;
+  if (tid == 0) {
+    kept = kGather;
+    base = kSteps;
+    last = found = 0;
   }
+  __syncthreads();
   if (tid == 0) {
     W.info[rel] = RowInfo{0, 0.0f, 0, 0, 0.0};
-    kept = kGather;
+    W.found[rel] = 0;
   }
-  fine[tid] = 0;
-  __syncthreads();
-  const Rsrc words = rsrc_of(gathered);
   auto keep = [&](uint64_t entry) {
     const double w = weigh(logit_of(entry));
     if (w >= rule.min_p) atomicAdd(&extra[(int)~(uint32_t)entry / kSeg], (unsigned long long)fixed(w, kFixed));
@@ -821,40 +828,33 @@ __global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, co
   double left = info.left;
   bool alone = info.mode == kAlone || n > kGather;
   int m = n;  // tokens to be sorted
-  if (!alone && (info.mode == kTopK || n <= kThreads)) {
+  if (!alone && (info.mode == kTopK || n <= 64)) {
     alone = n > kSort;
-    for (int i = tid; i < min(n, kSort); i += kThreads) list[i] = get8(words, i);
+    for (int i = tid; i < min(n, kSort); i += kLast) list[i] = gathered[i];
+    __syncthreads();
   } else if (!alone) {
     // by 256ths of the step: those above the one in which the limit falls are kept
     const Steps step(rule, info.mode);
     auto part = [&](uint64_t entry) { return step.part(logit_of(entry), info.top_step - info.step); };
     const bool weights = info.mode == kTopP;
-#pragma unroll 1
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t e = get8(words, i);
+    for (int i = tid; i < n; i += kLast) {
+      const uint64_t e = gathered[i];
       atomicAdd(&fine[part(e)], weights ? (unsigned long long)fixed(weigh(logit_of(e)), kFixed) : 1ull);
     }
     __syncthreads();
-    const double have = (double)fine[tid] / (weights ? kFixed : 1.0), before = block_before<kThreads>(have, room);
+    const double have = tid < kSteps ? (double)fine[tid] / (weights ? kFixed : 1.0) : 0.0, before = block_before<kLast>(have, room);
     // (where roundings of the sums leave the limit unreached: the last one there is)
-    if (tid == 0) {
-      base = kSteps;
-      found = 0;
-    }
-    __syncthreads();
     if (have > 0.0) {
       if (before + have >= left) atomicMin(&base, tid);
-      atomicMax(&found, tid);
+      atomicMax(&last, tid);
     }
     __syncthreads();
-    const int at_part = base < kSteps ? base : found;
+    const int at_part = base < kSteps ? base : last;
+    if (tid == at_part) left_of = left - before;
     __syncthreads();
-    if (tid == 0) found = 0;
-    if (tid == at_part) room[0] = left - before;
-    __syncthreads();
-    left = room[0];
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t e = get8(words, i);
+    left = left_of;
+    for (int i = tid; i < n; i += kLast) {
+      const uint64_t e = gathered[i];
       const int q = part(e);
       if (q < at_part) keep(e);
       if (q == at_part) {
@@ -866,34 +866,33 @@ __global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, co
     m = found;
     alone = m > kSort;
   }
-  for (int i = tid; i < min(n, kGather); i += kThreads) gathered[i] = 0;
-  __syncthreads();
+  for (int i = tid; i < min(n, kGather); i += kLast) gathered[i] = 0;
   if (alone) {
-    whole_row<T, kThreads>(A, row, reinterpret_cast<float *>(list));
+    whole_row<T, kLast>(A, row, table, reinterpret_cast<float *>(list));
     return;
   }
   Cut cut = {0, -1};
   if (info.mode != kMinP) {
     if (m > kSort / 2) sort_equal(list, m);
-    else if (m > kThreads / 2) sort_down(list, list + kSort / 2, m, froom, room);
+    else if (m > 64) sort_down(list, list + kSort / 2, m, froom, room);
     else sort_few(list, m);
-    // the limits, kThreads sorted tokens at a time (a second time for top-p of top-k)
+    // the limits, kLast sorted tokens at a time (a second time for top-p of top-k)
     const int top = info.mode == kTopK ? min(rule.top_k, m) : info.mode == kManyK ? min((int)left, m) : m;
     int keeps = top;
     if (rule.top_p < 1.0) {
       double target = left;
       if (info.mode == kTopK) {
         double sum = 0.0;
-        for (int i = tid; i < top; i += kThreads) sum += weigh(logit_of(list[i]));
-        target = rule.top_p * block_sum<kThreads>(sum, room);
+        for (int i = tid; i < top; i += kLast) sum += weigh(logit_of(list[i]));
+        target = rule.top_p * block_sum<kLast>(sum, room);
       }
       double before = 0.0;
 #pragma unroll 1
-      for (int i0 = 0; i0 < top; i0 += kThreads) {
+      for (int i0 = 0; i0 < top; i0 += kLast) {
         const int i = i0 + tid;
         const double w = i < top ? weigh(logit_of(list[i])) : 0.0;
         double all;
-        const double c = before + block_before<kThreads>(w, room, &all);
+        const double c = before + block_before<kLast>(w, room, &all);
         if (i < top && i > 0 && c >= target) atomicMin(&kept, i);  // the first that is not needed
         __syncthreads();
         if (kept < top) break;
@@ -904,12 +903,12 @@ __global__ __launch_bounds__(kThreads) void second_kernel(const SampleArgs A, co
     // (nothing is there where the limit falls behind the last token: all are kept)
     const uint64_t lowest = keeps ? list[keeps - 1] : 0xffffffffull;
     cut = Cut{(uint32_t)(lowest >> 32), (int)~(uint32_t)lowest};
-    for (int i = tid; i < keeps; i += kThreads) keep(list[i]);
+    for (int i = tid; i < keeps; i += kLast) keep(list[i]);
     __syncthreads();
-    for (int i = tid; i < segs; i += kThreads) seg_sum[i] += (double)extra[i] / kFixed;
+    if (tid < segs) seg_sum[tid] += (double)extra[tid] / kFixed;
     __syncthreads();
   }
-  choose<T, kThreads>(A, row, segs, seg_sum, weigh, cut, rule.min_p, reinterpret_cast<float *>(list));
+  choose<T, kLast>(A, row, segs, seg_sum, weigh, cut, rule.min_p, reinterpret_cast<float *>(list));
 }
 
 bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -929,10 +928,10 @@ struct Plan {
 Plan make_plan(int64_t rows, int64_t vocab) {
   Plan P = {(vocab + kSeg - 1) / kSeg, 0, 0};
   if (P.segs == 1) return P;
-  const size_t each = sizeof(RowInfo) + kGather * 8 + 16 + (size_t)P.segs * (sizeof(SegInfo) + 8 + kSteps * 12);
+  const size_t each = sizeof(RowInfo) + kGather * 8 + 4 + (size_t)P.segs * (sizeof(SegInfo) + 8 + kSteps * 12);
   P.pass = (int64_t)(kWsBytes / each);
   if (P.pass > rows) P.pass = rows;
-  P.bytes = (size_t)P.pass * each;
+  P.bytes = ((size_t)P.pass * each + 15) / 16 * 16;
   return P;
 }
 
@@ -975,17 +974,22 @@ extern "C" int tq_sample(int dtype, int64_t rows, int64_t vocab, const void *log
   W.weight = (uint64_t *)(p += n * kGather * 8);
   W.seg_sum = (double *)(p += ns * kSteps * 8);
   W.count = (uint32_t *)(p += ns * 8);
-  W.counters = (uint32_t *)(p += ns * kSteps * 4);
+  W.found = (uint32_t *)(p += ns * kSteps * 4);
+  const bool limits = top_k || top_p || min_p;
   for (int64_t r = 0; r < rows; r += P.pass) {
     A.row0 = (int)r;
-    const dim3 grid((unsigned)((rows - r < P.pass ? rows - r : P.pass) * P.segs)), block(kThreads);
-    if (dtype == TQ_F16) {
-      hipLaunchKernelGGL((first_kernel<_Float16>), grid, block, 0, st, A, W);
-      hipLaunchKernelGGL((second_kernel<_Float16>), grid, block, 0, st, A, W);
-    } else {
-      hipLaunchKernelGGL((first_kernel<float>), grid, block, 0, st, A, W);
-      hipLaunchKernelGGL((second_kernel<float>), grid, block, 0, st, A, W);
-    }
+    const int64_t m = rows - r < P.pass ? rows - r : P.pass;
+    const dim3 each((unsigned)(m * P.segs)), one((unsigned)m);
+#define TQ_SAMPLE(T)                                                                  \
+  {                                                                                   \
+    hipLaunchKernelGGL((segment_kernel<T>), each, dim3(kThreads), 0, st, A, W);       \
+    hipLaunchKernelGGL((limit_kernel<T>), one, dim3(kThreads), 0, st, A, W);          \
+    if (!limits) continue;                                                            \
+    hipLaunchKernelGGL((gather_kernel<T>), each, dim3(kThreads), 0, st, A, W);        \
+    hipLaunchKernelGGL((token_kernel<T>), one, dim3(kLast), 0, st, A, W);             \
+  }
+    if (dtype == TQ_F16) TQ_SAMPLE(_Float16) else TQ_SAMPLE(float)
+#undef TQ_SAMPLE
   }
   return hipGetLastError() == hipSuccess ? TQ_OK : TQ_ERR_HIP;
 }
