@@ -507,6 +507,39 @@ int tq_kv_attn(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, in
                int64_t sinks, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
                void *stream);
 
+/* Workspace bytes of tq_kv_attn_shared (0 on a bad shape); same zero-fill rule as
+ * tq_gemv_workspace_bytes.  Not monotonic in the shape; never above 2^28.6 bytes. */
+size_t tq_kv_attn_shared_workspace_bytes(int64_t rows, int64_t seqs, int64_t groups, int64_t q_heads,
+                                         int64_t kv_heads, int64_t head_dim, int64_t max_prefix_len,
+                                         int64_t max_own_len);
+
+/* tq_kv_attn without a window, for groups of sequences that share their first
+ * tokens (the pages run their model behind system prompts that all requests
+ * share): group g has the sequences cu_seqs[g] .. cu_seqs[g+1] - 1 (cu_seqs
+ * [groups + 1], int32, ascending from 0; sequences behind the last group share
+ * nothing), whose first prefix_len[g] tokens (int32) are the same: the page table
+ * rows of a group's sequences name the same pages there.  Whole pages are shared:
+ * what prefix_len has beyond a multiple of 64 counts as the sequences' own.
+ * Every row must stand behind its group's prefix (kv_len - its sequence's rows >=
+ * prefix_len); a row before the end sees all of the prefix all the same.
+ * Results are those of tq_kv_attn on the same arguments but for the rounding of
+ * weights and sums, and so are the other arguments' conditions.  A prefix is read
+ * once for each tile of its group's rows, not for each sequence; sequences of many
+ * rows fill tiles of their own, and run as tq_kv_attn does.
+ * max_prefix_len, max_own_len: the largest prefix_len, and the largest kv_len less
+ * its group's prefix_len, which set kernels and splits (larger ones are right too,
+ * only slower).  prefix_len and cu_seqs are read on the device, as the other
+ * arrays; bad entries lead to no access outside the arrays.  1 <= groups <= 2^20.
+ * Two launches, or one. */
+int tq_kv_attn_shared(int64_t rows, int64_t seqs, int64_t groups, int64_t q_heads, int64_t kv_heads,
+                      int64_t head_dim, const void *q, int64_t q_stride, const int32_t *cu_rows,
+                      const int32_t *kv_len, const int32_t *cu_seqs, const int32_t *prefix_len,
+                      const int32_t *page_table, int64_t max_pages, const uint8_t *k_cache,
+                      const uint8_t *v_cache, const float *k_scale, const float *v_scale,
+                      int64_t num_pages, int64_t max_prefix_len, int64_t max_own_len,
+                      float softmax_scale, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
+                      void *stream);
+
 /* Scratch bytes of tq_linear_attn (0 when it needs none, or on a bad shape).
  * Scratch is device memory that needs no contents and is left with any: it
  * must not be a workspace of the other calls, which have to find theirs zero.

@@ -47,7 +47,8 @@ EXPORTS = ("tq_status_str", "tq_packed_bytes", "tq_pack", "tq_unpack", "tq_quant
            "tq_debug_gemv_quant_rows_sums", "tq_workspace_clear", "tq_workspace_check",
            "tq_rope_table", "tq_kv_append", "tq_kv_attn_workspace_bytes", "tq_kv_attn",
            "tq_residual_norm", "tq_debug_kv_read", "tq_linear_attn_scratch_bytes", "tq_linear_attn",
-           "tq_sample_workspace_bytes", "tq_sample")
+           "tq_sample_workspace_bytes", "tq_sample",
+           "tq_kv_attn_shared_workspace_bytes", "tq_kv_attn_shared")
 
 
 class TqLayer(ctypes.Structure):
@@ -105,6 +106,9 @@ def _load():
         "tq_kv_attn": ([I64, I64, I64, I64, I64, P, I64, P, P, P, I64, P, P, P, P, I64, I64, F, I64, I64, P, I64,
                         P, SZ, P], I),
         "tq_residual_norm": ([I, I, I, I64, I64, P, P, P, I64, F64, P, P, P, F64, P, P, P, P], I),
+        "tq_kv_attn_shared_workspace_bytes": ([I64, I64, I64, I64, I64, I64, I64, I64], SZ),
+        "tq_kv_attn_shared": ([I64, I64, I64, I64, I64, I64, P, I64, P, P, P, P, P, I64, P, P, P, P, I64, I64, I64, F, P,
+                               I64, P, SZ, P], I),
         "tq_linear_attn_scratch_bytes": ([I64, I64, I64, I64, I64], SZ),
         "tq_linear_attn": ([I, I64, I64, I64, I64, I64, P, I64, P, I64, P, P, P, P, I64, F, P, I64, P, SZ, P], I),
         "tq_sample_workspace_bytes": ([I64, I64], SZ),
@@ -515,6 +519,49 @@ def tq_kv_attn(q, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scal
         wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
     rc = lib.tq_kv_attn(rows, seqs, q_heads, heads, dim, qp, qs, *cache, max_kv_len,
                         dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, op, os_, wp, wb, st)
+    if rc:
+        raise TQError(rc, what)
+
+
+def tq_kv_attn_shared_workspace_bytes(rows, seqs, groups, q_heads, kv_heads, head_dim, max_prefix_len, max_own_len) -> int:
+    return int(lib.tq_kv_attn_shared_workspace_bytes(rows, seqs, groups, q_heads, kv_heads, head_dim, max_prefix_len, max_own_len))
+
+
+def kv_attn_shared_workspace(rows, seqs, groups, q_heads, kv_heads, head_dim, max_prefix_len, max_own_len, device="cuda"):
+    """A zero-filled workspace tensor for tq_kv_attn_shared (None when it needs none)."""
+    import torch
+    nbytes = tq_kv_attn_shared_workspace_bytes(rows, seqs, groups, q_heads, kv_heads, head_dim, max_prefix_len, max_own_len)
+    return torch.zeros((nbytes + 15) // 16 * 4, dtype=torch.int32, device=device) if nbytes else None
+
+
+def tq_kv_attn_shared(q, cu_rows, kv_len, cu_seqs, prefix_len, page_table, k_cache, v_cache, k_scale, v_scale, out, max_prefix_len,
+                      max_own_len, softmax_scale=None, ws=None, stream=None) -> None:
+    """tq_kv_attn (without a window) for groups of sequences that share their
+    first pages: group g has the sequences cu_seqs[g] .. cu_seqs[g+1] - 1 (int32
+    [groups + 1]), whose first prefix_len[g] tokens (int32 [groups]) lie in the
+    same pages, and is read from them once for all its rows.  max_prefix_len,
+    max_own_len: the largest prefix, and the largest kv_len less its prefix (host
+    numbers)."""
+    what, T = "tq_kv_attn_shared", _Torch.get()
+    dev, st = _current(T, stream, k_cache)
+    seqs, heads, dim, cache = _cache_need(what, T, cu_rows, kv_len, page_table, k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 3 or prefix_len.dim() != 1:
+        raise ValueError(f"{what}: q must have three dimensions, prefix_len one")
+    groups = prefix_len.shape[0]
+    cs = _need(what, "cu_seqs", cu_seqs, T.i32, (groups + 1,), dev)
+    pl = _need(what, "prefix_len", prefix_len, T.i32, (groups,), dev)
+    rows, q_heads, _ = q.shape
+    shape = (rows, q_heads, dim)
+    qp, qs = _rows_need(what, "q", q, T.f16, shape, dev)
+    op, os_ = _rows_need(what, "out", out, T.f16, shape, dev)
+    wp, wb = None, 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"{what}: ws must be contiguous and on the current GPU")
+        wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
+    cu, kv, *rest = cache
+    rc = lib.tq_kv_attn_shared(rows, seqs, groups, q_heads, heads, dim, qp, qs, cu, kv, cs, pl, *rest, max_prefix_len, max_own_len,
+                               dim ** -0.5 if softmax_scale is None else softmax_scale, op, os_, wp, wb, st)
     if rc:
         raise TQError(rc, what)
 

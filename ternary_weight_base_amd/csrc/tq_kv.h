@@ -35,19 +35,24 @@ __device__ __forceinline__ int slot_base(int cu, int i, int mul) {
 
 // The last sequence whose base is <= w, searched 64 ways at a time by the
 // lanes of a wave (every lane active; one round for up to 64 sequences).
-template <int DIV, int ADD>
-__device__ __forceinline__ int find_seq(const int *cu, int seqs, int rows, int w, int mul) {
+// `first_row(i)`: a sequence's first row.
+template <int DIV, int ADD, typename Rows>
+__device__ __forceinline__ int find_seq(const Rows &first_row, int seqs, int w, int mul) {
   int lo = 0, hi = seqs;
   const int lane = threadIdx.x & 63;
   while (hi - lo > 1) {
     const int step = (int)((uint32_t)(hi - lo + 63) / 64u);
     const int i = lo + lane * step;
-    const bool le = i < hi && slot_base<DIV, ADD>(cu_at(cu, i, rows), i, mul) <= w;
+    const bool le = i < hi && slot_base<DIV, ADD>(first_row(min(i, hi)), i, mul) <= w;
     const int k = max((int)__popcll(__ballot(le)), 1);
     lo += (k - 1) * step;
     hi = min(hi, lo + step);
   }
   return __builtin_amdgcn_readfirstlane(lo);
+}
+template <int DIV, int ADD>
+__device__ __forceinline__ int find_seq(const int *cu, int seqs, int rows, int w, int mul) {
+  return find_seq<DIV, ADD>([=](int i) { return cu_at(cu, i, rows); }, seqs, w, mul);
 }
 
 // Cache bytes as fp16 c = b - 128, exact: a byte under the fp16
