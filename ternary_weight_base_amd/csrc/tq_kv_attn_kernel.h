@@ -88,18 +88,21 @@ struct AttnArgs {
   int slots, solo;    // prefill: row tiles; units that stay whole
   int nsplit, chunk;  // prefill: pieces of the others at most; pages of a piece at least
   int whole;          // decode: units of up to so many pages stay whole
-  // sequences that share a prefix (below): their groups, the prefix part's results
+  // sequences that share a prefix (below): their groups, the prefixes' results
   const int *cu_seqs, *prefix;
-  float *mid_o, *mid_ml;
+  float *mid;
+  int64_t mid_ml;                         // where the (maximum, sum) pairs start, without tiles
   int groups, all_seqs;
+  int pre_slots, pre_nsplit, pre_chunk;   // the prefix launch's tiles of 128 rows (nsplit 0: results row by row)
 };
 
 // Which keys a launch is about.  kAllKeys: all that a row sees.  Sequences that
 // share their first pages (a prefix of whole pages a group of sequences) take two
 // launches.  kPrefixKeys: the prefixes, whose "sequences" are the groups, with the
 // rows of all their sequences, every one of which sees all of the prefix; the
-// results (outputs over the prefix, maximum and sum) go to mid.  kOwnKeys: the
-// keys behind the prefix, joined with what mid holds, which is left zero.
+// results (sums of weighted values, maximum and sum of the weights) go to mid: row
+// by row, or as the pieces of tiles of 128 rows.  kOwnKeys: the keys behind the
+// prefix, joined with what mid holds, which is left zero.
 enum Keys { kAllKeys = 0, kPrefixKeys, kOwnKeys };
 
 // The first row of sequence (or group) i.
@@ -113,18 +116,23 @@ template <int KEYS>
 __device__ __forceinline__ int keys_of(const AttnArgs &A, int s) {
   return KEYS == kPrefixKeys ? max(A.prefix[s], 0) / kPage * kPage : max(A.kv_len[s], 0);
 }
-// Pages before a sequence's own: of the last group that starts at or before it and
-// is not empty, if it is in it.
-template <int KEYS>
-__device__ __forceinline__ int pages_before(const AttnArgs &A, int s) {
-  if (KEYS != kOwnKeys) return 0;
+// The group of a sequence: the last one that starts at or before it, if it is in
+// it; else -1.
+__device__ __forceinline__ int group_of(const AttnArgs &A, int s) {
   int lo = 0, hi = A.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (A.cu_seqs[mid] <= s) lo = mid;
     else hi = mid;
   }
-  return A.cu_seqs[lo] <= s && s < A.cu_seqs[lo + 1] ? max(A.prefix[lo], 0) / kPage : 0;
+  return A.cu_seqs[lo] <= s && s < A.cu_seqs[lo + 1] ? lo : -1;
+}
+// Pages before a sequence's own.
+template <int KEYS>
+__device__ __forceinline__ int pages_before(const AttnArgs &A, int s) {
+  if (KEYS != kOwnKeys) return 0;
+  const int g = group_of(A, s);
+  return g >= 0 ? max(A.prefix[g], 0) / kPage : 0;
 }
 
 // The visible pages of a row tile whose positions are pmin .. pmax: pages
@@ -351,22 +359,91 @@ __device__ __forceinline__ bool last_split(uint32_t *counter, int splits) {
 // 1 / sum of weights; 0 for a row that saw no key.
 __device__ __forceinline__ float inverse(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
 
-// A row's (maximum, sum) over its prefix joined to those of its own keys: the
-// factor that the sums over its own keys take, `w` the one of the prefix's outputs.
-// All lanes of a row load, then one of them (the same wave's) leaves zeros.
-__device__ __forceinline__ float with_mid(float *ml, bool zero, float M, float L, float &w) {
-  const float l = ml[1], m = l > 0.0f || l != l ? ml[0] : kNone;  // (nothing there: a group without a prefix)
-  asm volatile("" ::: "memory");
-  if (zero) ml[0] = ml[1] = 0.0f;
-  const float most = fmaxf(M, m), f = __builtin_amdgcn_exp2f(M - most), g = __builtin_amdgcn_exp2f(m - most) * l;
-  const float inv = inverse(f * L + g);
-  w = g * inv;
+// What the prefix launch left of a sequence's rows in mid: for each row `pieces`
+// results `step` floats apart.
+constexpr int kPreRows = 128, kPrePieces = 32;
+struct Before {
+  int pieces, first, slot0;  // the group's first row and first tile
+  int64_t step;
+  __device__ __forceinline__ Before() : pieces(0), first(0), slot0(0), step(0) {}
+  __device__ __forceinline__ Before(const AttnArgs &A, int s, int D) : pieces(0), first(0), slot0(0), step(0) {
+    const int g = group_of(A, s);
+    if (g < 0) return;
+    pieces = 1;
+    if (A.pre_nsplit == 0) return;
+    const int count = (int)min((int64_t)(max(A.prefix[g], 0) / kPage), A.max_pages);
+    const int per = max(A.pre_chunk, (int)((uint32_t)(count + A.pre_nsplit - 1) / (uint32_t)A.pre_nsplit));
+    pieces = max((int)((uint32_t)(count + per - 1) / (uint32_t)per), 1);
+    first = row_at<kPrefixKeys>(A, g);
+    slot0 = slot_base<kPreRows, 1>(first, g, A.group);
+    step = partial_floats(kPreRows, D);
+  }
+  // where the first result of a row (of query head `head`) has its sums, and its (maximum, sum)
+  __device__ __forceinline__ void at(const AttnArgs &A, int row, int head, int D, int64_t &o, int64_t &ml) const {
+    if (A.pre_nsplit == 0) {
+      const int64_t i = (int64_t)row * (A.hkv * A.group) + head;
+      o = i * D;
+      ml = A.mid_ml + 2 * i;
+      return;
+    }
+    const uint32_t h = (uint32_t)head / (uint32_t)A.group, f = (row - first) * A.group + ((uint32_t)head - h * A.group);
+    // (a row that the prefix launch has no tile of, by arrays out of order: the last one's)
+    const int slot = min(max(slot0 + (int)(f / (uint32_t)kPreRows), 0), A.pre_slots - 1);
+    const int64_t base = ((int64_t)(A.pre_slots - 1 - slot) * A.hkv + h) * A.pre_nsplit * step;
+    const int r = f % (uint32_t)kPreRows;
+    o = base + r * D;
+    ml = base + kPreRows * D + 2 * r;
+  }
+};
+
+// A row's (maximum, sum) over its own keys joined to those over its prefix by 16
+// lanes, `j` each one's number: `w` takes the prefix's pieces' factors, and the
+// one that the sums over its own keys take is returned.  Leaves zeros (`live`).
+__device__ __forceinline__ float join_before(float *mid, int64_t ml, const Before &B, int j, bool live, float M, float L,
+                                             float *w) {
+  float m[kPrePieces / 16], l[kPrePieces / 16], most = M, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPrePieces / 16; i++) {
+    const int k = 16 * i + j;
+    m[i] = kNone;
+    l[i] = 0.0f;
+    if (live && k < B.pieces) {
+      float *p = mid + ml + k * B.step;
+      m[i] = p[0];
+      l[i] = p[1];
+      p[0] = p[1] = 0.0f;
+      if (!(l[i] > 0.0f || l[i] != l[i])) m[i] = kNone;  // nothing there
+    }
+    most = fmaxf(most, m[i]);
+  }
+  most = tqdev::row16_max(most);
+#pragma unroll
+  for (int i = 0; i < kPrePieces / 16; i++) {
+    m[i] = __builtin_amdgcn_exp2f(m[i] - most);
+    sum += m[i] * l[i];
+  }
+  const float f = __builtin_amdgcn_exp2f(M - most), inv = inverse(f * L + tqdev::row16_sum(sum));
+#pragma unroll
+  for (int i = 0; i < kPrePieces / 16; i++)
+    if (live && 16 * i + j < B.pieces) w[16 * i + j] = m[i] * inv;
   return f * inv;
 }
-__device__ __forceinline__ f4 take_mid(float *p) {
-  const f4 v = *reinterpret_cast<const f4 *>(p);
-  *reinterpret_cast<f4 *>(p) = (f4){0, 0, 0, 0};
-  return v;
+// The prefix's part of four outputs; leaves zeros.
+__device__ __forceinline__ f4 take_before(float *mid, int64_t o, const Before &B, const float *w) {
+  f4 sum = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int k0 = 0; k0 < B.pieces; k0 += 8) {
+    f4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) v[k] = *reinterpret_cast<const f4 *>(mid + o + min(k0 + k, B.pieces - 1) * B.step);
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (k0 + k < B.pieces) {
+        sum += w[k0 + k] * v[k];
+        *reinterpret_cast<f4 *>(mid + o + (k0 + k) * B.step) = (f4){0, 0, 0, 0};
+      }
+  }
+  return sum;
 }
 
 // The last piece's join of a tile of R rows: the partial results, piece k's at
@@ -377,8 +454,8 @@ __device__ __forceinline__ f4 take_mid(float *p) {
 // where the rows are fewer than the threads, the pieces are dealt over
 // `parts` groups of threads that meet in LDS.  The words read are left zero
 // for the next call, whatever its shape.
-// (`more(row, M, L)` may add to a row's maximum and sum, and returns the factor that
-// the pieces' sums and weights then take; M, L: the row's own, final ones.)
+// `more(row, j, live, M, L)`, by 16 lanes a row (j: each one's number), returns the
+// factor of the pieces' sums, whose weights have the maximum M and the sum L.
 template <int R, int D, int NT, int MAXP, typename At, typename Out, typename More>
 __device__ __forceinline__ void join(int tid, Rsrc part, int pieces, int nrows, float *lds, const At &at, const Out &out,
                                      const More &more) {
@@ -425,7 +502,7 @@ __device__ __forceinline__ void join(int tid, Rsrc part, int pieces, int nrows, 
       L += m[i] * l[i];
     }
     L = tqdev::row16_sum(L);
-    const float inv = more(rr, j == 0 && r < nrows, M, L);
+    const float inv = more(rr, j, r < nrows, M, L);
 #pragma unroll
     for (int i = 0; i < kPer16; i++) {
       const int k = 16 * i + j;
@@ -685,7 +762,7 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
     float join[WHOLE ? 1 : kJoinFloats<R, kDecPieces + 2, kDecThreads>];
   };
   __shared__ __attribute__((aligned(16))) Shared S;
-  __shared__ float mid_weight[KEYS == kOwnKeys ? R : 1];
+  __shared__ float pre_w[KEYS == kOwnKeys ? R * kPrePieces : 1], keep[KEYS == kOwnKeys ? R : 1];
   const int wg = blockIdx.x;
   List<R, KEYS> list;
   int at = 0, stop = 1, per = 1;
@@ -897,13 +974,11 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
     __syncthreads();
     // outputs 4 c .. 4 c + 3 of a row, for the rows that are there
     constexpr int kQuads = D / 4, kRound = kDecThreads / kQuads;
-    auto mid_at = [&](int row) {
-      const uint32_t f = u.f0 + row;
-      return (int64_t)(u.begin + f / (uint32_t)A.group) * (A.hkv * A.group) + h * A.group + f % (uint32_t)A.group;
-    };
+    auto token_of = [&](int row) { return u.begin + (int)((uint32_t)(u.f0 + row) / (uint32_t)A.group); };
+    auto head_of = [&](int row) { return h * A.group + (int)((uint32_t)(u.f0 + row) % (uint32_t)A.group); };
     auto write_out = [&](int row, int d, f4 o) {
       if constexpr (KEYS == kPrefixKeys) {
-        *reinterpret_cast<f4 *>(A.mid_o + mid_at(row) * D + d) = o;
+        *reinterpret_cast<f4 *>(A.mid + ((int64_t)token_of(row) * (A.hkv * A.group) + head_of(row)) * D + d) = o;
         return;
       }
       const uint32_t f = u.f0 + row;
@@ -912,6 +987,35 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
       *reinterpret_cast<h4 *>(dst) = (h4){(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]};
     };
     const int mine = (2 * wg + (u.first == wg)) * PF;
+    auto put_sums = [&](int row, float M, float L) {  // (kPrefixKeys)
+      float *ml = A.mid + A.mid_ml + 2 * ((int64_t)token_of(row) * (A.hkv * A.group) + head_of(row));
+      ml[0] = M;
+      ml[1] = L;
+    };
+    const Before before = KEYS == kOwnKeys ? Before(A, s, D) : Before();
+    auto join_row = [&](int row, int j, bool live, float M, float L) {  // (kOwnKeys)
+      int64_t o, ml;
+      before.at(A, token_of(row), head_of(row), D, o, ml);
+      return join_before(A.mid, ml, before, j, live, M, L, pre_w + row * kPrePieces);
+    };
+    auto taken = [&](int row, int d) {
+      int64_t o, ml;
+      before.at(A, token_of(row), head_of(row), D, o, ml);
+      return take_before(A.mid, o + d, before, pre_w + row * kPrePieces);
+    };
+    if (KEYS == kOwnKeys && u.pieces == 1) {
+      for (int r0 = 0; r0 < u.nrows; r0 += kDecThreads / 16) {
+        const int row = r0 + tid / 16, rr = min(row, u.nrows - 1);
+        float M = kNone, L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kDecWaves; w++) M = fmaxf(M, S.w.m[w][rr]);
+#pragma unroll
+        for (int w = 0; w < kDecWaves; w++) L += __builtin_amdgcn_exp2f(S.w.m[w][rr] - M) * S.w.l[w][rr];
+        const float f = join_row(rr, tid & 15, row < u.nrows, M, L);
+        if ((tid & 15) == 0 && row < u.nrows) keep[row] = f;
+      }
+      __syncthreads();
+    }
     for (int row = tid / kQuads; row < u.nrows; row += kRound) {
       const int c = tid % kQuads;
       float M = kNone, L = 0.0f;
@@ -928,18 +1032,14 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
         store_dev(parts, mine + row * D + 4 * c, o);
         if (c == 0) store_dev2(parts, mine + R * D + 2 * row, M, L);
       } else {
-        float *ml = KEYS == kAllKeys ? nullptr : A.mid_ml + 2 * mid_at(row);
-        float keep = inverse(L);
-        f4 pre = {0, 0, 0, 0};
         if constexpr (KEYS == kPrefixKeys) {
-          if (c == 0) ml[0] = M, ml[1] = L;
+          if (c == 0) put_sums(row, M, L);
+          write_out(row, 4 * c, o);
+        } else if constexpr (KEYS == kOwnKeys) {
+          write_out(row, 4 * c, o * keep[row] + taken(row, 4 * c));
+        } else {
+          write_out(row, 4 * c, o * inverse(L));
         }
-        if constexpr (KEYS == kOwnKeys) {
-          float w;
-          keep = with_mid(ml, c == 0, M, L, w);
-          pre = w * take_mid(A.mid_o + mid_at(row) * D + 4 * c);
-        }
-        write_out(row, 4 * c, o * keep + pre);
       }
     }
     if constexpr (WHOLE) {
@@ -949,20 +1049,18 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 3 : 2) void decode_kernel(const 
         join<R, D, kDecThreads, kDecPieces + 2>(
             tid, parts, u.pieces, u.nrows, S.join, [&](int k) { return (2 * (u.first + k) + (k == 0)) * PF; },
             [&](int row, int d, f4 o) {
-              if constexpr (KEYS == kOwnKeys) o += mid_weight[row] * take_mid(A.mid_o + mid_at(row) * D + d);
+              if constexpr (KEYS == kOwnKeys) o += taken(row, d);
               write_out(row, d, o);
             },
-            [&](int row, bool first, float M, float L) {
+            [&](int row, int j, bool live, float M, float L) {
               if constexpr (KEYS == kPrefixKeys) {
-                if (first) A.mid_ml[2 * mid_at(row)] = M, A.mid_ml[2 * mid_at(row) + 1] = L;
+                if (j == 0 && live) put_sums(row, M, L);
+                return 1.0f;
+              } else if constexpr (KEYS == kOwnKeys) {
+                return join_row(row, j, live, M, L);
+              } else {
+                return inverse(L);
               }
-              if constexpr (KEYS == kOwnKeys) {
-                float w;
-                const float keep = with_mid(A.mid_ml + 2 * mid_at(row), first, M, L, w);
-                if (first) mid_weight[row] = w;
-                return keep;
-              }
-              return inverse(L);
             });
       if (at >= stop) return;
       list.load(A, lane);  // (not kept in registers through the unit)
@@ -1046,10 +1144,12 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
   constexpr int kThreads = NW * 64, kTileRows = NW * kWaveRows;
   union Shared {
     Lds<D> page[2];
-    float join[kJoinFloats<kTileRows, kPreSplits, kThreads>];
+    struct {
+      float join[kJoinFloats<kTileRows, kPreSplits, kThreads>];
+      float pre_w[KEYS == kOwnKeys ? kTileRows * kPrePieces : 1], row_ml[KEYS == kOwnKeys ? kTileRows : 1][2];
+    } end;
   };
   __shared__ __attribute__((aligned(16))) Shared S;
-  __shared__ float mid_weight[KEYS == kOwnKeys ? kTileRows : 1];
   const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place P;
@@ -1344,6 +1444,30 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
     for (int r = 0; r < 16; r++) o[d][r] = (o[d][r] + corr) * unit;
 
   // element r of o[d] is output 32 d + 8 (r / 4) + 4 half + r % 4
+  if constexpr (KEYS == kPrefixKeys) {
+    // every piece as it is: the launch over the own keys joins them
+    float *to = A.mid + ((int64_t)P.tile * A.nsplit + P.split) * partial_floats(kTileRows, D);
+    if (valid) {
+#pragma unroll
+      for (int d = 0; d < D / 32; d++)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<f4 *>(to + row * D + 32 * d + 2 * r + 4 * half) =
+              (f4){o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]};
+      if (half == 0) {
+        to[kTileRows * D + 2 * row] = m;
+        to[kTileRows * D + 2 * row + 1] = l;
+      }
+    }
+    return;
+  }
+  const Before before = KEYS == kOwnKeys ? Before(A, P.s, D) : Before();
+  auto join_row = [&](int jr, int j, bool live, float M, float L) {  // (kOwnKeys)
+    const uint32_t f = P.f0 + jr;
+    int64_t at, ml;
+    before.at(A, P.begin + f / (uint32_t)A.group, P.h * A.group + f % (uint32_t)A.group, D, at, ml);
+    return join_before(A.mid, ml, before, j, live, M, L, S.end.pre_w + jr * kPrePieces);
+  };
   if (P.splits > 1) {
     Rsrc base = make_rsrc(A.partials + (int64_t)P.tile * A.nsplit * partial_floats(kTileRows, D));
     const int at = P.split * partial_floats(kTileRows, D);
@@ -1355,59 +1479,55 @@ __global__ __launch_bounds__(NW * 64, 2) void prefill_kernel(const AttnArgs A) {
           store_dev(base, at + row * D + 32 * d + 2 * r + 4 * half, (f4){o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]});
       if (half == 0) store_dev2(base, at + kTileRows * D + 2 * row, m, l);
     }
-    auto mid_at = [&](int jr) {
-      const uint32_t f = P.f0 + jr;
-      return (int64_t)(P.begin + f / (uint32_t)A.group) * (A.hkv * A.group) + P.h * A.group + f % (uint32_t)A.group;
-    };
     if (last_split(A.counters + P.tile, P.splits))
       join<kTileRows, D, kThreads, kPreSplits>(
-          threadIdx.x, base, P.splits, P.nrows, S.join, [](int k) { return k * partial_floats(kTileRows, D); },
+          threadIdx.x, base, P.splits, P.nrows, S.end.join, [](int k) { return k * partial_floats(kTileRows, D); },
           [&](int jr, int d, f4 v) {
-            if constexpr (KEYS == kPrefixKeys) {
-              *reinterpret_cast<f4 *>(A.mid_o + mid_at(jr) * D + d) = v;
-              return;
-            }
-            if constexpr (KEYS == kOwnKeys) v += mid_weight[jr] * take_mid(A.mid_o + mid_at(jr) * D + d);
             const uint32_t f = P.f0 + jr;
-            *reinterpret_cast<h4 *>(A.out + (int64_t)(P.begin + f / (uint32_t)A.group) * A.out_stride +
-                                    (P.h * A.group + f % (uint32_t)A.group) * D + d) =
+            const int t = P.begin + f / (uint32_t)A.group, qh = P.h * A.group + f % (uint32_t)A.group;
+            if constexpr (KEYS == kOwnKeys) {
+              int64_t at, ml;
+              before.at(A, t, qh, D, at, ml);
+              v += take_before(A.mid, at + d, before, S.end.pre_w + jr * kPrePieces);
+            }
+            *reinterpret_cast<h4 *>(A.out + (int64_t)t * A.out_stride + qh * D + d) =
                 (h4){(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
           },
-          [&](int jr, bool first, float M, float L) {
-            if constexpr (KEYS == kPrefixKeys) {
-              if (first) A.mid_ml[2 * mid_at(jr)] = M, A.mid_ml[2 * mid_at(jr) + 1] = L;
-            }
-            if constexpr (KEYS == kOwnKeys) {
-              float w;
-              const float keep = with_mid(A.mid_ml + 2 * mid_at(jr), first, M, L, w);
-              if (first) mid_weight[jr] = w;
-              return keep;
-            }
-            return inverse(L);
+          [&](int jr, int j, bool live, float M, float L) {
+            if constexpr (KEYS == kOwnKeys) return join_row(jr, j, live, M, L);
+            else return inverse(L);
           });
     return;
   }
-  if (valid) {
-    const int64_t at = (int64_t)(P.begin + tok) * (A.hkv * A.group) + head;
-    float inv = inverse(l), w = 0.0f;
-    if constexpr (KEYS == kOwnKeys) inv = with_mid(A.mid_ml + 2 * at, half == 0, m, l, w);
-    if constexpr (KEYS == kPrefixKeys) {
-      if (half == 0) A.mid_ml[2 * at] = m, A.mid_ml[2 * at + 1] = l;
+  float inv = inverse(l);
+  int64_t pre_o = 0;
+  if constexpr (KEYS == kOwnKeys) {
+    // 16 lanes a row, its maximum and sum through LDS, the factor on the way back
+    if (half == 0) {
+      S.end.row_ml[row][0] = m;
+      S.end.row_ml[row][1] = l;
     }
+    __syncthreads();
+    for (int r0 = 0; r0 < P.nrows; r0 += kThreads / 16) {
+      const int jr = r0 + threadIdx.x / 16, rr = min(jr, P.nrows - 1);
+      const float f = join_row(rr, threadIdx.x & 15, jr < P.nrows, S.end.row_ml[rr][0], S.end.row_ml[rr][1]);
+      if ((threadIdx.x & 15) == 0 && jr < P.nrows) S.end.row_ml[jr][1] = f;
+    }
+    __syncthreads();
+    inv = S.end.row_ml[row][1];
+    int64_t ml;
+    before.at(A, P.begin + tok, head, D, pre_o, ml);
+  }
+  if (valid) {
     _Float16 *dst = A.out + (int64_t)(P.begin + tok) * A.out_stride + head * D;
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         f4 v = (f4){o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]} * inv;
-        float *mid = A.mid_o + at * D + 32 * d + 2 * r + 4 * half;
-        if constexpr (KEYS == kPrefixKeys) {
-          *reinterpret_cast<f4 *>(mid) = v;
-          continue;
-        }
-        if constexpr (KEYS == kOwnKeys) v += w * take_mid(mid);
-        *reinterpret_cast<h4 *>(dst + 32 * d + 2 * r + 4 * half) =
-            (h4){(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+        const int e = 32 * d + 2 * r + 4 * half;
+        if constexpr (KEYS == kOwnKeys) v += take_before(A.mid, pre_o + e, before, S.end.pre_w + row * kPrePieces);
+        *reinterpret_cast<h4 *>(dst + e) = (h4){(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
       }
   }
 }

@@ -6,33 +6,99 @@
 // kernels for one sequence's rows (tq_kv_attn_kernel.h) read it once for all of
 // them.  A first launch takes the prefixes and leaves each row's output, maximum
 // and sum in the workspace; a second one takes the sequences' own keys and joins
-// the two, o = (2^(m1 - m) l1 o1 + 2^(m2 - m) l2 o2) / (2^(m1 - m) l1 + 2^(m2 - m) l2).
+// the two, o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  Calls in which a prefix
+// is read too few times to pay for that run as tq_kv_attn.
+//
+// Bound: the prefix by the matrix, vector and LDS pipes (as a prompt), own keys by
+// HBM.  Measured, 64 query and 8 KV heads of 128: 64 tokens on up to 1001 own tokens
+// behind 16384, 78 us, of them the prefix 49 (700 TFLOP/s) and the own keys, with 34
+// MB of the prefix's pieces read and cleared, 28; read for each sequence it was 261.
 #include "tq_kv_attn_kernel.h"
 
 namespace {
 
 constexpr size_t kMidBytes = (size_t)1 << 27;  // of the prefixes' results at most
+// Workgroups of the prefix launch, two a CU, where its keys are cut (64 tokens behind
+// 16384: 100 us, with one a CU 108, with four 119), and pages of a piece at least.
+constexpr int kPreFill = 2 * kCus, kPreLeast = 4;
 
 struct SharedPlan {
   bool shared;  // else one launch over all keys
   Plan prefix, own;
+  int64_t slots;    // of the prefix launch's tiles of 128 rows; 0: tiles of 16 or 32, results row by row
+  int64_t mid_ml;
   size_t bytes;
 };
+
+// us that a tile of `tile_rows` rows takes for a page of 64 keys with all CUs at work
+// on such tiles: from calls of 8 to 128 sequences on 2000 to 33000 tokens.
+double page_us(int tile_rows, int64_t head_dim) {
+  const bool wide = head_dim == 128;
+  return tile_rows == kTileRows ? (wide ? 0.0047 : 0.0030) : tile_rows == 2 * kRows ? (wide ? 0.0026 : 0.0012) : (wide ? 0.0016 : 0.00105);
+}
+double tiles_us(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t keys, int tile_rows) {
+  const int64_t each = (rows * (q_heads / kv_heads) + seqs - 1) / seqs, tiles = (each + tile_rows - 1) / tile_rows * seqs * kv_heads;
+  return (double)(tiles * ((keys + kPage - 1) / kPage)) * page_us(tile_rows, head_dim);
+}
 
 SharedPlan make_shared_plan(int64_t rows, int64_t seqs, int64_t groups, int64_t q_heads, int64_t kv_heads,
                             int64_t head_dim, int64_t max_prefix, int64_t max_own) {
   SharedPlan P = {};
-  const size_t mid = (size_t)(rows * q_heads * (head_dim + 2)) * 4;
-  P.shared = max_prefix >= kPage && mid <= kMidBytes;
-  if (!P.shared) {
-    P.own = make_plan(rows, seqs, q_heads, kv_heads, head_dim, max_prefix + max_own);
-    P.bytes = P.own.bytes;
-    return P;
+  const int64_t flat = rows * (q_heads / kv_heads), pages = max_prefix / kPage;
+  const Plan all = make_plan(rows, seqs, q_heads, kv_heads, head_dim, max_prefix + max_own);
+  P.bytes = all.bytes;
+  if (pages == 0) return P;
+  SharedPlan S = {};
+  size_t mid;
+  if (flat <= 2 * kRows * groups) {
+    S.prefix = make_plan(rows, groups, q_heads, kv_heads, head_dim, max_prefix);
+    S.mid_ml = rows * q_heads * head_dim;
+    mid = (size_t)(rows * q_heads * (head_dim + 2)) * 4;
+  } else {
+    Plan &T = S.prefix;
+    S.slots = flat / kTileRows + groups;
+    const int64_t full = (flat + kTileRows - 1) / kTileRows, units = (full > groups ? full : groups) * kv_heads;
+    const size_t piece = (size_t)partial_floats(kTileRows, (int)head_dim) * 4 * (size_t)(S.slots * kv_heads);
+    int64_t n = kPreFill / units;
+    if (n > kPrePieces) n = kPrePieces;
+    if (n > pages / kPreLeast) n = pages / kPreLeast;
+    if (n > (int64_t)(kMidBytes / piece)) n = (int64_t)(kMidBytes / piece);
+    if (n < 1) n = 1;
+    T.tile_rows = kTileRows;
+    T.waves = kPreWaves;
+    T.wgs = S.slots * kv_heads * n;
+    T.nsplit = (int)n;
+    T.chunk = (int)((pages + n - 1) / n);
+    mid = piece * (size_t)n;
   }
-  P.prefix = make_plan(rows, groups, q_heads, kv_heads, head_dim, max_prefix);
-  P.own = make_plan(rows, seqs, q_heads, kv_heads, head_dim, max_own + kPage - 1);  // (with the prefix's last part of a page)
-  P.bytes = P.prefix.bytes + P.own.bytes + mid;
-  return P;
+  if (mid > kMidBytes) return P;
+  S.own = make_plan(rows, seqs, q_heads, kv_heads, head_dim, max_own);
+  // Own parts of a few pages in tiles of 16 rows, three workgroups of four waves a CU:
+  // their end (the join with the prefix) is as long as their keys.  (64 x 4 rows, 300 own
+  // tokens behind 2048: 64 against 90 us with tiles of 32; 64 x 1, 2000 behind 8192: 85
+  // against 90 with cut units.)
+  const int64_t own_pages = (max_own + kPage - 1) / kPage, own_units = (flat / kRows + seqs) * kv_heads;
+  if (S.own.tile_rows != kTileRows && own_units > kCus &&
+      own_pages <= (S.own.tile_rows == kRows ? 2 * kWhole : kWhole)) {
+    S.own = Plan{};
+    S.own.tile_rows = kRows;
+    S.own.waves = 4;
+    S.own.wgs = own_units;
+    S.own.nsplit = 1;
+    S.own.chunk = 0x7fffffff;
+  }
+  // Two launches where they should take less time: what a page takes a tile, what a
+  // launch takes besides, and the prefix's results, written, read and cleared.  (8 x 1
+  // rows, 300 behind 2048: 15.6 us in one, 23.2 in two; 4 x 1 behind 8192 18.7 and 38,
+  // 16 x 1 38 and 36, 64 x 1 121 and 54, 64 x 1 behind 16384 261 and 78; 16 x 150,
+  // 32 heads, 203 behind 4096, 205 and 225.)
+  const double one = 9.0 + tiles_us(rows, seqs, q_heads, kv_heads, head_dim, max_prefix + max_own, all.tile_rows);
+  const double two = 24.0 + tiles_us(rows, groups < seqs ? groups : seqs, q_heads, kv_heads, head_dim, max_prefix, S.prefix.tile_rows) +
+                     tiles_us(rows, seqs, q_heads, kv_heads, head_dim, max_own, S.own.tile_rows) + (double)mid * 2.0 / 8.5e6;
+  if (one <= two) return P;
+  S.shared = true;
+  S.bytes = S.prefix.bytes + S.own.bytes + mid;
+  return S;
 }
 
 int check_lens(int64_t groups, int64_t max_prefix, int64_t max_own) {
@@ -95,8 +161,11 @@ extern "C" int tq_kv_attn_shared(int64_t rows, int64_t seqs, int64_t groups, int
   A.cu_seqs = cu_seqs; A.prefix = prefix_len; A.groups = (int)groups; A.all_seqs = (int)seqs;
   hipStream_t st = (hipStream_t)stream;
   char *p = (char *)ws;
-  A.mid_o = (float *)(p + P.prefix.bytes + P.own.bytes);
-  A.mid_ml = A.mid_o + rows * q_heads * head_dim;
+  A.mid = (float *)(p + P.prefix.bytes + P.own.bytes);
+  A.mid_ml = P.mid_ml;
+  A.pre_slots = (int)P.slots;
+  A.pre_nsplit = P.slots ? P.prefix.nsplit : 0;
+  A.pre_chunk = P.prefix.chunk;
   set_plan(A, P.prefix, groups, p);
   launch_attn<kPrefixKeys>(P.prefix, head_dim, A, st);
   set_plan(A, P.own, seqs, p + P.prefix.bytes);

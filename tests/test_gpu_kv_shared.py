@@ -89,51 +89,77 @@ def users(n, own, rows=1, seed=0):
     return [(rows, int(max(rows, rng.integers(1, own + 1)))) for _ in range(n)]
 
 
+def shares(c):
+    """Whether the call takes two launches: its workspace is then not that of tq_kv_attn."""
+    import ternary_weight_base_amd as tq
+    n, (hq, hkv, dim) = (c["q"].shape[0], len(c["kv"])), c["heads"]
+    return tq.tq_kv_attn_shared_workspace_bytes(*n, len(c["prefix"]), hq, hkv, dim, c["most_prefix"], c["most_own"]) != \
+        tq.tq_kv_attn_workspace_bytes(*n, hq, hkv, dim, c["most_prefix"] + c["most_own"])
+
+
+# What the call is told of its largest prefix and own part sets the kernels: larger
+# numbers than there are take small inputs through all of them.  {name: (heads,
+# groups, [(max_prefix_len, max_own_len; 0: as it is)...] that take two launches)}
+LONG = 1 << 17
 CASES = {
-    # one group: tiles of 16 rows, whole and cut prefixes, one user
-    "one_user": ((8, 2, 128), [(640, [(1, 30)])]),
-    "two_users": ((16, 8, 128), [(2000, users(2, 90))]),
-    "long": ((16, 8, 64), [(9000, users(2, 200))]),
-    # tiles of 32 rows
-    "five_users": ((16, 4, 128), [(900, users(5, 300))]),
-    "five_users_long": ((16, 4, 64), [(5000, users(5, 1500, rows=2))]),
-    # tiles of 128 rows, whole and cut
-    "many": ((64, 8, 128), [(2048, users(40, 200))]),
-    "many_64": ((16, 4, 64), [(1024, users(130, 70))]),
-    "many_long": ((32, 2, 128), [(6000, users(40, 300))]),
-    "many_rows": ((16, 2, 64), [(700, users(30, 60, rows=5))]),
-    # own parts in shares of all pages and in pieces
-    "long_own": ((8, 8, 64), [(128, users(30, 4000))]),
-    "long_own_rows": ((16, 4, 128), [(192, users(12, 3000, rows=4))]),
-    # own parts by the kernel for many rows
-    "questions": ((8, 2, 64), [(512, [(100, 120), (90, 300), (120, 121), (60, 60)])]),
-    "questions_128": ((16, 2, 128), [(640, [(40, 900), (30, 31), (37, 1500)])]),
+    "one_user": ((8, 2, 128), [(640, [(1, 30)])], []),
+    # the prefix in tiles of 16 rows, cut; own parts whole, cut, in shares
+    "two_users": ((16, 8, 128), [(2000, users(2, 90))], [(LONG, 0), (LONG, 30000)]),
+    "two_users_64": ((16, 8, 64), [(9000, users(2, 200))], [(LONG, 0), (LONG, 30000)]),
+    # ... in tiles of 32 rows
+    "five_users": ((16, 4, 128), [(900, users(5, 300))], [(LONG, 0), (LONG, 30000)]),
+    "five_users_64": ((16, 4, 64), [(5000, users(5, 1500, rows=2))], [(LONG, 0), (LONG, 30000)]),
+    # ... whole, for many groups of few users
+    "many_groups": ((8, 8, 64), [(64 * (i % 6), users(5, 40, seed=i)) for i in range(60)], [(1024, 0)]),
+    "many_groups_128": ((32, 8, 128), [(64 * (i % 4) + 9, users(6, 30, seed=i)) for i in range(40)], [(1024, 0)]),
+    "many_groups_16": ((16, 8, 128), [(64 * (i % 5), users(6, 30, seed=i)) for i in range(40)], [(1024, 0)]),
+    # ... in tiles of 128 rows, in 32 pieces, fewer, one
+    "many": ((64, 8, 128), [(2048, users(40, 200))], [(LONG, 0), (8192, 0)]),
+    "many_64": ((16, 4, 64), [(1024, users(130, 70))], [(LONG, 0), (8192, 3000)]),
+    "many_heads": ((64, 64, 64), [(300, users(150, 20))], [(320, 0), (4096, 0)]),
+    "many_rows": ((16, 2, 64), [(700, users(30, 60, rows=5))], [(LONG, 0), (LONG, 30000)]),
+    "many_long": ((32, 2, 128), [(6000, users(40, 300))], [(LONG, 0), (LONG, 30000)]),
+    # own parts of thousands of tokens, several rows
+    "long_own": ((8, 8, 64), [(128, users(30, 4000))], [(LONG, 0)]),
+    "long_own_rows": ((16, 4, 128), [(192, users(12, 3000, rows=4))], [(LONG, 0), (LONG, 900)]),
+    # own parts by the kernel for many rows: whole, cut
+    "questions": ((16, 2, 64), [(512, [(8, 20), (7, 300), (5, 121), (6, 60)] * 16)], [(LONG, 0), (LONG, 3000)]),
+    "questions_128": ((16, 2, 128), [(640, [(9, 900), (8, 31), (10, 1500)] * 8)], [(LONG, 0)]),
+    "questions_few": ((8, 2, 64), [(512, [(70, 120), (60, 300), (50, 121), (60, 60)])], [(LONG, 0), (LONG, 2000)]),
     # groups of all sizes; prefixes of no page, of a part of one, of pages and a part
-    "groups": ((8, 2, 128), [(0, users(3, 80)), (63, users(1, 5)), (64, users(4, 200)), (1000, users(20, 90)), (65, [(1, 1), (1, 64), (1, 63)])]),
-    "groups_rows": ((24, 4, 64), [(300, users(9, 300, rows=3)), (4100, users(2, 20, rows=2)), (128, [(0, 5), (7, 9), (0, 0)])]),
-    # some groups without sequences
-    "empty_groups": ((8, 4, 64), [(128, []), (640, users(3, 40)), (64, []), (256, users(1, 10)), (512, [])]),
+    "groups": ((8, 2, 128), [(0, users(3, 80)), (63, users(1, 5)), (64, users(4, 200)), (1000, users(20, 90)), (65, [(1, 1), (1, 64), (1, 63)])],
+               [(LONG, 0), (LONG, 3000)]),
+    "groups_rows": ((24, 4, 64), [(300, users(9, 300, rows=3)), (4100, users(2, 20, rows=2)), (128, [(0, 5), (7, 9), (0, 0)])],
+                    [(LONG, 0), (LONG, 30000)]),
+    "empty_groups": ((8, 4, 64), [(128, []), (640, users(3, 40)), (64, []), (256, users(1, 10)), (512, [])], []),
+    "empty_groups_more": ((8, 4, 64), [(128, []), (640, users(13, 40)), (64, []), (256, users(4, 10)), (512, [])], [(LONG, 0), (LONG, 30000)]),
 }
 
 
 @pytest.mark.parametrize("name", CASES)
 def test_cases(name):
-    say(f"shared {name}")
-    heads, groups = CASES[name]
+    heads, groups, told = CASES[name]
     c = make(heads, groups, seed=len(name))
-    verify(c, call(c))
+    most = c["most_prefix"], c["most_own"]
+    for p, o in [(0, 0)] + told:
+        c["most_prefix"], c["most_own"] = p or most[0], o or most[1]
+        say(f"shared {name} {c['most_prefix']} {c['most_own']}")
+        assert shares(c) or not p
+        verify(c, call(c))
 
 
 @pytest.mark.parametrize("heads", [(8, 2, 128), (5, 1, 64), (6, 6, 64), (64, 8, 128), (33, 3, 128)], ids=str)
 def test_sequences_outside_the_groups_and_padding(heads):
     c = make(heads, [(320, users(4, 100)), (128, users(2, 60))], seed=3, alone=[(1, 77), (0, 0), (3, 500), (1, 1)], pad=4)
+    c["most_prefix"] = 1 << 22
+    assert shares(c)
     verify(c, call(c))
 
 
 @pytest.mark.parametrize("prefix", [0, 64, 1000])
 def test_lengths_larger_than_there_are(prefix):
     """max_prefix_len and max_own_len only set the kernels."""
-    for most_prefix, most_own in ((prefix, 130), (60000, 130), (max(prefix, 64), 50000), (20000, 20000)):
+    for most_prefix, most_own in ((prefix, 130), (LONG, 130), (max(prefix, 64), 50000), (LONG, 20000)):
         c = make((8, 2, 64), [(prefix, users(6, 130))], seed=4)
         c["most_prefix"], c["most_own"] = most_prefix, most_own
         verify(c, call(c))
@@ -141,6 +167,7 @@ def test_lengths_larger_than_there_are(prefix):
 
 def test_strided_rows():
     c = make((6, 2, 64), [(200, users(5, 100, rows=2))], seed=5)
+    c["most_prefix"] = LONG
     rows = c["q"].shape[0]
     wide = torch.full((rows, 6 * 64 + 40), math.nan, dtype=torch.float16, device="cuda")
     wide[:, :384] = dev(c["q"]).view(rows, 384)
@@ -160,15 +187,16 @@ def test_missing_pages_and_scales_of_any_kind():
     c["ks"][c["table"][0, 1]] = 0
     c["vs"][c["table"][0, 2]] = 0
     c["vs"][c["table"][9, 0]] = 0
-    verify(c, call(c))
+    for c["most_prefix"] in (640, LONG):
+        verify(c, call(c))
 
 
 def test_rows_that_see_nothing():
     """A prefix and own pages that are all missing: zeros."""
     c = make((4, 2, 64), [(128, users(3, 40))], seed=7)
     c["table"][:] = -1
-    out = call(c)
-    assert not bool(out.any())
+    for c["most_prefix"] in (128, LONG):
+        assert not bool(call(c).any())
 
 
 def test_large_scores_on_one_side():
@@ -177,6 +205,7 @@ def test_large_scores_on_one_side():
         c = make((8, 2, 128), [(512, users(20, 100))], seed=8 + where, flat_scales=True)
         pages = c["table"][0, :8] if where == 0 else np.setdiff1d(np.arange(c["ks"].shape[0]), c["table"][0, :8])
         c["ks"][pages] *= 256
+        c["most_prefix"] = LONG
         verify(c, call(c))
 
 
@@ -184,10 +213,11 @@ def test_the_same_as_without_sharing():
     """Against tq_kv_attn on the same arrays: two results of the same rows within both tolerances."""
     import ternary_weight_base_amd as tq
     c = make((16, 4, 128), [(1500, users(17, 400)), (300, users(5, 80, rows=2))], seed=10)
+    most = int(c["kv"].max())
+    c["most_prefix"] = LONG
     out = call(c)
     a = {n: dev(c[n]) for n in ("q", "cu", "kv", "table", "k", "v", "ks", "vs")}
     plain = torch.empty_like(a["q"])
-    most = int(c["kv"].max())
     ws = tq.kv_attn_workspace(c["q"].shape[0], len(c["kv"]), 16, 4, 128, most)
     tq.tq_kv_attn(a["q"], a["cu"], a["kv"], a["table"], a["k"], a["v"], a["ks"], a["vs"], plain, most, ws=ws)
     verify(c, plain)
@@ -202,10 +232,10 @@ def test_bad_arrays_stay_inside():
         if cu is not None:
             c["cu"] = np.array(cu, np.int32)
         import ternary_weight_base_amd as tq
-        ws = tq.kv_attn_shared_workspace(6, 6, 3, 8, 2, 64, 640, 50)
+        ws = tq.kv_attn_shared_workspace(6, 6, 3, 8, 2, 64, LONG, 50)
         a = {n: dev(c[n]) for n in ("q", "cu", "kv", "cu_seqs", "prefix", "table", "k", "v", "ks", "vs")}
         out = torch.empty_like(a["q"])
-        tq.tq_kv_attn_shared(a["q"], a["cu"], a["kv"], a["cu_seqs"], a["prefix"], a["table"], a["k"], a["v"], a["ks"], a["vs"], out, 640, 50, ws=ws)
+        tq.tq_kv_attn_shared(a["q"], a["cu"], a["kv"], a["cu_seqs"], a["prefix"], a["table"], a["k"], a["v"], a["ks"], a["vs"], out, LONG, 50, ws=ws)
         torch.cuda.synchronize()
 
 
@@ -223,12 +253,13 @@ def test_captured_with_changing_groups():
         for n in ("k", "v", "ks", "vs"):
             c[n] = np.pad(c[n], ((0, more),) + ((0, 0),) * (c[n].ndim - 1))
         c["q"] = np.pad(c["q"], ((0, 12 - c["q"].shape[0]), (0, 0), (0, 0)))
-        c["most_prefix"], c["most_own"] = 2000, 900
-    ws = tq.kv_attn_shared_workspace(12, 12, 2, *heads, 2000, 900)
+        c["most_prefix"], c["most_own"] = LONG, 900
+        assert shares(c)
+    ws = tq.kv_attn_shared_workspace(12, 12, 2, *heads, LONG, 900)
     a = {n: dev(cases[0][n]) for n in ("q", "cu", "kv", "cu_seqs", "prefix", "table", "k", "v", "ks", "vs")}
     out = torch.empty_like(a["q"])
     run = lambda: tq.tq_kv_attn_shared(a["q"], a["cu"], a["kv"], a["cu_seqs"], a["prefix"], a["table"], a["k"], a["v"], a["ks"], a["vs"],
-                                       out, 2000, 900, ws=ws)
+                                       out, LONG, 900, ws=ws)
     run()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()

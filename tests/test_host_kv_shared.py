@@ -26,10 +26,14 @@ def test_kv_attn_shared_validates_on_host():
         assert _call(**{name: MIS}) == ALIGN, name
     for name in ("cu", "kv", "cs", "pl", "tb", "ks", "vs"):
         assert _call(**{name: ODD}) == ALIGN, name
-    need = tq.tq_kv_attn_shared_workspace_bytes(4, 3, 2, 8, 2, 128, 640, 256)
-    assert need > 0
-    assert _call(wb=need - 1) == SIZE
-    assert _call(ws=None, wb=0) == NULL
+    many = dict(rows=64, seqs=64, xp=16384, xo=300)  # two launches
+    need = tq.tq_kv_attn_shared_workspace_bytes(64, 64, 2, 8, 2, 128, 16384, 300)
+    assert need > tq.tq_kv_attn_workspace_bytes(64, 64, 8, 2, 128, 16684) > 0
+    assert _call(**many, wb=need - 1) == SIZE and _call(**many, ws=None, wb=0) == NULL
+    few = dict(rows=4, seqs=4, groups=1, xp=8192, xo=300)  # one, as tq_kv_attn
+    need = tq.tq_kv_attn_shared_workspace_bytes(4, 4, 1, 8, 2, 128, 8192, 300)
+    assert need == tq.tq_kv_attn_workspace_bytes(4, 4, 8, 2, 128, 8492) > 0
+    assert _call(**few, wb=need - 1) == SIZE and _call(**few, ws=None, wb=0) == NULL
     for bad in ((0, 1, 1, 8, 2, 128, 64, 9), (1, 1, 0, 8, 2, 128, 64, 9), (1, 1, 1, 8, 3, 128, 64, 9), (1, 1, 1, 8, 2, 100, 64, 9),
                 (1, 1, 1, 8, 2, 128, 64, 0), (1, 1, 1, 8, 2, 128, -1, 9)):
         assert tq.tq_kv_attn_shared_workspace_bytes(*bad) == 0
