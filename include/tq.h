@@ -543,7 +543,7 @@ int tq_kv_attn_shared(int64_t rows, int64_t seqs, int64_t groups, int64_t q_head
 /* Scratch bytes of tq_linear_attn (0 when it needs none, or on a bad shape).
  * Scratch is device memory that needs no contents and is left with any: it
  * must not be a workspace of the other calls, which have to find theirs zero.
- * At most 2^27 bytes and a state for each KV head, or what 128 rows of all KV
+ * At most 2^27 bytes and two states for each KV head, or what 128 rows of all KV
  * heads take (6 kv_heads head_dim^2 bytes) where that is more; not monotonic. */
 size_t tq_linear_attn_scratch_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
                                     int64_t head_dim);

@@ -25,6 +25,7 @@
 #include <stdint.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "tq.h"
 #include "tq_device.h"
@@ -61,7 +62,8 @@ struct LinArgs {
   float scale;
   int rows, seqs, hq, hkv, group;
   // a pass over the chunks: slots slot0 .. slot0 + slots - 1
-  float *u, *carry;
+  float *u, *carry;  // carry: where the pass leaves the state of a sequence that goes on behind it
+  const float *carried;  // ... and where the last one left it
   _Float16 *snap;
   Meta *meta;
   int slot0, slots, parts;
@@ -256,7 +258,7 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
     const int base = slot_base<kChunk, 1>(first, s, 1), slot = max(base, A.slot0);
     if (n <= 0 || slot >= min(base + (n + kChunk - 1) / kChunk, A.slot0 + A.slots)) return;
     const int from = A.from[s];
-    const float *p = base < slot ? A.carry + (int64_t)h * (D * D) : A.states + ((int64_t)from * A.hkv + h) * (D * D);
+    const float *p = base < slot ? A.carried + (int64_t)h * (D * D) : A.states + ((int64_t)from * A.hkv + h) * (D * D);
     float m = 0.0f;
     if (base < slot || state_ok(A, from)) {
 #pragma unroll
@@ -427,9 +429,9 @@ __global__ __launch_bounds__(64) void scan_kernel(const LinArgs A) {
   f4 x[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; i++) x[i] = *reinterpret_cast<const f4 *>(u + min(i, count - 1) * step);
-  float *carry = A.carry + (int64_t)h * (D * D) + at;
+  float *carry = A.carry + (int64_t)h * (D * D) + at;  // (one sequence may read it as another one writes: two of them)
   f4 S = {0, 0, 0, 0};
-  if (lo > base) S = *reinterpret_cast<const f4 *>(carry);
+  if (lo > base) S = *reinterpret_cast<const f4 *>(A.carried + (int64_t)h * (D * D) + at);
   else if (state_ok(A, from)) S = *reinterpret_cast<const f4 *>(A.states + ((int64_t)from * A.hkv + h) * (D * D) + at);
   _Float16 *snap = A.snap + r0 * (D * D) + at;
   Meta *meta = A.meta + r0;
@@ -751,7 +753,7 @@ Plan make_plan(int64_t rows, int64_t seqs, int64_t kv_heads, int64_t head_dim) {
   P.pass = (int64_t)(kPassBytes / each);
   if (P.pass < 1) P.pass = 1;
   if (P.pass > P.slots) P.pass = P.slots;
-  P.carry_bytes = P.pass < P.slots ? state * 4 : 0;
+  P.carry_bytes = P.pass < P.slots ? state * 8 : 0;
   P.meta_bytes = (size_t)(P.pass * kv_heads) * sizeof(Meta);
   P.u_bytes = (size_t)P.pass * state * 4;
   P.bytes = P.carry_bytes + P.meta_bytes + P.u_bytes + P.u_bytes / 2;
@@ -772,8 +774,11 @@ bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) ==
 
 template <int D, typename T>
 void launch_passes(LinArgs A, const Plan &P, hipStream_t st) {
+  float *carried = A.carry + (int64_t)A.hkv * D * D;
   for (int64_t s0 = 0; s0 < P.slots; s0 += P.pass) {
     A.slot0 = (int)s0;
+    std::swap(A.carry, carried);
+    A.carried = carried;
     A.slots = (int)(P.slots - s0 < P.pass ? P.slots - s0 : P.pass);
     const int64_t units = (int64_t)A.slots * A.hkv;
     hipLaunchKernelGGL((chunk_state_kernel<D, T>), dim3((unsigned)(units + (int64_t)A.seqs * A.hkv)), dim3(512), 0, st, A);

@@ -140,6 +140,12 @@ def test_many_passes():
     verify(c, *call(c))
 
 
+def test_sequences_across_two_borders_of_one_pass():
+    """The second sequence ends in the pass that the third one is cut in: each has its own state between passes."""
+    c = make((64, 64, 128), [2300, 2600, 600], torch.float16, "heads", seed=17)
+    verify(c, *call(c))
+
+
 def test_a_sequences_results_do_not_depend_on_the_others():
     """Nor on its cut into calls beyond the forms' rounding: chunks again from a state left behind."""
     c = make((8, 2, 64), [256, 300], torch.float16, "rows", seed=11)

@@ -45,7 +45,7 @@ def test_scratch():
     for rows in (17, 500, 4096, 1 << 20):
         for hq, hkv, d in ((64, 8, 128), (64, 64, 128), (16, 16, 64), (256, 256, 128)):
             if rows * hq < 1 << 30:
-                assert b(rows, 1, hq, hkv, d) <= max((1 << 27) + 4 * hkv * d * d, 6 * hkv * d * d + 16 * hkv)
+                assert b(rows, 1, hq, hkv, d) <= max((1 << 27) + 8 * hkv * d * d, 6 * hkv * d * d + 16 * hkv)
 
 
 def test_binding_checks():
