@@ -564,15 +564,16 @@ size_t tq_linear_attn_scratch_bytes(int64_t rows, int64_t seqs, int64_t q_heads,
  *     sequence of the call writes must be no other's start, and no two write
  *     the same (those states and outputs are then unspecified).  A sequence
  *     without rows neither reads nor writes a state.
- *   out: fp16, rows out_stride elements apart (a multiple of 8).
+ *   out: fp16, rows out_stride elements apart (a multiple of 8, at most 2^22).
  * Up to 16 rows a sequence, on average, the recurrence runs row by row in fp32
  * (one launch, no scratch); more run in chunks of 128 rows (three launches for
  * up to 2^27 bytes of scratch), where states keep fp32's accuracy; for the
- * outputs fp32 values and the states before each chunk are rounded to fp16.  A sequence of many rows
- * beside many single tokens is better a call of its own.  Non-finite inputs make
- * their sequence's outputs and state for that KV head (from the chunk on that
- * holds them) unspecified, those of no other.  qkv, states, out and scratch
- * 16-byte aligned; out does not overlap qkv. */
+ * outputs fp32 values and the states before each chunk are rounded to fp16
+ * (scaled: no size overflows).  A sequence of many rows beside many single
+ * tokens is better a call of its own.  Non-finite inputs make their sequence's
+ * outputs and state for that KV head (from the chunk on that holds them)
+ * unspecified, those of no other.  qkv, states, out and scratch 16-byte aligned;
+ * out does not overlap qkv. */
 int tq_linear_attn(int dtype, int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
                    int64_t head_dim, const void *qkv, int64_t row_stride, const float *log_decay,
                    int64_t decay_stride, const int32_t *cu_rows, const int32_t *state_from,

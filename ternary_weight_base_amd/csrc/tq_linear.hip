@@ -506,14 +506,18 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   typedef typename std::conditional<kWide, f4, h8>::type Piece;
   constexpr int kPieces = D / 16 * (kWide ? 2 : 1);
   Piece raw[kPieces];
-  auto send_for = [&](int i) {
+  // fp32 queries come in two halves, the second once the operands made of the last
+  // ones are done with: all at once do not fit into the registers
+  constexpr int kFirst = kWide ? kPieces / 2 : kPieces;
+  auto send_for = [&](int i, int from, int to) {
     const int row = 32 * block_of(i) + n, head = h * A.group + g0 + min(head_of(i), heads - 1);
     const T *qp = (const T *)A.qkv + (int64_t)(c.begin + min(row, c.n - 1)) * A.row_stride + head * D + 8 * half;
 #pragma unroll
     for (int j = 0; j < kPieces; j++)
-      raw[j] = *reinterpret_cast<const Piece *>(qp + (kWide ? 16 * (j >> 1) + 4 * (j & 1) : 16 * j));
+      if (j >= from && j < to) raw[j] = *reinterpret_cast<const Piece *>(qp + (kWide ? 16 * (j >> 1) + 4 * (j & 1) : 16 * j));
   };
-  if (heads > 0) send_for(0);
+  if (heads <= 0) return;
+  send_for(0, 0, kPieces);
   const int64_t rs = (int64_t)rel * A.hkv + h;
   const int es = A.meta[rs].e;
   const T *kp = (const T *)A.qkv + (int64_t)c.begin * A.row_stride + (A.hq + h) * D;
@@ -604,34 +608,22 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   const float scale_m = frexpf(A.scale, &scale_e);
   const Turned<D> turned;
 
+  // Outputs go through a buffer whose end drops the rows that are not there, so
+  // that every round has the same stores behind its loads: the wait for the next
+  // queries is then not a wait for the stores.
+  const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(A.out + (int64_t)c.begin * A.out_stride, 0, 0x7fffffff, 0x00027000);
+  constexpr uint32_t kNowhere = 0x80000000u;
+
   // one round: rows 32 RB + n of a head
-  auto rows = [&](auto block, int i) {
+  auto rows = [&](auto block, int i, const h8 (&qf)[kTerms][D / 16], int bq) {
     constexpr int RB = decltype(block)::value;
-    const int row = 32 * RB + n, head = h * A.group + g0 + head_of(i);
-    h8 qf[kTerms][D / 16];
-    float mq = 0.0f;
+    const int row = 32 * RB + n, head = h * A.group + g0 + head_of(i), eq = kWide ? bq : 14;
+    if (32 * RB >= c.n || head_of(i) >= heads) {
+      send_for(min(i + 1, rounds - 1), kFirst, kPieces);
 #pragma unroll
-    for (int j = 0; j < kPieces; j++)
-#pragma unroll
-      for (int r = 0; r < (kWide ? 4 : 8); r++) mq = fmaxf(mq, fabsf((float)raw[j][r]));
-    const int bq = exponent(half_max(mq)), eq = kWide ? bq : 14;
-    if constexpr (kWide) {
-      const float f = power(14 - eq);
-#pragma unroll
-      for (int j = 0; j < D / 16; j++) {
-        float x[8];
-#pragma unroll
-        for (int r = 0; r < 8; r++) x[r] = (float)raw[kPieces / (D / 16) * j + (r >> 2)][r & 3] * f;
-        two_terms(x, qf[0][j], qf[kTerms - 1][j]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPieces; j++)
-#pragma unroll
-        for (int r = 0; r < 8; r++) qf[0][j][r] = (_Float16)raw[j][r];
+      for (int k = 0; k < D / 16; k++) __builtin_amdgcn_raw_buffer_store_b128((u4){0, 0, 0, 0}, out, kNowhere, 0, 0);
+      return;
     }
-    if (i + 1 < rounds) send_for(i + 1);
-    if (32 * RB >= c.n || head_of(i) >= heads) return;
     // o^T: o[d][r] is element 32 d + 8 (r / 4) + 4 half + r % 4 of the row, in
     // units of 2^x: weights are below 2^15 in it, the state's part below 2^97
     const int xs = eq - 14 + es;
@@ -676,6 +668,7 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
         }
       }
       __builtin_amdgcn_s_setprio(0);
+      if (t == RB) send_for(min(i + 1, rounds - 1), kFirst, kPieces);
       // weights: two fp16 terms, so that they lose nothing to the outputs' rounding
       const int j0 = 32 * t + 8 * half;
       h8 p[2], pl[2];
@@ -708,7 +701,7 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
     // that fp16 holds is not changed)
     const float last = scale_m * power(x + scale_e);
     // two quads' halves change places between the halves of the wave: 16 bytes a lane
-    _Float16 *dst = A.out + (int64_t)(c.begin + row) * A.out_stride + head * D + 8 * half;
+    const uint32_t to = row < c.n ? 2u * (uint32_t)(row * (int)A.out_stride + head * D + 8 * half) : kNowhere;
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
 #pragma unroll
@@ -721,19 +714,46 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
         }
         const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
         const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-        if (row < c.n) *reinterpret_cast<u4 *>(dst + 32 * d + 2 * r) = (u4){a[0], b[0], a[1], b[1]};
+        __builtin_amdgcn_raw_buffer_store_b128((u4){a[0], b[0], a[1], b[1]}, out, to + 2 * (32 * d + 2 * r), 0, 0);
       }
   };
 #pragma unroll 1
   for (int i = 0; i < rounds; i++) {
+    // the queries that have arrived, as operands (fp32: scaled, in two terms)
+    h8 qf[kTerms][D / 16];
+    float mq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPieces; j++)
+#pragma unroll
+      for (int r = 0; r < (kWide ? 4 : 8); r++) mq = fmaxf(mq, fabsf((float)raw[j][r]));
+    const int bq = exponent(half_max(mq));
+    if constexpr (kWide) {
+      const float f = power(14 - bq);
+#pragma unroll
+      for (int j = 0; j < D / 16; j++) {
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 8; r++) x[r] = (float)raw[kPieces / (D / 16) * j + (r >> 2)][r & 3] * f;
+        two_terms(x, qf[0][j], qf[kTerms - 1][j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPieces; j++)
+#pragma unroll
+        for (int r = 0; r < 8; r++) qf[0][j][r] = (_Float16)raw[j][r];
+    }
+    send_for(min(i + 1, rounds - 1), 0, kFirst);  // (again the last one's behind it, from the cache)
     switch (block_of(i)) {
-      case 0: rows(std::integral_constant<int, 0>(), i); break;
-      case 1: rows(std::integral_constant<int, 1>(), i); break;
-      case 2: rows(std::integral_constant<int, 2>(), i); break;
-      default: rows(std::integral_constant<int, 3>(), i); break;
+      case 0: rows(std::integral_constant<int, 0>(), i, qf, bq); break;
+      case 1: rows(std::integral_constant<int, 1>(), i, qf, bq); break;
+      case 2: rows(std::integral_constant<int, 2>(), i, qf, bq); break;
+      default: rows(std::integral_constant<int, 3>(), i, qf, bq); break;
     }
   }
 }
+
+// (a chunk's outputs are addressed in 31 bits)
+constexpr int64_t kMaxOutStride = (int64_t)1 << 22;
 
 constexpr int kCus = 256;
 
@@ -813,7 +833,7 @@ extern "C" int tq_linear_attn(int dtype, int64_t rows, int64_t seqs, int64_t q_h
   if (row_stride < (q_heads + 2 * kv_heads) * head_dim || row_stride % 8 != 0 || row_stride > ((int64_t)1 << 31) ||
       (decay_stride != 0 && decay_stride < kv_heads) || decay_stride > ((int64_t)1 << 31) || num_states < 1 ||
       num_states > 0x7fffffff || out_stride < q_heads * head_dim || out_stride % 8 != 0 ||
-      out_stride > ((int64_t)1 << 31))
+      out_stride > kMaxOutStride)
     return TQ_ERR_SHAPE;
   if (!(scale > -3.0e38f && scale < 3.0e38f)) return TQ_ERR_VALUE;
   if (!aligned_to(qkv, 16) || !aligned_to(states, 16) || !aligned_to(out, 16) || !aligned_to(scratch, 16) ||

@@ -22,7 +22,7 @@ def test_linear_attn_validates_on_host():
     assert _call(dt=2) == DTYPE and _call(dt=-1) == DTYPE
     for bad in ({"rows": 0}, {"rows": (1 << 24) + 1}, {"seqs": 0}, {"hq": 0}, {"hkv": 0}, {"hq": 7}, {"d": 32}, {"d": 96}, {"d": 256},
                 {"num": 0}, {"num": 1 << 31}, {"stride": 12 * 128 - 8}, {"stride": 12 * 128 + 4}, {"gs": 1}, {"gs": -2}, {"os": 1016},
-                {"os": 1028}, {"rows": 1 << 22, "hq": 256, "hkv": 256, "stride": 768 * 128, "os": 256 * 128}):
+                {"os": 1028}, {"os": (1 << 22) + 8}, {"rows": 1 << 22, "hq": 256, "hkv": 256, "stride": 768 * 128, "os": 256 * 128}):
         assert _call(**bad) == SHAPE, bad
     for bad in (float("nan"), float("inf"), -float("inf")):
         assert _call(sc=bad) == VALUE, bad
