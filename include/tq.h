@@ -529,8 +529,9 @@ size_t tq_kv_attn_shared_workspace_bytes(int64_t rows, int64_t seqs, int64_t gro
  * max_prefix_len, max_own_len: the largest prefix_len, and the largest kv_len less
  * its group's prefix_len, which set kernels and splits (larger ones are right too,
  * only slower).  prefix_len and cu_seqs are read on the device, as the other
- * arrays; bad entries lead to no access outside the arrays.  1 <= groups <= 2^20.
- * Two launches, or one. */
+ * arrays; bad entries lead to no access outside the arrays, but may leave a
+ * workspace that has to be cleared before its next use (tq_workspace_clear).
+ * 1 <= groups <= 2^20.  Two launches, or one. */
 int tq_kv_attn_shared(int64_t rows, int64_t seqs, int64_t groups, int64_t q_heads, int64_t kv_heads,
                       int64_t head_dim, const void *q, int64_t q_stride, const int32_t *cu_rows,
                       const int32_t *kv_len, const int32_t *cu_seqs, const int32_t *prefix_len,

@@ -177,6 +177,18 @@ def test_strided_rows():
     assert bool(torch.isnan(room[:, 384:]).all())
 
 
+def test_in_place():
+    """out may be q: own parts whole, cut, and rows of a prompt."""
+    for heads, groups, told in (((8, 2, 64), [(200, users(5, 100, rows=2))], 0), ((16, 8, 128), [(2000, users(2, 90))], 30000),
+                                ((16, 2, 64), [(512, [(8, 20), (7, 300), (5, 121), (6, 60)] * 4)], 3000)):
+        c = make(heads, groups, seed=12)
+        c["most_own"] = max(told, c["most_own"])
+        for c["most_prefix"] in (LONG, 1 << 22):  # in one launch or two, in two
+            assert shares(c) or c["most_prefix"] == LONG
+            q = dev(c["q"])
+            verify(c, call(c, q=q, out=q))
+
+
 def test_missing_pages_and_scales_of_any_kind():
     """Pages outside the cache are not seen, in the prefix and behind it; pages of zeros."""
     c = make((8, 2, 128), [(640, users(9, 300)), (128, users(2, 70))], seed=6)
