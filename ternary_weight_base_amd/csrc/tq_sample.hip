@@ -80,15 +80,23 @@ __device__ __forceinline__ double power2(double t, const double *table) {
   return ldexp(s * table[k & (kParts - 1)], k >> 6);
 }
 
-// The table, 2^(i / 64), by 64 threads: exp's series at up to 0.3466, whose 14th
-// term is below 2^-57.  (A barrier before its use.)
+// The table, 2^(i / 64): exp's series at up to 0.3466, whose 14th term is below 2^-57.
+struct Powers {
+  double v[kParts];
+  constexpr Powers() : v() {
+    for (int i = 0; i < kParts; i++) {
+      const double f = (i < kParts / 2 ? i : i - kParts) * (0.6931471805599453 / kParts);
+      double s = 1.0;
+      for (int k = 13; k > 0; k--) s = s * f / k + 1.0;
+      v[i] = i < kParts / 2 ? s : 2.0 * s;
+    }
+  }
+};
+__device__ constexpr Powers kPowers;
+
+// ... into LDS.  (A barrier before its use.)
 __device__ __forceinline__ void fill_table(double *table) {
-  const int i = threadIdx.x;
-  if (i >= kParts) return;
-  const double f = (i < kParts / 2 ? i : i - kParts) * (0.6931471805599453 / kParts);
-  double s = 1.0;
-  for (int k = 13; k > 0; k--) s = fma(s, f / k, 1.0);
-  table[i] = i < kParts / 2 ? s : 2.0 * s;
+  if (threadIdx.x < kParts) table[threadIdx.x] = kPowers.v[threadIdx.x];
 }
 
 // A weight (at most 1) in steps of 1 / steps, a power of two up to 2^48, to the
@@ -262,6 +270,16 @@ __device__ __forceinline__ void stage(const T *x, bool wide, int vocab, int seg,
   }
 }
 
+// Where a running sum over the lanes from `before` on exceeds `target`: the first
+// lane, or the last one that adds something; the sum before it.
+__device__ __forceinline__ int crossing(double own, double before, double target, double &from) {
+  const double upto = before + wave_upto(own);
+  const uint64_t some = __ballot(own > 0.0), above = __ballot(own > 0.0 && upto > target);
+  const int at = above ? __builtin_ctzll(above) : some ? 63 - __builtin_clzll(some) : 0;
+  from = lane_value(upto - own, at);
+  return at;
+}
+
 // The token of a segment (its logits in LDS) at which the running sum from
 // `before` on exceeds `target`: the first one, or the last that weighs something;
 // its weight.  A wave has 64 consecutive tokens of each NT.
@@ -290,13 +308,10 @@ __device__ int pick(const float *xs, int seg, const Weigher &weigh, const Cut &c
   __syncthreads();
   // the cell that crosses the target, or the last with a sum: every wave finds it
   static_assert(kCells == 64, "a cell a lane");
-  const double own = cell[lane], upto = before + wave_upto(own);
-  const uint64_t some = __ballot(own > 0.0), above = __ballot(own > 0.0 && upto > target);
-  const int at = above ? __builtin_ctzll(above) : some ? 63 - __builtin_clzll(some) : 0;
-  const double from = lane_value(upto - own, at);
-  const double w = weight_of(at * 64 + lane), r = from + wave_upto(w);
-  const uint64_t some1 = __ballot(w > 0.0), above1 = __ballot(w > 0.0 && r > target);
-  const int l = above1 ? __builtin_ctzll(above1) : some1 ? 63 - __builtin_clzll(some1) : 0;
+  double from;
+  const int at = crossing(cell[lane], before, target, from);
+  const double w = weight_of(at * 64 + lane);
+  const int l = crossing(w, from, target, from);
   weight = lane_value(w, l);
   return seg * kSeg + at * 64 + l;
 }
@@ -306,12 +321,10 @@ __device__ __forceinline__ void answer(const SampleArgs &A, int row, int token, 
   if (A.logprob) A.logprob[row] = token < 0 ? -__builtin_inff() : weight == total ? 0.0f : (float)log(weight / total);
 }
 
-// The token from the segments' sums of kept weights (in LDS); xs: room for a
-// segment's logits.
-template <typename T, int NT>
-__device__ void choose(const SampleArgs &A, int row, int segs, const double *seg_sum, const Weigher &weigh, const Cut &cut,
-                       double min_p, float *xs) {
-  // every wave finds the segment by itself: a lane has four of them
+// The segment in which the running sum of the segments' sums (in LDS) exceeds u
+// times all of them; the sum before it, that target and all.
+__device__ int find_segment(float u, int segs, const double *seg_sum, double &from, double &target, double &total) {
+  // every wave finds it by itself: a lane has four of them
   static_assert(kMaxSegs <= 256, "four segments a lane");
   const int lane = threadIdx.x & 63;
   double mine[4], own = 0.0;
@@ -320,9 +333,9 @@ __device__ void choose(const SampleArgs &A, int row, int segs, const double *seg
     mine[j] = 4 * lane + j < segs ? seg_sum[4 * lane + j] : 0.0;
     own += mine[j];
   }
-  const double upto = wave_upto(own), total = lane_value(upto, 63);
-  const float u = A.u[row];
-  const double target = (u > 0.0f ? (double)u : 0.0) * total;
+  const double upto = wave_upto(own);
+  total = lane_value(upto, 63);
+  target = (u > 0.0f ? (double)u : 0.0) * total;
   double r = upto - own, before_above = 0.0, before_some = 0.0;
   int above = -1, some = -1;
 #pragma unroll
@@ -339,10 +352,18 @@ __device__ void choose(const SampleArgs &A, int row, int segs, const double *seg
   }
   const uint64_t has_above = __ballot(above >= 0), has_some = __ballot(some >= 0);
   const int l = has_above ? __builtin_ctzll(has_above) : has_some ? 63 - __builtin_clzll(has_some) : 0;
-  const int seg = 4 * l + max(__builtin_amdgcn_readlane(has_above ? above : some, l), 0);
-  const double from = lane_value(has_above ? before_above : before_some, l);
+  from = lane_value(has_above ? before_above : before_some, l);
+  return 4 * l + max(__builtin_amdgcn_readlane(has_above ? above : some, l), 0);
+}
+
+// The token from the segments' sums of kept weights (in LDS); xs: room for a
+// segment's logits.
+template <typename T, int NT>
+__device__ void choose(const SampleArgs &A, int row, int segs, const double *seg_sum, const Weigher &weigh, const Cut &cut,
+                       double min_p, float *xs) {
+  double from, target, total, weight;
+  const int seg = find_segment(A.u[row], segs, seg_sum, from, target, total);
   stage<T, NT>((const T *)A.logits + row * A.row_stride, A.wide, A.vocab, seg, xs);
-  double weight;
   const int i = pick<NT>(xs, seg, weigh, cut, min_p, from, target, weight);
   if (threadIdx.x == 0) answer(A, row, i, weight, total);
 }
@@ -501,9 +522,40 @@ __device__ __forceinline__ float block_most(float v, float *room) {
   return v;
 }
 
+// A thread's logits of a segment, -inf behind the vocabulary.
+template <typename T>
+struct Own {
+  static constexpr int kV = 16 / sizeof(T);
+  float v[kOwn];
+  bool packed;  // 16 bytes of consecutive ones at a time
+  __device__ __forceinline__ Own(const SampleArgs &A, int row, int seg) {
+    typedef T Wide __attribute__((ext_vector_type(kV)));
+    const T *x = (const T *)A.logits + row * A.row_stride + seg * kSeg;
+    const int n = A.vocab - seg * kSeg, tid = threadIdx.x;
+    packed = A.wide && n >= kSeg;
+    if (packed) {
+      Wide w[kOwn / kV];
+#pragma unroll
+      for (int i = 0; i < kOwn / kV; i++) w[i] = reinterpret_cast<const Wide *>(x)[i * kThreads + tid];
+#pragma unroll
+      for (int i = 0; i < kOwn; i++) v[i] = clean((float)w[i / kV][i % kV]);
+    } else {
+      T w[kOwn];
+#pragma unroll
+      for (int i = 0; i < kOwn; i++) w[i] = i * kThreads + tid < n ? x[i * kThreads + tid] : (T)-__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < kOwn; i++) v[i] = clean((float)w[i]);
+    }
+  }
+  // the place of the j-th in the segment
+  __device__ __forceinline__ int at(int j) const {
+    const int tid = threadIdx.x;
+    return packed ? (j / kV * kThreads + tid) * kV + j % kV : j * kThreads + tid;
+  }
+};
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void segment_kernel(const SampleArgs A, const SampleWs W) {
-  __shared__ __attribute__((aligned(16))) float xs[kSeg];
   __shared__ uint32_t count[kSteps];
   __shared__ unsigned long long weight[kSteps];
   __shared__ double room[kThreads / 64], table[kParts];
@@ -511,7 +563,7 @@ __global__ __launch_bounds__(kThreads) void segment_kernel(const SampleArgs A, c
   __shared__ int where;
   const int tid = threadIdx.x, segs = A.segs;
   const int rel = blockIdx.x / (uint32_t)segs, seg = blockIdx.x % (uint32_t)segs, row = A.row0 + rel;
-  stage<T, kThreads>((const T *)A.logits + row * A.row_stride, A.wide, A.vocab, seg, xs);
+  const Own<T> x(A, row, seg);
   const Rule rule = rule_of(A, row);
   const int mode = mode_of(A, rule);
   const Steps step(rule, mode);
@@ -520,26 +572,24 @@ __global__ __launch_bounds__(kThreads) void segment_kernel(const SampleArgs A, c
   count[tid] = 0;
   weight[tid] = 0;
   __syncthreads();
-  float most = xs[tid];
+  float most = x.v[0];
 #pragma unroll
-  for (int j = 1; j < kOwn; j++) most = fmaxf(most, xs[j * kThreads + tid]);
+  for (int j = 1; j < kOwn; j++) most = fmaxf(most, x.v[j]);
   most = block_most<kThreads>(most, froom);
   const Weigher weigh = {most, rule.per, table};
   SegInfo mine = {most, 0, 0.0};
   const int64_t at = (int64_t)rel * segs + seg;
   if (rule.greedy) {
-#pragma unroll 1
-    for (int j = 0; j < kOwn; j++)
-      if (xs[j * kThreads + tid] == most) {
-        atomicMin(&where, seg * kSeg + j * kThreads + tid);
-        break;
-      }
+    int first = kSeg;
+#pragma unroll
+    for (int j = kOwn - 1; j >= 0; j--) first = x.v[j] == most ? x.at(j) : first;
+    if (first < kSeg) atomicMin(&where, seg * kSeg + first);
     __syncthreads();
     mine.index = where;
   } else if (mode == kDone) {
     double sum = 0.0;
-#pragma unroll 4
-    for (int j = 0; j < kOwn; j++) sum += weigh(xs[j * kThreads + tid]);
+#pragma unroll
+    for (int j = 0; j < kOwn; j++) sum += weigh(x.v[j]);
     mine.sum = block_sum<kThreads>(sum, room);
   } else if (mode == kTopK || mode == kManyK || mode == kTopP) {
     // (a thread's run of the same step is added at once: equal logits would queue)
@@ -552,9 +602,9 @@ __global__ __launch_bounds__(kThreads) void segment_kernel(const SampleArgs A, c
       atomicAdd(&count[run], n);
       if (mode == kTopP) atomicAdd(&weight[run], sum);
     };
-#pragma unroll 4
+#pragma unroll
     for (int j = 0; j < kOwn; j++) {
-      const float v = xs[j * kThreads + tid];
+      const float v = x.v[j];
       if (v > -__builtin_inff()) {
         const int b = min(top - step(v), kSteps - 1);
         if (b != run) {
@@ -668,7 +718,6 @@ __device__ __forceinline__ float logit_of(uint64_t entry) {  // of a key and ind
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void gather_kernel(const SampleArgs A, const SampleWs W) {
-  __shared__ __attribute__((aligned(16))) float xs[kSeg];
   __shared__ double room[kThreads / 64], table[kParts];
   __shared__ int base;
   const int tid = threadIdx.x, segs = A.segs;
@@ -676,7 +725,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const SampleArgs A, co
   const RowInfo info = W.info[rel];
   if (info.mode == kDone || info.mode == kAlone) return;
   const int64_t at = (int64_t)rel * segs + seg;
-  stage<T, kThreads>((const T *)A.logits + row * A.row_stride, A.wide, A.vocab, seg, xs);
+  const Own<T> x(A, row, seg);
   const Rule rule = rule_of(A, row);
   const Steps step(rule, info.mode);
   const Weigher weigh = {info.most, rule.per, table};
@@ -688,9 +737,9 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const SampleArgs A, co
   __syncthreads();
   double sum = 0.0;
   uint32_t mine = 0;  // this thread's tokens that are gathered
-#pragma unroll 4
+#pragma unroll
   for (int j = 0; j < kOwn; j++) {
-    const float v = xs[j * kThreads + tid];
+    const float v = x.v[j];
     const int b = info.mode == kMinP ? -1 : min(info.top_step - step(v), kSteps - 1);
     if (!(v > -__builtin_inff()) || b > info.step) continue;
     if (b == info.step || info.mode == kTopK) {
@@ -711,11 +760,13 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const SampleArgs A, co
   __syncthreads();
   to += base;
   uint64_t *gathered = W.gathered + (int64_t)rel * kGather;
-#pragma unroll 1
-  for (; mine; mine &= mine - 1, to++) {
-    const int i = __builtin_ctz(mine) * kThreads + tid;
-    if (to < kGather) gathered[to] = (uint64_t)key_of(xs[i]) << 32 | (uint32_t)~(seg * kSeg + i);
-  }
+  if (mine == 0) return;
+#pragma unroll
+  for (int j = 0; j < kOwn; j++)
+    if (mine >> j & 1) {
+      if (to < kGather) gathered[to] = (uint64_t)key_of(x.v[j]) << 32 | (uint32_t)~(seg * kSeg + x.at(j));
+      to++;
+    }
 }
 
 // Sorts n <= kSort words in descending order (room behind them for the next
@@ -742,25 +793,39 @@ __device__ __forceinline__ void sort_equal(uint64_t *v, int n) {
 // The same for up to kSort / 2 words, `other` with room for as many: by kLast equal
 // parts of the range between the least and the largest logit, and within a part by
 // counting larger ones; where a part holds many (nearly equal logits) as above.
-__device__ __forceinline__ void sort_down(uint64_t *v, uint64_t *other, int n, float *froom, double *room) {
+__device__ __forceinline__ void sort_down(uint64_t *v, uint64_t *other, int n, double *room) {
   constexpr int kCrowd = 64;
-  __shared__ int count[kLast], next[kLast];
+  __shared__ int count[kLast], next[kLast], crowded;
+  __shared__ float ends[kLast / 64][2];
   const int tid = threadIdx.x;
   float lo = __builtin_inff(), hi = -__builtin_inff();
   for (int i = tid; i < n; i += kLast) {
     lo = fminf(lo, logit_of(v[i]));
     hi = fmaxf(hi, logit_of(v[i]));
   }
+  hi = tqdev::wave_max64(hi);
+  lo = -tqdev::wave_max64(-lo);
+  if ((tid & 63) == 0) {
+    ends[tid >> 6][0] = lo;
+    ends[tid >> 6][1] = hi;
+  }
   count[tid] = 0;
-  hi = block_most<kLast>(hi, froom);
-  lo = -block_most<kLast>(-lo, froom);
+  if (tid == 0) crowded = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kLast / 64; i++) {
+    lo = fminf(lo, ends[i][0]);
+    hi = fmaxf(hi, ends[i][1]);
+  }
   const float per = hi > lo ? (float)kLast / (hi - lo) : 0.0f;
   auto part = [&](uint64_t e) { return (int)fminf(fmaxf((hi - logit_of(e)) * per, 0.0f), (float)(kLast - 1)); };
   for (int i = tid; i < n; i += kLast) atomicAdd(&count[part(v[i])], 1);
   __syncthreads();
   const int mine = count[tid];
+  if (mine > kCrowd) crowded = 1;
   next[tid] = (int)block_before<kLast>((double)mine, room);
-  if (block_most<kLast>((float)mine, froom) > (float)kCrowd) {
+  __syncthreads();
+  if (crowded) {
     sort_equal(v, n);
     return;
   }
@@ -793,9 +858,8 @@ __device__ __forceinline__ void sort_few(uint64_t *v, int n) {
 template <typename T>
 __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const SampleWs W) {
   __shared__ __attribute__((aligned(16))) uint64_t list[kSort];
-  __shared__ double room[kLast / 64], seg_sum[kMaxSegs], table[kParts], left_of;
-  __shared__ float froom[kLast / 64];
-  __shared__ unsigned long long extra[kMaxSegs], fine[kSteps];
+  __shared__ double room[kLast / 64], seg_sum[kMaxSegs], table[kParts], left_of, one[64];
+  __shared__ unsigned long long extra[kMaxSegs], fine[kSteps], cell[kSeg / 64];
   __shared__ int found, base, last, kept;
   const int tid = threadIdx.x, segs = A.segs, rel = blockIdx.x, row = A.row0 + rel;
   const RowInfo info = W.info[rel];
@@ -811,6 +875,10 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
     extra[tid] = 0;
   }
   if (tid < kSteps) fine[tid] = 0;
+  if (tid < 64) {
+    cell[tid] = 0;
+    one[tid] = 0.0;
+  }
   if (tid == 0) {
     kept = kGather;
     base = kSteps;
@@ -821,9 +889,11 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
     W.info[rel] = RowInfo{0, 0.0f, 0, 0, 0.0};
     W.found[rel] = 0;
   }
+  // (what weighs something has a step: with u of 1 the last kept token is taken)
+  auto steps_of = [&](double w) { return (unsigned long long)max(fixed(w, kFixed), (uint64_t)1); };
   auto keep = [&](uint64_t entry) {
     const double w = weigh(logit_of(entry));
-    if (w >= rule.min_p) atomicAdd(&extra[(int)~(uint32_t)entry / kSeg], (unsigned long long)fixed(w, kFixed));
+    if (w > 0.0 && w >= rule.min_p) atomicAdd(&extra[(int)~(uint32_t)entry / kSeg], steps_of(w));
   };
   double left = info.left;
   bool alone = info.mode == kAlone || n > kGather;
@@ -837,9 +907,13 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
     const Steps step(rule, info.mode);
     auto part = [&](uint64_t entry) { return step.part(logit_of(entry), info.top_step - info.step); };
     const bool weights = info.mode == kTopP;
-    for (int i = tid; i < n; i += kLast) {
-      const uint64_t e = gathered[i];
-      atomicAdd(&fine[part(e)], weights ? (unsigned long long)fixed(weigh(logit_of(e)), kFixed) : 1ull);
+    uint64_t own[kGather / kLast];  // all sent for at once
+#pragma unroll
+    for (int i = 0; i < kGather / kLast; i++) own[i] = i * kLast + tid < n ? gathered[i * kLast + tid] : 0;
+#pragma unroll
+    for (int i = 0; i < kGather / kLast; i++) {
+      const uint64_t e = own[i];
+      if (e) atomicAdd(&fine[part(e)], weights ? (unsigned long long)fixed(weigh(logit_of(e)), kFixed) : 1ull);
     }
     __syncthreads();
     const double have = tid < kSteps ? (double)fine[tid] / (weights ? kFixed : 1.0) : 0.0, before = block_before<kLast>(have, room);
@@ -853,9 +927,10 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
     if (tid == at_part) left_of = left - before;
     __syncthreads();
     left = left_of;
-    for (int i = tid; i < n; i += kLast) {
-      const uint64_t e = gathered[i];
-      const int q = part(e);
+#pragma unroll
+    for (int i = 0; i < kGather / kLast; i++) {
+      const uint64_t e = own[i];
+      const int q = e ? part(e) : kSteps;
       if (q < at_part) keep(e);
       if (q == at_part) {
         const int k = atomicAdd(&found, 1);
@@ -874,18 +949,43 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
   Cut cut = {0, -1};
   if (info.mode != kMinP) {
     if (m > kSort / 2) sort_equal(list, m);
-    else if (m > 64) sort_down(list, list + kSort / 2, m, froom, room);
+    else if (m > 64) sort_down(list, list + kSort / 2, m, room);
     else sort_few(list, m);
-    // the limits, kLast sorted tokens at a time (a second time for top-p of top-k)
-    const int top = info.mode == kTopK ? min(rule.top_k, m) : info.mode == kManyK ? min((int)left, m) : m;
+    if (info.mode == kTopK) {
+      // all tokens that may be kept are in the list, one a thread: the limit, the
+      // segment, its 64 tokens and the token by their sums alone
+      const int top = min(rule.top_k, m);
+      const uint64_t entry = tid < top ? list[tid] : 0;
+      double w = tid < top ? weigh(logit_of(entry)) : 0.0;
+      if (rule.top_p < 1.0) {
+        double all;
+        const double c = block_before<kLast>(w, room, &all);
+        if (tid > 0 && tid < top && c >= rule.top_p * all) atomicMin(&kept, tid);  // the first that is not needed
+        __syncthreads();
+        if (tid >= kept) w = 0.0;
+      }
+      if (!(w >= rule.min_p)) w = 0.0;
+      const int index = (int)~(uint32_t)entry;
+      if (w > 0.0) atomicAdd(&extra[index / kSeg], steps_of(w));
+      __syncthreads();
+      if (tid < segs) seg_sum[tid] = (double)extra[tid] / kFixed;
+      __syncthreads();
+      double from, target, total;
+      const int seg = find_segment(A.u[row], segs, seg_sum, from, target, total);
+      if (w > 0.0 && index / kSeg == seg) atomicAdd(&cell[index % kSeg / 64], steps_of(w));
+      __syncthreads();
+      const int at = seg * (kSeg / 64) + crossing((double)cell[tid & 63] / kFixed, from, target, from);
+      if (w > 0.0 && index / 64 == at) one[index % 64] = w;
+      __syncthreads();
+      const int l = crossing(one[tid & 63], from, target, from);
+      if (tid == 0) answer(A, row, at * 64 + l, one[l], total);
+      return;
+    }
+    // the limit, kLast sorted tokens at a time
+    const int top = info.mode == kManyK ? min((int)left, m) : m;
     int keeps = top;
     if (rule.top_p < 1.0) {
-      double target = left;
-      if (info.mode == kTopK) {
-        double sum = 0.0;
-        for (int i = tid; i < top; i += kLast) sum += weigh(logit_of(list[i]));
-        target = rule.top_p * block_sum<kLast>(sum, room);
-      }
+      const double target = left;
       double before = 0.0;
 #pragma unroll 1
       for (int i0 = 0; i0 < top; i0 += kLast) {
