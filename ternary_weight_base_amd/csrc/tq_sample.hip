@@ -23,6 +23,7 @@ namespace {
 constexpr int kSeg = 4096;           // tokens of a segment
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxSegs = kMaxVocab / kSeg;
+constexpr int kParts = 64;           // of a power of two, in the table of weights
 
 struct SampleArgs {
   const void *logits;
@@ -38,7 +39,7 @@ struct SampleArgs {
 
 // A row's settings.
 struct Rule {
-  double per;       // log2 e / temperature
+  double per;       // 64 log2 e / temperature
   double top_p, min_p;
   int top_k;        // vocab: all
   bool greedy;
@@ -48,7 +49,7 @@ __device__ __forceinline__ Rule rule_of(const SampleArgs &A, int row) {
   Rule r;
   const float t = A.temperature ? A.temperature[row] : 1.0f;
   r.greedy = !(t > 0.0f);
-  r.per = r.greedy ? 0.0 : 1.4426950408889634 / (double)t;
+  r.per = r.greedy ? 0.0 : kParts * 1.4426950408889634 / (double)t;
   const int k = A.top_k ? A.top_k[row] : 0;
   r.top_k = k > 0 ? min(k, A.vocab) : A.vocab;
   const float p = A.top_p ? A.top_p[row] : 1.0f;
@@ -67,17 +68,17 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// 2^t for t <= 0, to some 2^-51 of it; 0 from 2^-1000 on (and for -inf, NaN): a
+// 2^(t / 64) for t <= 0, to some 2^-51 of it; 0 from 2^-1000 on (and for -inf, NaN): a
 // power of two, a 64th of one from a table in LDS and exp's series up to its fifth
-// power for the rest, |r| <= 0.0055 (the next term is below 2^-54).
-constexpr int kParts = 64;
+// power for the rest, up to (ln 2) / 128 (the next term is below 2^-54).
 __device__ __forceinline__ double power2(double t, const double *table) {
-  if (!(t > -1000.0)) return 0.0;
-  const double n = rint(t * kParts), r = (t - n * (1.0 / kParts)) * 0.6931471805599453;
+  constexpr double c = 0.6931471805599453 / kParts;
+  const double u = fmax(t, -1100.0 * kParts), n = rint(u), r = u - n;
   const int k = (int)n;
-  const double r2 = r * r;
-  const double s = fma(fma(fma(1.0 / 120.0, r, 1.0 / 24.0), r2, fma(1.0 / 6.0, r, 0.5)), r2, 1.0 + r);
-  return ldexp(s * table[k & (kParts - 1)], k >> 6);
+  const double s = fma(r, fma(r, fma(r, fma(r, fma(r, c * c * c * c * c / 120.0, c * c * c * c / 24.0), c * c * c / 6.0), c * c / 2.0), c), 1.0);
+  // (the power of two goes into the exponent: no result is below 2^-1001)
+  const uint64_t b = __builtin_bit_cast(uint64_t, s * table[k & (kParts - 1)]) + ((uint64_t)((uint32_t)(k >> 6) << 20) << 32);
+  return t > -1000.0 * kParts ? __builtin_bit_cast(double, b) : 0.0;
 }
 
 // The table, 2^(i / 64): exp's series at up to 0.3466, whose 14th term is below 2^-57.
@@ -113,7 +114,7 @@ struct Weigher {
   const double *table;
   __device__ __forceinline__ double operator()(float x) const {
     if (most == __builtin_inff()) return x == most ? 1.0 : 0.0;
-    return x == -__builtin_inff() ? 0.0 : power2(((double)x - (double)most) * per, table);
+    return power2(((double)x - (double)most) * per, table);  // (-inf: 0)
   }
 };
 
@@ -442,22 +443,30 @@ __global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
 //  - a row without limits gets its token; else the step is found in which the
 //    limit falls;
 //  - the tokens of that step (top-k up to kFewK: of all steps down to it) are
-//    gathered, and each segment's weights in the steps above summed;
-//  - the gathered ones are narrowed down by a finer step, what is left is sorted and
+//    gathered, with their weights and 256ths of the step, and each segment's weights
+//    in the steps above summed;
+//  - the gathered ones are narrowed down by the 256ths, what is left is sorted and
 //    cut, and the token taken.
 // A row that gathers more than kGather tokens or has more than kSort left (flat
 // logits), or has a larger top_k and top_p too, is done by the last launch's
-// workgroup alone, as above.  (Instead of the launches for a row, the last of its
+// workgroup alone, as above.  Bound: a row's workgroups by their instructions (a CU
+// issues one a cycle) and dependent trips to memory, the segments' for many rows by
+// the weights in double (64 rows of 131072 by top-p: 18 us, by top-k, which needs none
+// there, 9, reading 34 MB).  (Instead of the launches for a row, the last of its
 // segments' workgroups did their work at first: 64 against 51 us for 64 rows, since
 // what it meets in had to be written past the caches and its room in LDS was
 // every workgroup's.)
 
 constexpr int kThreads = 256, kOwn = kSeg / kThreads;
-constexpr int kLast = 1024;     // threads of the last launch
+constexpr int kLast = 512;      // threads of the last launch (one row 22 us; 1024: 23, 256: 24)
 constexpr int kSteps = 256;     // the last one: everything below the others
 constexpr int kGather = 16384;  // tokens of a row
 constexpr int kSort = 4096;     // ... of them sorted
 constexpr int kFewK = 1024;
+// Threads of the second launch, steps that they take at once (256 threads: 64 rows by
+// top-p 55 against 51 us; 1024: 53, and one row 22 against 21).
+constexpr int kLimit = 512, kQuarters = 4, kTogether = kLimit / kQuarters;
+constexpr int kLine = 32;       // words of a cache line
 constexpr double kFixed = 0x1p48;  // weights as integers: kGather of them stay in 62 bits
 
 enum Mode { kDone = 0, kTopK, kManyK, kTopP, kMinP, kAlone };
@@ -489,10 +498,11 @@ struct SampleWs {
   RowInfo *info;
   SegInfo *seg;
   double *seg_sum;
-  uint32_t *found;     // a row's gathered tokens
+  uint32_t *found;     // a row's gathered tokens, a cache line each (one line for 32 rows: 24 against 14 us)
   uint32_t *count;     // [row][segment][step]
   uint64_t *weight;
   uint64_t *gathered;  // [row][kGather]: key, then the index's complement
+  uint64_t *worth;     // ... with its 256th of the step, whether it reaches min_p, its weight (kTopP, kManyK)
 };
 
 // The steps are of an eighth of a logit (for top-p of the temperature, where that
@@ -501,7 +511,7 @@ struct SampleWs {
 struct Steps {
   float per;
   __device__ __forceinline__ Steps(const Rule &r, int mode)
-      : per(mode == kTopP ? fminf(8.0f * fmaxf((float)(r.per * 0.6931471805599453), 1.0f), 1e30f) : 8.0f) {}
+      : per(mode == kTopP ? fminf(8.0f * fmaxf((float)(r.per * (0.6931471805599453 / kParts)), 1.0f), 1e30f) : 8.0f) {}
   __device__ __forceinline__ int operator()(float x) const { return (int)floorf(fminf(fmaxf(x * per, -1e9f), 1e9f)); }
   // the 256th of step `at` (of the grid) that x lies in, from its upper end; below the step: the last
   __device__ __forceinline__ int part(float x, int at) const {
@@ -547,6 +557,18 @@ struct Own {
       for (int i = 0; i < kOwn; i++) v[i] = clean((float)w[i]);
     }
   }
+  // Four at a time, the next ones moved down: f(value, number in the thread).  (All
+  // at once are so much code that fetching it takes longer than the moves.)
+  template <typename F>
+  __device__ __forceinline__ void each(const F &f) {
+#pragma unroll 1
+    for (int g = 0; g < kOwn; g += 4) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) f(v[j], g + j);
+#pragma unroll
+      for (int j = 4; j < kOwn; j++) v[j - 4] = v[j];
+    }
+  }
   // the place of the j-th in the segment
   __device__ __forceinline__ int at(int j) const {
     const int tid = threadIdx.x;
@@ -563,7 +585,7 @@ __global__ __launch_bounds__(kThreads) void segment_kernel(const SampleArgs A, c
   __shared__ int where;
   const int tid = threadIdx.x, segs = A.segs;
   const int rel = blockIdx.x / (uint32_t)segs, seg = blockIdx.x % (uint32_t)segs, row = A.row0 + rel;
-  const Own<T> x(A, row, seg);
+  Own<T> x(A, row, seg);
   const Rule rule = rule_of(A, row);
   const int mode = mode_of(A, rule);
   const Steps step(rule, mode);
@@ -588,39 +610,34 @@ __global__ __launch_bounds__(kThreads) void segment_kernel(const SampleArgs A, c
     mine.index = where;
   } else if (mode == kDone) {
     double sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < kOwn; j++) sum += weigh(x.v[j]);
+    x.each([&](float v, int) { sum += weigh(v); });
     mine.sum = block_sum<kThreads>(sum, room);
   } else if (mode == kTopK || mode == kManyK || mode == kTopP) {
     // (a thread's run of the same step is added at once: equal logits would queue)
     const int top = step(most);
+    const bool weights = mode == kTopP;
     int run = -1;
-    uint32_t n = 0;
     unsigned long long sum = 0;
     auto add = [&]() {
       if (run < 0) return;
-      atomicAdd(&count[run], n);
-      if (mode == kTopP) atomicAdd(&weight[run], sum);
+      if (weights) atomicAdd(&weight[run], sum);
+      else atomicAdd(&count[run], (uint32_t)sum);
     };
-#pragma unroll
-    for (int j = 0; j < kOwn; j++) {
-      const float v = x.v[j];
-      if (v > -__builtin_inff()) {
-        const int b = min(top - step(v), kSteps - 1);
-        if (b != run) {
-          add();
-          run = b;
-          n = 0;
-          sum = 0;
-        }
-        n++;
-        if (mode == kTopP) sum += fixed(weigh(v), kFixed);
+    x.each([&](float v, int) {
+      if (!(v > -__builtin_inff())) return;
+      const int b = min(top - step(v), kSteps - 1);
+      if (b != run) {
+        add();
+        run = b;
+        sum = 0;
       }
-    }
+      sum += weights ? fixed(weigh(v), kFixed) : 1ull;
+    });
     add();
     __syncthreads();
-    W.count[at * kSteps + tid] = count[tid];
-    if (mode == kTopP) {
+    if (!weights) {
+      W.count[at * kSteps + tid] = count[tid];
+    } else {
       W.weight[at * kSteps + tid] = weight[tid];
       mine.sum = block_sum<kThreads>((double)weight[tid] / kFixed, room);
     }
@@ -629,11 +646,11 @@ __global__ __launch_bounds__(kThreads) void segment_kernel(const SampleArgs A, c
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void limit_kernel(const SampleArgs A, const SampleWs W) {
+__global__ __launch_bounds__(kLimit) void limit_kernel(const SampleArgs A, const SampleWs W) {
   __shared__ __attribute__((aligned(16))) float xs[kSeg];
-  __shared__ double room[kThreads / 64], seg_sum[kMaxSegs], share[kMaxSegs], part[kThreads / 64][64], table[kParts];
-  __shared__ float froom[kThreads / 64];
-  __shared__ int seg_step[kMaxSegs], where;
+  __shared__ double room[kLimit / 64], seg_sum[kMaxSegs], share[kMaxSegs], part[kQuarters][kTogether], upto[kTogether], table[kParts];
+  __shared__ float froom[kLimit / 64];
+  __shared__ int seg_step[kMaxSegs], first[kTogether / 64], where;
   const int tid = threadIdx.x, segs = A.segs, rel = blockIdx.x, row = A.row0 + rel;
   SegInfo mine = {-__builtin_inff(), 0, 0.0};
   if (tid < segs) mine = W.seg[(int64_t)rel * segs + tid];
@@ -642,16 +659,18 @@ __global__ __launch_bounds__(kThreads) void limit_kernel(const SampleArgs A, con
   const Steps step(rule, mode);
   fill_table(table);
   if (tid == 0) where = 0x7fffffff;
-  const float most = block_most<kThreads>(mine.most, froom);
+  const float most = block_most<kLimit>(mine.most, froom);
   const bool none = most == -__builtin_inff();
   const Weigher weigh = {most, rule.per, table};
   const int top = step(most);
   if (tid < segs) {
-    W.seg[(int64_t)rel * segs + tid] = SegInfo{0.0f, 0, 0.0};
     share[tid] = weigh(mine.most);  // of a segment's unit
     seg_sum[tid] = mine.sum * share[tid];
     // (a segment without a token that may come counts from far below)
     seg_step[tid] = mine.most == -__builtin_inff() ? 2 * kSteps : min(top - step(mine.most), 2 * kSteps);
+    // (the next launch takes, and clears, what it needs to sum the weights above a step)
+    const bool more = mode == kTopP && !none;
+    W.seg[(int64_t)rel * segs + tid] = SegInfo{0.0f, more ? seg_step[tid] : 0, more ? share[tid] : 0.0};
     if (mine.most == most) atomicMin(&where, mine.index);
   }
   __syncthreads();
@@ -660,51 +679,59 @@ __global__ __launch_bounds__(kThreads) void limit_kernel(const SampleArgs A, con
     return;
   }
   if (mode == kDone) {
-    choose<T, kThreads>(A, row, segs, seg_sum, weigh, Cut{0, -1}, 0.0, xs);
+    choose<T, kLimit>(A, row, segs, seg_sum, weigh, Cut{0, -1}, 0.0, xs);
     return;
   }
   RowInfo info = {mode, most, kSteps - 1, top, 0.0};
   if (mode == kTopK || mode == kManyK || mode == kTopP) {
-    // 64 steps at a time (mostly the first ones are enough), a lane each: the
-    // segments' contents are summed by the waves in turn
+    // kTogether steps at a time (mostly the first ones are enough, and one workgroup
+    // reads them slowly), a thread a step and a quarter of the segments
     const uint32_t *c = W.count + (int64_t)rel * segs * kSteps;
     const uint64_t *w = W.weight + (int64_t)rel * segs * kSteps;
-    const int lane = tid & 63, wave = tid >> 6;
+    const int at = tid % kTogether, quarter = tid / kTogether;
     double target = (double)rule.top_k, before = 0.0;
-    if (mode == kTopP) target = rule.top_p * block_sum<kThreads>(tid < segs ? seg_sum[tid] : 0.0, room);
+    if (mode == kTopP) target = rule.top_p * block_sum<kLimit>(tid < segs ? seg_sum[tid] : 0.0, room);
 #pragma unroll 1
-    for (int s0 = 0; s0 < kSteps; s0 += 64) {
-      const int t = s0 + lane;
+    for (int s0 = 0; s0 < kSteps; s0 += kTogether) {
+      const int t = s0 + at;
       double have = 0.0;
       if (mode == kTopP) {
 #pragma unroll 8
-        for (int i = wave; i < segs; i += kThreads / 64) {
+        for (int i = quarter; i < segs; i += kQuarters) {
           const int b = t - seg_step[i];
           const uint64_t v = w[i * kSteps + max(b, 0)];
           have += b >= 0 ? (double)v / kFixed * share[i] : 0.0;
         }
       } else {
 #pragma unroll 8
-        for (int i = wave; i < segs; i += kThreads / 64) {
+        for (int i = quarter; i < segs; i += kQuarters) {
           const int b = t - seg_step[i];
           const uint32_t v = c[i * kSteps + max(b, 0)];
           have += b >= 0 ? (double)v : 0.0;
         }
       }
-      part[wave][lane] = have;
+      part[quarter][at] = have;
       __syncthreads();
-      have = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+      have = 0.0;
+      // (the last step is not whole: other segments' last steps belong to it too)
+      if (tid < kTogether && t < kSteps - 1) have = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+      double all;
+      const double from = before + block_before<kLimit>(have, room, &all);
+      const uint64_t there = __ballot(have > 0.0 && from + have >= target);
+      if (tid < kTogether) {
+        if ((tid & 63) == 0) first[tid / 64] = there ? tid + __builtin_ctzll(there) : kTogether;
+        upto[tid] = from;
+      }
       __syncthreads();
-      if (t == kSteps - 1) have = 0.0;  // (not whole: other segments' last steps belong to it too)
-      const double upto = before + wave_upto(have);
-      const uint64_t there = __ballot(have > 0.0 && upto >= target);
-      if (there) {
-        const int l = __builtin_ctzll(there);
-        info.step = s0 + l;
-        before = lane_value(upto - have, l);
+      int to = kTogether;
+#pragma unroll
+      for (int i = 0; i < kTogether / 64; i++) to = min(to, first[i]);
+      if (to < kTogether) {
+        info.step = s0 + to;
+        before = upto[to];
         break;
       }
-      before = lane_value(upto, 63);  // (nothing above reaches the target: the last step)
+      before += all;  // (nothing above reaches the target: the last step)
     }
     info.left = target - before;
   }
@@ -716,6 +743,11 @@ __device__ __forceinline__ float logit_of(uint64_t entry) {  // of a key and ind
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// A weight in steps; what weighs something has one, so that with u of 1 the last kept
+// token is taken.
+__device__ __forceinline__ uint64_t steps_of(double w) { return max(fixed(w, kFixed), (uint64_t)1); }
+constexpr int kPartBit = 56, kKeepBit = 55;  // above a weight of at most 2^48 steps
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void gather_kernel(const SampleArgs A, const SampleWs W) {
   __shared__ double room[kThreads / 64], table[kParts];
@@ -725,29 +757,43 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const SampleArgs A, co
   const RowInfo info = W.info[rel];
   if (info.mode == kDone || info.mode == kAlone) return;
   const int64_t at = (int64_t)rel * segs + seg;
-  const Own<T> x(A, row, seg);
+  Own<T> x(A, row, seg);
   const Rule rule = rule_of(A, row);
   const Steps step(rule, info.mode);
   const Weigher weigh = {info.most, rule.per, table};
-  if (info.mode != kMinP) {
+  // the weights above the step: of top-p from the segment's steps, else one by one
+  const bool by_steps = info.mode == kTopP && rule.min_p == 0.0;
+  double sum = 0.0;
+  if (info.mode == kTopP) {
+    const SegInfo mine = W.seg[at];
+    if (tid < info.step - mine.index) sum = (double)W.weight[at * kSteps + tid] / kFixed * mine.sum;
+    if (!by_steps) sum = 0.0;
+    W.weight[at * kSteps + tid] = 0;
+  } else if (info.mode != kMinP) {
     W.count[at * kSteps + tid] = 0;
-    if (info.mode == kTopP) W.weight[at * kSteps + tid] = 0;
   }
   if (info.mode != kTopK) fill_table(table);
   __syncthreads();
-  double sum = 0.0;
+  if (info.mode == kTopP && tid == 0) W.seg[at] = SegInfo{0.0f, 0, 0.0};
   uint32_t mine = 0;  // this thread's tokens that are gathered
+  if (info.mode == kTopK || by_steps) {
 #pragma unroll
-  for (int j = 0; j < kOwn; j++) {
-    const float v = x.v[j];
-    const int b = info.mode == kMinP ? -1 : min(info.top_step - step(v), kSteps - 1);
-    if (!(v > -__builtin_inff()) || b > info.step) continue;
-    if (b == info.step || info.mode == kTopK) {
-      mine |= 1u << j;
-    } else {
-      const double w = weigh(v);
-      if (w >= rule.min_p) sum += w;
+    for (int j = 0; j < kOwn; j++) {
+      const int b = min(info.top_step - step(x.v[j]), kSteps - 1);
+      if (x.v[j] > -__builtin_inff() && (info.mode == kTopK ? b <= info.step : b == info.step)) mine |= 1u << j;
     }
+  } else {
+    Own<T> y = x;
+    y.each([&](float v, int j) {
+      const int b = info.mode == kMinP ? -1 : min(info.top_step - step(v), kSteps - 1);
+      if (!(v > -__builtin_inff()) || b > info.step) return;
+      if (b == info.step) {
+        mine |= 1u << j;
+      } else {
+        const double w = weigh(v);
+        if (w >= rule.min_p) sum += w;
+      }
+    });
   }
   if (info.mode != kTopK) {
     sum = block_sum<kThreads>(sum, room);
@@ -756,17 +802,25 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const SampleArgs A, co
   double all;
   int to = (int)block_before<kThreads>((double)__popc(mine), room, &all);
   if (all == 0.0) return;
-  if (tid == 0) base = (int)atomicAdd(W.found + rel, (uint32_t)all);
+  if (tid == 0) base = (int)atomicAdd(W.found + rel * kLine, (uint32_t)all);
   __syncthreads();
   to += base;
   uint64_t *gathered = W.gathered + (int64_t)rel * kGather;
-  if (mine == 0) return;
+  uint64_t *worth = W.worth + (int64_t)rel * kGather;
 #pragma unroll
   for (int j = 0; j < kOwn; j++)
     if (mine >> j & 1) {
       if (to < kGather) gathered[to] = (uint64_t)key_of(x.v[j]) << 32 | (uint32_t)~(seg * kSeg + x.at(j));
       to++;
     }
+  if (info.mode == kTopK) return;
+  // (their weights once they lie next to each other: few lanes have one at the same j)
+  __syncthreads();
+  for (int i = base + tid; i < min(base + (int)all, kGather); i += kThreads) {
+    const float v = logit_of(gathered[i]);
+    const double w = weigh(v);
+    worth[i] = (uint64_t)step.part(v, info.top_step - info.step) << kPartBit | (uint64_t)(w > 0.0 && w >= rule.min_p) << kKeepBit | steps_of(w);
+  }
 }
 
 // Sorts n <= kSort words in descending order (room behind them for the next
@@ -858,16 +912,16 @@ __device__ __forceinline__ void sort_few(uint64_t *v, int n) {
 template <typename T>
 __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const SampleWs W) {
   __shared__ __attribute__((aligned(16))) uint64_t list[kSort];
-  __shared__ double room[kLast / 64], seg_sum[kMaxSegs], table[kParts], left_of, one[64];
+  __shared__ double room[kLast / 64], seg_sum[kMaxSegs], table[kParts], one[64], upto[kSteps];
   __shared__ unsigned long long extra[kMaxSegs], fine[kSteps], cell[kSeg / 64];
-  __shared__ int found, base, last, kept;
+  __shared__ int found, kept, first[kSteps / 64], last[kSteps / 64];
   const int tid = threadIdx.x, segs = A.segs, rel = blockIdx.x, row = A.row0 + rel;
   const RowInfo info = W.info[rel];
   if (info.mode == kDone) return;
-  const int n = (int)W.found[rel];
+  const int n = (int)W.found[rel * kLine];
   const Rule rule = rule_of(A, row);
   const Weigher weigh = {info.most, rule.per, table};
-  uint64_t *gathered = W.gathered + (int64_t)rel * kGather;
+  uint64_t *gathered = W.gathered + (int64_t)rel * kGather, *worth = W.worth + (int64_t)rel * kGather;
   fill_table(table);
   if (tid < segs) {
     seg_sum[tid] = W.seg_sum[(int64_t)rel * segs + tid];
@@ -881,19 +935,16 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
   }
   if (tid == 0) {
     kept = kGather;
-    base = kSteps;
-    last = found = 0;
+    found = 0;
   }
   __syncthreads();
   if (tid == 0) {
     W.info[rel] = RowInfo{0, 0.0f, 0, 0, 0.0};
-    W.found[rel] = 0;
+    W.found[rel * kLine] = 0;
   }
-  // (what weighs something has a step: with u of 1 the last kept token is taken)
-  auto steps_of = [&](double w) { return (unsigned long long)max(fixed(w, kFixed), (uint64_t)1); };
   auto keep = [&](uint64_t entry) {
     const double w = weigh(logit_of(entry));
-    if (w > 0.0 && w >= rule.min_p) atomicAdd(&extra[(int)~(uint32_t)entry / kSeg], steps_of(w));
+    if (w > 0.0 && w >= rule.min_p) atomicAdd(&extra[(int)~(uint32_t)entry / kSeg], (unsigned long long)steps_of(w));
   };
   double left = info.left;
   bool alone = info.mode == kAlone || n > kGather;
@@ -904,34 +955,36 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
     __syncthreads();
   } else if (!alone) {
     // by 256ths of the step: those above the one in which the limit falls are kept
-    const Steps step(rule, info.mode);
-    auto part = [&](uint64_t entry) { return step.part(logit_of(entry), info.top_step - info.step); };
     const bool weights = info.mode == kTopP;
-    uint64_t own[kGather / kLast];  // all sent for at once
-#pragma unroll
-    for (int i = 0; i < kGather / kLast; i++) own[i] = i * kLast + tid < n ? gathered[i * kLast + tid] : 0;
-#pragma unroll
-    for (int i = 0; i < kGather / kLast; i++) {
-      const uint64_t e = own[i];
-      if (e) atomicAdd(&fine[part(e)], weights ? (unsigned long long)fixed(weigh(logit_of(e)), kFixed) : 1ull);
+    constexpr uint64_t kWeight = ((uint64_t)1 << kKeepBit) - 1;
+#pragma unroll 4
+    for (int i = tid; i < n; i += kLast) {
+      const uint64_t v = worth[i];
+      atomicAdd(&fine[v >> kPartBit], weights ? (unsigned long long)(v & kWeight) : 1ull);
     }
     __syncthreads();
     const double have = tid < kSteps ? (double)fine[tid] / (weights ? kFixed : 1.0) : 0.0, before = block_before<kLast>(have, room);
-    // (where roundings of the sums leave the limit unreached: the last one there is)
-    if (have > 0.0) {
-      if (before + have >= left) atomicMin(&base, tid);
-      atomicMax(&last, tid);
+    const uint64_t some = __ballot(have > 0.0), there = __ballot(have > 0.0 && before + have >= left);
+    if (tid < kSteps) upto[tid] = before;
+    if (tid < kSteps && (tid & 63) == 0) {
+      first[tid / 64] = there ? tid + __builtin_ctzll(there) : kSteps;
+      last[tid / 64] = some ? tid + 63 - __builtin_clzll(some) : 0;
     }
     __syncthreads();
-    const int at_part = base < kSteps ? base : last;
-    if (tid == at_part) left_of = left - before;
-    __syncthreads();
-    left = left_of;
+    // (where roundings of the sums leave the limit unreached: the last one there is)
+    int at_part = kSteps, end = 0;
 #pragma unroll
-    for (int i = 0; i < kGather / kLast; i++) {
-      const uint64_t e = own[i];
-      const int q = e ? part(e) : kSteps;
-      if (q < at_part) keep(e);
+    for (int i = 0; i < kSteps / 64; i++) {
+      at_part = min(at_part, first[i]);
+      end = max(end, last[i]);
+    }
+    if (at_part == kSteps) at_part = end;
+    left -= upto[at_part];
+#pragma unroll 4
+    for (int i = tid; i < n; i += kLast) {
+      const uint64_t v = worth[i], e = gathered[i];
+      const int q = (int)(v >> kPartBit);
+      if (q < at_part && (v >> kKeepBit & 1)) atomicAdd(&extra[(int)~(uint32_t)e / kSeg], (unsigned long long)(v & kWeight));
       if (q == at_part) {
         const int k = atomicAdd(&found, 1);
         if (k < kSort) list[k] = e;
@@ -942,6 +995,8 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
     alone = m > kSort;
   }
   for (int i = tid; i < min(n, kGather); i += kLast) gathered[i] = 0;
+  if (info.mode != kTopK)
+    for (int i = tid; i < min(n, kGather); i += kLast) worth[i] = 0;
   if (alone) {
     whole_row<T, kLast>(A, row, table, reinterpret_cast<float *>(list));
     return;
@@ -955,27 +1010,51 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
       // all tokens that may be kept are in the list, one a thread: the limit, the
       // segment, its 64 tokens and the token by their sums alone
       const int top = min(rule.top_k, m);
-      const uint64_t entry = tid < top ? list[tid] : 0;
-      double w = tid < top ? weigh(logit_of(entry)) : 0.0;
-      if (rule.top_p < 1.0) {
-        double all;
-        const double c = block_before<kLast>(w, room, &all);
-        if (tid > 0 && tid < top && c >= rule.top_p * all) atomicMin(&kept, tid);  // the first that is not needed
-        __syncthreads();
-        if (tid >= kept) w = 0.0;
+      constexpr int kPer = kFewK / kLast;
+      int index[kPer];
+      double w[kPer], own = 0.0;
+#pragma unroll
+      for (int j = 0; j < kPer; j++) {
+        const int i = tid * kPer + j;
+        const uint64_t entry = i < top ? list[i] : 0;
+        index[j] = (int)~(uint32_t)entry;
+        w[j] = i < top ? weigh(logit_of(entry)) : 0.0;
+        own += w[j];
       }
-      if (!(w >= rule.min_p)) w = 0.0;
-      const int index = (int)~(uint32_t)entry;
-      if (w > 0.0) atomicAdd(&extra[index / kSeg], steps_of(w));
+      if (rule.top_p < 1.0) {
+        double all, c = block_before<kLast>(own, room, &all);
+        int spare = kGather;  // the first that is not needed
+#pragma unroll
+        for (int j = 0; j < kPer; j++) {
+          const int i = tid * kPer + j;
+          if (i > 0 && i < top && c >= rule.top_p * all) spare = min(spare, i);
+          c += w[j];
+        }
+        const uint64_t some = __ballot(spare < kGather);
+        if (some) {
+          spare = __builtin_amdgcn_readlane(spare, __builtin_ctzll(some));
+          if ((tid & 63) == 0) atomicMin(&kept, spare);
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < kPer; j++) {
+        if (tid * kPer + j >= kept || !(w[j] >= rule.min_p)) w[j] = 0.0;
+        if (w[j] > 0.0) atomicAdd(&extra[index[j] / kSeg], (unsigned long long)steps_of(w[j]));
+      }
       __syncthreads();
       if (tid < segs) seg_sum[tid] = (double)extra[tid] / kFixed;
       __syncthreads();
       double from, target, total;
       const int seg = find_segment(A.u[row], segs, seg_sum, from, target, total);
-      if (w > 0.0 && index / kSeg == seg) atomicAdd(&cell[index % kSeg / 64], steps_of(w));
+#pragma unroll
+      for (int j = 0; j < kPer; j++)
+        if (w[j] > 0.0 && index[j] / kSeg == seg) atomicAdd(&cell[index[j] % kSeg / 64], (unsigned long long)steps_of(w[j]));
       __syncthreads();
       const int at = seg * (kSeg / 64) + crossing((double)cell[tid & 63] / kFixed, from, target, from);
-      if (w > 0.0 && index / 64 == at) one[index % 64] = w;
+#pragma unroll
+      for (int j = 0; j < kPer; j++)
+        if (w[j] > 0.0 && index[j] / 64 == at) one[index[j] % 64] = w[j];
       __syncthreads();
       const int l = crossing(one[tid & 63], from, target, from);
       if (tid == 0) answer(A, row, at * 64 + l, one[l], total);
@@ -993,7 +1072,8 @@ __global__ __launch_bounds__(kLast) void token_kernel(const SampleArgs A, const 
         const double w = i < top ? weigh(logit_of(list[i])) : 0.0;
         double all;
         const double c = before + block_before<kLast>(w, room, &all);
-        if (i < top && i > 0 && c >= target) atomicMin(&kept, i);  // the first that is not needed
+        const uint64_t spare = __ballot(i < top && i > 0 && c >= target);
+        if (spare && (tid & 63) == 0) atomicMin(&kept, i + __builtin_ctzll(spare));  // the first that is not needed
         __syncthreads();
         if (kept < top) break;
         before += all;
@@ -1028,7 +1108,7 @@ struct Plan {
 Plan make_plan(int64_t rows, int64_t vocab) {
   Plan P = {(vocab + kSeg - 1) / kSeg, 0, 0};
   if (P.segs == 1) return P;
-  const size_t each = sizeof(RowInfo) + kGather * 8 + 4 + (size_t)P.segs * (sizeof(SegInfo) + 8 + kSteps * 12);
+  const size_t each = sizeof(RowInfo) + (kGather * 4 + kLine) * 4 + (size_t)P.segs * (sizeof(SegInfo) + 8 + kSteps * 12);
   P.pass = (int64_t)(kWsBytes / each);
   if (P.pass > rows) P.pass = rows;
   P.bytes = ((size_t)P.pass * each + 15) / 16 * 16;
@@ -1071,6 +1151,7 @@ extern "C" int tq_sample(int dtype, int64_t rows, int64_t vocab, const void *log
   W.info = (RowInfo *)p;
   W.seg = (SegInfo *)(p += n * sizeof(RowInfo));
   W.gathered = (uint64_t *)(p += ns * sizeof(SegInfo));
+  W.worth = (uint64_t *)(p += n * kGather * 8);
   W.weight = (uint64_t *)(p += n * kGather * 8);
   W.seg_sum = (double *)(p += ns * kSteps * 8);
   W.count = (uint32_t *)(p += ns * 8);
@@ -1083,7 +1164,7 @@ extern "C" int tq_sample(int dtype, int64_t rows, int64_t vocab, const void *log
 #define TQ_SAMPLE(T)                                                                  \
   {                                                                                   \
     hipLaunchKernelGGL((segment_kernel<T>), each, dim3(kThreads), 0, st, A, W);       \
-    hipLaunchKernelGGL((limit_kernel<T>), one, dim3(kThreads), 0, st, A, W);          \
+    hipLaunchKernelGGL((limit_kernel<T>), one, dim3(kLimit), 0, st, A, W);            \
     if (!limits) continue;                                                            \
     hipLaunchKernelGGL((gather_kernel<T>), each, dim3(kThreads), 0, st, A, W);        \
     hipLaunchKernelGGL((token_kernel<T>), one, dim3(kLast), 0, st, A, W);             \
