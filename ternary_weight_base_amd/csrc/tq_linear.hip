@@ -39,6 +39,7 @@ using namespace tqkv;
 
 constexpr int kChunk = 128;     // rows of a chunk
 constexpr int kStep = 64;       // ... of them that U's kernel takes at once
+constexpr int kScanRun = 8;    // chunks of a wave's run in the scan
 constexpr int kFewRows = 16;    // up to so many rows a sequence (on average): the recurrence
 constexpr size_t kPassBytes = (size_t)1 << 27;  // scratch of a pass over the chunks
 constexpr int kNoState = -100000;  // exponent of a snapshot that is zero
@@ -413,16 +414,19 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
   if (tid == 0) meta->most_u = m;
 }
 
-// The states before each chunk (fp16, scaled), and the last one: a thread has
-// four elements of a state, its next chunks' on their way.  Bound: latency, chunk
-// after chunk (32 chunks of 8 KV heads of 128, 25 MB: 14 us, without the loads or
-// without the stores 12.4; two elements a thread 14.2).
-template <int D>
-__global__ __launch_bounds__(64) void scan_kernel(const LinArgs A) {
+// The states before each chunk (fp16, scaled), and the last one: 256 elements a
+// workgroup, four a thread, and a run of kRun chunks a wave.  With four waves, each
+// takes its run from zero first, S' = P S + T; what the runs before it make of the
+// state it gets from their P and T.  Bound: latency (32 chunks of 8 KV heads of 128,
+// 25 MB: 9 us; one wave after chunk after chunk 14).
+template <int D, int kWaves>
+__global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
   constexpr uint32_t kBlocks = D * D / 256;
-  constexpr int kAhead = 8;
+  constexpr int kRun = kScanRun, kSpan = kRun * kWaves;
+  __shared__ f4 runs[kWaves > 1 ? kWaves : 1][64];
   const uint32_t blk = blockIdx.x % kBlocks, sh = blockIdx.x / kBlocks;
-  const int h = sh % (uint32_t)A.hkv, s = sh / (uint32_t)A.hkv, lane = threadIdx.x, at = blk * 256 + lane * 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = sh % (uint32_t)A.hkv, s = sh / (uint32_t)A.hkv, at = blk * 256 + lane * 4;
   const int begin = cu_at(A.cu, s, A.rows), n = cu_at(A.cu, s + 1, A.rows) - begin;
   if (n <= 0) return;
   const int base = slot_base<kChunk, 1>(begin, s, 1), end = base + (n + kChunk - 1) / kChunk;
@@ -432,40 +436,80 @@ __global__ __launch_bounds__(64) void scan_kernel(const LinArgs A) {
   const int64_t r0 = (int64_t)(lo - A.slot0) * A.hkv + h;
   const float *u = A.u + r0 * (D * D) + at;
   const int64_t step = (int64_t)A.hkv * (D * D);
-  f4 x[kAhead];
+  _Float16 *snap = A.snap + r0 * (D * D) + at;
+  Meta *meta = A.meta + r0;
+  f4 x[kRun];
+  float decay, most;  // of chunk c0 + lane
+  auto send_for = [&](int c0) {
 #pragma unroll
-  for (int i = 0; i < kAhead; i++) x[i] = *reinterpret_cast<const f4 *>(u + min(i, count - 1) * step);
+    for (int i = 0; i < kRun; i++) x[i] = *reinterpret_cast<const f4 *>(u + min(c0 + wave * kRun + i, count - 1) * step);
+    const Meta m = meta[(int64_t)min(c0 + lane, count - 1) * A.hkv];
+    decay = c0 + lane < count ? __builtin_amdgcn_exp2f(m.decay) : 1.0f;
+    most = c0 + lane < count ? m.most_u : 0.0f;
+  };
+  send_for(0);
   float *carry = A.carry + (int64_t)h * (D * D) + at;  // (one sequence may read it as another one writes: two of them)
   f4 S = {0, 0, 0, 0};
   if (lo > base) S = *reinterpret_cast<const f4 *>(A.carried + (int64_t)h * (D * D) + at);
   else if (state_ok(A, from)) S = *reinterpret_cast<const f4 *>(A.states + ((int64_t)from * A.hkv + h) * (D * D) + at);
-  _Float16 *snap = A.snap + r0 * (D * D) + at;
-  Meta *meta = A.meta + r0;
   float bound = meta->most_s;  // of |S|, from the chunks' largest elements
-  float decay = 0.0f, most = 0.0f;  // of chunk c0 + lane
-  for (int c0 = 0; c0 < count; c0 += kAhead) {
-    if ((c0 & 63) == 0) {
-      const Meta m = meta[(int64_t)min(c0 + lane, count - 1) * A.hkv];
-      decay = __builtin_amdgcn_exp2f(m.decay);
-      most = m.most_u;
+  auto of_chunk = [](float v, int c) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), c)); };
+#pragma unroll 1
+  for (int c0 = 0; c0 < count; c0 += kSpan) {
+    const int c1 = c0 + wave * kRun;
+    f4 mine = S;  // this run's start, and a bound of it
+    float reach = bound;
+    if constexpr (kWaves > 1) {
+      f4 T = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kRun; i++) {
+        if (c1 + i >= count) x[i] = (f4){0, 0, 0, 0};
+        T = T * of_chunk(decay, wave * kRun + i) + x[i];
+      }
+      runs[wave][lane] = T;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWaves; w++) {
+        if (w == wave) {
+          mine = S;
+          reach = bound;
+        }
+        if (c0 + w * kRun >= count) break;
+        float P = 1.0f;
+#pragma unroll
+        for (int i = 0; i < kRun; i++) {
+          const float a = of_chunk(decay, w * kRun + i);
+          P *= a;
+          bound = bound * a + of_chunk(most, w * kRun + i);
+        }
+        S = S * P + runs[w][lane];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; i++) {
-      const int c = c0 + i;
+    for (int i = 0; i < kRun; i++) {
+      const int c = c1 + i;
       if (c >= count) break;
-      const int e = bound > 0.0f ? exponent(bound) - 15 : kNoState;
-      const int sh16 = bound > 0.0f ? -e : 0;
+      const int e = reach > 0.0f ? exponent(reach) - 15 : kNoState;
+      const int sh16 = reach > 0.0f ? -e : 0;
       h4 o;
 #pragma unroll
-      for (int j = 0; j < 4; j++) o[j] = (_Float16)ldexpf(S[j], sh16);
+      for (int j = 0; j < 4; j++) o[j] = (_Float16)ldexpf(mine[j], sh16);
       *reinterpret_cast<h4 *>(snap + c * step) = o;
       if (blk == 0 && lane == 0) meta[(int64_t)c * A.hkv].e = e;
-      const float a = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(decay), c & 63));
-      bound = bound * a + __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(most), c & 63));
-      S = S * a + x[i];
-      x[i] = *reinterpret_cast<const f4 *>(u + min(c + kAhead, count - 1) * step);
+      const float a = of_chunk(decay, wave * kRun + i);
+      reach = reach * a + of_chunk(most, wave * kRun + i);
+      mine = mine * a + x[i];
+    }
+    if constexpr (kWaves == 1) {
+      S = mine;
+      bound = reach;
+    }
+    if (c0 + kSpan < count) {
+      send_for(c0 + kSpan);
+      if constexpr (kWaves > 1) __syncthreads();  // (the runs are read)
     }
   }
+  if (wave) return;
   if (hi < end) *reinterpret_cast<f4 *>(carry) = S;
   else if (state_ok(A, to)) *reinterpret_cast<f4 *>(A.states + ((int64_t)to * A.hkv + h) * (D * D) + at) = S;
 }
@@ -795,7 +839,7 @@ int check_shape(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads, i
   if (rc != TQ_OK) return rc;
   const Plan P = make_plan(rows, seqs, kv_heads, head_dim);
   const int64_t blocks = head_dim * head_dim / 256;
-  const bool ok = P.chunked ? grid_ok(P.pass * q_heads + seqs * kv_heads, 512) && grid_ok(seqs * kv_heads * blocks, 64)
+  const bool ok = P.chunked ? grid_ok(P.pass * q_heads + seqs * kv_heads, 512) && grid_ok(seqs * kv_heads * blocks, 256)
                             : grid_ok(seqs * kv_heads * (head_dim / 64), 256);
   return ok ? TQ_OK : TQ_ERR_SHAPE;
 }
@@ -812,7 +856,11 @@ void launch_passes(LinArgs A, const Plan &P, hipStream_t st) {
     A.slots = (int)(P.slots - s0 < P.pass ? P.slots - s0 : P.pass);
     const int64_t units = (int64_t)A.slots * A.hkv;
     hipLaunchKernelGGL((chunk_state_kernel<D, T>), dim3((unsigned)(units + (int64_t)A.seqs * A.hkv)), dim3(512), 0, st, A);
-    hipLaunchKernelGGL((scan_kernel<D>), dim3((unsigned)((int64_t)A.seqs * A.hkv * (D * D / 256))), dim3(64), 0, st, A);
+    // four waves where sequences have more chunks than a run, on average (64 sequences
+    // of 100 rows: 187 us with four waves, 111 with one)
+    const dim3 blocks((unsigned)((int64_t)A.seqs * A.hkv * (D * D / 256)));
+    if (P.slots > kScanRun * (int64_t)A.seqs) hipLaunchKernelGGL((scan_kernel<D, 4>), blocks, dim3(256), 0, st, A);
+    else hipLaunchKernelGGL((scan_kernel<D, 1>), blocks, dim3(64), 0, st, A);
     // the query heads of a KV head over as many workgroups as fill the CUs
     const int most = A.group >= 2 ? A.group / 2 : 1;
     int64_t parts = kCus / units;
