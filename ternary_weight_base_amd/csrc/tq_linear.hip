@@ -156,8 +156,18 @@ struct Chunk {
   int s, begin, n, local;
 };
 __device__ __forceinline__ bool find_chunk(const LinArgs &A, int slot, Chunk &c) {
-  c.s = find_seq<kChunk, 1>(A.cu, A.seqs, A.rows, slot, 1);
-  const int first = cu_at(A.cu, c.s, A.rows), end = cu_at(A.cu, c.s + 1, A.rows);
+  int first, end;
+  if (A.seqs < 64) {  // (a lane an entry: no second trip to memory for what was found)
+    const int lane = threadIdx.x & 63, v = cu_at(A.cu, min(lane, A.seqs), A.rows);
+    const bool le = lane < A.seqs && slot_base<kChunk, 1>(v, lane, 1) <= slot;
+    c.s = max((int)__popcll(__ballot(le)), 1) - 1;
+    first = __builtin_amdgcn_readlane(v, c.s);
+    end = __builtin_amdgcn_readlane(v, c.s + 1);
+  } else {
+    c.s = find_seq<kChunk, 1>(A.cu, A.seqs, A.rows, slot, 1);
+    first = cu_at(A.cu, c.s, A.rows);
+    end = cu_at(A.cu, c.s + 1, A.rows);
+  }
   c.local = slot - slot_base<kChunk, 1>(first, c.s, 1);
   if (c.local < 0 || c.local >= (end - first + kChunk - 1) / kChunk || end <= first) return false;
   c.begin = first + c.local * kChunk;
@@ -171,12 +181,7 @@ __device__ __forceinline__ void decay_sums(const LinArgs &A, const Chunk &c, int
   const int lane = threadIdx.x & 63;
   const double d0 = 2 * lane < c.n ? log2_decay(A, c.begin + 2 * lane, h) : 0.0;
   const double d1 = 2 * lane + 1 < c.n ? log2_decay(A, c.begin + 2 * lane + 1, h) : 0.0;
-  double sum = d0 + d1;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double o = __shfl_up(sum, d);
-    if (lane >= d) sum += o;
-  }
+  const double sum = tqdev::wave_upto(d0 + d1);
   g1 = sum;
   g0 = sum - d1;
 }
@@ -591,10 +596,9 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
       }
     }
     u4 sp[D * (D / 8) / NT];
-    if (es != kNoState) {
+    // (sent for before its exponent is known: without a state it is not used)
 #pragma unroll
-      for (int i = 0; i < D * (D / 8) / NT; i++) sp[i] = reinterpret_cast<const u4 *>(A.snap + rs * (D * D))[i * NT + tid];
-    }
+    for (int i = 0; i < D * (D / 8) / NT; i++) sp[i] = reinterpret_cast<const u4 *>(A.snap + rs * (D * D))[i * NT + tid];
     if (wave == 0) {
       double d0, d1;
       decay_sums(A, c, h, d0, d1);

@@ -137,23 +137,6 @@ __device__ __forceinline__ double block_sum(double v, double *room) {
   for (int i = 1; i < NT / 64; i++) s += room[i];
   return s;
 }
-// Sums of the lanes up to this one.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double from_below(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xF, false);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double wave_upto(double v) {
-  v += from_below<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
-  v += from_below<0x112, 0xF>(v);
-  v += from_below<0x114, 0xF>(v);
-  v += from_below<0x118, 0xF>(v);
-  v += from_below<0x142, 0xA>(v);  // lane 15 of rows 0, 2 to rows 1, 3
-  v += from_below<0x143, 0xC>(v);  // lane 31 to rows 2, 3
-  return v;
-}
 __device__ __forceinline__ double lane_value(double v, int lane) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
   const uint32_t lo = __builtin_amdgcn_readlane((int)b, lane), hi = __builtin_amdgcn_readlane((int)(b >> 32), lane);
@@ -164,7 +147,7 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
 template <int NT>
 __device__ __forceinline__ double block_before(double v, double *room, double *all = nullptr) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const double sum = wave_upto(v);
+  const double sum = tqdev::wave_upto(v);
   __syncthreads();
   if (lane == 63) room[wave] = sum;
   __syncthreads();
@@ -274,7 +257,7 @@ __device__ __forceinline__ void stage(const T *x, bool wide, int vocab, int seg,
 // Where a running sum over the lanes from `before` on exceeds `target`: the first
 // lane, or the last one that adds something; the sum before it.
 __device__ __forceinline__ int crossing(double own, double before, double target, double &from) {
-  const double upto = before + wave_upto(own);
+  const double upto = before + tqdev::wave_upto(own);
   const uint64_t some = __ballot(own > 0.0), above = __ballot(own > 0.0 && upto > target);
   const int at = above ? __builtin_ctzll(above) : some ? 63 - __builtin_clzll(some) : 0;
   from = lane_value(upto - own, at);
@@ -334,7 +317,7 @@ __device__ int find_segment(float u, int segs, const double *seg_sum, double &fr
     mine[j] = 4 * lane + j < segs ? seg_sum[4 * lane + j] : 0.0;
     own += mine[j];
   }
-  const double upto = wave_upto(own);
+  const double upto = tqdev::wave_upto(own);
   total = lane_value(upto, 63);
   target = (u > 0.0f ? (double)u : 0.0) * total;
   double r = upto - own, before_above = 0.0, before_some = 0.0;

@@ -39,6 +39,24 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return (r[0] + r[1]) + (r[2] + r[3]);
 }
 
+// Sums of the lanes up to this one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double from_below(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_upto(double v) {
+  v += from_below<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v += from_below<0x112, 0xF>(v);
+  v += from_below<0x114, 0xF>(v);
+  v += from_below<0x118, 0xF>(v);
+  v += from_below<0x142, 0xA>(v);  // lane 15 of rows 0, 2 to rows 1, 3
+  v += from_below<0x143, 0xC>(v);  // lane 31 to rows 2, 3
+  return v;
+}
+
 // A double rounded to fp32, kept as such: where the result is rounded on to
 // fp16 the compiler would otherwise merge the two roundings into one from
 // the double, a long software conversion.  (The two together are off by at
