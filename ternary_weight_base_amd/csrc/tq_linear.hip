@@ -249,7 +249,8 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
   constexpr int kSteps = kChunk / kStep, kPer = kStep * (D / 8) / 512;  // pieces of 8 elements a thread and step
   constexpr int kNb = D == 128 ? 2 : 1;  // column blocks of 32 a wave
   constexpr int kTile = kStep * 2 * D;
-  __shared__ __attribute__((aligned(16))) uint8_t kh[kTile], kl[kTile], vh[kTile], vl[kWide ? kTile : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t kh[2 * kTile], vh[kTile], vl[kWide ? kTile : 16];
+  uint8_t *const kl = kh + kTile;
   __shared__ float w[kChunk], red[2][8];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -391,7 +392,7 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
   __syncthreads();
   if constexpr (D == 64) {  // the halves' sums meet
     float *half = reinterpret_cast<float *>(kh);  // [4 waves][16][64], over kh and kl
-    static_assert(sizeof(kh) + sizeof(kl) >= 4 * 16 * 64 * 4, "room for the sums of four waves");
+    static_assert(sizeof(kh) >= 4 * 16 * 64 * 4, "room for the sums of four waves");
     if (wave >= 4) {
 #pragma unroll
       for (int r = 0; r < 16; r++) half[((wave - 4) * 16 + r) * 64 + lane] = acc[0][r];
@@ -540,7 +541,7 @@ __device__ __forceinline__ float half_max(float v) {
 // range by what their scores can reach, head_dim max |q| max |k|.
 //
 // Bound: 4096 fp32 rows, 64 and 8 heads of 128, 240 MB and 17 GFLOP (44 issued, for
-// second terms and whole blocks): 65 to 70 us, of them some 10 before the first
+// second terms and whole blocks): 61 to 67 us, of them some 10 before the first
 // product, one workgroup a CU (137 KB of LDS).  Matrix pipes busy 33 %, VALU 30 %.
 template <int D, typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
@@ -672,9 +673,10 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(A.out + (int64_t)c.begin * A.out_stride, 0, 0x7fffffff, 0x00027000);
   constexpr uint32_t kNowhere = 0x80000000u;
 
-  // one round: rows 32 RB + n of a head
-  auto rows = [&](auto block, int i, const h8 (&qf)[kTerms][D / 16], int bq) {
-    constexpr int RB = decltype(block)::value;
+  // one round: rows 32 RB + n of a head.  (One copy for all four blocks, its tiles in a
+  // loop: with a copy a block, 28 to 43 KB of code against 11 to 15, most of which a
+  // wave runs once, fetching it took longer: 3 x 2051 fp16 rows 39 against 34 us.)
+  auto rows = [&](int RB, int i, const h8 (&qf)[kTerms][D / 16], int bq) {
     const int row = 32 * RB + n, head = h * A.group + g0 + head_of(i), eq = kWide ? bq : 14;
     if (32 * RB >= c.n || head_of(i) >= heads) {
       send_for(min(i + 1, rounds - 1), kFirst, kPieces);
@@ -707,8 +709,8 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
         for (int r = 0; r < 16; r++) o[d][r] *= f;
     }
     const int xp = max((eq - 14) + (ek - 14) + (ev - 14) - x, -300);
-#pragma unroll
-    for (int t = 0; t <= RB; t++) {
+    auto tile = [&](auto last_tile, int t) {
+      constexpr bool kLast = decltype(last_tile)::value;
       // scores S^T = K Q^T: sc[r] is token 32 t + 16 (r / 8) + 8 half + r % 8
       f16x sc = (f16x)(0.0f);
       const int key = 32 * t + row_token(n);
@@ -726,18 +728,18 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
         }
       }
       __builtin_amdgcn_s_setprio(0);
-      if (t == RB) send_for(min(i + 1, rounds - 1), kFirst, kPieces);
+      if (kLast) send_for(min(i + 1, rounds - 1), kFirst, kPieces);
       // weights: two fp16 terms, so that they lose nothing to the outputs' rounding
       const int j0 = 32 * t + 8 * half;
       h8 p[2], pl[2];
-      const float f = t == RB ? 0.0f : ldexpf(__builtin_amdgcn_exp2f((gh - ghi[32 * t + 31]) + (gl - glo[32 * t + 31])), xp);
+      const float f = kLast ? 0.0f : ldexpf(__builtin_amdgcn_exp2f((gh - ghi[32 * t + 31]) + (gl - glo[32 * t + 31])), xp);
 #pragma unroll
       for (int u = 0; u < 2; u++) {
         float w[8];
 #pragma unroll
         for (int r = 0; r < 8; r++) {
           const int j = j0 + 16 * u + r;
-          if (t == RB) {
+          if (kLast) {
             w[r] = sc[8 * u + r] * ldexpf(__builtin_amdgcn_exp2f((gh - ghi[j]) + (gl - glo[j])), xp);
             w[r] = j <= row ? w[r] : 0.0f;
           } else {
@@ -754,7 +756,10 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, p[u], o[d], 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, pl[u], o[d], 0, 0, 0);
         }
-    }
+    };
+#pragma unroll 1
+    for (int t = 0; t < RB; t++) tile(std::false_type(), t);
+    tile(std::true_type(), RB);
     // (held within fp32's exponents: sums are 0 or 2^-48 to 2^98, so a result
     // that fp16 holds is not changed)
     const float last = scale_m * power(x + scale_e);
@@ -801,12 +806,7 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
         for (int r = 0; r < 8; r++) qf[0][j][r] = (_Float16)raw[j][r];
     }
     send_for(min(i + 1, rounds - 1), 0, kFirst);  // (again the last one's behind it, from the cache)
-    switch (block_of(i)) {
-      case 0: rows(std::integral_constant<int, 0>(), i, qf, bq); break;
-      case 1: rows(std::integral_constant<int, 1>(), i, qf, bq); break;
-      case 2: rows(std::integral_constant<int, 2>(), i, qf, bq); break;
-      default: rows(std::integral_constant<int, 3>(), i, qf, bq); break;
-    }
+    rows(block_of(i), i, qf, bq);
   }
 }
 
