@@ -543,7 +543,7 @@ __device__ __forceinline__ float half_max(float v) {
 //
 // Bound: 4096 fp32 rows, 64 and 8 heads of 128, 240 MB and 17 GFLOP (44 issued, for
 // second terms and whole blocks): 61 to 67 us, of them some 10 before the first
-// product, one workgroup a CU (137 KB of LDS).  Matrix pipes busy 33 %, VALU 30 %.
+// product, one workgroup a CU (137 KB of LDS).  Matrix pipes busy 32 %, VALU 29 %.
 template <int D, typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   constexpr bool kWide = std::is_same<T, float>::value;
@@ -715,9 +715,6 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
       // scores S^T = K Q^T: sc[r] is token 32 t + 16 (r / 8) + 8 half + r % 8
       f16x sc = (f16x)(0.0f);
       const int key = 32 * t + row_token(n);
-      // (a wave in its products goes first, so that the SIMD's two waves do not
-      // stay side by side in them: a prompt of 4096 rows 92.8 against 95.3 us)
-      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int j = 0; j < D / 16; j++) {
         const h8 a = *reinterpret_cast<const h8 *>(&kt[0][key][16 * j + 8 * half]);
@@ -728,7 +725,6 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
           sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, qf[0][j], sc, 0, 0, 0);
         }
       }
-      __builtin_amdgcn_s_setprio(0);
       if (kLast) send_for(min(i + 1, rounds - 1), kFirst, kPieces);
       // weights: two fp16 terms, so that they lose nothing to the outputs' rounding
       const int j0 = 32 * t + 8 * half;
