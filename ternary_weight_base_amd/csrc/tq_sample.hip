@@ -319,7 +319,8 @@ __device__ int find_segment(float u, int segs, const double *seg_sum, double &fr
   }
   const double upto = tqdev::wave_upto(own);
   total = lane_value(upto, 63);
-  target = (u > 0.0f ? (double)u : 0.0) * total;
+  // (from u = 1 on nothing crosses, whatever the sums' roundings: the last that weighs something)
+  target = u >= 1.0f ? (double)__builtin_inff() : (u > 0.0f ? (double)u : 0.0) * total;
   double r = upto - own, before_above = 0.0, before_some = 0.0;
   int above = -1, some = -1;
 #pragma unroll

@@ -177,6 +177,22 @@ def test_ties_go_to_the_lower_index():
     assert lp[0] == 0 and lp[1] == 0 and abs(lp[2] + math.log(3)) < 1e-6 and abs(lp[3] + math.log(5001)) < 1e-5
 
 
+def test_the_last_kept_token_weighs_little():
+    """u of 1 and above: the last kept token, whatever its weight beside the others, on each way to it."""
+    x = np.full((6, 9000), -math.inf, np.float32)
+    x[:, 17] = 0.0
+    x[:, 1000:2400] = -30.0
+    x[:, 8999] = -45.0
+    u = [1.0, 2.0, 1.0, 1.0, 1.0, 1.0 - 2.0 ** -24]
+    for extra in ({}, {"k": [1402] * 6}, {"k": [1402, 1401, 1, 2, 1400, 900]}, {"p": [0.99] * 6}):
+        assert verify(x, u, **extra) >= 5
+    # (weights far below 1 are all near a min_p of their size: the tokens themselves; exp(-30) 9.4e-14, exp(-45) 2.9e-20)
+    for extra, last in (({"k": [1402] * 6}, 8999), ({"k": [1000] * 6}, 1998), ({"m": [1e-30] * 6}, 8999), ({"k": [1402] * 6, "m": [1e-15] * 6}, 2399),
+                        ({"k": [1000] * 6, "m": [1e-14] * 6}, 1998), ({"p": [0.99] * 6, "m": [1e-14] * 6}, 17)):
+        token, _ = call(x, u, **extra)
+        assert token[:5].tolist() == [last] * 5, (extra, token)
+
+
 def test_ends_of_the_ranges():
     inf, nan, big = math.inf, math.nan, 3e38
     x = np.full((12, 5000), -inf, np.float32)
