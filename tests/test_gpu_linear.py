@@ -140,6 +140,24 @@ def test_many_passes():
     verify(c, *call(c))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32], ids=str)
+def test_long_sequences(dtype):
+    """More chunks than the scan's four runs of eight hold, and a sequence of one beside them."""
+    for lengths in ([4500, 130], [1025, 1150], [2049, 1, 2170]):
+        c = make((2, 1, 64), lengths, dtype, "rows", seed=18)
+        verify(c, *call(c))
+
+
+@pytest.mark.parametrize("seqs", [62, 63, 64, 65, 130])
+def test_many_sequences_in_chunks(seqs):
+    """Sequences found by a lane each, or searched for."""
+    n = [(37 * i) % 61 + (200 if i % 29 == 5 else 0) for i in range(seqs)]
+    n[-1] = 140
+    c = make((2, 2, 64), n, torch.float16, "heads", seed=seqs)
+    assert sum(n) > 16 * seqs
+    verify(c, *call(c))
+
+
 def test_sequences_across_two_borders_of_one_pass():
     """The second sequence ends in the pass that the third one is cut in: each has its own state between passes."""
     c = make((64, 64, 128), [2300, 2600, 600], torch.float16, "heads", seed=17)
