@@ -19,7 +19,8 @@ namespace {
 
 constexpr size_t kMidBytes = (size_t)1 << 27;  // of the prefixes' results at most
 // Workgroups of the prefix launch, two a CU, where its keys are cut (64 tokens behind
-// 16384: 100 us, with one a CU 108, with four 119), and pages of a piece at least.
+// 16384: 79 us, with one a CU 87, with three 90; 37 x 2 rows behind four prefixes 46, 59
+// and 46), and pages of a piece at least.
 constexpr int kPreFill = 2 * kCus, kPreLeast = 4;
 
 struct SharedPlan {
