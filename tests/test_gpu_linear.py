@@ -130,6 +130,19 @@ def test_strided_rows_and_padding(n):
     assert bool(torch.isnan(room[:, 384:]).all())
 
 
+@pytest.mark.parametrize("n", [[3, 2, 8], [129, 40]], ids=["rows", "chunks"])
+def test_rows_far_apart(n):
+    """Rows of qkv 2^25 elements apart and of out 2^22: byte offsets past 32 and up to 31 bits."""
+    c = make((2, 1, 64), n, torch.float16, "rows", seed=19)
+    rows = sum(n)
+    qkv = torch.empty((rows, 1 << 25), dtype=torch.float16, device="cuda")[:, :4 * 64]
+    qkv.copy_(c["qkv"])
+    room = torch.full((rows, 1 << 22), math.nan, dtype=torch.float16, device="cuda")
+    got, states = call(c, qkv=qkv, out=room[:, :128].unflatten(1, (2, 64)))
+    verify(c, got, states)
+    assert bool(torch.isnan(room[:, 128:]).all())
+
+
 def test_many_passes():
     """More chunks than one pass's scratch holds: sequences cut at its border, one of them in place."""
     import ternary_weight_base_amd as tq

@@ -155,6 +155,16 @@ def test_strided_rows(dtype):
         assert verify(wide[:, :vocab], rng.random(6), **settings(rng, "all", 6)) >= 5
 
 
+def test_rows_far_apart():
+    """Rows 2^30 elements apart: byte offsets past 32 bits."""
+    rng = np.random.default_rng(17)
+    room = torch.empty((4, 1 << 30), dtype=torch.float16, device="cuda")
+    for vocab in (1000, 9001):
+        room[:, :vocab] = dev(logits(rng, 4, vocab, "usual", "float16"))
+        room[:, vocab:vocab + 4096] = math.inf
+        assert verify(room[:, :vocab], rng.random(4), **settings(rng, "all", 4)) >= 3
+
+
 def test_the_place_of_u():
     """Each token's share of [0, 1): u at its borders and outside."""
     x = np.log(np.array([[1, 2, 4, 1]], dtype=np.float64)).astype(np.float32).repeat(9, 0)
