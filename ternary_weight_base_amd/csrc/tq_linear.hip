@@ -340,7 +340,8 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
       mk = fmaxf(mk, red[0][i]);
       mv = fmaxf(mv, red[1][i]);
     }
-    const int ek = exponent(mk), ev = exponent(mv), now = max(unit, ek + ev);
+    // (rows of zeros have no size: the others' unit is not theirs)
+    const int ek = exponent(mk), ev = exponent(mv), size = mk > 0.0f && mv > 0.0f ? ek + ev : -1000, now = max(unit, size);
     if (now != unit) {
 #pragma unroll
       for (int b = 0; b < kNb; b++)
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
         for (int r = 0; r < 16; r++) acc[b][r] = ldexpf(acc[b][r], max(unit - now, -200));
     }
     unit = now;
-    const int shift = 14 - ek + max(ek + ev - now, -300);
+    const int shift = 14 - ek + max(size - now, -300);
     const float fv = power(14 - ev);
 #pragma unroll
     for (int i = 0; i < kPer; i++) {

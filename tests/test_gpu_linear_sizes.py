@@ -1,0 +1,113 @@
+"""tq_linear_attn in chunks where the sizes of rows differ by far more than
+fp16 holds: zeros, rows that a reset has made nothing of, large rows behind
+small ones, states that a chunk forgets.  Against the recurrence in float64,
+each row by what it sees itself."""
+import math
+
+import pytest
+
+from gpu_util import say
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+INF = math.inf
+TYPES = {"f16": torch.float16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def reach(c):
+    """For each row and KV head R_t = 2^g_t R_{t-1} + max|k_t| max|v_t|, R from the
+    start's largest element: a bound of the state, of what is not forgotten alone.
+    -> [rows][hkv], {sequence: its last}"""
+    hq, hkv, dim = c["heads"]
+    rows = c["qkv"].shape[0]
+    x = c["qkv"].double().reshape(rows, hq + 2 * hkv, dim).abs().amax(2)
+    g = (c["decay"].double() / math.log(2)).clamp(max=0).expand(rows, hkv)
+    out, last = torch.zeros_like(g), {}
+    for s, start in enumerate(c["from"]):
+        R = torch.zeros(hkv, dtype=torch.float64, device="cuda")
+        if 0 <= start < c["states"].shape[0]:
+            R = c["states"][start].double().abs().amax((1, 2))
+        for r in range(c["cu"][s], c["cu"][s + 1]):
+            R = torch.exp2(g[r]) * R + x[r, hq:hq + hkv] * x[r, hq + hkv:]
+            out[r] = R
+        last[s] = R
+    return out, last
+
+
+def verify(c, out, states):
+    """Tolerances of the chunked form.  Relative to the magnitudes (sums of the terms'
+    absolute values) as linear_util derives them, with the log2 decays of rows that
+    keep something.  Beside them what lies below fp16's least step, 2^-24, half of
+    which a rounding loses: factors are scaled so that each row's largest element is
+    in 2^13 .. 2^14, and a row's weights so that a bound of them, up to 8 times R
+    (two powers of two and a power of two between), is 2^14 for states and, by
+    dim max|q| R times another 2, 2^15 for outputs.
+    States: 2^-25 of 2^14, 8 times, in keys and values of 128 rows: 2^(-39 + 3 + 1 + 7)
+    = 2^-28 R.  Outputs: weights 2^(-25 - 15 + 4 + 7) = 2^-29, queries, keys, values
+    2^-38 each, the state before the chunk 2^-38: together below 2^-28 dim max|q| R."""
+    from linear_util import U, linear, out_tolerance, state_tolerance
+    hq, hkv, dim = c["heads"]
+    cu, rows = c["cu"], c["qkv"].shape[0]
+    ref, mag, left, _ = linear(c["qkv"], c["decay"], cu, c["from"], c["to"], c["states"], c["scale"], hq, hkv, dim)
+    bound, last = reach(c)
+    g = (c["decay"].double() / math.log(2)).clamp(max=0).expand(rows, hkv)
+    g = torch.where(g > -1000, -g, 0)
+    most_q = c["qkv"].double()[:, :hq * dim].reshape(rows, hkv, hq // hkv, dim).abs().amax(3)
+    for s in range(len(c["from"])):
+        a, b = cu[s], cu[s + 1]
+        fall = g[a:b].sum(0)
+        sh = (b - a, hkv, hq // hkv, dim)
+        small = 2.0 ** -28 * dim * abs(c["scale"]) * (most_q[a:b] * bound[a:b, :, None])[..., None]
+        r, got = ref[a:b].reshape(sh), out[a:b].double().reshape(sh)
+        tol = out_tolerance(r, mag[a:b].reshape(sh), 0.0, b - a, fall.reshape(1, hkv, 1, 1), dim, True) + small
+        err = (got - r).abs()
+        err = torch.where(torch.isinf(got) & (got * r > 0) & (r.abs() + tol >= 65520), 0, err)
+        bad = ~(err <= tol)
+        say(f"  outputs: {float((err / tol).nan_to_num(INF).max()):.3g} of the tolerance")
+        assert not bool(bad.any()), f"row {int(bad.flatten(1).any(1).nonzero()[0])} of sequence {s}: {float((err / tol).max())} of the tolerance"
+        if c["to"][s] not in left:
+            continue
+        S, M, _ = left[c["to"][s]]
+        err = (states[c["to"][s]].double() - S).abs()
+        relative = (440 + 4 * math.ceil((b - a) / 128) + 2 * fall[:, None, None]) * U * M
+        assert bool((relative <= state_tolerance(M, b - a, fall[:, None, None], True)).all())
+        tol = relative + 2.0 ** -28 * last[s][:, None, None]
+        say(f"  state: {float((err / tol.clamp(min=1e-300)).nan_to_num(INF).max()):.3g} of the tolerance")
+        assert bool((err <= tol).all()), f"state of sequence {s}: {float((err / tol.clamp(min=1e-300)).max())} of the tolerance"
+
+
+def make(heads, n, dtype, seed, size=1.0):
+    from test_gpu_linear import make as m
+    c = m(heads, n, TYPES[dtype], "rows", seed, size=size)
+    c["from"] = [-1] * len(n)
+    return c
+
+
+def run(c):
+    from test_gpu_linear import call
+    verify(c, *call(c))
+
+
+def part(c, which):
+    hq, hkv, dim = c["heads"]
+    return {"rows": slice(None), "queries": slice(0, hq * dim), "keys": slice(hq * dim, (hq + hkv) * dim),
+            "values": slice((hq + hkv) * dim, None)}[which]
+
+
+@pytest.mark.parametrize("which", ["rows", "keys", "values"])
+@pytest.mark.parametrize("dtype,size", [("f16", 1e-4), ("f32", 1e-6), ("f32", 1e-9)])
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64)], ids=str)
+def test_zeros_before_small_rows(heads, dtype, size, which):
+    """Padded or gated rows: half a chunk of zeros."""
+    say(f"zeros {heads} {dtype} {size} {which}")
+    c = make(heads, [128, 200], dtype, seed=40, size=size)
+    for first in (0, 128 + 128):
+        c["qkv"][first:first + 64, part(c, which)] = 0
+    run(c)
