@@ -19,7 +19,8 @@
 // Products run on v_mfma_f32_32x32x16_f16, sums in fp32.  fp16 operands are
 // scaled by powers of two into its range, so no size of input overflows it.
 // U is of two fp16 terms a factor (fp16 inputs: the keys with their weights
-// two, the values are exact), so the state keeps fp32's accuracy.  For the
+// two, the values are exact), each row scaled by its own size and by what is left
+// of it at the chunk's end.  For the
 // outputs, which are fp16, queries, keys and weights have two terms each; fp32
 // values and the states before a chunk are rounded to fp16 once.
 #include <hip/hip_runtime.h>
@@ -235,6 +236,33 @@ __device__ __forceinline__ void two_terms(const float (&x)[8], h8 &hi, h8 &lo) {
 // 2^e as a factor, e within fp32's exponents
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 
+// The largest of a row's values, which D / 8 consecutive lanes hold.
+template <int D>
+__device__ __forceinline__ float row_most(float v) {
+  if constexpr (D == 128) return tqdev::row16_max(v);
+  v = fmaxf(v, __int_as_float(tqdev::dpp_move<tqdev::kDppSwap1>(__float_as_int(v))));
+  v = fmaxf(v, __int_as_float(tqdev::dpp_move<tqdev::kDppSwap2>(__float_as_int(v))));
+  return fmaxf(v, __int_as_float(tqdev::dpp_move<0x141>(__float_as_int(v))));  // (the 8 lanes mirrored)
+}
+
+// Eight values of a row scaled to below 2^14 by its largest one's exponent, which
+// is returned; `some`: not all of the row are 0.
+template <int D>
+__device__ __forceinline__ int scale_row(float (&v)[8], bool &some) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
+  m = row_most<D>(m);
+  some = m > 0.0f;
+  const int e = __builtin_amdgcn_frexp_expf(m);
+#pragma unroll
+  for (int j = 0; j < 8; j++) v[j] = ldexpf(v[j], 14 - e);
+  return e;
+}
+
+// Size (an exponent) of a row whose key or value is zero: far below any other's.
+constexpr int kNothing = -4000;
+
 // e with |v| < 2^e, at least -100 (so that scaling by 2^(14 - e) stays finite)
 __device__ __forceinline__ int exponent(float v) { return max(__builtin_amdgcn_frexp_expf(v), -100); }
 
@@ -251,17 +279,18 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
   constexpr int kTile = kStep * 2 * D;
   __shared__ __attribute__((aligned(16))) uint8_t kh[2 * kTile], vh[kTile], vl[kWide ? kTile : 16];
   uint8_t *const kl = kh + kTile;
-  __shared__ float w[kChunk], red[2][8];
+  __shared__ float left[kChunk], red[8];
+  __shared__ int size[kChunk];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = blockIdx.x % (uint32_t)A.hkv, rel = blockIdx.x / (uint32_t)A.hkv;
   auto most_of = [&](float m) {  // over the workgroup, in thread 0
     m = tqdev::wave_max64(m);
-    if (lane == 0) red[0][wave] = m;
+    if (lane == 0) red[wave] = m;
     __syncthreads();
-    float r = red[0][0];
+    float r = red[0];
 #pragma unroll
-    for (int i = 1; i < 8; i++) r = fmaxf(r, red[0][i]);
+    for (int i = 1; i < 8; i++) r = fmaxf(r, red[i]);
     return r;
   };
   if (rel >= A.slots) {
@@ -306,8 +335,8 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
     double g0, g1;
     decay_sums(A, c, h, g0, g1);
     const double all = __shfl(g1, 63);
-    w[2 * lane] = __builtin_amdgcn_exp2f((float)(all - g0));
-    w[2 * lane + 1] = __builtin_amdgcn_exp2f((float)(all - g1));
+    left[2 * lane] = (float)(all - g0);
+    left[2 * lane + 1] = (float)(all - g1);
     if (lane == 0) meta->decay = (float)all;
   }
   const int mb = D == 128 ? wave & 3 : wave & 1, nb0 = D == 128 ? 2 * (wave >> 2) : (wave >> 1) & 1;
@@ -315,59 +344,37 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
   f16x acc[kNb];
 #pragma unroll
   for (int b = 0; b < kNb; b++) acc[b] = (f16x)(0.0f);
-  int unit = kNoState;  // acc holds U * 2^(28 - unit)
+  // each row by the exponents of its own largest key and value
+#pragma unroll
+  for (int t = 0; t < kSteps; t++)
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      const int p = i * 512 + tid;
+      bool a, b;
+      const int e = scale_row<D>(k[t][i], a) + scale_row<D>(v[t][i], b);
+      if (p % (D / 8) == 0) size[t * kStep + p / (D / 8)] = a && b ? e : kNothing;
+    }
+  __syncthreads();
+  // the largest that is left at the chunk's end: acc holds U * 2^(28 - unit)
+  const int unit = (int)ceilf(tqdev::wave_max64(fmaxf(left[lane] + (float)size[lane], left[64 + lane] + (float)size[64 + lane])));
 #pragma unroll
   for (int t = 0; t < kSteps; t++) {
     if (t * kStep >= c.n) break;
-    float mk = 0.0f, mv = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPer; i++)
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        mk = fmaxf(mk, fabsf(k[t][i][j]));
-        mv = fmaxf(mv, fabsf(v[t][i][j]));
-      }
-    mk = tqdev::wave_max64(mk);
-    mv = tqdev::wave_max64(mv);
-    if (lane == 0) {
-      red[0][wave] = mk;
-      red[1][wave] = mv;
-    }
-    __syncthreads();  // (and the last step's operands are read)
-    mk = mv = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      mk = fmaxf(mk, red[0][i]);
-      mv = fmaxf(mv, red[1][i]);
-    }
-    // (rows of zeros have no size: the others' unit is not theirs)
-    const int ek = exponent(mk), ev = exponent(mv), size = mk > 0.0f && mv > 0.0f ? ek + ev : -1000, now = max(unit, size);
-    if (now != unit) {
-#pragma unroll
-      for (int b = 0; b < kNb; b++)
-#pragma unroll
-        for (int r = 0; r < 16; r++) acc[b][r] = ldexpf(acc[b][r], max(unit - now, -200));
-    }
-    unit = now;
-    const int shift = 14 - ek + max(size - now, -300);
-    const float fv = power(14 - ev);
+    if (t) __syncthreads();  // (the last step's operands are read)
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
-      const int p = i * 512 + tid, row = p / (D / 8), at = piece_at<D>(row, p % (D / 8));
-      const float f = ldexpf(w[t * kStep + row], shift);
-      float kw[8], vs[8];
+      const int p = i * 512 + tid, row = p / (D / 8), at = piece_at<D>(row, p % (D / 8)), all = t * kStep + row;
+      const float f = __builtin_amdgcn_exp2f(left[all] + (float)(size[all] - unit));
+      float kw[8];
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        kw[j] = k[t][i][j] * f;
-        vs[j] = v[t][i][j] * fv;
-      }
+      for (int j = 0; j < 8; j++) kw[j] = k[t][i][j] * f;
       h8 a, b, x, y;
       two_terms(kw, a, b);
       if constexpr (kWide) {
-        two_terms(vs, x, y);
+        two_terms(v[t][i], x, y);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = (_Float16)vs[j];  // exact
+        for (int j = 0; j < 8; j++) x[j] = (_Float16)v[t][i][j];  // (exact but for what is 2^-37 of the row's largest)
       }
       *reinterpret_cast<h8 *>(kh + at) = a;
       *reinterpret_cast<h8 *>(kl + at) = b;

@@ -41,7 +41,7 @@ def reach(c):
     return out, last
 
 
-def verify(c, out, states):
+def verify(c, out, states, outputs=True):
     """Tolerances of the chunked form.  Relative to the magnitudes (sums of the terms'
     absolute values) as linear_util derives them, with the log2 decays of rows that
     keep something.  Beside them what lies below fp16's least step, 2^-24, half of
@@ -69,7 +69,7 @@ def verify(c, out, states):
         tol = out_tolerance(r, mag[a:b].reshape(sh), 0.0, b - a, fall.reshape(1, hkv, 1, 1), dim, True) + small
         err = (got - r).abs()
         err = torch.where(torch.isinf(got) & (got * r > 0) & (r.abs() + tol >= 65520), 0, err)
-        bad = ~(err <= tol)
+        bad = ~(err <= tol) & outputs
         say(f"  outputs: {float((err / tol).nan_to_num(INF).max()):.3g} of the tolerance")
         assert not bool(bad.any()), f"row {int(bad.flatten(1).any(1).nonzero()[0])} of sequence {s}: {float((err / tol).max())} of the tolerance"
         if c["to"][s] not in left:
@@ -90,9 +90,9 @@ def make(heads, n, dtype, seed, size=1.0):
     return c
 
 
-def run(c):
+def run(c, outputs=True):
     from test_gpu_linear import call
-    verify(c, *call(c))
+    verify(c, *call(c), outputs=outputs)
 
 
 def part(c, which):
@@ -111,3 +111,42 @@ def test_zeros_before_small_rows(heads, dtype, size, which):
     for first in (0, 128 + 128):
         c["qkv"][first:first + 64, part(c, which)] = 0
     run(c)
+
+
+# (row, times): rows before the reset at 90 of a chunk, in its first half or its second
+FORGOTTEN = {"one": [10], "second half": [70], "several": [0, 31, 32, 63, 64, 89]}
+
+
+def forgotten(heads, dtype, times, rows, n=300):
+    """The second chunk has rows `times` as large as the others, forgotten at its 90th."""
+    c = make(heads, [n], dtype, seed=41)
+    for r in rows:
+        c["qkv"][128 + r, c["heads"][0] * heads[2]:] *= times
+    c["decay"][128 + 90] = -INF
+    return c
+
+
+@pytest.mark.parametrize("rows", FORGOTTEN)
+@pytest.mark.parametrize("dtype,times", [("f16", 12000.0), ("f32", 1e4), ("f32", 1e6), ("f32", 1e10), ("f32", 1e15)])
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64)], ids=str)
+def test_states_behind_forgotten_rows(heads, dtype, times, rows):
+    say(f"forgotten {heads} {dtype} {times} {rows}")
+    # the state of the second chunk's end, and one that the third one is added to
+    run(forgotten(heads, dtype, times, FORGOTTEN[rows], n=256), outputs=False)
+    run(forgotten(heads, dtype, times, FORGOTTEN[rows]), outputs=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64)], ids=str)
+def test_states_of_rows_of_all_sizes(heads, dtype):
+    """Keys and values each by their own power of two, decays that halve and more."""
+    say(f"all sizes {heads} {dtype}")
+    c = make(heads, [333], dtype, seed=42)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(42)
+    most = 10 if dtype == "f16" else 60
+    for which in ("keys", "values"):
+        e = torch.randint(-most, most + 1, (333, 1), generator=g, device="cuda")
+        c["qkv"][:, part(c, which)] *= torch.exp2(e.float()).to(TYPES[dtype])
+    c["decay"] *= 20
+    run(c, outputs=False)
