@@ -697,8 +697,8 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
     // units of 2^x: weights are below 2^15 in it, the state's part below 2^97
     const int xs = eq - 14 + es;
     int x = bq + bk + kLogD + ev - 29;
-    if (es != kNoState) x = max(x, xs - 60);
-    const float gh = ghi[row], gl = glo[row];
+    const float gh = ghi[row], gl = glo[row], whole = floorf(gh);
+    if (es != kNoState) x = max(x, xs + (int)whole - 60);  // (of what is left of it at this row)
     f16x o[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; d++) o[d] = (f16x)(0.0f);
@@ -711,7 +711,7 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qf[0][j], o[d], 0, 0, 0);
           if constexpr (kWide) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qf[1][j], o[d], 0, 0, 0);
         }
-      const float f = ldexpf(__builtin_amdgcn_exp2f(gh + gl), max(xs - x, -300));
+      const float f = ldexpf(__builtin_amdgcn_exp2f((gh - whole) + gl), max(xs + (int)whole - x, -300));
 #pragma unroll
       for (int d = 0; d < D / 32; d++)
 #pragma unroll
