@@ -19,7 +19,7 @@
 // Products run on v_mfma_f32_32x32x16_f16, sums in fp32.  fp16 operands are
 // scaled by powers of two into its range, so no size of input overflows it.
 // U is of two fp16 terms a factor (fp16 inputs: the keys with their weights
-// two, the values are exact), each row scaled by its own size and by what is left
+// two, the values are exact down to 2^-38 of the row's largest), each row scaled by its own size and by what is left
 // of it at the chunk's end.  For the
 // outputs, which are fp16, queries, keys and weights have two terms each; fp32
 // values and the states before a chunk are rounded to fp16 once.
@@ -45,6 +45,7 @@ constexpr int kFewRows = 16;    // up to so many rows a sequence (on average): t
 constexpr size_t kPassBytes = (size_t)1 << 27;  // scratch of a pass over the chunks
 constexpr int kNoState = -100000;  // exponent of a snapshot that is zero
 
+typedef float f8 __attribute__((ext_vector_type(8)));
 typedef float f16x __attribute__((ext_vector_type(16)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
@@ -80,16 +81,11 @@ __device__ __forceinline__ double log2_decay(const LinArgs &A, int row, int h) {
   return fmin(fmax(g, -2000.0), 0.0);
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+__device__ __forceinline__ f8 load8(const float *p) {
   const f4 a = *reinterpret_cast<const f4 *>(p), b = *reinterpret_cast<const f4 *>(p + 4);
-#pragma unroll
-  for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-__device__ __forceinline__ void load8(const _Float16 *p, float (&v)[8]) {
-  const h8 a = *reinterpret_cast<const h8 *>(p);
-#pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = (float)a[i];
-}
+__device__ __forceinline__ h8 load8(const _Float16 *p) { return *reinterpret_cast<const h8 *>(p); }
 
 // ---- few rows a sequence ---------------------------------------------------
 
@@ -187,6 +183,21 @@ __device__ __forceinline__ void decay_sums(const LinArgs &A, const Chunk &c, int
   g0 = sum - d1;
 }
 
+// The largest of the lanes up to this one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float most_below(float v) {  // (or its own)
+  const int b = __float_as_int(v);
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, ROWS, 0xF, false)));
+}
+__device__ __forceinline__ float wave_most_upto(float v) {
+  v = most_below<0x111, 0xF>(v);  // (the moves of wave_upto)
+  v = most_below<0x112, 0xF>(v);
+  v = most_below<0x114, 0xF>(v);
+  v = most_below<0x118, 0xF>(v);
+  v = most_below<0x142, 0xA>(v);
+  return most_below<0x143, 0xC>(v);
+}
+
 // A tile of fp16 rows in LDS whose operands are read transposed (below):
 // 64-byte blocks of a row in an order that puts the same block of four
 // consecutive rows into different banks.  -> byte offset of a block
@@ -222,7 +233,7 @@ struct Turned {
 
 // x as two fp16 terms, together within 2^-20 of it (or the least fp16 step):
 // the first cut off, two elements an instruction.
-__device__ __forceinline__ void two_terms(const float (&x)[8], h8 &hi, h8 &lo) {
+__device__ __forceinline__ void two_terms(const f8 &x, h8 &hi, h8 &lo) {
   typedef __fp16 c2 __attribute__((ext_vector_type(2)));
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
@@ -236,35 +247,55 @@ __device__ __forceinline__ void two_terms(const float (&x)[8], h8 &hi, h8 &lo) {
 // 2^e as a factor, e within fp32's exponents
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 
-// The largest of a row's values, which D / 8 consecutive lanes hold.
-template <int D>
-__device__ __forceinline__ float row_most(float v) {
-  if constexpr (D == 128) return tqdev::row16_max(v);
-  v = fmaxf(v, __int_as_float(tqdev::dpp_move<tqdev::kDppSwap1>(__float_as_int(v))));
-  v = fmaxf(v, __int_as_float(tqdev::dpp_move<tqdev::kDppSwap2>(__float_as_int(v))));
-  return fmaxf(v, __int_as_float(tqdev::dpp_move<0x141>(__float_as_int(v))));  // (the 8 lanes mirrored)
+// The largest of what D / 8 consecutive lanes hold.
+template <int D, typename V, typename F>
+__device__ __forceinline__ V row_most(V v, const F &most) {
+  auto step = [&](int moved) { v = most(v, __builtin_bit_cast(V, moved)); };
+  step(tqdev::dpp_move<tqdev::kDppSwap1>(__builtin_bit_cast(int, v)));
+  step(tqdev::dpp_move<tqdev::kDppSwap2>(__builtin_bit_cast(int, v)));
+  if (D == 128) {
+    step(tqdev::dpp_move<tqdev::kDppRor4>(__builtin_bit_cast(int, v)));
+    step(tqdev::dpp_move<tqdev::kDppRor8>(__builtin_bit_cast(int, v)));
+  } else {
+    step(tqdev::dpp_move<0x141>(__builtin_bit_cast(int, v)));  // (eight lanes mirrored)
+  }
+  return v;
 }
-
-// Eight values of a row scaled to below 2^14 by its largest one's exponent, which
-// is returned; `some`: not all of the row are 0.
-template <int D>
-__device__ __forceinline__ int scale_row(float (&v)[8], bool &some) {
+// The exponent of a row's largest value (`some`: not all are 0), by which eight values a
+// lane are scaled to below 2^14, unless SCALE says no.
+template <int D, bool SCALE = true>
+__device__ __forceinline__ int scale_row(f8 &v, bool &some) {
   float m = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
-  m = row_most<D>(m);
+  m = row_most<D>(m, [](float a, float b) { return fmaxf(a, b); });
   some = m > 0.0f;
   const int e = __builtin_amdgcn_frexp_expf(m);
 #pragma unroll
-  for (int j = 0; j < 8; j++) v[j] = ldexpf(v[j], 14 - e);
+  for (int j = 0; j < 8; j++)
+    if (SCALE) v[j] = ldexpf(v[j], 14 - e);
+  return e;
+}
+template <int D, bool SCALE = true>
+__device__ __forceinline__ int scale_row(h8 &v, bool &some) {
+  // (values without their signs are in the order of their bits: two at a time)
+  typedef uint16_t s2 __attribute__((ext_vector_type(2)));
+  typedef uint16_t s8 __attribute__((ext_vector_type(8)));
+  const s8 bits = __builtin_bit_cast(s8, __builtin_bit_cast(u4, v) & 0x7fff7fffu);
+  const s2 a = __builtin_elementwise_max(bits.s01, bits.s23), b = __builtin_elementwise_max(bits.s45, bits.s67);
+  s2 m = __builtin_elementwise_max(a, b);
+  m = row_most<D>(m, [](s2 x, s2 y) { return __builtin_elementwise_max(x, y); });
+  const float most = tqdev::half_bits(m[0] > m[1] ? m[0] : m[1]);
+  some = most > 0.0f;
+  const int e = __builtin_amdgcn_frexp_expf(most);
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    if (SCALE) v[j] = __builtin_amdgcn_ldexph(v[j], 14 - e);
   return e;
 }
 
 // Size (an exponent) of a row whose key or value is zero: far below any other's.
 constexpr int kNothing = -4000;
-
-// e with |v| < 2^e, at least -100 (so that scaling by 2^(14 - e) stays finite)
-__device__ __forceinline__ int exponent(float v) { return max(__builtin_amdgcn_frexp_expf(v), -100); }
 
 // U of a chunk and KV head, 64 rows at a time; further workgroups take the
 // largest element of the state that each sequence starts the pass from.  Bound: one
@@ -317,18 +348,17 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
   const T *kp = (const T *)A.qkv + (int64_t)c.begin * A.row_stride + (A.hq + h) * D;
   const T *vp = kp + A.hkv * D;
   // all rows are sent for at once
-  float k[kSteps][kPer][8], v[kSteps][kPer][8];
+  typedef typename std::conditional<kWide, f8, h8>::type Eight;
+  Eight k[kSteps][kPer], v[kSteps][kPer];
 #pragma unroll
   for (int t = 0; t < kSteps; t++)
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
       const int p = i * 512 + tid, row = t * kStep + p / (D / 8), at = p % (D / 8) * 8;
+      k[t][i] = v[t][i] = (Eight)(0);
       if (row < c.n) {
-        load8(kp + row * A.row_stride + at, k[t][i]);
-        load8(vp + row * A.row_stride + at, v[t][i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) k[t][i][j] = v[t][i][j] = 0.0f;
+        k[t][i] = load8(kp + row * A.row_stride + at);
+        v[t][i] = load8(vp + row * A.row_stride + at);
       }
     }
   if (wave == 0) {
@@ -365,16 +395,13 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
     for (int i = 0; i < kPer; i++) {
       const int p = i * 512 + tid, row = p / (D / 8), at = piece_at<D>(row, p % (D / 8)), all = t * kStep + row;
       const float f = __builtin_amdgcn_exp2f(left[all] + (float)(size[all] - unit));
-      float kw[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) kw[j] = k[t][i][j] * f;
+      const f8 kw = __builtin_convertvector(k[t][i], f8) * f;
       h8 a, b, x, y;
       two_terms(kw, a, b);
       if constexpr (kWide) {
         two_terms(v[t][i], x, y);
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = (_Float16)v[t][i][j];  // (exact but for what is 2^-37 of the row's largest)
+        x = v[t][i];
       }
       *reinterpret_cast<h8 *>(kh + at) = a;
       *reinterpret_cast<h8 *>(kl + at) = b;
@@ -504,7 +531,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
     for (int i = 0; i < kRun; i++) {
       const int c = c1 + i;
       if (c >= count) break;
-      const int e = reach > 0.0f ? exponent(reach) - 15 : kNoState;
+      const int e = reach > 0.0f ? __builtin_amdgcn_frexp_expf(fminf(reach, 3.0e38f)) - 15 : kNoState;
       const int sh16 = reach > 0.0f ? -e : 0;
       h4 o;
 #pragma unroll
@@ -544,10 +571,15 @@ __device__ __forceinline__ float half_max(float v) {
 // queries on their way meanwhile.  The block of 32 rows changes from head to
 // head, so that the waves' shares of the causal triangle come out even.
 //
-// A weight 2^(G_i - G_j) is a factor of the row and one of the token, both at
-// most 1, with the sum up to the end of the token's 32 between them; among the
-// row's own 32 tokens it is made as it stands.  Weights are put into fp16's
-// range by what their scores can reach, head_dim max |q| max |k|.
+// Values, and fp32 keys and queries, have the unit of their own row (fp16 keys and
+// queries stay as they are), and a row's weights, which take up the keys' and values',
+// one by what they can reach: with z_j the exponent of a token's largest key times its
+// largest value, h_j = z_j - G_j and H_i the largest h_j up to i (and 60 below the
+// state's), a weight is at most 2^(h_j - H_i) times head_dim max |q|, whatever was
+// forgotten before the row or comes behind it.  2^(h_j - H_i) is a factor of the row and
+// one of the token, both at most 1, with H at the end of the token's 32 between them;
+// among the row's own 32 tokens it is made as it stands.  (H_i is raised so that
+// H_i + G_i is whole.)
 //
 // Bound: 4096 fp32 rows, 64 and 8 heads of 128, 240 MB and 17 GFLOP (44 issued, for
 // second terms and whole blocks): 61 to 67 us, of them some 10 before the first
@@ -559,8 +591,10 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   constexpr int kLogD = D == 128 ? 7 : 6;
   __shared__ __attribute__((aligned(16))) _Float16 kt[kTerms][kChunk][D + 8];
   __shared__ __attribute__((aligned(16))) uint8_t vt[kChunk * 2 * D], stt[D * 2 * D];
-  __shared__ __attribute__((aligned(16))) float ghi[kChunk], glo[kChunk], wt[kChunk];
-  __shared__ float red[2][NW];
+  // of tokens: h in two terms, 2^(h - H of its 32); of rows and of 32 tokens: H
+  __shared__ __attribute__((aligned(16))) float hhi[kChunk], hlo[kChunk], wt[kChunk];
+  __shared__ float khi[kChunk], klo[kChunk], block[kChunk / 32];
+  __shared__ int size[kChunk], bias[kWide ? 1 : kChunk], ex[kChunk];  // z; 14 less an fp16 key's exponent; H + G
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t part = blockIdx.x % (uint32_t)A.parts, rh = blockIdx.x / (uint32_t)A.parts;
@@ -591,47 +625,33 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   const int es = A.meta[rs].e;
   const T *kp = (const T *)A.qkv + (int64_t)c.begin * A.row_stride + (A.hq + h) * D;
   const T *vp = kp + A.hkv * D;
-  int bk, ek = 14, ev = 14;  // |k| < 2^bk; kt holds k * 2^(14 - ek), vt v * 2^(14 - ev): fp16 inputs are taken as they are
   {
-    float k[kPer][8], v[kPer][8], mk = 0.0f, mv = 0.0f;
+    typedef typename std::conditional<kWide, f8, h8>::type Eight;
+    Eight k[kPer], v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
       const int p = i * NT + tid, row = p / (D / 8), at = p % (D / 8) * 8;
+      k[i] = v[i] = (Eight)(0);
       if (row < c.n) {
-        load8(kp + row * A.row_stride + at, k[i]);
-        load8(vp + row * A.row_stride + at, v[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) k[i][j] = v[i][j] = 0.0f;
+        k[i] = load8(kp + row * A.row_stride + at);
+        v[i] = load8(vp + row * A.row_stride + at);
       }
     }
     u4 sp[D * (D / 8) / NT];
     // (sent for before its exponent is known: without a state it is not used)
 #pragma unroll
     for (int i = 0; i < D * (D / 8) / NT; i++) sp[i] = reinterpret_cast<const u4 *>(A.snap + rs * (D * D))[i * NT + tid];
-    if (wave == 0) {
-      double d0, d1;
-      decay_sums(A, c, h, d0, d1);
-      const double last = __shfl(d1, lane | 15);  // up to the end of the row's 32
-      ghi[2 * lane] = (float)d0;
-      glo[2 * lane] = (float)(d0 - (double)(float)d0);
-      wt[2 * lane] = __builtin_amdgcn_exp2f((float)(last - d0));
-      ghi[2 * lane + 1] = (float)d1;
-      glo[2 * lane + 1] = (float)(d1 - (double)(float)d1);
-      wt[2 * lane + 1] = __builtin_amdgcn_exp2f((float)(last - d1));
-    }
+    double g0 = 0.0, g1 = 0.0;
+    if (wave == 0) decay_sums(A, c, h, g0, g1);
 #pragma unroll
-    for (int i = 0; i < kPer; i++)
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        mk = fmaxf(mk, fabsf(k[i][j]));
-        mv = fmaxf(mv, fabsf(v[i][j]));
+    for (int i = 0; i < kPer; i++) {
+      const int p = i * NT + tid;
+      bool a, b;
+      const int ek = scale_row<D, kWide>(k[i], a), ev = scale_row<D>(v[i], b);
+      if (p % (D / 8) == 0) {
+        size[p / (D / 8)] = a && b ? ek + ev : kNothing;
+        if (!kWide) bias[p / (D / 8)] = 14 - ek;
       }
-    mk = tqdev::wave_max64(mk);
-    mv = tqdev::wave_max64(mv);
-    if (lane == 0) {
-      red[0][wave] = mk;
-      red[1][wave] = mv;
     }
     if (es != kNoState) {
 #pragma unroll
@@ -640,35 +660,40 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
         *reinterpret_cast<u4 *>(stt + piece_at<D>(p / (D / 8), p % (D / 8))) = sp[i];
       }
     }
-    __syncthreads();
-    mk = mv = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NW; i++) {
-      mk = fmaxf(mk, red[0][i]);
-      mv = fmaxf(mv, red[1][i]);
-    }
-    bk = exponent(mk);
-    if (kWide) {
-      ek = bk;
-      ev = exponent(mv);
-    }
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
       const int p = i * NT + tid, row = p / (D / 8), at = p % (D / 8);
       h8 a, l, b;
       if constexpr (kWide) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) k[i][j] *= power(14 - ek);
         two_terms(k[i], a, l);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        if (!kWide) a[j] = (_Float16)k[i][j];
-        b[j] = (_Float16)(kWide ? v[i][j] * power(14 - ev) : v[i][j]);
+        b = __builtin_convertvector(v[i], h8);
+      } else {
+        a = k[i];
+        b = v[i];
       }
       *reinterpret_cast<h8 *>(&kt[0][row][8 * at]) = a;
       if constexpr (kWide) *reinterpret_cast<h8 *>(&kt[1][row][8 * at]) = l;
       *reinterpret_cast<h8 *>(vt + piece_at<D>(row, at)) = b;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      double h0 = size[2 * lane] - g0, h1 = size[2 * lane + 1] - g1;
+      // (largest ones to fp32's accuracy are enough: a weight may then pass its bound by as much)
+      const float least = es != kNoState ? (float)(es + 15 - kLogD - 60) : -1e9f;
+      const float m1 = fmaxf(wave_most_upto(fmaxf((float)h0, (float)h1)), least);
+      const float before = __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(least), __float_as_int(m1), 0x138, 0xF, 0xF, false));
+      const float m0 = fmaxf(before, (float)h0), last = __shfl(m1, lane | 15);  // up to the row, up to the end of its 32
+      const double e0 = ceil((double)m0 + g0), e1 = ceil((double)m1 + g1), k0 = e0 - g0, k1 = e1 - g1;
+      const int r = 2 * lane;
+      if (!kWide) h0 += bias[r], h1 += bias[r + 1];  // (keys as they are)
+      ex[r] = (int)e0, ex[r + 1] = (int)e1;
+      khi[r] = (float)k0, klo[r] = (float)(k0 - (double)(float)k0);
+      khi[r + 1] = (float)k1, klo[r + 1] = (float)(k1 - (double)(float)k1);
+      hhi[r] = (float)h0, hlo[r] = (float)(h0 - (double)(float)h0);
+      hhi[r + 1] = (float)h1, hlo[r + 1] = (float)(h1 - (double)(float)h1);
+      wt[r] = __builtin_amdgcn_exp2f((float)(h0 - (double)last));
+      wt[r + 1] = __builtin_amdgcn_exp2f((float)(h1 - (double)last));
+      if ((lane & 15) == 15) block[lane >> 4] = last;
     }
   }
   __syncthreads();
@@ -686,7 +711,7 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   // loop: with a copy a block, 28 to 43 KB of code against 11 to 15, most of which a
   // wave runs once, fetching it took longer: 3 x 2051 fp16 rows 39 against 34 us.)
   auto rows = [&](int RB, int i, const h8 (&qf)[kTerms][D / 16], int bq) {
-    const int row = 32 * RB + n, head = h * A.group + g0 + head_of(i), eq = kWide ? bq : 14;
+    const int row = 32 * RB + n, head = h * A.group + g0 + head_of(i);
     if (32 * RB >= c.n || head_of(i) >= heads) {
       send_for(min(i + 1, rounds - 1), kFirst, kPieces);
 #pragma unroll
@@ -694,11 +719,10 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
       return;
     }
     // o^T: o[d][r] is element 32 d + 8 (r / 4) + 4 half + r % 4 of the row, in
-    // units of 2^x: weights are below 2^15 in it, the state's part below 2^97
-    const int xs = eq - 14 + es;
-    int x = bq + bk + kLogD + ev - 29;
-    const float gh = ghi[row], gl = glo[row], whole = floorf(gh);
-    if (es != kNoState) x = max(x, xs + (int)whole - 60);  // (of what is left of it at this row)
+    // units of 2^(ex + bq + kLogD - 29): weights are below 2^15 in it, the state's part
+    // below 2^97 (fp32 queries are scaled by 2^(14 - bq), fp16 ones as they are)
+    const float kh = khi[row], kl = klo[row];
+    const float unit = power((kWide ? 0 : 14 - bq) - 13 - kLogD);
     f16x o[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; d++) o[d] = (f16x)(0.0f);
@@ -711,13 +735,13 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qf[0][j], o[d], 0, 0, 0);
           if constexpr (kWide) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, qf[1][j], o[d], 0, 0, 0);
         }
-      const float f = ldexpf(__builtin_amdgcn_exp2f((gh - whole) + gl), max(xs + (int)whole - x, -300));
+      float f = __builtin_amdgcn_exp2f(((float)(es + 15 - kLogD) - kh) - kl);
+      if (!kWide) f = ldexpf(f, 14 - bq);
 #pragma unroll
       for (int d = 0; d < D / 32; d++)
 #pragma unroll
         for (int r = 0; r < 16; r++) o[d][r] *= f;
     }
-    const int xp = max((eq - 14) + (ek - 14) + (ev - 14) - x, -300);
     auto tile = [&](auto last_tile, int t) {
       constexpr bool kLast = decltype(last_tile)::value;
       // scores S^T = K Q^T: sc[r] is token 32 t + 16 (r / 8) + 8 half + r % 8
@@ -737,15 +761,15 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
       // weights: two fp16 terms, so that they lose nothing to the outputs' rounding
       const int j0 = 32 * t + 8 * half;
       h8 p[2], pl[2];
-      const float f = kLast ? 0.0f : ldexpf(__builtin_amdgcn_exp2f((gh - ghi[32 * t + 31]) + (gl - glo[32 * t + 31])), xp);
+      const float f = kLast ? 0.0f : __builtin_amdgcn_exp2f((block[t] - kh) - kl) * unit;
 #pragma unroll
       for (int u = 0; u < 2; u++) {
-        float w[8];
+        f8 w;
 #pragma unroll
         for (int r = 0; r < 8; r++) {
           const int j = j0 + 16 * u + r;
           if (kLast) {
-            w[r] = sc[8 * u + r] * ldexpf(__builtin_amdgcn_exp2f((gh - ghi[j]) + (gl - glo[j])), xp);
+            w[r] = sc[8 * u + r] * (__builtin_amdgcn_exp2f((hhi[j] - kh) + (hlo[j] - kl)) * unit);
             w[r] = j <= row ? w[r] : 0.0f;
           } else {
             w[r] = sc[8 * u + r] * (wt[j] * f);
@@ -765,9 +789,9 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
 #pragma unroll 1
     for (int t = 0; t < RB; t++) tile(std::false_type(), t);
     tile(std::true_type(), RB);
-    // (held within fp32's exponents: sums are 0 or 2^-48 to 2^98, so a result
-    // that fp16 holds is not changed)
-    const float last = scale_m * power(x + scale_e);
+    // (held within fp32's exponents: sums are 0 or 2^-48 to 2^98, but for a state that is
+    // nothing beside them, so a result that fp16 holds is not changed)
+    const float last = scale_m * power(ex[row] + bq + kLogD - 29 + scale_e);
     // two quads' halves change places between the halves of the wave: 16 bytes a lane
     const uint32_t to = row < c.n ? 2u * (uint32_t)(row * (int)A.out_stride + head * D + 8 * half) : kNowhere;
 #pragma unroll
@@ -794,14 +818,13 @@ __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
     for (int j = 0; j < kPieces; j++)
 #pragma unroll
       for (int r = 0; r < (kWide ? 4 : 8); r++) mq = fmaxf(mq, fabsf((float)raw[j][r]));
-    const int bq = exponent(half_max(mq));
+    const int bq = __builtin_amdgcn_frexp_expf(half_max(mq));
     if constexpr (kWide) {
-      const float f = power(14 - bq);
 #pragma unroll
       for (int j = 0; j < D / 16; j++) {
-        float x[8];
+        f8 x;
 #pragma unroll
-        for (int r = 0; r < 8; r++) x[r] = (float)raw[kPieces / (D / 16) * j + (r >> 2)][r & 3] * f;
+        for (int r = 0; r < 8; r++) x[r] = ldexpf((float)raw[kPieces / (D / 16) * j + (r >> 2)][r & 3], 14 - bq);
         two_terms(x, qf[0][j], qf[kTerms - 1][j]);
       }
     } else {

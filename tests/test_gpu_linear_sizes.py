@@ -170,3 +170,55 @@ def test_outputs_behind_a_forgotten_state(heads, dtype, decay):
             c["decay"] *= 10
             c["decay"] -= 1.5
         run(c)
+
+
+@pytest.mark.parametrize("rows", FORGOTTEN)
+@pytest.mark.parametrize("dtype,times", [("f16", 12000.0), ("f32", 1e4), ("f32", 1e6), ("f32", 1e10), ("f32", 1e15)])
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64), (1, 1, 128)], ids=str)
+def test_outputs_behind_forgotten_rows(heads, dtype, times, rows):
+    say(f"forgotten, outputs {heads} {dtype} {times} {rows}")
+    run(forgotten(heads, dtype, times, FORGOTTEN[rows]))
+
+
+@pytest.mark.parametrize("which", ["keys", "values", "queries"])
+@pytest.mark.parametrize("dtype,e", [("f16", 13), ("f32", 28), ("f32", 32), ("f32", 40), ("f32", 70)])
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64), (1, 1, 128)], ids=str)
+def test_outputs_before_a_large_row(heads, dtype, e, which):
+    """A key, value or query 2^e as large at the end of the chunk, and in the middle of 32 rows."""
+    say(f"before a large row {heads} {dtype} {e} {which}")
+    c = make(heads, [300], dtype, seed=44)
+    for r in (127, 128 + 77):
+        c["qkv"][r, part(c, which)] *= 2.0 ** e
+        c["decay"][r + 1] = -INF
+    run(c)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64), (1, 1, 128)], ids=str)
+def test_outputs_of_rows_of_all_sizes(heads, dtype):
+    """Queries, keys and values each by their own power of two, decays that halve and more."""
+    say(f"all sizes, outputs {heads} {dtype}")
+    for seed in (45, 46):
+        c = make(heads, [333], dtype, seed=seed)
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        most = 10 if dtype == "f16" else 36
+        for which in ("queries", "keys", "values"):
+            e = torch.randint(-most, most + 1, (333, 1), generator=g, device="cuda")
+            c["qkv"][:, part(c, which)] *= torch.exp2(e.float()).to(TYPES[dtype])
+        c["decay"] *= 20
+        c["scale"] *= 2.0 ** (-most // 2)
+        run(c)
+
+
+def test_small_rows_of_fp32():
+    """Keys near fp32's least normal numbers, values (or queries) that make up for them."""
+    for heads in ((4, 2, 128), (2, 2, 64)):
+        c = make(heads, [200], "f32", seed=47)
+        c["qkv"][:, part(c, "keys")] *= 2.0 ** -115
+        c["qkv"][:, part(c, "values")] *= 2.0 ** 100
+        c["qkv"][:, part(c, "queries")] *= 2.0 ** 15
+        run(c)
+        c["qkv"][:, part(c, "keys")] *= 2.0 ** 115
+        c["qkv"][:, part(c, "queries")] *= 2.0 ** -130
+        run(c)
