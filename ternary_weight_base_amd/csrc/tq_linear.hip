@@ -231,17 +231,11 @@ struct Turned {
   }
 };
 
-// x as two fp16 terms, together within 2^-20 of it (or the least fp16 step):
-// the first cut off, two elements an instruction.
+// x as two fp16 terms, together within 2^-23 of it (or half the least fp16 step), two
+// elements an instruction.
 __device__ __forceinline__ void two_terms(const f8 &x, h8 &hi, h8 &lo) {
-  typedef __fp16 c2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const c2 a = __builtin_amdgcn_cvt_pkrtz(x[i], x[i + 1]);
-    const c2 b = __builtin_amdgcn_cvt_pkrtz(x[i] - (float)a[0], x[i + 1] - (float)a[1]);
-    hi[i] = (_Float16)a[0], hi[i + 1] = (_Float16)a[1];
-    lo[i] = (_Float16)b[0], lo[i + 1] = (_Float16)b[1];
-  }
+  hi = __builtin_convertvector(x, h8);
+  lo = __builtin_convertvector(x - __builtin_convertvector(hi, f8), h8);
 }
 
 // 2^e as a factor, e within fp32's exponents

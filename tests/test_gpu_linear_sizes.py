@@ -222,3 +222,24 @@ def test_small_rows_of_fp32():
         c["qkv"][:, part(c, "keys")] *= 2.0 ** 115
         c["qkv"][:, part(c, "queries")] *= 2.0 ** -130
         run(c)
+
+
+@pytest.mark.parametrize("n", [128, 1500])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("heads", [(2, 2, 128), (2, 2, 64)], ids=str)
+def test_states_have_fp32s_accuracy(heads, dtype, n):
+    """Root mean squares over a state, of terms of either sign, relative to the
+    state's: a factor of two terms is off by up to 2^-23 evenly (2^-23.8 in the mean
+    square, 2^-23.3 for two factors), the product of the second terms, 2^-11 each,
+    is not taken (2^-11.8 each: 2^-23.6), a weight is an exp2 within 2^-23, and 24
+    steps of 16 products a chunk are added in fp32 (2^-24.8 of a partial sum, some
+    0.7 of the whole, each: 2^-23).  Together sqrt(2^-46.6 + 2^-47.2 + 2 * 2^-46) =
+    2^-22.2, where an fp32 product and sum of 128 rows has about 2^-23."""
+    from linear_util import linear
+    from test_gpu_linear import call
+    c = make(heads, [n], dtype, seed=48)
+    _, states = call(c)
+    S = linear(c["qkv"], c["decay"], c["cu"], c["from"], c["to"], c["states"], c["scale"], *heads)[2][c["to"][0]][0]
+    got = float((states[c["to"][0]].double() - S).norm() / S.norm())
+    say(f"states {heads} {dtype} {n}: {got:.3g}")
+    assert got <= 2.0 ** -22
