@@ -103,7 +103,9 @@ SharedPlan make_shared_plan(int64_t rows, int64_t seqs, int64_t groups, int64_t 
 }
 
 int check_lens(int64_t groups, int64_t max_prefix, int64_t max_own) {
-  return groups < 1 || groups > ((int64_t)1 << 20) || max_prefix < 0 || max_own < 1 || max_prefix + max_own > 0x7fffffff - kPage
+  // (each by itself first: their sum could pass 64 bits)
+  return groups < 1 || groups > ((int64_t)1 << 20) || max_prefix < 0 || max_own < 1 || max_prefix > 0x7fffffff ||
+                 max_own > 0x7fffffff || max_prefix + max_own > 0x7fffffff - kPage
              ? TQ_ERR_SHAPE
              : TQ_OK;
 }

@@ -39,6 +39,15 @@ def test_kv_attn_shared_validates_on_host():
         assert tq.tq_kv_attn_shared_workspace_bytes(*bad) == 0
 
 
+def test_lengths_at_the_end_of_64_bits():
+    """Their sum is not taken before each is known to be small."""
+    end = (1 << 63) - 1
+    for xp, xo in ((end, 1), (end, end), (0, end), (end - 63, 256), (1 << 62, 1 << 62), ((1 << 31) - 1, 1), (1, (1 << 31) - 64)):
+        assert _call(xp=xp, xo=xo) == SHAPE, (xp, xo)
+        assert _call(rows=64, seqs=64, xp=xp, xo=xo) == SHAPE, (xp, xo)
+        assert tq.tq_kv_attn_shared_workspace_bytes(64, 64, 2, 8, 2, 128, xp, xo) == 0, (xp, xo)
+
+
 def test_workspace_is_bounded():
     most = max(tq.tq_kv_attn_shared_workspace_bytes(rows, seqs, groups, hq, hkv, dim, prefix, own)
                for rows in (1, 33, 130, 1040, 4096, 30000) for seqs in (1, 20, 64, 300) for groups in (1, 4, 20) if groups <= seqs
