@@ -449,15 +449,43 @@ __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
   if (tid == 0) meta->most_u = m;
 }
 
+// The sum over a lane's eight.
+__device__ __forceinline__ float row_sum8(float v) {
+  v += __int_as_float(tqdev::dpp_move<tqdev::kDppSwap1>(__float_as_int(v)));
+  v += __int_as_float(tqdev::dpp_move<tqdev::kDppSwap2>(__float_as_int(v)));
+  return v + __int_as_float(tqdev::dpp_move<0x141>(__float_as_int(v)));
+}
+
 // The states before each chunk (fp16, scaled), and the last one: 256 elements a
 // workgroup, four a thread, and a run of kRun chunks a wave.  With four waves, each
 // takes its run from zero first, S' = P S + T; what the runs before it make of the
 // state it gets from their P and T.  Bound: latency (32 chunks of 8 KV heads of 128,
 // 25 MB: 8 us; by one wave, chunk after chunk, 14).
+//
+// A decay is a product of two factors (of which the second is mostly 1): one alone may be
+// below fp32's least number while what it leaves of a large state is not.
+struct Factors {
+  float a, b;
+  __device__ __forceinline__ Factors(float log2) {
+    const float whole = ceilf(log2);
+    const int e = max((int)whole, -1000), e1 = max(e, -125);
+    a = ldexpf(__builtin_amdgcn_exp2f(log2 - whole), e1);
+    b = ldexpf(1.0f, e - e1);
+  }
+  __device__ __forceinline__ Factors(float a, float b) : a(a), b(b) {}
+  __device__ __forceinline__ Factors at(int lane) const {
+    return Factors(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(a), lane)),
+                   __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(b), lane)));
+  }
+  template <typename V>
+  __device__ __forceinline__ V operator*(V v) const { return v * a * b; }
+};
+
 template <int D, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
   constexpr uint32_t kBlocks = D * D / 256;
   constexpr int kRun = kScanRun, kSpan = kRun * kWaves;
+  static_assert(kRun == 8, "a run's decays are summed over eight lanes");
   __shared__ f4 runs[kWaves > 1 ? kWaves : 1][64];
   // (heads fastest, as in the other launches, so that a head stays on an XCD: 8.1 against 8.9 us)
   const uint32_t rest = blockIdx.x / (uint32_t)A.hkv, blk = rest % kBlocks;
@@ -475,12 +503,15 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
   _Float16 *snap = A.snap + r0 * (D * D) + at;
   Meta *meta = A.meta + r0;
   f4 x[kRun];
-  float decay, most;  // of chunk c0 + lane
+  Factors decay(0.0f), decay8(0.0f);  // of chunk c0 + lane, of the run that it is in
+  float most;
   auto send_for = [&](int c0) {
 #pragma unroll
     for (int i = 0; i < kRun; i++) x[i] = *reinterpret_cast<const f4 *>(u + min(c0 + wave * kRun + i, count - 1) * step);
     const Meta m = meta[(int64_t)min(c0 + lane, count - 1) * A.hkv];
-    decay = c0 + lane < count ? __builtin_amdgcn_exp2f(m.decay) : 1.0f;
+    const float d = c0 + lane < count ? m.decay : 0.0f;
+    decay = Factors(d);
+    if (kWaves > 1) decay8 = Factors(row_sum8(d));
     most = c0 + lane < count ? m.most_u : 0.0f;
   };
   send_for(0);
@@ -489,7 +520,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
   if (lo > base) S = *reinterpret_cast<const f4 *>(A.carried + (int64_t)h * (D * D) + at);
   else if (state_ok(A, from)) S = *reinterpret_cast<const f4 *>(A.states + ((int64_t)from * A.hkv + h) * (D * D) + at);
   float bound = meta->most_s;  // of |S|, from the chunks' largest elements
-  auto of_chunk = [](float v, int c) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), c)); };
+  auto most_of = [&](int c) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(most), c)); };
 #pragma unroll 1
   for (int c0 = 0; c0 < count; c0 += kSpan) {
     const int c1 = c0 + wave * kRun;
@@ -500,7 +531,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
 #pragma unroll
       for (int i = 0; i < kRun; i++) {
         if (c1 + i >= count) x[i] = (f4){0, 0, 0, 0};
-        T = T * of_chunk(decay, wave * kRun + i) + x[i];
+        T = decay.at(wave * kRun + i) * T + x[i];
       }
       runs[wave][lane] = T;
       __syncthreads();
@@ -511,14 +542,9 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
           reach = bound;
         }
         if (c0 + w * kRun >= count) break;
-        float P = 1.0f;
 #pragma unroll
-        for (int i = 0; i < kRun; i++) {
-          const float a = of_chunk(decay, w * kRun + i);
-          P *= a;
-          bound = bound * a + of_chunk(most, w * kRun + i);
-        }
-        S = S * P + runs[w][lane];
+        for (int i = 0; i < kRun; i++) bound = decay.at(w * kRun + i) * bound + most_of(w * kRun + i);
+        S = decay8.at(w * kRun) * S + runs[w][lane];
       }
     }
 #pragma unroll
@@ -532,9 +558,9 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
       for (int j = 0; j < 4; j++) o[j] = (_Float16)ldexpf(mine[j], sh16);
       *reinterpret_cast<h4 *>(snap + c * step) = o;
       if (blk == 0 && lane == 0) meta[(int64_t)c * A.hkv].e = e;
-      const float a = of_chunk(decay, wave * kRun + i);
-      reach = reach * a + of_chunk(most, wave * kRun + i);
-      mine = mine * a + x[i];
+      const Factors f = decay.at(wave * kRun + i);
+      reach = f * reach + most_of(wave * kRun + i);
+      mine = f * mine + x[i];
     }
     if constexpr (kWaves == 1) {
       S = mine;

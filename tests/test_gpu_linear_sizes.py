@@ -243,3 +243,18 @@ def test_states_have_fp32s_accuracy(heads, dtype, n):
     got = float((states[c["to"][0]].double() - S).norm() / S.norm())
     say(f"states {heads} {dtype} {n}: {got:.3g}")
     assert got <= 2.0 ** -22
+
+
+@pytest.mark.parametrize("dtype,size", [("f32", 1e-9), ("f16", 1e-4)])
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64)], ids=str)
+def test_what_strong_decays_leave_of_a_large_state(heads, dtype, size):
+    """Decays of a chunk, or of eight, below fp32's least number, and what they leave is still the largest part."""
+    say(f"large state decays {heads} {dtype}")
+    for n, decay in (([128], -0.85), ([140], -0.85), ([1500], -0.1), ([1025, 40], -0.1), ([40, 77], -2.0)):
+        c = make(heads, n, dtype, seed=49, size=size)
+        c["from"] = list(range(len(n)))
+        c["to"] = [len(n) + i for i in range(len(n))]
+        c["states"] *= 2.0 ** 120 / size ** 2
+        c["states"].clamp_(-2.0 ** 123, 2.0 ** 123)
+        c["decay"] = torch.full_like(c["decay"], decay)
+        run(c)
