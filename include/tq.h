@@ -549,12 +549,14 @@ int tq_kv_attn_shared(int64_t rows, int64_t seqs, int64_t groups, int64_t q_head
 size_t tq_linear_attn_scratch_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t kv_heads,
                                     int64_t head_dim);
 
-/* Linear attention with a decay for each head and a recurrent state (the
- * pages' model keeps one beside its KV cache, "Ternary Bonsai 2 27B：8GB 显卡硬塞
- * 27B 三元模型…"): for each KV head, over a sequence's rows t in order,
+/* Linear attention with a decay for each head and a recurrent state: for each
+ * KV head, over a sequence's rows t in order,
  *   S_t = exp(log_decay[t]) S_{t-1} + k_t v_t^T,  out_t = scale q_t^T S_t
- * with S fp32 [head_dim][head_dim], key index first.  Rows, heads and cu_rows as
- * above; a row of qkv (dtype, row_stride a multiple of 8) as in tq_kv_append.
+ * with S fp32 [head_dim][head_dim], key index first.  (The pages' model keeps a
+ * recurrent state beside its KV cache, "Ternary Bonsai 2 27B：8GB 显卡硬塞 27B 三元模型…",
+ * but they give no formula for it.  This is the one above: a model whose state follows
+ * another, as a delta rule or a decay for each key element, cannot use this call.)
+ * Rows, heads and cu_rows as above; a row of qkv (dtype, row_stride a multiple of 8) as in tq_kv_append.
  *   log_decay: fp32, [kv_heads] for all rows (decay_stride 0) or rows
  *     decay_stride >= kv_heads elements apart.  Above 0 (growth) counts as 0,
  *     very low (-inf too) as a factor of 0.
@@ -569,9 +571,14 @@ size_t tq_linear_attn_scratch_bytes(int64_t rows, int64_t seqs, int64_t q_heads,
  * Up to 16 rows a sequence, on average, the recurrence runs row by row in fp32
  * (one launch, no scratch); more run in chunks of 128 rows (three launches for
  * up to 2^27 bytes of scratch), where states keep fp32's accuracy; for the
- * outputs fp32 values and the states before each chunk are rounded to fp16
- * (scaled: no size overflows).  A sequence of many rows beside many single
- * tokens is better a call of its own.  Non-finite inputs make their sequence's
+ * outputs fp32 values and the states before each chunk are rounded to fp16.
+ * Operands are fp16 scaled for each row, so no size overflows; with
+ * R_t = exp(log_decay[t]) R_{t-1} + max|k_t| max|v_t| (R before the first row: the
+ * largest element of the start), parts of a state below 2^-28 R_t, and of an output
+ * below 2^-28 scale head_dim max|q_t| R_t, may be lost.
+ * The form is chosen for the call: a sequence of many rows beside many single
+ * tokens is better a call of its own (900 rows beside 63 single tokens, 64 and 8
+ * heads of 128: 2.8 ms, row after row; in two calls 47 us).  Non-finite inputs make their sequence's
  * outputs and state for that KV head (from the chunk on that holds them)
  * unspecified, those of no other.  qkv, states, out and scratch 16-byte aligned;
  * out does not overlap qkv. */
@@ -630,7 +637,11 @@ size_t tq_sample_workspace_bytes(int64_t rows, int64_t vocab);
  * logprob (fp32, may be NULL): ln of the token's w over the kept tokens' sum (0
  * where the largest logit is taken).
  * Weights and sums are in double; a row's token does not depend on the other
- * rows.  1 <= rows <= 2^20, 1 <= vocab <= 2^20.  logits 16-byte aligned (its
+ * rows.  Some rows are done by one workgroup and take 0.9 ms where 0.03 is usual (131072
+ * logits): with a top_k above 1024 and a top_p below 1; and of nearly equal logits,
+ * more than 16384 tokens within an eighth (of the temperature, if below 1, for top_p)
+ * of the one in which the limit falls, or 4096 from there up for a top_k up to 1024.
+ * 1 <= rows <= 2^20, 1 <= vocab <= 2^20.  logits 16-byte aligned (its
  * rows need not be). */
 int tq_sample(int dtype, int64_t rows, int64_t vocab, const void *logits, int64_t row_stride,
               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,

@@ -46,7 +46,8 @@
 //   64 sequences of up to 32 K tokens  436 us   6.2 TB/s
 //   8 sequences of up to 6001, 4 rows   27 us   2.6 TB/s
 //   a prompt of 4096 tokens            315 us   870 TFLOP/s
-// decode_kernel<128, 2, false> takes 256 registers and spills 11 more.
+// decode_kernel<128, 2, false> takes 256 registers and spills 12 more (over own keys
+// behind a prefix 23, over a prefix 10), and prefill_kernel<128> over own keys 4.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

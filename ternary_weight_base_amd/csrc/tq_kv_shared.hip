@@ -92,7 +92,9 @@ SharedPlan make_shared_plan(int64_t rows, int64_t seqs, int64_t groups, int64_t 
   // launch takes besides, and the prefix's results, written, read and cleared.  (8 x 1
   // rows, 300 behind 2048: 15.6 us in one, 23.2 in two; 4 x 1 behind 8192 18.7 and 38,
   // 16 x 1 38 and 36, 64 x 1 121 and 54, 64 x 1 behind 16384 261 and 78; 16 x 150,
-  // 32 heads, 203 behind 4096, 205 and 225.)
+  // 32 heads, 203 behind 4096, 205 and 225.  Of 22 calls around the border 17
+  // take the faster way, four lose 5 to 10 % and one 16 %: 16 x 20, 32 heads, 200 behind
+  // 4096, 65 in one against 56 in two, for 50 and 60 by the estimate.)
   const double one = 9.0 + tiles_us(rows, seqs, q_heads, kv_heads, head_dim, max_prefix + max_own, all.tile_rows);
   const double two = 24.0 + tiles_us(rows, groups < seqs ? groups : seqs, q_heads, kv_heads, head_dim, max_prefix, S.prefix.tile_rows) +
                      tiles_us(rows, seqs, q_heads, kv_heads, head_dim, max_own, S.own.tile_rows) + (double)mid * 2.0 / 8.5e6;

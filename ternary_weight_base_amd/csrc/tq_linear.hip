@@ -16,13 +16,16 @@
 // in three launches: every chunk's U; the states before each chunk, element by
 // element along the chunks; every chunk's outputs.
 //
-// Products run on v_mfma_f32_32x32x16_f16, sums in fp32.  fp16 operands are
-// scaled by powers of two into its range, so no size of input overflows it.
-// U is of two fp16 terms a factor (fp16 inputs: the keys with their weights
-// two, the values are exact down to 2^-38 of the row's largest), each row scaled by its own size and by what is left
-// of it at the chunk's end.  For the
-// outputs, which are fp16, queries, keys and weights have two terms each; fp32
-// values and the states before a chunk are rounded to fp16 once.
+// Products run on v_mfma_f32_32x32x16_f16, sums in fp32.  fp16 operands are scaled by
+// powers of two, each row by its own size and by what is left of it where it is used, so
+// that no size of input overflows them and no row takes another's bits.
+// U is of two fp16 terms a factor (fp16 inputs: the keys with their weights two, the
+// values are exact down to 2^-38 of the row's largest): a term is within 2^-22 of itself,
+// the state as near as fp32 sums (a prompt's: 1.1e-7 off, plain fp32 0.8e-7).
+// For the outputs, which are fp16, queries, keys and weights have two terms each; fp32
+// values and the states before a chunk are rounded to fp16 once (outputs 0.00029 off
+// in place of 0.00021, which their own rounding is).  Second terms of those would take
+// 64 KB more LDS than a CU has beside fp32 keys of 128, and a third more products.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -294,7 +297,7 @@ constexpr int kNothing = -4000;
 // U of a chunk and KV head, 64 rows at a time; further workgroups take the
 // largest element of the state that each sequence starts the pass from.  Bound: one
 // workgroup a CU in turn waits for its rows, converts and multiplies them (4096 fp32
-// rows of 8 KV heads of 128, 50 MB: 16.5 us, of them 6.5 the loads and 3 the stores;
+// rows of 8 KV heads of 128, 50 MB: 14 to 16.5 us, of them 6.5 the loads and 3 the stores;
 // in halves of 64 columns, two workgroups a CU, no faster).
 template <int D, typename T>
 __global__ __launch_bounds__(512) void chunk_state_kernel(const LinArgs A) {
@@ -456,14 +459,8 @@ __device__ __forceinline__ float row_sum8(float v) {
   return v + __int_as_float(tqdev::dpp_move<0x141>(__float_as_int(v)));
 }
 
-// The states before each chunk (fp16, scaled), and the last one: 256 elements a
-// workgroup, four a thread, and a run of kRun chunks a wave.  With four waves, each
-// takes its run from zero first, S' = P S + T; what the runs before it make of the
-// state it gets from their P and T.  Bound: latency (32 chunks of 8 KV heads of 128,
-// 25 MB: 8 us; by one wave, chunk after chunk, 14).
-//
-// A decay is a product of two factors (of which the second is mostly 1): one alone may be
-// below fp32's least number while what it leaves of a large state is not.
+// A decay, as a product of two factors (of which the second is mostly 1): one alone may
+// be below fp32's least number while what it leaves of a large state is not.
 struct Factors {
   float a, b;
   __device__ __forceinline__ Factors(float log2) {
@@ -481,6 +478,11 @@ struct Factors {
   __device__ __forceinline__ V operator*(V v) const { return v * a * b; }
 };
 
+// The states before each chunk (fp16, scaled), and the last one: 256 elements a
+// workgroup, four a thread, and a run of kRun chunks a wave.  With four waves, each
+// takes its run from zero first, S' = P S + T; what the runs before it make of the
+// state it gets from their P and T.  Bound: latency (32 chunks of 8 KV heads of 128,
+// 25 MB: 9 us; by one wave, chunk after chunk, 14; decays as one factor: 8).
 template <int D, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
   constexpr uint32_t kBlocks = D * D / 256;
@@ -602,8 +604,8 @@ __device__ __forceinline__ float half_max(float v) {
 // H_i + G_i is whole.)
 //
 // Bound: 4096 fp32 rows, 64 and 8 heads of 128, 240 MB and 17 GFLOP (44 issued, for
-// second terms and whole blocks): 61 to 67 us, of them some 10 before the first
-// product, one workgroup a CU (137 KB of LDS).  Matrix pipes busy 32 %, VALU 29 %.
+// second terms and whole blocks): 60 to 69 us, of them some 10 before the first
+// product, one workgroup a CU (139 KB of LDS).  Matrix pipes busy 34 %, VALU 33 %.
 template <int D, typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void chunk_out_kernel(const LinArgs A) {
   constexpr bool kWide = std::is_same<T, float>::value;

@@ -432,8 +432,10 @@ __global__ __launch_bounds__(NT) void row_kernel(const SampleArgs A) {
 //  - the gathered ones are narrowed down by the 256ths, what is left is sorted and
 //    cut, and the token taken.
 // A row that gathers more than kGather tokens or has more than kSort left (flat
-// logits), or has a larger top_k and top_p too, is done by the last launch's
-// workgroup alone, as above.  Bound: a row's workgroups by their instructions (a CU
+// logits), or has a top_k above kFewK and top_p too, is done by the last launch's
+// workgroup alone, as above: one row of 131072 logits by top-k and top-p takes 26 us
+// with a top_k of 1024 and 853 with 1025, 64 rows 35 and 991 (kFewK tokens are two
+// a thread of that launch; top-k beyond it alone 26 and 39).  Bound: a row's workgroups by their instructions (a CU
 // issues one a cycle) and dependent trips to memory, the segments' for many rows by
 // the weights in double (64 rows of 131072 by top-p: 18 us, by top-k, which needs none
 // there, 9, reading 34 MB).  (Instead of the launches for a row, the last of its
