@@ -521,7 +521,9 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
   f4 S = {0, 0, 0, 0};
   if (lo > base) S = *reinterpret_cast<const f4 *>(A.carried + (int64_t)h * (D * D) + at);
   else if (state_ok(A, from)) S = *reinterpret_cast<const f4 *>(A.states + ((int64_t)from * A.hkv + h) * (D * D) + at);
-  float bound = meta->most_s;  // of |S|, from the chunks' largest elements
+  // of |S|, from the chunks' largest elements, held within fp32 (an infinite one would stay, as NaN, behind a reset)
+  auto within = [](float v) { return fminf(v, 3.4e38f); };
+  float bound = within(meta->most_s);
   auto most_of = [&](int c) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(most), c)); };
 #pragma unroll 1
   for (int c0 = 0; c0 < count; c0 += kSpan) {
@@ -545,7 +547,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
         }
         if (c0 + w * kRun >= count) break;
 #pragma unroll
-        for (int i = 0; i < kRun; i++) bound = decay.at(w * kRun + i) * bound + most_of(w * kRun + i);
+        for (int i = 0; i < kRun; i++) bound = within(decay.at(w * kRun + i) * bound + most_of(w * kRun + i));
         S = decay8.at(w * kRun) * S + runs[w][lane];
       }
     }
@@ -553,7 +555,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
     for (int i = 0; i < kRun; i++) {
       const int c = c1 + i;
       if (c >= count) break;
-      const int e = reach > 0.0f ? __builtin_amdgcn_frexp_expf(fminf(reach, 3.0e38f)) - 15 : kNoState;
+      const int e = reach > 0.0f ? __builtin_amdgcn_frexp_expf(reach) - 15 : kNoState;
       const int sh16 = reach > 0.0f ? -e : 0;
       h4 o;
 #pragma unroll
@@ -561,7 +563,7 @@ __global__ __launch_bounds__(kWaves * 64) void scan_kernel(const LinArgs A) {
       *reinterpret_cast<h4 *>(snap + c * step) = o;
       if (blk == 0 && lane == 0) meta[(int64_t)c * A.hkv].e = e;
       const Factors f = decay.at(wave * kRun + i);
-      reach = f * reach + most_of(wave * kRun + i);
+      reach = within(f * reach + most_of(wave * kRun + i));
       mine = f * mine + x[i];
     }
     if constexpr (kWaves == 1) {

@@ -258,3 +258,19 @@ def test_what_strong_decays_leave_of_a_large_state(heads, dtype, size):
         c["states"].clamp_(-2.0 ** 123, 2.0 ** 123)
         c["decay"] = torch.full_like(c["decay"], decay)
         run(c)
+
+
+@pytest.mark.parametrize("n", [400, 1300])
+def test_sizes_whose_sum_passes_fp32(n):
+    """Elements of a state near fp32's largest, in different places: their sum, a bound of the state, is
+    infinite, and is forgotten with them at a reset."""
+    say(f"sum passes fp32 {n}")
+    c = make((1, 1, 64), [n], "f32", seed=50)
+    c["from"] = [0]
+    c["states"][0, 0, 0, 0] = 3e38
+    c["qkv"][:, 65:66] = 0   # nothing else is added there
+    c["qkv"][5, 64:] = 0
+    c["qkv"][5, 64 + 1], c["qkv"][5, 128 + 1] = 1e19, 2e19
+    c["decay"][:] = 0
+    c["decay"][128 + 40] = -INF
+    run(c)
